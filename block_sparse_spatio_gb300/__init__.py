@@ -1,7 +1,7 @@
 """Python binding of the block-sparse spatio-temporal attention library.
 
 Argument marshalling only: every step runs in the CUDA library ``libbss.so``
-(C ABI in ``include/bss.h``).  PyTorch supplies device memory and the current
+(C ABI in ``include/bss.h`` and ``include/bss_block.h``).  PyTorch supplies device memory and the current
 stream.  There is no CPU or PyTorch fallback: if the library is missing or was
 not built for this GPU, every call raises.
 
@@ -28,6 +28,10 @@ ATTN_BQ_SUPPORTED = (128, 256)  # query rows per tile it runs (one or two 128-ro
 ATTN_BKV_SUPPORTED = (64, 128)  # keys per tile it runs (routing, dense control and fused permutation: 128)
 CLASS_SHIFT = 30
 TILE_INDEX_MASK = (1 << 30) - 1
+DTYPE_BF16, DTYPE_F32 = 0, 1
+NORM_NONE, NORM_LAYER, NORM_RMS = 0, 1, 2                      # residual_norm
+HEAD_NORM_NONE, HEAD_NORM_HEAD, HEAD_NORM_TOKEN = 0, 1, 2      # heads_from_tokens: Q/K norm over a head or a token
+PAIR_INTERLEAVED, PAIR_HALVES = 0, 1                           # rotary pairs: channels (2p, 2p + 1) or (p, p + R/2)
 STAT_NAMES = ("full", "boundary", "pad", "skip", "retained_pairs", "exact_retained_pairs", "columns")
 STATUS_NAMES = {0: "BSS_OK", 1: "BSS_ERR_INVALID_ARG", 2: "BSS_ERR_UNSUPPORTED", 3: "BSS_ERR_CUDA",
                 4: "BSS_ERR_TIMEOUT", 5: "BSS_ERR_OOM"}
@@ -73,6 +77,47 @@ class MaskParams:
                            self.temporal_raster_window, self.sink_frames, self.temporal_permuted, self.rounding)
 
 
+class _Rotary(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p * 3), ("length", ctypes.c_int32 * 3), ("pairs", ctypes.c_int32 * 3),
+                ("offset", ctypes.c_int32 * 3), ("pairing", ctypes.c_int32)]
+
+
+class _TokenTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _HeadsOptions(ctypes.Structure):
+    _fields_ = [("norm", ctypes.c_int32), ("eps", ctypes.c_float), ("weight_dtype", ctypes.c_int32),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rotary", ctypes.POINTER(_Rotary))]
+
+
+class _ResidualNormArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "rows_per_group")]
+                + [(n, ctypes.c_int32) for n in ("channels", "stream_dtype", "branch_dtype", "param_dtype", "norm",
+                                                 "y_norm")]
+                + [(n, ctypes.c_float) for n in ("eps", "residual_scale")]
+                + [(n, ctypes.c_void_p) for n in ("x", "y", "r", "h")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "y_stride", "r_stride", "h_stride")]
+                + [(n, ctypes.c_void_p) for n in ("gate", "scale", "shift")]
+                + [(n, ctypes.c_int64) for n in ("gate_stride", "scale_stride", "shift_stride")]
+                + [(n, ctypes.c_void_p) for n in ("weight", "bias", "y_weight", "stats", "y_stats")])
+
+
+class _ResidualNormGrads(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "rows_per_group")]
+                + [(n, ctypes.c_int32) for n in ("channels", "stream_dtype", "branch_dtype", "param_dtype", "norm",
+                                                 "y_norm")]
+                + [("residual_scale", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("r", "y", "dr", "dh", "dx", "dy")]
+                + [(n, ctypes.c_int64) for n in ("r_stride", "y_stride", "dr_stride", "dh_stride", "dx_stride",
+                                                 "dy_stride")]
+                + [(n, ctypes.c_void_p) for n in ("stats", "y_stats", "gate", "scale")]
+                + [(n, ctypes.c_int64) for n in ("gate_stride", "scale_stride")]
+                + [(n, ctypes.c_void_p) for n in ("weight", "bias", "y_weight", "dgate", "dscale", "dshift", "dweight",
+                                                  "dbias", "dy_weight", "workspace")]
+                + [("workspace_bytes", ctypes.c_int64)])
+
+
 EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bss_tile_map_copy_csr",
             "bss_destroy_tile_map", "bss_permute", "bss_sparse_attention", "bss_dense_attention",
             "bss_get_device_status", "bss_status_string", "bss_last_error_message", "bss_version",
@@ -80,7 +125,10 @@ EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bs
             "bss_sparse_attention_fused", "bss_permute_flagged", "bss_sparse_attention_split",
             "bss_diag_wait_timeout", "bss_attention_step", "bss_step_workspace_create",
             "bss_step_workspace_destroy", "bss_step_workspace_wait_stream", "bss_attention_step_host",
-            "bss_permute_flagged_multi")
+            "bss_permute_flagged_multi", "bss_rotary_table", "bss_heads_from_tokens",
+            "bss_heads_from_tokens_backward_workspace", "bss_heads_from_tokens_backward",
+            "bss_attention_step_tokens", "bss_residual_norm", "bss_residual_norm_backward_workspace",
+            "bss_residual_norm_backward")
 
 
 def load(path: str | None = None):
@@ -144,6 +192,24 @@ def load(path: str | None = None):
     lib.bss_step_workspace_wait_stream.restype = st
     lib.bss_attention_step_host.argtypes = [p, p, p, p, p, p, p, p, p]
     lib.bss_attention_step_host.restype = st
+    TT, HO, i64p = ctypes.POINTER(_TokenTensor), ctypes.POINTER(_HeadsOptions), ctypes.POINTER(ctypes.c_int64)
+    lib.bss_rotary_table.argtypes = [p, i32, i32, i32, ctypes.c_double, p, p]
+    lib.bss_rotary_table.restype = st
+    lib.bss_heads_from_tokens.argtypes = [TT, TT, TT, p, p, p, p, i32, MP, HO, p]
+    lib.bss_heads_from_tokens.restype = st
+    lib.bss_heads_from_tokens_backward_workspace.argtypes = [i32, MP, i32, i64p]
+    lib.bss_heads_from_tokens_backward_workspace.restype = st
+    lib.bss_heads_from_tokens_backward.argtypes = [p, p, p, TT, TT, TT, TT, TT, p, p, p, i32, MP, HO, p,
+                                                   ctypes.c_int64, p]
+    lib.bss_heads_from_tokens_backward.restype = st
+    lib.bss_attention_step_tokens.argtypes = [TT, TT, TT, p, p, p, p, i32, HO, p, p, p, p]
+    lib.bss_attention_step_tokens.restype = st
+    lib.bss_residual_norm.argtypes = [ctypes.POINTER(_ResidualNormArgs), p]
+    lib.bss_residual_norm.restype = st
+    lib.bss_residual_norm_backward_workspace.argtypes = [ctypes.POINTER(_ResidualNormGrads), i64p]
+    lib.bss_residual_norm_backward_workspace.restype = st
+    lib.bss_residual_norm_backward.argtypes = [ctypes.POINTER(_ResidualNormGrads), p]
+    lib.bss_residual_norm_backward.restype = st
     _lib = lib
     return lib
 
@@ -538,3 +604,391 @@ def attention_step_host(hQ, hK, hV, hO, tile_map: TileMap, head_is_temporal, wor
                                           tile_map.handle, workspace.handle, ctypes.c_void_p(done.cuda_event),
                                           _stream(stream)))
     return done
+
+
+# ---------------------------------------------------------------- around the attention step (include/bss_block.h)
+
+def _on_one_device(*named):
+    """Every given tensor on the current device (kernels are launched there)."""
+    import torch
+    current = torch.cuda.current_device()
+    for t, n in named:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        if t.device.index != current:
+            raise ValueError(f"{n} is on {t.device}, the current device is cuda:{current}")
+
+
+def _exact(t, name, dtype, shape):
+    """A given contiguous tensor of this type and shape."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _dtype_code(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _one_dtype(*named):
+    """The code of the one type that every given tensor has."""
+    code = None
+    for t, n in named:
+        if t is None:
+            continue
+        c = _dtype_code(t, n)
+        if code is not None and c != code:
+            raise ValueError(f"{', '.join(m for u, m in named if u is not None)} must have one type")
+        code = c
+    return DTYPE_F32 if code is None else code
+
+
+def _workspace(workspace, nbytes, stream):
+    """The caller's workspace, or one from torch's allocator that belongs to the
+    stream the call runs on."""
+    import torch
+    if workspace is not None:
+        _on_one_device((workspace, "workspace"))
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        return workspace
+    if nbytes == 0:
+        return None
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+
+
+def rotary_table(length: int, pairs: int, base: float = 10000.0, dim: int | None = None, positions=None, out=None,
+                 stream=None):
+    """(cos, sin) of one rotary axis, float32 [length][pairs][2] (``bss_rotary_table``):
+    position i (or positions[i], a float64 CUDA tensor) times base^(-2 j / dim) for
+    pair j; dim defaults to 2 * pairs.  Angles are taken in 64 bits."""
+    import torch
+    if length <= 0 or pairs <= 0:
+        raise ValueError("length and pairs must be positive")
+    if out is None:
+        out = torch.empty(length, pairs, 2, dtype=torch.float32, device="cuda")
+    _on_one_device((out, "out"), (positions, "positions"))
+    _exact(out, "out", torch.float32, (length, pairs, 2))
+    _exact(positions, "positions", torch.float64, (length,))
+    _check(load().bss_rotary_table(_ptr(positions), length, pairs, 2 * pairs if dim is None else dim, float(base),
+                                   _ptr(out), _stream(stream)))
+    return out
+
+
+@dataclass(frozen=True)
+class Rotary:
+    """Rotary positions of the (time, height, width) axes for ``heads_from_tokens``.
+
+    time, height, width: float32 CUDA tables [positions][pairs][2] of (cos, sin)
+    (``rotary_table`` makes one), None or 0 pairs for an axis that turns nothing;
+    the pairs of the three are dealt to the channels in this order.  Token (f, h,
+    w) uses rows offset + (f, h, w).  pairing: PAIR_INTERLEAVED or PAIR_HALVES."""
+    time: object = None
+    height: object = None
+    width: object = None
+    offset: tuple = (0, 0, 0)
+    pairing: int = PAIR_INTERLEAVED
+
+    def __post_init__(self):
+        import torch
+        r = _Rotary()
+        for i, (t, n) in enumerate(((self.time, "time"), (self.height, "height"), (self.width, "width"))):
+            if t is None:
+                continue
+            if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != 2:
+                raise ValueError(f"rotary table {n} must be a tensor [positions][pairs][2]")
+            _dev_tensor(t, f"rotary table {n}", torch.float32)
+            r.table[i], r.length[i], r.pairs[i] = t.data_ptr(), t.shape[0], t.shape[1]
+        if len(self.offset) != 3:
+            raise ValueError("offset must have three entries")
+        for i in range(3):
+            r.offset[i] = self.offset[i]
+        r.pairing = self.pairing
+        object.__setattr__(self, "_c", r)
+
+    def tables(self):
+        return (self.time, "rotary table time"), (self.height, "rotary table height"), (self.width, "rotary table width")
+
+
+def _token_tensor(t, name, shape):
+    """A [N][H][d] bf16 tensor with any token and head strides -> its C form."""
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape} (tokens, heads, channels)")
+    s = t.stride()
+    if s[2] != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    return ctypes.byref(_TokenTensor(t.data_ptr(), s[0], s[1]))
+
+
+def _heads_options(H, d, rotary, q_weight, k_weight, norm, eps):
+    import torch
+    if norm == HEAD_NORM_NONE and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights are given without a norm")
+    if rotary is not None and not isinstance(rotary, Rotary):
+        raise ValueError("rotary must be a Rotary")
+    width = H * d if norm == HEAD_NORM_TOKEN else d
+    code = _one_dtype((q_weight, "q_weight"), (k_weight, "k_weight"))
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _exact(w, n, w.dtype, (width,))
+    return _HeadsOptions(norm, eps, code, None if q_weight is None else q_weight.data_ptr(),
+                         None if k_weight is None else k_weight.data_ptr(),
+                         None if rotary is None else ctypes.pointer(rotary._c)), width
+
+
+def _heads_of(*tensors, axis):
+    for t in tensors:
+        if t is not None:
+            if t.dim() != 3:
+                raise ValueError("Q, K and V have three dimensions")
+            return t.shape[axis]
+    raise ValueError("no tensor given")
+
+
+def heads_from_tokens(q, k, v, Qh, Kh, Vh, params: MaskParams, head_is_temporal=None, rotary: Rotary | None = None,
+                      q_weight=None, k_weight=None, norm: int = HEAD_NORM_NONE, eps: float = 1e-6, stream=None):
+    """Qh, Kh, Vh <- the heads of token-major q, k, v in one pass (``bss_heads_from_tokens``).
+
+    q, k, v: bf16 [N][H][d] CUDA tensors whose tokens and heads may be strided
+    (views of a packed projection, or of head-major tensors) or broadcast; Qh,
+    Kh, Vh: contiguous bf16 [H][N][d], heads with flag 1 in (H,W,F) order, the
+    others in (F,H,W) order -- what ``sparse_attention`` takes.  Q and K are
+    RMS-normed over each head (HEAD_NORM_HEAD, weights [d]) or over all heads of a
+    token (HEAD_NORM_TOKEN, weights [H * d]) and turned by ``rotary``.  Each pair
+    (q, Qh), (k, Kh), (v, Vh) may be None."""
+    import torch
+    H, d, N = _heads_of(q, k, v, axis=1), params.head_dim, params.N
+    _on_one_device((q, "q"), (k, "k"), (v, "v"), (Qh, "Qh"), (Kh, "Kh"), (Vh, "Vh"), (q_weight, "q_weight"),
+                   (k_weight, "k_weight"), (head_is_temporal, "head_is_temporal"),
+                   *(rotary.tables() if isinstance(rotary, Rotary) else ()))
+    for t, n in ((Qh, "Qh"), (Kh, "Kh"), (Vh, "Vh")):
+        _exact(t, n, torch.bfloat16, (H, N, d))
+    _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,))
+    options, _ = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps)
+    shape = (N, H, d)
+    _check(load().bss_heads_from_tokens(_token_tensor(q, "q", shape), _token_tensor(k, "k", shape),
+                                        _token_tensor(v, "v", shape), _ptr(Qh), _ptr(Kh), _ptr(Vh),
+                                        _ptr(head_is_temporal), H, ctypes.byref(params.c()), ctypes.byref(options),
+                                        _stream(stream)))
+    return Qh, Kh, Vh
+
+
+def heads_from_tokens_backward(dQh, dKh, dVh, dq, dk, dv, params: MaskParams, head_is_temporal=None,
+                               rotary: Rotary | None = None, q=None, k=None, q_weight=None, k_weight=None,
+                               dq_weight=None, dk_weight=None, norm: int = HEAD_NORM_NONE, eps: float = 1e-6,
+                               workspace=None, stream=None):
+    """Gradients of ``heads_from_tokens`` (``bss_heads_from_tokens_backward``).
+
+    dQh, dKh, dVh: bf16 [H][N][d] in the layout of its outputs; dq, dk, dv: bf16
+    [N][H][d] outputs, strided as the inputs may be (e.g. views of one packed
+    gradient).  With a norm, q and k are the forward inputs, and dq_weight,
+    dk_weight optional float32 outputs of the weights' shapes, overwritten.
+    workspace: memory for the weights' partial sums (taken from torch's allocator
+    when None)."""
+    import torch
+    H, d, N = _heads_of(dQh, dKh, dVh, axis=0), params.head_dim, params.N
+    _on_one_device((dQh, "dQh"), (dKh, "dKh"), (dVh, "dVh"), (dq, "dq"), (dk, "dk"), (dv, "dv"), (q, "q"), (k, "k"),
+                   (q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"), (dk_weight, "dk_weight"),
+                   (head_is_temporal, "head_is_temporal"),
+                   *(rotary.tables() if isinstance(rotary, Rotary) else ()))
+    for t, n in ((dQh, "dQh"), (dKh, "dKh"), (dVh, "dVh")):
+        _exact(t, n, torch.bfloat16, (H, N, d))
+    _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,))
+    options, width = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps)
+    _exact(dq_weight, "dq_weight", torch.float32, (width,))
+    _exact(dk_weight, "dk_weight", torch.float32, (width,))
+    shape, lib, mp = (N, H, d), load(), params.c()
+    if dq_weight is not None or dk_weight is not None:
+        need = ctypes.c_int64()
+        _check(lib.bss_heads_from_tokens_backward_workspace(H, ctypes.byref(mp), norm, ctypes.byref(need)))
+        workspace = _workspace(workspace, need.value, stream)
+    else:
+        workspace = None
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib.bss_heads_from_tokens_backward(_ptr(dQh), _ptr(dKh), _ptr(dVh), _token_tensor(q, "q", shape),
+                                              _token_tensor(k, "k", shape), _token_tensor(dq, "dq", shape),
+                                              _token_tensor(dk, "dk", shape), _token_tensor(dv, "dv", shape),
+                                              _ptr(dq_weight), _ptr(dk_weight), _ptr(head_is_temporal), H,
+                                              ctypes.byref(mp), ctypes.byref(options), _ptr(workspace), nbytes,
+                                              _stream(stream)))
+    return dq, dk, dv
+
+
+def attention_step_tokens(q, k, v, O, tile_map: TileMap, head_is_temporal, Qh, Kh, Vh, rotary: Rotary | None = None,
+                          q_weight=None, k_weight=None, norm: int = HEAD_NORM_NONE, eps: float = 1e-6, lse=None,
+                          stream=None):
+    """The per-layer path from token-major projections (``bss_attention_step_tokens``):
+    ``heads_from_tokens`` into the workspaces Qh, Kh, Vh, then block-sparse
+    attention with every head's O rows in (F,H,W) order, in two launches.  lse as
+    in ``attention_step``."""
+    import torch
+    p = tile_map.params
+    H, d, N = _heads_of(q, axis=1), p.head_dim, p.N
+    named = [(O, "O"), (Qh, "Qh"), (Kh, "Kh"), (Vh, "Vh")]
+    _on_one_device((q, "q"), (k, "k"), (v, "v"), *named, (q_weight, "q_weight"), (k_weight, "k_weight"),
+                   (head_is_temporal, "head_is_temporal"), (lse, "lse"),
+                   *(rotary.tables() if isinstance(rotary, Rotary) else ()))
+    for t, n in named:
+        if t is None:
+            raise ValueError(f"{n} must be a CUDA tensor")
+        _exact(t, n, torch.bfloat16, (H, N, d))
+    _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,))
+    _exact(lse, "lse", torch.float32, (H, N))
+    options, _ = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps)
+    shape = (N, H, d)
+    _check(load().bss_attention_step_tokens(_token_tensor(q, "q", shape), _token_tensor(k, "k", shape),
+                                            _token_tensor(v, "v", shape), _ptr(O), _ptr(lse), tile_map.handle,
+                                            _ptr(head_is_temporal), H, ctypes.byref(options), _ptr(Qh), _ptr(Kh),
+                                            _ptr(Vh), _stream(stream)))
+    return O
+
+
+def _row_tensor(t, name, dtype, rows, channels, like=None):
+    """(pointer, row stride) of a given [rows][channels] tensor with any row stride."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != (rows, channels):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be ({rows}, {channels})")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    s = t.stride()
+    if s[1] != 1:
+        raise ValueError(f"{name}: the channels of a row must be contiguous")
+    return t.data_ptr(), s[0]
+
+
+def _row_shape(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor [rows][channels]")
+    return t.shape
+
+
+def residual_norm(x, y=None, r=None, h=None, gate=None, scale=None, shift=None, weight=None, bias=None, y_weight=None,
+                  norm: int = NORM_LAYER, y_norm: int = NORM_NONE, rows_per_group: int | None = None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, stats=None, y_stats=None, stream=None):
+    """The residual update of a block and the norm in front of the next one, in
+    one pass (``bss_residual_norm``)::
+
+        r = residual_scale * x + gate * y_norm(y) * y_weight
+        h = (norm(r) * weight + bias) * (1 + scale) + shift
+
+    x, r: [rows][channels] bf16 or float32 (the stream); y, h: bf16, or float32
+    with a float32 stream.  Without y only h is made, from x.  r may be x, and h
+    may be y (in place).  gate, scale, shift: [groups][channels], row i in group
+    i // rows_per_group (default: one group); weight, bias, y_weight: [channels];
+    all of these float32 or all bf16, all optional.  norm, y_norm: NORM_*.  stats,
+    y_stats: float32 [rows][2] outputs, (mean, 1 / deviation) of each row, for the
+    backward pass.  Returns (r, h)."""
+    import torch
+    rows, channels = _row_shape(x, "x")
+    _on_one_device((x, "x"), (y, "y"), (r, "r"), (h, "h"), (gate, "gate"), (scale, "scale"), (shift, "shift"),
+                   (weight, "weight"), (bias, "bias"), (y_weight, "y_weight"), (stats, "stats"), (y_stats, "y_stats"))
+    if rows_per_group is None:
+        rows_per_group = rows
+    if rows_per_group <= 0:
+        raise ValueError("rows_per_group must be positive")
+    groups = -(-rows // rows_per_group)
+    a = _ResidualNormArgs(rows=rows, rows_per_group=rows_per_group, channels=channels, norm=norm, y_norm=y_norm, eps=eps,
+                          residual_scale=residual_scale)
+    a.stream_dtype = _dtype_code(x, "x")
+    a.branch_dtype = _one_dtype((y, "y"), (h, "h")) if y is not None or h is not None else DTYPE_BF16
+    a.param_dtype = _one_dtype((gate, "gate"), (scale, "scale"), (shift, "shift"), (weight, "weight"), (bias, "bias"),
+                               (y_weight, "y_weight"))
+    a.x, a.x_stride = _row_tensor(x, "x", None, rows, channels)
+    a.y, a.y_stride = _row_tensor(y, "y", None, rows, channels)
+    a.r, a.r_stride = _row_tensor(r, "r", x.dtype, rows, channels)
+    a.h, a.h_stride = _row_tensor(h, "h", None, rows, channels)
+    a.gate, a.gate_stride = _row_tensor(gate, "gate", None, groups, channels)
+    a.scale, a.scale_stride = _row_tensor(scale, "scale", None, groups, channels)
+    a.shift, a.shift_stride = _row_tensor(shift, "shift", None, groups, channels)
+    for t, n in ((weight, "weight"), (bias, "bias"), (y_weight, "y_weight")):
+        if t is not None:
+            _exact(t, n, t.dtype, (channels,))
+            setattr(a, n, t.data_ptr())
+    for t, n in ((stats, "stats"), (y_stats, "y_stats")):
+        if t is not None:
+            _exact(t, n, torch.float32, (rows, 2))
+            setattr(a, n, t.data_ptr())
+    _check(load().bss_residual_norm(ctypes.byref(a), _stream(stream)))
+    return r, h
+
+
+def residual_norm_backward(r, y=None, dr=None, dh=None, dx=None, dy=None, stats=None, y_stats=None, gate=None,
+                           scale=None, weight=None, bias=None, y_weight=None, dgate=None, dscale=None, dshift=None,
+                           dweight=None, dbias=None, dy_weight=None, norm: int = NORM_LAYER, y_norm: int = NORM_NONE,
+                           rows_per_group: int | None = None, residual_scale: float = 1.0, workspace=None,
+                           stream=None):
+    """Gradients of ``residual_norm`` (``bss_residual_norm_backward``).
+
+    r: the updated stream it wrote (x when there was no y), with the stats it
+    kept; dr, dh: gradients of r and h (one may be None).  Outputs: dx (required;
+    may be dr), dy (with y; may be dh), and any of dgate, dscale, dshift (float32
+    [groups][channels]) and dweight, dbias, dy_weight (float32 [channels]), all
+    overwritten.  Every sum over rows is taken in a fixed order.  workspace:
+    memory for partial sums (taken from torch's allocator when None)."""
+    import torch
+    rows, channels = _row_shape(dx, "dx")
+    rest = [(r, "r"), (y, "y"), (dr, "dr"), (dh, "dh"), (dx, "dx"), (dy, "dy"), (stats, "stats"), (y_stats, "y_stats"),
+            (gate, "gate"), (scale, "scale"), (weight, "weight"), (bias, "bias"), (y_weight, "y_weight"),
+            (dgate, "dgate"), (dscale, "dscale"), (dshift, "dshift"), (dweight, "dweight"), (dbias, "dbias"),
+            (dy_weight, "dy_weight")]
+    _on_one_device(*rest)
+    if rows_per_group is None:
+        rows_per_group = rows
+    if rows_per_group <= 0:
+        raise ValueError("rows_per_group must be positive")
+    groups = -(-rows // rows_per_group)
+    a = _ResidualNormGrads(rows=rows, rows_per_group=rows_per_group, channels=channels, norm=norm, y_norm=y_norm,
+                           residual_scale=residual_scale)
+    a.stream_dtype = _one_dtype((dx, "dx"), (dr, "dr"), (r, "r"))
+    a.branch_dtype = _one_dtype((y, "y"), (dy, "dy"), (dh, "dh")) if y is not None or dh is not None else DTYPE_BF16
+    a.param_dtype = _one_dtype((gate, "gate"), (scale, "scale"), (weight, "weight"), (bias, "bias"),
+                               (y_weight, "y_weight"))
+    for t, n in rest[:6]:
+        p, stride = _row_tensor(t, n, None, rows, channels)
+        setattr(a, n, p)
+        setattr(a, n + "_stride", stride)
+    a.gate, a.gate_stride = _row_tensor(gate, "gate", None, groups, channels)
+    a.scale, a.scale_stride = _row_tensor(scale, "scale", None, groups, channels)
+    for t, n, shape in ((stats, "stats", (rows, 2)), (y_stats, "y_stats", (rows, 2)), (dgate, "dgate", (groups, channels)),
+                        (dscale, "dscale", (groups, channels)), (dshift, "dshift", (groups, channels)),
+                        (dweight, "dweight", (channels,)), (dbias, "dbias", (channels,)),
+                        (dy_weight, "dy_weight", (channels,))):
+        if t is not None:
+            _exact(t, n, torch.float32, shape)
+            setattr(a, n, t.data_ptr())
+    for t, n in ((weight, "weight"), (bias, "bias"), (y_weight, "y_weight")):
+        if t is not None:
+            _exact(t, n, t.dtype, (channels,))
+            setattr(a, n, t.data_ptr())
+    lib = load()
+    need = ctypes.c_int64()
+    _check(lib.bss_residual_norm_backward_workspace(ctypes.byref(a), ctypes.byref(need)))
+    workspace = _workspace(workspace, need.value, stream)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(lib.bss_residual_norm_backward(ctypes.byref(a), _stream(stream)))
+    return dx, dy

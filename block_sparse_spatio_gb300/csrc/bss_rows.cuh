@@ -1,0 +1,177 @@
+// bss_rows.cuh -- what the row operators around the attention step share:
+// 8-channel vectors of bf16 or float rows, sums over parts of a block, the
+// fixed-order sum of per-block partial results, and host-side overlap checks of
+// strided tensors.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "bss_block.h"
+#include "bss_internal.h"
+
+namespace bss {
+
+// ---------------------------------------------------------------- vectors
+// Rows move in vectors of 8 channels: 16 bytes of bf16, 32 of float.
+template <typename T>
+struct Raw8 {
+    uint4 q[sizeof(T) / 2];
+};
+
+// Row data is read once: keep it out of L1.  Not the read-only path, since an
+// output may alias its input exactly (a thread reads before it writes).
+__device__ __forceinline__ uint4 ld_row(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_row(void* p, const uint4& v) {
+    asm volatile("st.global.cs.v4.u32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw(const T* p) {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.q[i] = ld_row(reinterpret_cast<const uint4*>(p) + i);
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> zero_raw() {
+    Raw8<T> r;
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.q[i] = make_uint4(0, 0, 0, 0);
+    return r;
+}
+
+__device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
+    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        v[4 * i] = __uint_as_float(r.q[i].x);
+        v[4 * i + 1] = __uint_as_float(r.q[i].y);
+        v[4 * i + 2] = __uint_as_float(r.q[i].z);
+        v[4 * i + 3] = __uint_as_float(r.q[i].w);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+    st_row(p, make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])));
+}
+
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        st_row(p + 4 * i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+}
+
+// Parameters (weights, modulations) are shared by many rows: read through L1.
+__device__ __forceinline__ void load_param8(const void* base, int64_t index, int dtype, float (&v)[8]) {
+    if (dtype == BSS_DTYPE_F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + index);
+        const float4 a = __ldg(p), b = __ldg(p + 1);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        Raw8<__nv_bfloat16> r;
+        r.q[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + index));
+        unpack(r, v);
+    }
+}
+
+__device__ __forceinline__ float load_param(const void* base, int64_t index, int dtype) {
+    return dtype == BSS_DTYPE_F32 ? __ldg(static_cast<const float*>(base) + index)
+                                  : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[index]);
+}
+
+// ---------------------------------------------------------------- sums
+// Sum over aligned groups of L lanes (L a power of two); every lane gets it.
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+
+// ---------------------------------------------------------------- host side
+inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The bytes that a strided tensor touches: `n` runs of `extent` bytes, `stride`
+// bytes apart.
+struct Region {
+    uintptr_t lo = 0;
+    int64_t n = 0, stride = 0, extent = 0;
+    bool self_overlap = false;
+    uintptr_t hi() const { return lo + static_cast<uintptr_t>((n - 1) * stride + extent); }
+};
+
+// rows x width elements
+inline Region region_2d(const void* p, int64_t rows, int64_t stride, int64_t width, int64_t esize) {
+    Region r;
+    r.lo = reinterpret_cast<uintptr_t>(p);
+    r.n = rows;
+    r.stride = rows > 1 ? stride * esize : 0;
+    r.extent = width * esize;
+    r.self_overlap = rows > 1 && stride < width;
+    return r;
+}
+
+// [n0][n1][width] elements with strides s0, s1: runs over the larger stride
+inline Region region_3d(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width, int64_t esize) {
+    if (n0 <= 1) s0 = 0;
+    if (n1 <= 1) s1 = 0;
+    if (n1 > 1 && (n0 <= 1 || s1 > s0)) {
+        int64_t t = n0;
+        n0 = n1, n1 = t;
+        t = s0, s0 = s1, s1 = t;
+    }
+    Region r;
+    r.lo = reinterpret_cast<uintptr_t>(p);
+    const int64_t inner = (n1 - 1) * s1 + width;
+    r.self_overlap = (n1 > 1 && s1 < width) || (n0 > 1 && s0 < inner);
+    if (n0 > 1 && s0 < inner) {  // interleaved or broadcast: one run over everything
+        r.n = 1;
+        r.extent = ((n0 - 1) * s0 + inner) * esize;
+        return r;
+    }
+    r.n = n0;
+    r.stride = s0 * esize;
+    r.extent = inner * esize;
+    return r;
+}
+
+// Whether two tensors certainly share no byte (views of one tensor that differ
+// in a column range are told apart when their runs have the same stride).
+inline bool disjoint(const Region& a, const Region& b) {
+    if (a.hi() <= b.lo || b.hi() <= a.lo) return true;
+    if (a.n <= 1 || b.n <= 1 || a.stride != b.stride || a.stride == 0) return false;
+    const int64_t s = a.stride;
+    int64_t d = static_cast<int64_t>(b.lo) - static_cast<int64_t>(a.lo);
+    d %= s;
+    if (d < 0) d += s;
+    return d >= a.extent && s - d >= b.extent;
+}
+
+}  // namespace bss

@@ -388,4 +388,7 @@ int32_t bss_version(void);
 }
 #endif
 
+/* The operators on either side of the attention step. */
+#include "bss_block.h"
+
 #endif /* BSS_H_ */
