@@ -15,11 +15,15 @@
 // HBM-bound: forward reads and writes Q, K, V once (12 bytes an element of one
 // tensor), backward reads dQ, dK, dV, Q, K and writes dq, dk, dv (16 bytes).
 //
-// A thread owns one 16-byte piece (8 channels) of one head and walks over
-// tokens, so the weights and, in the backward pass, the weights' gradients stay
-// in its registers.  d / 8 neighbouring lanes hold a head's row: global rows are
-// read and written whole (128 or 256 bytes).  The angles of a block's tokens are
-// gathered into shared memory once and used by all heads of Q and K.
+// A warp takes a whole token: lane l holds the 16-byte pieces (8 channels) l,
+// l + 32, ... of its heads, so a piece's place in its head, and with it the angles
+// of its rotary pairs, is the same for all the heads of Q and K that the lane
+// holds, a token's coordinates are the same for the warp, and the norm's sums need
+// no barrier.  Every lane copies its own pieces of the next token into its own
+// slots of shared memory (cp.async, two stages) while it works on this one: loads
+// stay in flight without holding registers, and the pieces are walked in a loop.
+// Wide tokens are shared by several warps when the norm is over the token, else
+// their heads go to several grid columns.
 #include <cstring>
 
 #include "bss_rows.cuh"
@@ -27,8 +31,7 @@
 namespace bss {
 namespace {
 
-constexpr int kMaxThreads = 1024;
-constexpr int kMaxTokenWidth = 8192;  // H * head_dim of the norm over a token: one thread a piece
+constexpr int kMaxTokenWidth = 8192;  // H * head_dim of the norm over a token
 
 struct RotaryDev {
     const float2* table[3];
@@ -45,360 +48,533 @@ struct HeadsArgs {
     int64_t xts[2], xhs[2];       // strides of x
     const void* weight[2];
     int32_t weight_dtype;
-    float eps;
+    float eps, inv_width;         // 1 / channels of the norm's mean
     RotaryDev rot;
     const uint8_t* flags;
-    uint32_t N, F, S, Ws, H;
-    int32_t heads_per_block;      // heads a block covers (all of them for the norm over a token)
-    int32_t groups;               // tokens side by side in a block
-    int32_t want_dweight;
-    float* partial;               // backward: [blocks][2][width]
+    FastDiv by_S, by_Ws;
+    uint32_t N, F, S, H;
+    int32_t pieces;               // 16-byte pieces of a head: 8 or 16
+    int32_t heads_per_block;      // heads of a token that a block's grid column covers
+    float* partial;               // backward: [blocks][2][width], or NULL
 };
 
-// Shared-memory layout of one buffer (two alternate between iterations).
-struct Smem {
-    int cs;       // float2 [tokens][d / 2]
-    int sums;     // float [tensors x values][tokens][heads padded to 4]
-    int bytes;    // of one buffer
-    int hpad;
+// The pieces a lane holds: piece `piece` of the heads head0, head0 + step, ...
+struct Lane {
+    int piece, head0, step, count;  // count: how many of them exist
+    uint32_t temporal;              // bit i: head i is permuted
 };
 
-__host__ __device__ inline Smem smem_layout(int tokens, int pieces, int heads, int values, bool rotary, bool token_norm) {
-    Smem s;
-    s.hpad = (heads + 3) & ~3;
-    s.cs = 0;
-    s.sums = rotary ? tokens * pieces * 4 * 8 : 0;
-    s.bytes = s.sums + (token_norm ? values * tokens * s.hpad * 4 : 0);
-    s.bytes = (s.bytes + 15) & ~15;
-    return s;
+// `warp`: which of the W warps of the token this is.
+template <int W, int VPT>
+__device__ __forceinline__ Lane lane_of(const HeadsArgs& a, int warp) {
+    Lane l;
+    const int lane = threadIdx.x & 31;
+    const int per = 32 / a.pieces;  // heads side by side in a warp
+    l.piece = lane & (a.pieces - 1);
+    const int first = blockIdx.y * a.heads_per_block;
+    const int last = min(static_cast<int>(a.H), first + a.heads_per_block);
+    l.head0 = first + warp * per + lane / a.pieces;
+    l.step = W * per;
+    l.count = l.head0 < last ? min(VPT, (last - l.head0 + l.step - 1) / l.step) : 0;
+    l.temporal = 0;
+    if (a.flags != nullptr)
+        for (int i = 0; i < l.count; ++i) l.temporal |= (a.flags[l.head0 + i * l.step] != 0 ? 1u : 0u) << i;
+    return l;
 }
 
-// (cos, sin) of the block's tokens, pair by pair; pairs past the rotated ones
-// get the identity.
-template <int P>
-__device__ __forceinline__ void fill_angles(const HeadsArgs& a, float2* cs, uint32_t token0, int tokens) {
-    constexpr int kPairs = P * 4;
-    for (int e = threadIdx.x; e < tokens * kPairs; e += blockDim.x) {
-        const uint32_t n = token0 + e / kPairs;
-        const int p = e % kPairs;
-        float2 v = make_float2(1.0f, 0.0f);
-        if (n < a.N && p < a.rot.first[3]) {
-            const uint32_t f = n / a.S, s = n - f * a.S;
-            const uint32_t h = s / a.Ws, w = s - h * a.Ws;
-            const int axis = p < a.rot.first[1] ? 0 : (p < a.rot.first[2] ? 1 : 2);
-            const int64_t row = (axis == 0 ? f : axis == 1 ? h : w) + a.rot.offset[axis];
-            v = __ldg(a.rot.table[axis] + row * a.rot.pairs[axis] + (p - a.rot.first[axis]));
-        }
-        cs[e] = v;
+struct Token {
+    uint32_t f, h, w, temporal_row;
+};
+
+__device__ __forceinline__ Token token_of(const HeadsArgs& a, uint32_t n) {
+    Token t;
+    t.f = a.by_S.div(n);
+    const uint32_t s = n - t.f * a.S;
+    t.temporal_row = s * a.F + t.f;
+    t.h = a.by_Ws.div(s);
+    t.w = s - t.h * a.by_Ws.d;
+    return t;
+}
+
+// A lane's rotary pairs: 4 interleaved ones, or for halves the 8 whose other
+// channels another lane holds.  Per pair the table entry of position 0, the
+// table's row length and the axis.
+template <bool HALVES>
+struct Pairs {
+    static constexpr int kCount = HALVES ? 8 : 4;
+    const float2* entry[kCount];
+    int32_t stride[kCount];
+    uint32_t axes;   // 2 bits a pair; 3: not rotated
+    int other;       // lane of the paired piece
+    float sign;      // of the sine there
+};
+
+template <bool HALVES>
+__device__ __forceinline__ Pairs<HALVES> pairs_of(const HeadsArgs& a, int piece) {
+    Pairs<HALVES> r;
+    int pair = piece * 4;
+    bool in = true;
+    r.other = threadIdx.x & 31;
+    r.sign = 1.0f;
+    if (HALVES) {
+        const int half = a.rot.first[3] / 8;  // pieces per half
+        const bool lower = piece < half;
+        in = piece < 2 * half;
+        const int other = in ? (lower ? piece + half : piece - half) : piece;
+        r.other = (threadIdx.x & 31 & ~(a.pieces - 1)) | other;
+        r.sign = lower ? -1.0f : 1.0f;
+        pair = (lower ? piece : other) * 8;
     }
+    r.axes = 0;
+#pragma unroll
+    for (int j = 0; j < Pairs<HALVES>::kCount; ++j) {
+        const int p = pair + j;
+        const int axis = !in || p >= a.rot.first[3] ? 3 : p < a.rot.first[1] ? 0 : p < a.rot.first[2] ? 1 : 2;
+        r.axes |= static_cast<uint32_t>(axis) << (2 * j);
+        r.entry[j] = axis == 3 ? nullptr
+                               : a.rot.table[axis] + static_cast<int64_t>(a.rot.offset[axis]) * a.rot.pairs[axis] +
+                                     (p - a.rot.first[axis]);
+        r.stride[j] = axis == 3 ? 0 : a.rot.pairs[axis];
+    }
+    return r;
 }
 
-// Turn 8 channels by their angles (sign = -1: back).  Interleaved pairs lie in
-// the thread; the two halves' channels in lanes R/16 pieces apart.
-template <int P, bool HALVES>
-__device__ __forceinline__ void rotate8(float (&v)[8], const float2* cs, int piece, int rotated, float sign) {
+// One token's angles for a lane's pairs; the identity where nothing turns.
+template <bool HALVES>
+struct Turn {
+    float2 c[HALVES ? 4 : 2], s[HALVES ? 4 : 2];
+};
+
+template <bool HALVES>
+__device__ __forceinline__ Turn<HALVES> load_turn(const Pairs<HALVES>& pr, const Token& t) {
+    Turn<HALVES> r;
+#pragma unroll
+    for (int j = 0; j < Pairs<HALVES>::kCount; ++j) {
+        const uint32_t axis = pr.axes >> (2 * j) & 3u;
+        float2 v = make_float2(1.0f, 0.0f);
+        const uint32_t at = axis == 0 ? t.f : axis == 1 ? t.h : t.w;
+        if (axis != 3) v = __ldg(pr.entry[j] + static_cast<int64_t>(at) * pr.stride[j]);
+        if (j & 1)
+            r.c[j / 2].y = v.x, r.s[j / 2].y = v.y;
+        else
+            r.c[j / 2].x = v.x, r.s[j / 2].x = v.y;
+    }
+    return r;
+}
+
+// Turn 8 channels by their angles, or back (BACK).  Interleaved pairs lie in the
+// thread (even channels apart from odd ones), those of halves in two lanes.
+template <bool HALVES, bool BACK>
+__device__ __forceinline__ void rotate8(V8& v, const Turn<HALVES>& t, const Pairs<HALVES>& pr) {
     if (!HALVES) {
-        const float4* c4 = reinterpret_cast<const float4*>(cs + piece * 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float4 c = c4[i];
-            const float a0 = v[4 * i], b0 = v[4 * i + 1], a1 = v[4 * i + 2], b1 = v[4 * i + 3];
-            v[4 * i] = a0 * c.x - sign * (b0 * c.y);
-            v[4 * i + 1] = b0 * c.x + sign * (a0 * c.y);
-            v[4 * i + 2] = a1 * c.z - sign * (b1 * c.w);
-            v[4 * i + 3] = b1 * c.z + sign * (a1 * c.w);
+            const float2 minus = make_float2(-t.s[i].x, -t.s[i].y);
+            const float2 a = v.p[2 * i], b = v.p[2 * i + 1];
+            v.p[2 * i] = __ffma2_rn(b, BACK ? t.s[i] : minus, __fmul2_rn(a, t.c[i]));
+            v.p[2 * i + 1] = __ffma2_rn(a, BACK ? minus : t.s[i], __fmul2_rn(b, t.c[i]));
         }
     } else {
-        const int half = rotated / 16;  // pieces per half
-        const bool lower = piece < half, in = piece < 2 * half;
-        const int other = in ? (lower ? piece + half : piece - half) : piece;
-        const int lane = (threadIdx.x & 31 & ~(P - 1)) | other;
-        const float4* c4 = reinterpret_cast<const float4*>(cs + (lower ? piece : other) * 8);
-        const float sg = lower ? -sign : sign;
+        const float2 sg = f2(BACK ? -pr.sign : pr.sign);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float o0 = __shfl_sync(0xFFFFFFFFu, v[2 * i], lane);
-            const float o1 = __shfl_sync(0xFFFFFFFFu, v[2 * i + 1], lane);
-            if (in) {
-                const float4 c = c4[i];
-                v[2 * i] = v[2 * i] * c.x + sg * (o0 * c.y);
-                v[2 * i + 1] = v[2 * i + 1] * c.z + sg * (o1 * c.w);
-            }
+            const float2 o = make_float2(__shfl_sync(0xFFFFFFFFu, v.p[i].x, pr.other),
+                                         __shfl_sync(0xFFFFFFFFu, v.p[i].y, pr.other));
+            v.p[i] = __ffma2_rn(o, __fmul2_rn(t.s[i], sg), __fmul2_rn(v.p[i], t.c[i]));
         }
     }
 }
 
-__device__ __forceinline__ uint32_t head_row(const HeadsArgs& a, uint32_t n, bool temporal) {
-    if (!temporal) return n;
-    const uint32_t f = n / a.S;
-    return (n - f * a.S) * a.F + f;
+// Sum over the lanes of a head (8 or 16).
+__device__ __forceinline__ float head_sum(float v, int pieces) {
+    v = lane_sum<8>(v);
+    return pieces == 16 ? v + __shfl_xor_sync(0xFFFFFFFFu, v, 8) : v;
 }
 
-// Sum of a token's per-head values in shared memory (padding heads hold 0).
-__device__ __forceinline__ float sum_heads(const float* p, int hpad) {
-    const float4* q = reinterpret_cast<const float4*>(p);
-    float s = 0.0f;
-    for (int i = 0; i < hpad / 4; ++i) {
-        const float4 v = q[i];
-        s += (v.x + v.y) + (v.z + v.w);
+// Sums of NV values (2 or 4) over a token's W warps; every thread gets them.
+// `buf` holds NV x W floats a use, used in turn with another, so the barrier of
+// one use also ends the reads of the one before.  Tokens side by side in a block
+// (`group`) wait apart from one another.
+template <int NV, int W>
+__device__ __forceinline__ void token_sum(float (&v)[NV], float* buf, int group, int warp) {
+    const float s = scatter_sum<NV, 32>(v);
+    if (scattered_writer<NV, 32>()) buf[warp * NV + scattered_index<NV, 32>()] = s;
+    if (W == 1)
+        __syncwarp();
+    else
+        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        v[i] = buf[i];
+#pragma unroll
+        for (int k = 1; k < W; ++k) v[i] += buf[k * NV + i];
     }
-    return s;
 }
 
-// What a thread owns: a piece of a head, in one of the block's token groups.
-struct Place {
-    int piece, head_local, group;
-    uint32_t head;
-    bool active;
-};
-
-template <int P>
-__device__ __forceinline__ Place place_of(const HeadsArgs& a) {
-    Place p;
-    const int per = a.heads_per_block * P;
-    p.group = threadIdx.x / per;
-    const int i = threadIdx.x - p.group * per;
-    p.head_local = i / P;
-    p.piece = i % P;
-    p.head = blockIdx.y * a.heads_per_block + p.head_local;
-    p.active = p.group < a.groups && p.head < a.H;
-    return p;
+// Shared memory by 32-bit address, so that a piece's place is an offset in the
+// instruction.
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
 }
 
-// NORM: BSS_HEAD_NORM_*; T: tokens a thread handles together.
-template <int P, bool HALVES, int NORM, int T>
-__global__ void __launch_bounds__(T == 1 ? kMaxThreads : 512) heads_forward_kernel(const __grid_constant__ HeadsArgs a) {
-    extern __shared__ __align__(16) unsigned char smem[];
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Eight floats a piece as two 16-byte planes `plane` bytes apart, pieces side by
+// side: lanes read and write them without bank conflicts.
+__device__ __forceinline__ V8 planes_load(uint32_t at, uint32_t plane) {
+    const uint4 a = lds128(at), b = lds128(at + plane);
+    V8 v;
+    v.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+    v.p[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+    v.p[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+    v.p[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    return v;
+}
+
+__device__ __forceinline__ void planes_store(uint32_t at, uint32_t plane, const V8& v) {
+    sts128(at, make_uint4(__float_as_uint(v.p[0].x), __float_as_uint(v.p[0].y), __float_as_uint(v.p[1].x),
+                          __float_as_uint(v.p[1].y)));
+    sts128(at + plane, make_uint4(__float_as_uint(v.p[2].x), __float_as_uint(v.p[2].y), __float_as_uint(v.p[3].x),
+                                  __float_as_uint(v.p[3].y)));
+}
+
+// The weights of 8 channels (ones where there are none).
+template <bool EO>
+__device__ __forceinline__ V8 weights_of(const void* w, int64_t at, int dtype) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 1.0f;
+    if (w != nullptr) load_param8(w, at, dtype, f);
+    return arrange<EO>(f);
+}
+
+// The norm over a token: the weights of Q and K into shared memory once a block,
+// [tensor][plane][piece of the token].
+template <bool EO>
+__device__ __forceinline__ void stage_weights(const HeadsArgs& a, uint32_t at) {
+    const int all = a.H * a.pieces;
+    for (int i = 0; i < 2; ++i)
+        for (int e = threadIdx.x; e < all; e += blockDim.x)
+            planes_store(at + (i * 2 * all + e) * 16, all * 16,
+                         weights_of<EO>(a.weight[i], static_cast<int64_t>(e) * 8, a.weight_dtype));
+}
+
+// A warp's slots: two stages of [tensor][VPT][32 lanes] pieces.  Those of pieces
+// that do not exist hold zeros throughout.
+template <int TENSORS, int VPT>
+__device__ __forceinline__ uint32_t slots_of(uint32_t at, int count) {
+    at += ((threadIdx.x >> 5) * (2 * TENSORS * VPT * 32) + (threadIdx.x & 31)) * 16;
+    for (int e = 0; e < 2 * TENSORS * VPT; ++e)
+        if (e % VPT >= count) sts128(at + e * 512, make_uint4(0, 0, 0, 0));
+    return at;
+}
+
+// Blocks of 4 warps an SM shall hold at least, by the registers a thread needs.
+__host__ __device__ constexpr int forward_blocks(int vpt) { return vpt <= 2 ? 5 : vpt <= 5 ? 4 : 3; }
+__host__ __device__ constexpr int backward_blocks(int vpt) { return vpt <= 2 ? 4 : 3; }
+
+// W warps share a token, a lane holds up to VPT pieces of a tensor.
+template <bool HALVES, int NORM, int W, int VPT>
+__global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel(const __grid_constant__ HeadsArgs a) {
+    extern __shared__ __align__(16) float4 planes[];  // weights of a norm over a token, then the slots
+    __shared__ float buf[2][4 * 2];
+    constexpr int kTokens = 4 / W;
+    constexpr uint32_t kStage = 3 * VPT * 512;
+    const int warp = threadIdx.x / 32 % W, group = threadIdx.x / 32 / W;
+    const Lane me = lane_of<W, VPT>(a, warp);
     const bool rotary = a.rot.first[3] > 0;
-    const Place me = place_of<P>(a);
-    const int tokens = a.groups * T;
-    const Smem lay = smem_layout(tokens, P, a.heads_per_block, 2, rotary, NORM == BSS_HEAD_NORM_TOKEN);
-    float2* cs = reinterpret_cast<float2*>(smem + lay.cs);
-    float* sums = reinterpret_cast<float*>(smem + lay.sums);
-    const uint32_t token0 = blockIdx.x * tokens;
-    const uint32_t n0 = token0 + me.group * T;
-    const bool temporal = me.active && a.flags != nullptr && a.flags[me.head] != 0;
-    const int64_t c0 = me.piece * 8;
-
-    Raw8<__nv_bfloat16> raw[3][T];
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            raw[i][t] = zero_raw<__nv_bfloat16>();
-            if (a.in[i] != nullptr && me.active && n0 + t < a.N)
-                raw[i][t] = load_raw(a.in[i] + static_cast<int64_t>(n0 + t) * a.ts[i] + me.head * a.hs[i] + c0);
-        }
-    if (rotary) fill_angles<P>(a, cs, token0, tokens);
-
-    // sums of squares: over a head's lanes, and for the norm over a token over
-    // the heads through shared memory
-    float ssq[2][T];
-    if (NORM != BSS_HEAD_NORM_NONE) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                float v[8], s = 0.0f;
-                unpack(raw[i][t], v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(v[j], v[j], s);
-                ssq[i][t] = lane_sum<P>(s);
-                if (NORM == BSS_HEAD_NORM_TOKEN && me.group < a.groups) {
-                    float* row = sums + (i * tokens + me.group * T + t) * lay.hpad;
-                    if (me.piece == 0) row[me.head_local] = ssq[i][t];
-                    if (me.head_local == 0 && me.piece < lay.hpad - a.heads_per_block)
-                        row[a.heads_per_block + me.piece] = 0.0f;
-                }
-            }
-    }
-    if (rotary || NORM == BSS_HEAD_NORM_TOKEN) __syncthreads();
-
+    const Pairs<HALVES> pr = pairs_of<HALVES>(a, me.piece);
+    const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
+    const uint32_t base = smem_u32(planes);
+    const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
+    const uint32_t slots = slots_of<3, VPT>(base + (NORM == BSS_HEAD_NORM_TOKEN ? 4 * all16 : 0), me.count);
+    const uint32_t step = gridDim.x * kTokens;
+    uint32_t n = blockIdx.x * kTokens + group;
+    // running addresses of the token to fetch, and the steps to the next piece and token
+    const char* src[3];
+    int64_t apart[3], ahead[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        if (a.in[i] == nullptr) continue;
-        float w[8];
-        const bool weighted = i < 2 && NORM != BSS_HEAD_NORM_NONE && a.weight[i < 2 ? i : 0] != nullptr;
-        if (weighted && me.active)
-            load_param8(a.weight[i < 2 ? i : 0], NORM == BSS_HEAD_NORM_TOKEN ? me.head * (P * 8) + c0 : c0,
-                        a.weight_dtype, w);
-        __nv_bfloat16* dst = a.out[i] + static_cast<int64_t>(me.active ? me.head : 0) * a.N * (P * 8) + c0;
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const uint32_t n = n0 + t;
-            const bool live = me.active && n < a.N;
-            if (i == 2) {
-                if (live) st_row(dst + static_cast<int64_t>(head_row(a, n, temporal)) * (P * 8), raw[i][t].q[0]);
-                continue;
-            }
-            float v[8];
-            unpack(raw[i][t], v);
-            if (NORM != BSS_HEAD_NORM_NONE) {
-                float s = ssq[i < 2 ? i : 0][t], width = P * 8;
-                if (NORM == BSS_HEAD_NORM_TOKEN && me.group < a.groups) {
-                    s = sum_heads(sums + (i * tokens + me.group * T + t) * lay.hpad, lay.hpad);
-                    width *= a.H;
-                }
-                const float r = rsqrtf(s / width + a.eps);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = weighted ? v[j] * r * w[j] : v[j] * r;
-            }
-            if (rotary) {
-                const int tok = me.group < a.groups ? me.group * T + t : 0;
-                rotate8<P, HALVES>(v, cs + tok * (P * 4), me.piece, 2 * a.rot.first[3], 1.0f);
-            }
-            if (live) store8(dst + static_cast<int64_t>(head_row(a, n, temporal)) * (P * 8), v);
-        }
+        src[i] = reinterpret_cast<const char*>(a.in[i] + n * a.ts[i] + me.head0 * a.hs[i] + me.piece * 8);
+        apart[i] = me.step * a.hs[i] * 2;
+        ahead[i] = step * a.ts[i] * 2;
     }
+    auto fetch = [&](bool exists, uint32_t to) {
+        if (exists) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                if (a.in[i] == nullptr) continue;
+                const char* p = src[i];
+#pragma unroll
+                for (int j = 0; j < VPT; ++j, p += apart[i])
+                    if (j < me.count) cp_async_16(to + (i * VPT + j) * 512, p);
+                src[i] += ahead[i];
+            }
+        }
+        cp_async_commit();
+    };
+    fetch(n < a.N, slots);
+    V8 w[2];
+    if (NORM == BSS_HEAD_NORM_TOKEN) {
+        stage_weights<!HALVES>(a, base);
+        __syncthreads();
+    } else if (NORM == BSS_HEAD_NORM_HEAD) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = weights_of<!HALVES>(a.weight[i], me.piece * 8, a.weight_dtype);
+    }
+    const int64_t head_bytes = static_cast<int64_t>(a.N) * row_bytes;
+    const int64_t head_step = me.step * head_bytes;
+    const int64_t dst = me.head0 * head_bytes + me.piece * 16;
+    uint32_t now = slots, other = slots + kStage;
+    int turn_buf = 0;
+    for (; n < a.N; n += step, turn_buf ^= 1) {
+        fetch(a.N - n > step, other);
+        const Token tok = token_of(a, n);
+        Turn<HALVES> turn;
+        if (rotary) turn = load_turn<HALVES>(pr, tok);
+        cp_async_wait_group<1>();
+        float r[2] = {0.0f, 0.0f};
+        if (NORM == BSS_HEAD_NORM_TOKEN) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (a.in[i] != nullptr)
+#pragma unroll
+                    for (int j = 0; j < VPT; ++j) {
+                        const V8 v = unpack_bf16<false>(lds128(now + (i * VPT + j) * 512));
+                        r[i] += dot(v, v);
+                    }
+            token_sum<2, W>(r, buf[turn_buf] + 2 * W * group, group, warp);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) r[i] = rsqrtf(r[i] * a.inv_width + a.eps);
+        }
+        int64_t at = dst;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j, at += head_step) {
+            const bool live = j < me.count;
+            const int64_t to = at + static_cast<int64_t>(me.temporal >> j & 1u ? tok.temporal_row : n) * row_bytes;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                if (a.in[i] == nullptr) continue;
+                uint4 o = lds128(now + (i * VPT + j) * 512);
+                if (i < 2) {
+                    V8 v = unpack_bf16<!HALVES>(o);
+                    if (NORM == BSS_HEAD_NORM_HEAD)
+                        v = mul(v, mul(w[i < 2 ? i : 0], rsqrtf(head_sum(dot(v, v), a.pieces) * a.inv_width + a.eps)));
+                    if (NORM == BSS_HEAD_NORM_TOKEN && live)
+                        v = mul(v, mul(planes_load(weights + i * 2 * all16 + j * (W * 512), all16), r[i < 2 ? i : 0]));
+                    if (rotary) rotate8<HALVES, false>(v, turn, pr);
+                    o = pack_bf16<!HALVES>(v);
+                }
+                if (live) st_row(reinterpret_cast<char*>(a.out[i]) + to, o);
+            }
+        }
+        const uint32_t t = now;
+        now = other, other = t;
+    }
+    cp_async_wait_group<0>();
 }
 
-template <int P, bool HALVES, int NORM, int T>
-__global__ void __launch_bounds__(T == 1 ? kMaxThreads : 512) heads_backward_kernel(const __grid_constant__ HeadsArgs a) {
-    extern __shared__ __align__(16) unsigned char smem[];
+// The norm over a token: W warps share one.  Its weight gradients stay in the
+// registers of the lane that holds the piece; those of a norm over a head too.
+template <bool HALVES, int NORM, int W, int VPT>
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blocks(VPT))
+    heads_backward_kernel(const __grid_constant__ HeadsArgs a) {
+    constexpr bool kToken = NORM == BSS_HEAD_NORM_TOKEN;
+    constexpr int kWarps = W > 4 ? W : 4, kTokens = kWarps / W;
+    constexpr int kTensors = NORM == BSS_HEAD_NORM_NONE ? 3 : 5;  // dQ, dK, dV, q, k
+    constexpr uint32_t kStage = kTensors * VPT * 512;
+    extern __shared__ __align__(16) float4 planes[];
+    __shared__ float4 buf4[2][kWarps];
+    const int warp = threadIdx.x / 32 % W, group = threadIdx.x / 32 / W;
+    const Lane me = lane_of<W, VPT>(a, warp);
     const bool rotary = a.rot.first[3] > 0;
-    const Place me = place_of<P>(a);
-    const int tokens = a.groups * T;
-    const Smem lay = smem_layout(tokens, P, a.heads_per_block, 4, rotary, NORM == BSS_HEAD_NORM_TOKEN);
-    const bool temporal = me.active && a.flags != nullptr && a.flags[me.head] != 0;
-    const int64_t c0 = me.piece * 8;
-    float w[2][8], dw[2][8];
+    const Pairs<HALVES> pr = pairs_of<HALVES>(a, me.piece);
+    const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
+    const uint32_t base = smem_u32(planes);
+    const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
+    const uint32_t slots = slots_of<kTensors, VPT>(base + (kToken ? 4 * all16 : 0), me.count);
+    const uint32_t step = gridDim.x * kTokens;
+    uint32_t n = blockIdx.x * kTokens + group;
+    const int64_t head_bytes = static_cast<int64_t>(a.N) * row_bytes;
+    const int64_t head_step = me.step * head_bytes;
+    const int64_t grad0 = me.head0 * head_bytes + me.piece * 16;
+    const char* src[2];
+    char* dst[3];
+    int64_t xapart[2], xahead[2], apart[3], ahead[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        dst[i] = reinterpret_cast<char*>(a.out[i] + n * a.ts[i] + me.head0 * a.hs[i] + me.piece * 8);
+        apart[i] = me.step * a.hs[i] * 2;
+        ahead[i] = step * a.ts[i] * 2;
+        if (i < 2) {
+            src[i] = reinterpret_cast<const char*>(a.x[i] + n * a.xts[i] + me.head0 * a.xhs[i] + me.piece * 8);
+            xapart[i] = me.step * a.xhs[i] * 2;
+            xahead[i] = step * a.xts[i] * 2;
+        }
+    }
+    auto fetch = [&](uint32_t m, bool exists, uint32_t to) {
+        if (exists) {
+            const Token tok = token_of(a, m);
+            int64_t at = grad0;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j, at += head_step) {
+                const int64_t from = at + static_cast<int64_t>(me.temporal >> j & 1u ? tok.temporal_row : m) * row_bytes;
+                if (j < me.count)
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        if (a.in[i] != nullptr)
+                            cp_async_16(to + (i * VPT + j) * 512, reinterpret_cast<const char*>(a.in[i]) + from);
+            }
+            if (NORM != BSS_HEAD_NORM_NONE)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (a.in[i] == nullptr) continue;
+                    const char* p = src[i];
+#pragma unroll
+                    for (int j = 0; j < VPT; ++j, p += xapart[i])
+                        if (j < me.count) cp_async_16(to + ((3 + i) * VPT + j) * 512, p);
+                    src[i] += xahead[i];
+                }
+        }
+        cp_async_commit();
+    };
+    fetch(n, n < a.N, slots);
+    constexpr int kHeld = kToken ? VPT : 1;
+    V8 w[2], dw[2][kHeld];
+    if (kToken) {
+        stage_weights<!HALVES>(a, base);
+        __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+        if (NORM == BSS_HEAD_NORM_HEAD) w[i] = weights_of<!HALVES>(a.weight[i], me.piece * 8, a.weight_dtype);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[i][j] = 1.0f, dw[i][j] = 0.0f;
-        if (NORM != BSS_HEAD_NORM_NONE && me.active && a.weight[i] != nullptr)
-            load_param8(a.weight[i], NORM == BSS_HEAD_NORM_TOKEN ? me.head * (P * 8) + c0 : c0, a.weight_dtype, w[i]);
+        for (int j = 0; j < kHeld; ++j) dw[i][j] = unpack_bf16<!HALVES>(make_uint4(0, 0, 0, 0));
     }
-    const uint32_t blocks = (a.N + tokens - 1) / tokens;
-    int buffer = 0;
-    for (uint32_t b = blockIdx.x; b < blocks; b += gridDim.x, buffer ^= 1) {
-        float2* cs = reinterpret_cast<float2*>(smem + buffer * lay.bytes + lay.cs);
-        float* sums = reinterpret_cast<float*>(smem + buffer * lay.bytes + lay.sums);
-        const uint32_t token0 = b * tokens;
-        const uint32_t n0 = token0 + me.group * T;
-        Raw8<__nv_bfloat16> g[3][T], x[2][T];
+    uint32_t now = slots, other = slots + kStage;
+    int turn_buf = 0;
+    for (; n < a.N; n += step, turn_buf ^= 1) {
+        fetch(n + step, a.N - n > step, other);
+        Turn<HALVES> turn;
+        if (rotary) turn = load_turn<HALVES>(pr, token_of(a, n));
+        cp_async_wait_group<1>();
+        float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // x^2 and g w x of Q, then of K
+        if (kToken) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
+            for (int i = 0; i < 2; ++i) {
+                if (a.in[i] == nullptr) continue;
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const uint32_t n = n0 + t;
-                g[i][t] = zero_raw<__nv_bfloat16>();
-                if (i < 2) x[i < 2 ? i : 0][t] = zero_raw<__nv_bfloat16>();
-                if (a.in[i] == nullptr || !me.active || n >= a.N) continue;
-                g[i][t] = load_raw(a.in[i] + (static_cast<int64_t>(me.head) * a.N + head_row(a, n, temporal)) * (P * 8) + c0);
-                if (NORM != BSS_HEAD_NORM_NONE && i < 2)
-                    x[i < 2 ? i : 0][t] = load_raw(a.x[i < 2 ? i : 0] + static_cast<int64_t>(n) * a.xts[i < 2 ? i : 0] +
-                                                   me.head * a.xhs[i < 2 ? i : 0] + c0);
+                for (int j = 0; j < VPT; ++j) {
+                    V8 v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
+                    if (rotary) rotate8<HALVES, true>(v, turn, pr);
+                    if (j >= me.count) continue;
+                    const V8 x = unpack_bf16<!HALVES>(lds128(now + ((3 + i) * VPT + j) * 512));
+                    sums[2 * i] += dot(x, x);
+                    sums[2 * i + 1] += dot(mul(v, planes_load(weights + i * 2 * all16 + j * (W * 512), all16)), x);
+                }
             }
-        if (rotary) {
-            fill_angles<P>(a, cs, token0, tokens);
-            __syncthreads();
+            token_sum<4, W>(sums, reinterpret_cast<float*>(buf4[turn_buf] + W * group), group, warp);
         }
-        float gr[2][T][8], ssq[2][T], gx[2][T];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int t = 0; t < T; ++t) {
-                unpack(g[i][t], gr[i][t]);
-                if (rotary) {
-                    const int tok = me.group < a.groups ? me.group * T + t : 0;
-                    rotate8<P, HALVES>(gr[i][t], cs + tok * (P * 4), me.piece, 2 * a.rot.first[3], -1.0f);
-                }
-                if (NORM == BSS_HEAD_NORM_NONE) continue;
-                float v[8], s = 0.0f, q = 0.0f;
-                unpack(x[i][t], v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s = fmaf(v[j], v[j], s);
-                    q = fmaf(gr[i][t][j] * w[i][j], v[j], q);
-                }
-                ssq[i][t] = lane_sum<P>(s);
-                gx[i][t] = lane_sum<P>(q);
-                if (NORM == BSS_HEAD_NORM_TOKEN && me.group < a.groups) {
-                    float* row = sums + (2 * i * tokens + me.group * T + t) * lay.hpad;
-                    float* row2 = row + tokens * lay.hpad;
-                    if (me.piece == 0) row[me.head_local] = ssq[i][t], row2[me.head_local] = gx[i][t];
-                    if (me.head_local == 0 && me.piece < lay.hpad - a.heads_per_block)
-                        row[a.heads_per_block + me.piece] = row2[a.heads_per_block + me.piece] = 0.0f;
-                }
-            }
-        if (NORM == BSS_HEAD_NORM_TOKEN) __syncthreads();
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
             if (a.in[i] == nullptr) continue;
+            char* to = dst[i];
+            dst[i] += ahead[i];
+            const int k = i < 2 ? i : 0;
+            float r = 0.0f, m = 0.0f;
+            if (kToken && i < 2) {
+                r = rsqrtf(sums[2 * k] * a.inv_width + a.eps);
+                m = -r * r * (sums[2 * k + 1] * a.inv_width);
+            }
 #pragma unroll
-            for (int t = 0; t < T; ++t) {
-                const uint32_t n = n0 + t;
-                if (!me.active || n >= a.N) continue;
-                __nv_bfloat16* dst = a.out[i] + static_cast<int64_t>(n) * a.ts[i] + me.head * a.hs[i] + c0;
-                if (i == 2) {
-                    st_row(dst, g[i][t].q[0]);
-                    continue;
-                }
-                constexpr int kTwo = 1;
-                const int k = i < 2 ? i : kTwo;
-                float v[8];
-                if (NORM != BSS_HEAD_NORM_NONE) {
-                    float s = ssq[k][t], q = gx[k][t], width = P * 8;
-                    if (NORM == BSS_HEAD_NORM_TOKEN) {
-                        const float* row = sums + (2 * k * tokens + me.group * T + t) * lay.hpad;
-                        s = sum_heads(row, lay.hpad);
-                        q = sum_heads(row + tokens * lay.hpad, lay.hpad);
-                        width *= a.H;
+            for (int j = 0; j < VPT; ++j, to += apart[i]) {
+                const bool live = j < me.count;
+                uint4 o = lds128(now + (i * VPT + j) * 512);
+                if (i < 2) {
+                    V8 v = unpack_bf16<!HALVES>(o);
+                    if (rotary) rotate8<HALVES, true>(v, turn, pr);
+                    if (NORM != BSS_HEAD_NORM_NONE) {
+                        const V8 x = unpack_bf16<!HALVES>(lds128(now + ((3 + k) * VPT + j) * 512));
+                        V8 gw = v;
+                        if (kToken) {
+                            if (live) gw = mul(v, planes_load(weights + k * 2 * all16 + j * (W * 512), all16));
+                        } else {
+                            gw = mul(v, w[k]);
+                            r = rsqrtf(head_sum(dot(x, x), a.pieces) * a.inv_width + a.eps);
+                            m = -r * r * (head_sum(dot(gw, x), a.pieces) * a.inv_width);
+                        }
+                        const V8 xr = mul(x, r);
+                        V8& d = dw[k][kToken ? j : 0];
+                        d = fma8(v, xr, d);  // zeros where there is no piece
+                        v = fma8(xr, m, mul(gw, r));
                     }
-                    const float r = rsqrtf(s / width + a.eps);
-                    const float m = r * r * (q / width);
-                    unpack(x[k][t], v);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        dw[k][j] = fmaf(gr[k][t][j], v[j] * r, dw[k][j]);
-                        v[j] = r * (gr[k][t][j] * w[k][j] - v[j] * m);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = gr[k][t][j];
+                    o = pack_bf16<!HALVES>(v);
                 }
-                store8(dst, v);
+                if (live) st_row(to, o);
             }
         }
+        const uint32_t t = now;
+        now = other, other = t;
     }
-    if (NORM == BSS_HEAD_NORM_NONE || !a.want_dweight) return;
-    // the block's share of the weight gradients: over its token groups, and for
-    // the norm over a head over its heads, in a fixed order
+    cp_async_wait_group<0>();
+    if (NORM == BSS_HEAD_NORM_NONE || a.partial == nullptr) return;
+    // the block's share of the weight gradients: over the tokens side by side in
+    // it, and for the norm over a head over its heads, in a fixed order
     __syncthreads();
-    float* acc = reinterpret_cast<float*>(smem);  // [2][threads][8]
+    if (kToken) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < kHeld; ++j)
+            if (j < me.count)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[(i * blockDim.x + threadIdx.x) * 8 + j] = dw[i][j];
+                for (int i = 0; i < 2; ++i)
+                    planes_store(weights + (group * 2 + i) * 2 * all16 + j * (W * 512), all16, dw[i][j]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            planes_store(base + (i * 2 * blockDim.x + threadIdx.x) * 16, blockDim.x * 16, dw[i][0]);
+    }
     __syncthreads();
-    const int per = a.heads_per_block * P;
-    const int width = NORM == BSS_HEAD_NORM_TOKEN ? per * 8 : P * 8;
-    const int sources = NORM == BSS_HEAD_NORM_TOKEN ? a.groups : a.groups * a.heads_per_block;
-    float* dst = a.partial + static_cast<int64_t>(blockIdx.y * gridDim.x + blockIdx.x) * 2 * width;
-    for (int e = threadIdx.x; e < 2 * width; e += blockDim.x) {
-        const int i = e / width, c = e - i * width;
+    // element of a channel: [source][tensor][plane][piece][4]
+    const int all = a.H * a.pieces, channels = kToken ? all * 8 : a.pieces * 8;
+    const int span = kToken ? all : blockDim.x;
+    const int sources = kToken ? kTokens : blockDim.x / a.pieces;
+    const int apart_src = kToken ? 4 * all : a.pieces;
+    const float* acc = reinterpret_cast<const float*>(planes);
+    float* out = a.partial + static_cast<int64_t>(blockIdx.y * gridDim.x + blockIdx.x) * 2 * channels;
+    for (int e = threadIdx.x; e < 2 * channels; e += blockDim.x) {
+        const int i = e / channels, c = e - i * channels;
+        int slot = 0;  // the channel's place among the four pairs of its piece
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (channel_of<!HALVES>(q / 2, q % 2) == c % 8) slot = q;
+        const int at = ((i * 2 + slot / 4) * span + c / 8) * 4 + slot % 4;
         float s = 0.0f;
-        for (int k = 0; k < sources; ++k) s += acc[i * blockDim.x * 8 + k * width + c];
-        dst[e] = s;
+        for (int k = 0; k < sources; ++k) s += acc[at + k * apart_src * 4];
+        out[e] = s;
     }
 }
 
-// out[c] = sum over the blocks' partials [blocks][2][width], blocks in order
-// within 8 lanes, the lanes' sums in order.
-__global__ void __launch_bounds__(256) heads_reduce_kernel(const float* __restrict__ partial, int blocks, int width,
-                                                           float* dq_weight, float* dk_weight) {
-    __shared__ float part[8][33];
-    const int c = blockIdx.x * 32 + threadIdx.x % 32, lane = threadIdx.x / 32;
+// out[c] = sum over the blocks' partials [blocks][2][width]: blocks in order
+// within 32 lanes, then the lanes' sums in order.
+__global__ void __launch_bounds__(1024) heads_reduce_kernel(const float* __restrict__ partial, int blocks, int width,
+                                                            float* dq_weight, float* dk_weight) {
+    __shared__ float part[32][33];
+    const int col = threadIdx.x % 32, lane = threadIdx.x / 32, c = blockIdx.x * 32 + col;
     float s = 0.0f;
-    if (c < 2 * width)
-        for (int b = lane; b < blocks; b += 8) s += partial[static_cast<int64_t>(b) * 2 * width + c];
-    part[lane][threadIdx.x % 32] = s;
+    if (c < 2 * width) {
+#pragma unroll 4
+        for (int b = lane; b < blocks; b += 32) s += partial[static_cast<int64_t>(b) * 2 * width + c];
+    }
+    part[lane][col] = s;
     __syncthreads();
     if (lane != 0 || c >= 2 * width) return;
     s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += part[k][threadIdx.x % 32];
+    for (int k = 0; k < 32; ++k) s += part[k][col];
     if (c < width) {
         if (dq_weight != nullptr) dq_weight[c] = s;
     } else if (dk_weight != nullptr) {
@@ -421,36 +597,47 @@ __global__ void rotary_table_kernel(const double* positions, int32_t length, int
 
 // ---------------------------------------------------------------- host side
 
-// How the heads are dealt to blocks: for the norm over a token one block holds
-// them all; otherwise up to 256 threads' worth, several tokens side by side when
-// the heads are few.
+// How a token's heads are dealt to warps and grid columns.
 struct Shape {
-    int heads_per_block, groups, threads, T, tokens;
-    uint32_t grid_y;
+    int warps, vpt, heads_per_block, threads, smem;
+    uint32_t grid_x, grid_y;
 };
 
-Shape shape_of(int32_t H, int pieces, int32_t norm, int T) {
-    Shape s;
-    s.heads_per_block = norm == BSS_HEAD_NORM_TOKEN ? H : (H * pieces <= 256 ? H : 256 / pieces);
-    const int per = s.heads_per_block * pieces;
-    s.groups = per >= 128 ? 1 : 128 / per;
-    s.threads = (per * s.groups + 31) / 32 * 32;
-    s.T = s.threads > 512 ? 1 : T;
-    s.tokens = s.groups * s.T;
-    s.grid_y = static_cast<uint32_t>((H + s.heads_per_block - 1) / s.heads_per_block);
-    return s;
+// Warps that share a token under the norm over a token.  Forward: one up to 2048
+// channels.  Backward: as many as leave a lane at most 3 pieces (4 of the widest).
+int warps_of(bool backward, int chunks) {
+    if (!backward) return chunks <= 8 ? 1 : 4;
+    return chunks <= 3 ? 1 : chunks <= 6 ? 2 : chunks <= 12 ? 4 : 8;
 }
 
-constexpr int kForwardTokens = 4, kBackwardTokens = 2;
-
-// Blocks of the backward pass: enough to fill the GPU, each walking over tokens
-// so that a block leaves one partial sum of the weight gradients.
-uint32_t backward_grid(const Shape& s, uint32_t N) {
-    const uint32_t blocks = (N + s.tokens - 1) / s.tokens;
-    const uint32_t per_sm = 1024 / s.threads > 0 ? 1024 / s.threads : 1;
-    uint32_t most = per_sm * static_cast<uint32_t>(num_sms()) / s.grid_y;
-    if (most < 1) most = 1;
-    return blocks < most ? blocks : most;
+Shape shape_of(int32_t H, int pieces, int32_t norm, uint32_t N, bool backward) {
+    Shape s;
+    const int per = 32 / pieces, total = (H + per - 1) / per;  // warp-wide rows of pieces
+    const bool token = norm == BSS_HEAD_NORM_TOKEN;
+    s.warps = token ? warps_of(backward, total) : 1;
+    const int columns = token ? 1 : (total + 4) / 5;  // up to 5 pieces a lane and column
+    const int held = (total + s.warps * columns - 1) / (s.warps * columns);
+    // the instances there are: 1, 2, 3, 5 and, for the norm over a token, 8 forward
+    // (the only one of 4 warps) and 4 backward (of 8 warps)
+    s.vpt = backward && s.warps == 8 ? held : !backward && s.warps == 4 ? 8 : held == 4 ? 5 : held > 5 ? 8 : held;
+    s.heads_per_block = columns == 1 ? H : held * per;
+    s.grid_y = static_cast<uint32_t>((H + s.heads_per_block - 1) / s.heads_per_block);
+    const int block_warps = s.warps > 4 ? s.warps : 4, tokens = block_warps / s.warps;
+    s.threads = 32 * block_warps;
+    // shared memory: two stages of every piece, the weights of the norm over a
+    // token; at the end of the backward pass the weight gradients
+    const int all = H * pieces * 64;
+    const int tensors = backward && norm != BSS_HEAD_NORM_NONE ? 5 : 3;
+    s.smem = (token ? all : 0) + block_warps * 2 * tensors * s.vpt * 512;
+    const int grads = token ? all * tokens : s.threads * 64;
+    if (backward && norm != BSS_HEAD_NORM_NONE && s.smem < grads) s.smem = grads;
+    // as many blocks as an SM holds, each walking over tokens
+    const uint32_t blocks = (N + tokens - 1) / tokens;
+    int per_sm = 224 * 1024 / (s.smem + 1024);
+    per_sm = per_sm < 1 ? 1 : per_sm > 1024 / s.threads ? 1024 / s.threads : per_sm;
+    const uint32_t fill = static_cast<uint32_t>(per_sm * num_sms()) / s.grid_y;
+    s.grid_x = blocks < fill ? blocks : (fill < 1 ? 1 : fill);
+    return s;
 }
 
 bss_status check_geometry(const bss_mask_params* params, int32_t H) {
@@ -532,50 +719,80 @@ bss_status set_options(const bss_heads_options* o, const bss_mask_params* p, int
 
 using Kernel = void (*)(const HeadsArgs);
 
-template <int P, bool HALVES, int T>
-Kernel pick_forward(int32_t norm) {
-    if (norm == BSS_HEAD_NORM_HEAD) return heads_forward_kernel<P, HALVES, BSS_HEAD_NORM_HEAD, T>;
-    if (norm == BSS_HEAD_NORM_TOKEN) return heads_forward_kernel<P, HALVES, BSS_HEAD_NORM_TOKEN, T>;
-    return heads_forward_kernel<P, HALVES, BSS_HEAD_NORM_NONE, T>;
-}
-
-template <int P, bool HALVES, int T>
-Kernel pick_backward(int32_t norm) {
-    if (norm == BSS_HEAD_NORM_HEAD) return heads_backward_kernel<P, HALVES, BSS_HEAD_NORM_HEAD, T>;
-    if (norm == BSS_HEAD_NORM_TOKEN) return heads_backward_kernel<P, HALVES, BSS_HEAD_NORM_TOKEN, T>;
-    return heads_backward_kernel<P, HALVES, BSS_HEAD_NORM_NONE, T>;
-}
-
-template <int P, bool HALVES>
-Kernel pick_tokens(bool backward, int32_t norm, int T) {
-    if (backward) return T == 1 ? pick_backward<P, HALVES, 1>(norm) : pick_backward<P, HALVES, kBackwardTokens>(norm);
-    return T == 1 ? pick_forward<P, HALVES, 1>(norm) : pick_forward<P, HALVES, kForwardTokens>(norm);
-}
-
-Kernel pick(bool backward, int pieces, int pairing, int32_t norm, int T) {
-    const bool halves = pairing == BSS_PAIR_HALVES;
-    if (pieces == 16)
-        return halves ? pick_tokens<16, true>(backward, norm, T) : pick_tokens<16, false>(backward, norm, T);
-    return halves ? pick_tokens<8, true>(backward, norm, T) : pick_tokens<8, false>(backward, norm, T);
-}
-
-bss_status launch(Kernel k, const HeadsArgs& a, dim3 grid, int threads, int smem, cudaStream_t stream,
-                  const char* what) {
-    if (smem > 48 * 1024) {
-        const bss_status st = cuda_check(
-            cudaFuncSetAttribute(reinterpret_cast<const void*>(k), cudaFuncAttributeMaxDynamicSharedMemorySize, smem),
-            "shared memory size");
-        if (st != BSS_OK) return st;
+template <bool HALVES, int NORM>
+Kernel pick_forward(const Shape& s) {
+    if (NORM == BSS_HEAD_NORM_TOKEN && s.warps == 4) return heads_forward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 4, 8>;
+    switch (s.vpt) {
+        case 1: return heads_forward_kernel<HALVES, NORM, 1, 1>;
+        case 2: return heads_forward_kernel<HALVES, NORM, 1, 2>;
+        case 3: return heads_forward_kernel<HALVES, NORM, 1, 3>;
+        case 5: return heads_forward_kernel<HALVES, NORM, 1, 5>;
+        default: return heads_forward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 1, 8>;
     }
-    k<<<grid, threads, smem, stream>>>(a);
+}
+
+template <bool HALVES, int NORM>
+Kernel pick_backward(const Shape& s) {
+    switch (s.vpt) {
+        case 1: return heads_backward_kernel<HALVES, NORM, 1, 1>;
+        case 2: return heads_backward_kernel<HALVES, NORM, 1, 2>;
+        case 3: return heads_backward_kernel<HALVES, NORM, 1, 3>;
+        default: return heads_backward_kernel<HALVES, NORM, 1, 5>;
+    }
+}
+
+template <bool HALVES>
+Kernel pick_backward_token(const Shape& s) {
+    switch (s.warps * 10 + s.vpt) {
+        case 11: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 1, 1>;
+        case 12: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 1, 2>;
+        case 13: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 1, 3>;
+        case 22: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 2, 2>;
+        case 23: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 2, 3>;
+        case 42: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 4, 2>;
+        case 43: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 4, 3>;
+        case 82: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 8, 2>;
+        case 83: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 8, 3>;
+        default: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 8, 4>;
+    }
+}
+
+template <bool HALVES>
+Kernel pick(bool backward, int32_t norm, const Shape& s) {
+    if (norm == BSS_HEAD_NORM_TOKEN)
+        return backward ? pick_backward_token<HALVES>(s) : pick_forward<HALVES, BSS_HEAD_NORM_TOKEN>(s);
+    if (norm == BSS_HEAD_NORM_HEAD)
+        return backward ? pick_backward<HALVES, BSS_HEAD_NORM_HEAD>(s) : pick_forward<HALVES, BSS_HEAD_NORM_HEAD>(s);
+    return backward ? pick_backward<HALVES, BSS_HEAD_NORM_NONE>(s) : pick_forward<HALVES, BSS_HEAD_NORM_NONE>(s);
+}
+
+// Launches at most the blocks of the shape, and no more than the GPU holds at
+// once; *blocks: how many.
+bss_status launch(bool backward, int pairing, int32_t norm, const HeadsArgs& a, const Shape& s, cudaStream_t stream,
+                  const char* what, int* blocks) {
+    const Kernel k = pairing == BSS_PAIR_HALVES ? pick<true>(backward, norm, s) : pick<false>(backward, norm, s);
+    int resident = 1;
+    const bss_status st = resident_blocks(reinterpret_cast<const void*>(k), s.threads, s.smem, &resident);
+    if (st != BSS_OK) return st;
+    const uint32_t fill = static_cast<uint32_t>(resident * num_sms()) / s.grid_y;
+    const uint32_t grid_x = s.grid_x < fill ? s.grid_x : (fill < 1 ? 1 : fill);
+    *blocks = static_cast<int>(grid_x * s.grid_y);
+    k<<<dim3(grid_x, s.grid_y), s.threads, s.smem, stream>>>(a);
     return cuda_check(cudaGetLastError(), what);
+}
+
+void set_shape(const Shape& s, int32_t norm, int32_t d, HeadsArgs* a) {
+    a->heads_per_block = s.heads_per_block;
+    a->pieces = d / 8;
+    a->inv_width = 1.0f / static_cast<float>(norm == BSS_HEAD_NORM_TOKEN ? a->H * d : d);
 }
 
 void set_geometry(const bss_mask_params* p, int32_t H, const uint8_t* flags, HeadsArgs* a) {
     a->F = p->F;
     a->S = static_cast<uint32_t>(p->Hs) * p->Ws;
-    a->Ws = p->Ws;
     a->N = a->S * a->F;
+    a->by_S = FastDiv(a->S);
+    a->by_Ws = FastDiv(p->Ws);
     a->H = H;
     a->flags = flags;
 }
@@ -641,14 +858,10 @@ bss_status bss_heads_from_tokens(const bss_token_tensor* q, const bss_token_tens
             if (j < i && a.out[i] != nullptr && a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
                 return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
         }
-    const int pieces = d / 8;
-    const Shape s = shape_of(H, pieces, options->norm, kForwardTokens);
-    const bool token_norm = options->norm == BSS_HEAD_NORM_TOKEN;
-    const Smem lay = smem_layout(s.tokens, pieces, s.heads_per_block, 2, a.rot.first[3] > 0, token_norm);
-    a.heads_per_block = s.heads_per_block;
-    a.groups = s.groups;
-    return launch(pick(false, pieces, pairing, options->norm, s.T), a, dim3((a.N + s.tokens - 1) / s.tokens, s.grid_y),
-                  s.threads, lay.bytes, stream, "heads launch");
+    const Shape s = shape_of(H, d / 8, options->norm, a.N, false);
+    set_shape(s, options->norm, d, &a);
+    int blocks = 0;
+    return launch(false, pairing, options->norm, a, s, stream, "heads launch", &blocks);
 }
 
 bss_status bss_heads_from_tokens_backward_workspace(int32_t H, const bss_mask_params* params, int32_t norm,
@@ -661,10 +874,9 @@ bss_status bss_heads_from_tokens_backward_workspace(int32_t H, const bss_mask_pa
     if (st != BSS_OK) return st;
     if ((st = check_norm(norm, H, params->head_dim)) != BSS_OK) return st;
     if (norm == BSS_HEAD_NORM_NONE) return BSS_OK;
-    const Shape s = shape_of(H, params->head_dim / 8, norm, kBackwardTokens);
+    const Shape s = shape_of(H, params->head_dim / 8, norm, static_cast<uint32_t>(params->F) * params->Hs * params->Ws, true);
     const int64_t width = norm == BSS_HEAD_NORM_TOKEN ? static_cast<int64_t>(H) * params->head_dim : params->head_dim;
-    *bytes = static_cast<int64_t>(backward_grid(s, static_cast<uint32_t>(params->F) * params->Hs * params->Ws)) *
-             s.grid_y * 2 * width * 4;
+    *bytes = static_cast<int64_t>(s.grid_x) * s.grid_y * 2 * width * 4;
     return BSS_OK;
 }
 
@@ -730,31 +942,23 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
             if (a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
                 return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
     }
-    const int pieces = d / 8;
-    const Shape s = shape_of(H, pieces, norm, kBackwardTokens);
-    const bool token_norm = norm == BSS_HEAD_NORM_TOKEN;
-    const Smem lay = smem_layout(s.tokens, pieces, s.heads_per_block, 4, a.rot.first[3] > 0, token_norm);
-    a.heads_per_block = s.heads_per_block;
-    a.groups = s.groups;
-    a.want_dweight = dq_weight != nullptr || dk_weight != nullptr;
-    const uint32_t grid_x = backward_grid(s, a.N);
-    const int width = token_norm ? H * d : d;
-    int smem = 2 * lay.bytes;
-    if (a.want_dweight) {
+    const Shape s = shape_of(H, d / 8, norm, a.N, true);
+    set_shape(s, norm, d, &a);
+    const bool want = dq_weight != nullptr || dk_weight != nullptr;
+    const int width = norm == BSS_HEAD_NORM_TOKEN ? H * d : d;
+    if (want) {
         if (!is_aligned(dq_weight, 16) || !is_aligned(dk_weight, 16))
             return set_error(BSS_ERR_INVALID_ARG, "weight gradients must be 16-byte aligned");
-        const int64_t need = static_cast<int64_t>(grid_x) * s.grid_y * 2 * width * 4;
+        const int64_t need = static_cast<int64_t>(s.grid_x) * s.grid_y * 2 * width * 4;
         if (workspace == nullptr || !is_aligned(workspace, 16) || workspace_bytes < need)
             return set_error(BSS_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and hold %lld bytes",
                              static_cast<long long>(need));
         a.partial = static_cast<float*>(workspace);
-        if (smem < 2 * s.threads * 32) smem = 2 * s.threads * 32;
     }
-    st = launch(pick(true, pieces, pairing, norm, s.T), a, dim3(grid_x, s.grid_y), s.threads, smem, stream,
-                "heads backward launch");
-    if (st != BSS_OK || !a.want_dweight) return st;
-    heads_reduce_kernel<<<(2 * width + 31) / 32, 256, 0, stream>>>(a.partial, static_cast<int>(grid_x * s.grid_y), width,
-                                                                  dq_weight, dk_weight);
+    int blocks = 0;
+    st = launch(true, pairing, norm, a, s, stream, "heads backward launch", &blocks);
+    if (st != BSS_OK || !want) return st;
+    heads_reduce_kernel<<<(2 * width + 31) / 32, 1024, 0, stream>>>(a.partial, blocks, width, dq_weight, dk_weight);
     return cuda_check(cudaGetLastError(), "weight gradient launch");
 }
 

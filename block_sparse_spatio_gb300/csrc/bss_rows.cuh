@@ -7,10 +7,12 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <type_traits>
+#include <mutex>
+#include <vector>
 
 #include "bss_block.h"
 #include "bss_internal.h"
+#include "bss_ptx.cuh"
 
 namespace bss {
 
@@ -106,6 +108,94 @@ __device__ __forceinline__ float load_param(const void* base, int64_t index, int
                                   : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[index]);
 }
 
+// ---------------------------------------------------------------- packed arithmetic
+// 8 channels as four pairs, computed two at a time (fma.rn.f32x2).
+struct V8 {
+    float2 p[4];
+};
+
+__device__ __forceinline__ float2 f2(float a) { return make_float2(a, a); }
+
+// Pairs (0,1) (2,3) (4,5) (6,7), or for EO the even and odd channels apart:
+// (0,2) (1,3) (4,6) (5,7).
+template <bool EO>
+__device__ __forceinline__ V8 unpack_bf16(const uint4& q) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    V8 v;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float l0 = __uint_as_float(w[i] << 16), h0 = __uint_as_float(w[i] & 0xFFFF0000u);
+        const float l1 = __uint_as_float(w[i + 1] << 16), h1 = __uint_as_float(w[i + 1] & 0xFFFF0000u);
+        v.p[i] = EO ? make_float2(l0, l1) : make_float2(l0, h0);
+        v.p[i + 1] = EO ? make_float2(h0, h1) : make_float2(l1, h1);
+    }
+    return v;
+}
+
+template <bool EO>
+__device__ __forceinline__ uint4 pack_bf16(const V8& v) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        w[i] = EO ? pack2(v.p[i].x, v.p[i + 1].x) : pack2(v.p[i].x, v.p[i].y);
+        w[i + 1] = EO ? pack2(v.p[i].y, v.p[i + 1].y) : pack2(v.p[i + 1].x, v.p[i + 1].y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <bool EO>
+__device__ __forceinline__ V8 arrange(const float (&f)[8]) {
+    V8 v;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        v.p[i] = EO ? make_float2(f[2 * i], f[2 * i + 2]) : make_float2(f[2 * i], f[2 * i + 1]);
+        v.p[i + 1] = EO ? make_float2(f[2 * i + 1], f[2 * i + 3]) : make_float2(f[2 * i + 2], f[2 * i + 3]);
+    }
+    return v;
+}
+
+// The channel of pair i's first and second value.
+template <bool EO>
+__device__ __forceinline__ int channel_of(int i, int second) {
+    return EO ? (i & 2) * 2 + (i & 1) + 2 * second : 2 * i + second;
+}
+
+__device__ __forceinline__ float dot(const V8& a, const V8& b) {
+    float2 s = __fmul2_rn(a.p[0], b.p[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) s = __ffma2_rn(a.p[i], b.p[i], s);
+    return s.x + s.y;
+}
+
+__device__ __forceinline__ V8 mul(const V8& a, const V8& b) {
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __fmul2_rn(a.p[i], b.p[i]);
+    return r;
+}
+
+__device__ __forceinline__ V8 mul(const V8& a, float b) {
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __fmul2_rn(a.p[i], f2(b));
+    return r;
+}
+
+// a * b + c
+__device__ __forceinline__ V8 fma8(const V8& a, const V8& b, const V8& c) {
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __ffma2_rn(a.p[i], b.p[i], c.p[i]);
+    return r;
+}
+
+__device__ __forceinline__ V8 fma8(const V8& a, float b, const V8& c) {
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __ffma2_rn(a.p[i], f2(b), c.p[i]);
+    return r;
+}
+
 // ---------------------------------------------------------------- sums
 // Sum over aligned groups of L lanes (L a power of two); every lane gets it.
 template <int L>
@@ -115,8 +205,86 @@ __device__ __forceinline__ float lane_sum(float v) {
     return v;
 }
 
+// Sums of NV values over aligned groups of L lanes, NV <= L: while there are
+// several values left the two halves of the group keep half of them each, so NV
+// sums cost little more than one.  A lane ends with the sum of value
+// scattered_index<NV, L>(lane).
+template <int NV, int L>
+__device__ __forceinline__ float scatter_sum(float (&v)[NV]) {
+    int o = L / 2;
+#pragma unroll
+    for (int n = NV / 2; n >= 1; n /= 2, o /= 2) {
+        const bool upper = (threadIdx.x & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+            const float send = upper ? v[i] : v[i + n];
+            v[i] = (upper ? v[i + n] : v[i]) + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+        }
+    }
+    if constexpr (NV < L)
+#pragma unroll
+        for (; o > 0; o /= 2) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+    return v[0];
+}
+
+// The value a lane holds after scatter_sum, and whether it is the one to write it.
+template <int NV, int L>
+__device__ __forceinline__ int scattered_index() {
+    return static_cast<int>(threadIdx.x % L) / (L / NV);
+}
+template <int NV, int L>
+__device__ __forceinline__ bool scattered_writer() {
+    return threadIdx.x % (L / NV) == 0;
+}
+
+// ---------------------------------------------------------------- integer division
+// n / d for n < 2^31 by a multiplication: with 2^(L-1) < d <= 2^L and
+// m = floor(2^32 (2^L - d) / d) + 1, n / d = (n m / 2^32 + n) / 2^L.
+struct FastDiv {
+    uint32_t d, m, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t by) : d(by), m(0), shift(0) {
+        while (shift < 31 && (1u << shift) < by) ++shift;
+        m = static_cast<uint32_t>(((uint64_t(1) << 32) * ((uint64_t(1) << shift) - by)) / by + 1);
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> shift; }
+};
+
 // ---------------------------------------------------------------- host side
 inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Blocks of a kernel that an SM holds at once, and the kernel allowed its dynamic
+// shared memory.  Asked of the runtime once per kernel, size and device.
+inline bss_status resident_blocks(const void* kernel, int threads, int smem, int* blocks) {
+    struct Known {
+        const void* kernel;
+        int device, threads, smem, blocks;
+    };
+    static std::mutex mutex;
+    static std::vector<Known> known;
+    int device = 0;
+    bss_status st = cuda_check(cudaGetDevice(&device), "current device");
+    if (st != BSS_OK) return st;
+    std::lock_guard<std::mutex> lock(mutex);
+    for (const Known& k : known)
+        if (k.kernel == kernel && k.device == device && k.threads == threads && k.smem == smem) {
+            *blocks = k.blocks;
+            return BSS_OK;
+        }
+    // the limit of a kernel only grows: another size of it may be in use
+    int most = smem;
+    for (const Known& k : known)
+        if (k.kernel == kernel && k.device == device && k.smem > most) most = k.smem;
+    if (most > 48 * 1024)
+        st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "shared memory size");
+    int n = 0;
+    if (st == BSS_OK)
+        st = cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem), "occupancy");
+    if (st != BSS_OK) return st;
+    *blocks = n < 1 ? 1 : n;
+    known.push_back({kernel, device, threads, smem, *blocks});
+    return BSS_OK;
+}
 
 // The bytes that a strided tensor touches: `n` runs of `extent` bytes, `stride`
 // bytes apart.
