@@ -73,6 +73,14 @@ class MaskParams:
         return self.F * self.S
 
     def c(self) -> _MaskParams:
+        """The C form (made once: the fields do not change, the library only reads it)."""
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = self._make_c()
+            object.__setattr__(self, "_c", c)
+        return c
+
+    def _make_c(self) -> _MaskParams:
         return _MaskParams(self.F, self.Hs, self.Ws, self.head_dim, self.spatial_frame_window,
                            self.temporal_raster_window, self.sink_frames, self.temporal_permuted, self.rounding)
 
@@ -228,6 +236,9 @@ def _ptr(t):
 def _stream(stream):
     import torch
     if stream is None:
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:  # the address alone: a Stream object costs 3 us
+            return ctypes.c_void_p(raw(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -608,51 +619,57 @@ def attention_step_host(hQ, hK, hV, hO, tile_map: TileMap, head_is_temporal, wor
 
 # ---------------------------------------------------------------- around the attention step (include/bss_block.h)
 
-def _on_one_device(*named):
-    """Every given tensor on the current device (kernels are launched there)."""
+def _current_device():
     import torch
-    current = torch.cuda.current_device()
-    for t, n in named:
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise ValueError(f"{n} must be a CUDA tensor")
-        if t.device.index != current:
-            raise ValueError(f"{n} is on {t.device}, the current device is cuda:{current}")
+    return torch.cuda.current_device()
 
 
-def _exact(t, name, dtype, shape):
-    """A given contiguous tensor of this type and shape."""
+def _on_device(t, name, device):
+    """A tensor on the current device, where kernels are launched."""
+    try:
+        on = t.get_device()
+    except AttributeError:
+        on = -1
+    if on != device:
+        raise ValueError(f"{name} must be a CUDA tensor" if on < 0 else
+                         f"{name} is on cuda:{on}, the current device is cuda:{device}")
+
+
+def _exact(t, name, dtype, shape, device):
+    """The address of a given contiguous tensor of this type and shape (None: None)."""
     if t is None:
-        return
+        return None
+    _on_device(t, name, device)
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _dtype_code(t, name):
+def _dtype_code(dtype, name):
     import torch
-    if t.dtype == torch.bfloat16:
+    if dtype == torch.bfloat16:
         return DTYPE_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return DTYPE_F32
-    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    raise ValueError(f"{name} must be bfloat16 or float32, got {dtype}")
 
 
 def _one_dtype(*named):
-    """The code of the one type that every given tensor has."""
-    code = None
+    """The type that every given tensor has (None when none is given)."""
+    dtype = None
     for t, n in named:
         if t is None:
             continue
-        c = _dtype_code(t, n)
-        if code is not None and c != code:
+        if dtype is None:
+            dtype = getattr(t, "dtype", None)
+            _dtype_code(dtype, n)
+        elif getattr(t, "dtype", None) != dtype:
             raise ValueError(f"{', '.join(m for u, m in named if u is not None)} must have one type")
-        code = c
-    return DTYPE_F32 if code is None else code
+    return dtype
 
 
 def _workspace(workspace, nbytes, stream):
@@ -660,7 +677,7 @@ def _workspace(workspace, nbytes, stream):
     stream the call runs on."""
     import torch
     if workspace is not None:
-        _on_one_device((workspace, "workspace"))
+        _on_device(workspace, "workspace", _current_device())
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         return workspace
@@ -684,85 +701,83 @@ def rotary_table(length: int, pairs: int, base: float = 10000.0, dim: int | None
         raise ValueError("length and pairs must be positive")
     if out is None:
         out = torch.empty(length, pairs, 2, dtype=torch.float32, device="cuda")
-    _on_one_device((out, "out"), (positions, "positions"))
-    _exact(out, "out", torch.float32, (length, pairs, 2))
-    _exact(positions, "positions", torch.float64, (length,))
-    _check(load().bss_rotary_table(_ptr(positions), length, pairs, 2 * pairs if dim is None else dim, float(base),
-                                   _ptr(out), _stream(stream)))
+    device = _current_device()
+    _check(load().bss_rotary_table(_exact(positions, "positions", torch.float64, (length,), device), length, pairs,
+                                   2 * pairs if dim is None else dim, float(base),
+                                   _exact(out, "out", torch.float32, (length, pairs, 2), device), _stream(stream)))
     return out
 
 
-@dataclass(frozen=True)
 class Rotary:
     """Rotary positions of the (time, height, width) axes for ``heads_from_tokens``.
 
     time, height, width: float32 CUDA tables [positions][pairs][2] of (cos, sin)
-    (``rotary_table`` makes one), None or 0 pairs for an axis that turns nothing;
-    the pairs of the three are dealt to the channels in this order.  Token (f, h,
-    w) uses rows offset + (f, h, w).  pairing: PAIR_INTERLEAVED or PAIR_HALVES."""
-    time: object = None
-    height: object = None
-    width: object = None
-    offset: tuple = (0, 0, 0)
-    pairing: int = PAIR_INTERLEAVED
+    (``rotary_table`` makes one), None for an axis that turns nothing; the pairs
+    of the three are dealt to the channels in this order.  Token (f, h, w) uses
+    rows offset + (f, h, w).  pairing: PAIR_INTERLEAVED or PAIR_HALVES.  Holds
+    the tables; what it was made from is not changed afterwards."""
+    __slots__ = ("time", "height", "width", "offset", "pairing", "device", "_pointer")
 
-    def __post_init__(self):
+    def __init__(self, time=None, height=None, width=None, offset=(0, 0, 0), pairing: int = PAIR_INTERLEAVED):
         import torch
-        r = _Rotary()
-        for i, (t, n) in enumerate(((self.time, "time"), (self.height, "height"), (self.width, "width"))):
+        self.time, self.height, self.width, self.offset, self.pairing = time, height, width, tuple(offset), pairing
+        address, length, pairs, device = [], [], [], None
+        for t, n in ((time, "time"), (height, "height"), (width, "width")):
             if t is None:
+                address.append(None)
+                length.append(0)
+                pairs.append(0)
                 continue
             if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != 2:
                 raise ValueError(f"rotary table {n} must be a tensor [positions][pairs][2]")
-            _dev_tensor(t, f"rotary table {n}", torch.float32)
-            r.table[i], r.length[i], r.pairs[i] = t.data_ptr(), t.shape[0], t.shape[1]
+            if device is None:
+                device = t.get_device()
+            address.append(_exact(t, f"rotary table {n}", torch.float32, t.shape, max(device, 0)))
+            length.append(t.shape[0])
+            pairs.append(t.shape[1])
         if len(self.offset) != 3:
             raise ValueError("offset must have three entries")
-        for i in range(3):
-            r.offset[i] = self.offset[i]
-        r.pairing = self.pairing
-        object.__setattr__(self, "_c", r)
-
-    def tables(self):
-        return (self.time, "rotary table time"), (self.height, "rotary table height"), (self.width, "rotary table width")
+        self.device = device
+        self._pointer = ctypes.pointer(_Rotary(tuple(address), tuple(length), tuple(pairs), self.offset, pairing))
 
 
-def _token_tensor(t, name, shape):
+def _token_tensor(t, name, shape, device):
     """A [N][H][d] bf16 tensor with any token and head strides -> its C form."""
     import torch
     if t is None:
         return None
+    _on_device(t, name, device)
     if t.dtype != torch.bfloat16:
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape} (tokens, heads, channels)")
-    s = t.stride()
-    if s[2] != 1:
+    tokens, heads, channels = t.stride()
+    if channels != 1:
         raise ValueError(f"{name}: the channels of a head must be contiguous")
-    return ctypes.byref(_TokenTensor(t.data_ptr(), s[0], s[1]))
+    return ctypes.byref(_TokenTensor(t.data_ptr(), tokens, heads))
 
 
-def _heads_options(H, d, rotary, q_weight, k_weight, norm, eps):
-    import torch
+def _heads_options(H, d, rotary, q_weight, k_weight, norm, eps, device):
     if norm == HEAD_NORM_NONE and (q_weight is not None or k_weight is not None):
         raise ValueError("weights are given without a norm")
-    if rotary is not None and not isinstance(rotary, Rotary):
-        raise ValueError("rotary must be a Rotary")
+    if rotary is not None:
+        if not isinstance(rotary, Rotary):
+            raise ValueError("rotary must be a Rotary")
+        if rotary.device is not None and rotary.device != device:
+            raise ValueError(f"the rotary tables are on cuda:{rotary.device}, the current device is cuda:{device}")
     width = H * d if norm == HEAD_NORM_TOKEN else d
-    code = _one_dtype((q_weight, "q_weight"), (k_weight, "k_weight"))
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _exact(w, n, w.dtype, (width,))
-    return _HeadsOptions(norm, eps, code, None if q_weight is None else q_weight.data_ptr(),
-                         None if k_weight is None else k_weight.data_ptr(),
-                         None if rotary is None else ctypes.pointer(rotary._c)), width
+    dtype = _one_dtype((q_weight, "q_weight"), (k_weight, "k_weight"))
+    code = DTYPE_F32 if dtype is None else _dtype_code(dtype, "weights")
+    return _HeadsOptions(norm, eps, code, _exact(q_weight, "q_weight", dtype, (width,), device),
+                         _exact(k_weight, "k_weight", dtype, (width,), device),
+                         None if rotary is None else rotary._pointer), width
 
 
 def _heads_of(*tensors, axis):
     for t in tensors:
         if t is not None:
-            if t.dim() != 3:
-                raise ValueError("Q, K and V have three dimensions")
+            if getattr(t, "ndim", 0) != 3:
+                raise ValueError("Q, K and V must be CUDA tensors of three dimensions")
             return t.shape[axis]
     raise ValueError("no tensor given")
 
@@ -780,18 +795,14 @@ def heads_from_tokens(q, k, v, Qh, Kh, Vh, params: MaskParams, head_is_temporal=
     (q, Qh), (k, Kh), (v, Vh) may be None."""
     import torch
     H, d, N = _heads_of(q, k, v, axis=1), params.head_dim, params.N
-    _on_one_device((q, "q"), (k, "k"), (v, "v"), (Qh, "Qh"), (Kh, "Kh"), (Vh, "Vh"), (q_weight, "q_weight"),
-                   (k_weight, "k_weight"), (head_is_temporal, "head_is_temporal"),
-                   *(rotary.tables() if isinstance(rotary, Rotary) else ()))
-    for t, n in ((Qh, "Qh"), (Kh, "Kh"), (Vh, "Vh")):
-        _exact(t, n, torch.bfloat16, (H, N, d))
-    _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,))
-    options, _ = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps)
-    shape = (N, H, d)
-    _check(load().bss_heads_from_tokens(_token_tensor(q, "q", shape), _token_tensor(k, "k", shape),
-                                        _token_tensor(v, "v", shape), _ptr(Qh), _ptr(Kh), _ptr(Vh),
-                                        _ptr(head_is_temporal), H, ctypes.byref(params.c()), ctypes.byref(options),
-                                        _stream(stream)))
+    device = _current_device()
+    options, _ = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps, device)
+    shape, heads = (N, H, d), (H, N, d)
+    _check(load().bss_heads_from_tokens(
+        _token_tensor(q, "q", shape, device), _token_tensor(k, "k", shape, device), _token_tensor(v, "v", shape, device),
+        _exact(Qh, "Qh", torch.bfloat16, heads, device), _exact(Kh, "Kh", torch.bfloat16, heads, device),
+        _exact(Vh, "Vh", torch.bfloat16, heads, device), _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,), device), H,
+        ctypes.byref(params.c()), ctypes.byref(options), _stream(stream)))
     return Qh, Kh, Vh
 
 
@@ -809,30 +820,24 @@ def heads_from_tokens_backward(dQh, dKh, dVh, dq, dk, dv, params: MaskParams, he
     when None)."""
     import torch
     H, d, N = _heads_of(dQh, dKh, dVh, axis=0), params.head_dim, params.N
-    _on_one_device((dQh, "dQh"), (dKh, "dKh"), (dVh, "dVh"), (dq, "dq"), (dk, "dk"), (dv, "dv"), (q, "q"), (k, "k"),
-                   (q_weight, "q_weight"), (k_weight, "k_weight"), (dq_weight, "dq_weight"), (dk_weight, "dk_weight"),
-                   (head_is_temporal, "head_is_temporal"),
-                   *(rotary.tables() if isinstance(rotary, Rotary) else ()))
-    for t, n in ((dQh, "dQh"), (dKh, "dKh"), (dVh, "dVh")):
-        _exact(t, n, torch.bfloat16, (H, N, d))
-    _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,))
-    options, width = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps)
-    _exact(dq_weight, "dq_weight", torch.float32, (width,))
-    _exact(dk_weight, "dk_weight", torch.float32, (width,))
-    shape, lib, mp = (N, H, d), load(), params.c()
+    device = _current_device()
+    options, width = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps, device)
+    shape, heads, lib, mp = (N, H, d), (H, N, d), load(), ctypes.byref(params.c())
+    nbytes = 0
     if dq_weight is not None or dk_weight is not None:
         need = ctypes.c_int64()
-        _check(lib.bss_heads_from_tokens_backward_workspace(H, ctypes.byref(mp), norm, ctypes.byref(need)))
+        _check(lib.bss_heads_from_tokens_backward_workspace(H, mp, norm, ctypes.byref(need)))
         workspace = _workspace(workspace, need.value, stream)
+        nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     else:
         workspace = None
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib.bss_heads_from_tokens_backward(_ptr(dQh), _ptr(dKh), _ptr(dVh), _token_tensor(q, "q", shape),
-                                              _token_tensor(k, "k", shape), _token_tensor(dq, "dq", shape),
-                                              _token_tensor(dk, "dk", shape), _token_tensor(dv, "dv", shape),
-                                              _ptr(dq_weight), _ptr(dk_weight), _ptr(head_is_temporal), H,
-                                              ctypes.byref(mp), ctypes.byref(options), _ptr(workspace), nbytes,
-                                              _stream(stream)))
+    _check(lib.bss_heads_from_tokens_backward(
+        _exact(dQh, "dQh", torch.bfloat16, heads, device), _exact(dKh, "dKh", torch.bfloat16, heads, device),
+        _exact(dVh, "dVh", torch.bfloat16, heads, device), _token_tensor(q, "q", shape, device), _token_tensor(k, "k", shape, device),
+        _token_tensor(dq, "dq", shape, device), _token_tensor(dk, "dk", shape, device), _token_tensor(dv, "dv", shape, device),
+        _exact(dq_weight, "dq_weight", torch.float32, (width,), device), _exact(dk_weight, "dk_weight", torch.float32, (width,), device),
+        _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,), device), H, mp, ctypes.byref(options),
+        None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream)))
     return dq, dk, dv
 
 
@@ -846,37 +851,35 @@ def attention_step_tokens(q, k, v, O, tile_map: TileMap, head_is_temporal, Qh, K
     import torch
     p = tile_map.params
     H, d, N = _heads_of(q, axis=1), p.head_dim, p.N
-    named = [(O, "O"), (Qh, "Qh"), (Kh, "Kh"), (Vh, "Vh")]
-    _on_one_device((q, "q"), (k, "k"), (v, "v"), *named, (q_weight, "q_weight"), (k_weight, "k_weight"),
-                   (head_is_temporal, "head_is_temporal"), (lse, "lse"),
-                   *(rotary.tables() if isinstance(rotary, Rotary) else ()))
+    named = ((O, "O"), (Qh, "Qh"), (Kh, "Kh"), (Vh, "Vh"))
+    device = _current_device()
     for t, n in named:
         if t is None:
             raise ValueError(f"{n} must be a CUDA tensor")
-        _exact(t, n, torch.bfloat16, (H, N, d))
-    _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,))
-    _exact(lse, "lse", torch.float32, (H, N))
-    options, _ = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps)
+    options, _ = _heads_options(H, d, rotary, q_weight, k_weight, norm, eps, device)
     shape = (N, H, d)
-    _check(load().bss_attention_step_tokens(_token_tensor(q, "q", shape), _token_tensor(k, "k", shape),
-                                            _token_tensor(v, "v", shape), _ptr(O), _ptr(lse), tile_map.handle,
-                                            _ptr(head_is_temporal), H, ctypes.byref(options), _ptr(Qh), _ptr(Kh),
-                                            _ptr(Vh), _stream(stream)))
+    O_p, Q_p, K_p, V_p = (_exact(t, n, torch.bfloat16, (H, N, d), device) for t, n in named)
+    _check(load().bss_attention_step_tokens(
+        _token_tensor(q, "q", shape, device), _token_tensor(k, "k", shape, device), _token_tensor(v, "v", shape, device), O_p,
+        _exact(lse, "lse", torch.float32, (H, N), device), tile_map.handle,
+        _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,), device), H, ctypes.byref(options), Q_p, K_p, V_p,
+        _stream(stream)))
     return O
 
 
-def _row_tensor(t, name, dtype, rows, channels, like=None):
-    """(pointer, row stride) of a given [rows][channels] tensor with any row stride."""
+def _row_tensor(t, name, dtype, shape, device):
+    """(address, row stride) of a given [rows][channels] tensor with any row stride."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != (rows, channels):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be ({rows}, {channels})")
-    if dtype is not None and t.dtype != dtype:
+    _on_device(t, name, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape}")
+    if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    s = t.stride()
-    if s[1] != 1:
+    rows, channels = t.stride()
+    if channels != 1:
         raise ValueError(f"{name}: the channels of a row must be contiguous")
-    return t.data_ptr(), s[0]
+    return t.data_ptr(), rows
 
 
 def _row_shape(t, name):
@@ -884,6 +887,15 @@ def _row_shape(t, name):
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
         raise ValueError(f"{name} must be a CUDA tensor [rows][channels]")
     return t.shape
+
+
+def _groups(rows, rows_per_group, channels):
+    """Rows per group and the shape of per-group parameters."""
+    if rows_per_group is None:
+        rows_per_group = rows
+    if rows <= 0 or rows_per_group <= 0:
+        raise ValueError("rows and rows_per_group must be positive")
+    return rows_per_group, (-(-rows // rows_per_group), channels)
 
 
 def residual_norm(x, y=None, r=None, h=None, gate=None, scale=None, shift=None, weight=None, bias=None, y_weight=None,
@@ -903,35 +915,26 @@ def residual_norm(x, y=None, r=None, h=None, gate=None, scale=None, shift=None, 
     y_stats: float32 [rows][2] outputs, (mean, 1 / deviation) of each row, for the
     backward pass.  Returns (r, h)."""
     import torch
-    rows, channels = _row_shape(x, "x")
-    _on_one_device((x, "x"), (y, "y"), (r, "r"), (h, "h"), (gate, "gate"), (scale, "scale"), (shift, "shift"),
-                   (weight, "weight"), (bias, "bias"), (y_weight, "y_weight"), (stats, "stats"), (y_stats, "y_stats"))
-    if rows_per_group is None:
-        rows_per_group = rows
-    if rows_per_group <= 0:
-        raise ValueError("rows_per_group must be positive")
-    groups = -(-rows // rows_per_group)
-    a = _ResidualNormArgs(rows=rows, rows_per_group=rows_per_group, channels=channels, norm=norm, y_norm=y_norm, eps=eps,
-                          residual_scale=residual_scale)
-    a.stream_dtype = _dtype_code(x, "x")
-    a.branch_dtype = _one_dtype((y, "y"), (h, "h")) if y is not None or h is not None else DTYPE_BF16
-    a.param_dtype = _one_dtype((gate, "gate"), (scale, "scale"), (shift, "shift"), (weight, "weight"), (bias, "bias"),
-                               (y_weight, "y_weight"))
-    a.x, a.x_stride = _row_tensor(x, "x", None, rows, channels)
-    a.y, a.y_stride = _row_tensor(y, "y", None, rows, channels)
-    a.r, a.r_stride = _row_tensor(r, "r", x.dtype, rows, channels)
-    a.h, a.h_stride = _row_tensor(h, "h", None, rows, channels)
-    a.gate, a.gate_stride = _row_tensor(gate, "gate", None, groups, channels)
-    a.scale, a.scale_stride = _row_tensor(scale, "scale", None, groups, channels)
-    a.shift, a.shift_stride = _row_tensor(shift, "shift", None, groups, channels)
-    for t, n in ((weight, "weight"), (bias, "bias"), (y_weight, "y_weight")):
-        if t is not None:
-            _exact(t, n, t.dtype, (channels,))
-            setattr(a, n, t.data_ptr())
-    for t, n in ((stats, "stats"), (y_stats, "y_stats")):
-        if t is not None:
-            _exact(t, n, torch.float32, (rows, 2))
-            setattr(a, n, t.data_ptr())
+    shape = rows, channels = _row_shape(x, "x")
+    device = _current_device()
+    group, mods = _groups(rows, rows_per_group, channels)
+    branch = _one_dtype((y, "y"), (h, "h"))
+    param = _one_dtype((gate, "gate"), (scale, "scale"), (shift, "shift"), (weight, "weight"), (bias, "bias"),
+                       (y_weight, "y_weight"))
+    x_p, x_s = _row_tensor(x, "x", x.dtype, shape, device)
+    y_p, y_s = _row_tensor(y, "y", branch, shape, device)
+    r_p, r_s = _row_tensor(r, "r", x.dtype, shape, device)
+    h_p, h_s = _row_tensor(h, "h", branch, shape, device)
+    gate_p, gate_s = _row_tensor(gate, "gate", param, mods, device)
+    scale_p, scale_s = _row_tensor(scale, "scale", param, mods, device)
+    shift_p, shift_s = _row_tensor(shift, "shift", param, mods, device)
+    a = _ResidualNormArgs(
+        rows, group, channels, _dtype_code(x.dtype, "x"), DTYPE_BF16 if branch is None else _dtype_code(branch, "h"),
+        DTYPE_F32 if param is None else _dtype_code(param, "weights"), norm, y_norm, eps, residual_scale, x_p, y_p, r_p,
+        h_p, x_s, y_s, r_s, h_s, gate_p, scale_p, shift_p, gate_s, scale_s, shift_s,
+        _exact(weight, "weight", param, (channels,), device), _exact(bias, "bias", param, (channels,), device),
+        _exact(y_weight, "y_weight", param, (channels,), device), _exact(stats, "stats", torch.float32, (rows, 2), device),
+        _exact(y_stats, "y_stats", torch.float32, (rows, 2), device))
     _check(load().bss_residual_norm(ctypes.byref(a), _stream(stream)))
     return r, h
 
@@ -950,45 +953,32 @@ def residual_norm_backward(r, y=None, dr=None, dh=None, dx=None, dy=None, stats=
     overwritten.  Every sum over rows is taken in a fixed order.  workspace:
     memory for partial sums (taken from torch's allocator when None)."""
     import torch
-    rows, channels = _row_shape(dx, "dx")
-    rest = [(r, "r"), (y, "y"), (dr, "dr"), (dh, "dh"), (dx, "dx"), (dy, "dy"), (stats, "stats"), (y_stats, "y_stats"),
-            (gate, "gate"), (scale, "scale"), (weight, "weight"), (bias, "bias"), (y_weight, "y_weight"),
-            (dgate, "dgate"), (dscale, "dscale"), (dshift, "dshift"), (dweight, "dweight"), (dbias, "dbias"),
-            (dy_weight, "dy_weight")]
-    _on_one_device(*rest)
-    if rows_per_group is None:
-        rows_per_group = rows
-    if rows_per_group <= 0:
-        raise ValueError("rows_per_group must be positive")
-    groups = -(-rows // rows_per_group)
-    a = _ResidualNormGrads(rows=rows, rows_per_group=rows_per_group, channels=channels, norm=norm, y_norm=y_norm,
-                           residual_scale=residual_scale)
-    a.stream_dtype = _one_dtype((dx, "dx"), (dr, "dr"), (r, "r"))
-    a.branch_dtype = _one_dtype((y, "y"), (dy, "dy"), (dh, "dh")) if y is not None or dh is not None else DTYPE_BF16
-    a.param_dtype = _one_dtype((gate, "gate"), (scale, "scale"), (weight, "weight"), (bias, "bias"),
-                               (y_weight, "y_weight"))
-    for t, n in rest[:6]:
-        p, stride = _row_tensor(t, n, None, rows, channels)
-        setattr(a, n, p)
-        setattr(a, n + "_stride", stride)
-    a.gate, a.gate_stride = _row_tensor(gate, "gate", None, groups, channels)
-    a.scale, a.scale_stride = _row_tensor(scale, "scale", None, groups, channels)
-    for t, n, shape in ((stats, "stats", (rows, 2)), (y_stats, "y_stats", (rows, 2)), (dgate, "dgate", (groups, channels)),
-                        (dscale, "dscale", (groups, channels)), (dshift, "dshift", (groups, channels)),
-                        (dweight, "dweight", (channels,)), (dbias, "dbias", (channels,)),
-                        (dy_weight, "dy_weight", (channels,))):
-        if t is not None:
-            _exact(t, n, torch.float32, shape)
-            setattr(a, n, t.data_ptr())
-    for t, n in ((weight, "weight"), (bias, "bias"), (y_weight, "y_weight")):
-        if t is not None:
-            _exact(t, n, t.dtype, (channels,))
-            setattr(a, n, t.data_ptr())
-    lib = load()
-    need = ctypes.c_int64()
-    _check(lib.bss_residual_norm_backward_workspace(ctypes.byref(a), ctypes.byref(need)))
+    shape = rows, channels = _row_shape(dx, "dx")
+    device = _current_device()
+    group, mods = _groups(rows, rows_per_group, channels)
+    branch = _one_dtype((y, "y"), (dh, "dh"), (dy, "dy"))
+    param = _one_dtype((gate, "gate"), (scale, "scale"), (weight, "weight"), (bias, "bias"), (y_weight, "y_weight"))
+    r_p, r_s = _row_tensor(r, "r", dx.dtype, shape, device)
+    y_p, y_s = _row_tensor(y, "y", branch, shape, device)
+    dr_p, dr_s = _row_tensor(dr, "dr", dx.dtype, shape, device)
+    dh_p, dh_s = _row_tensor(dh, "dh", branch, shape, device)
+    dx_p, dx_s = _row_tensor(dx, "dx", dx.dtype, shape, device)
+    dy_p, dy_s = _row_tensor(dy, "dy", branch, shape, device)
+    gate_p, gate_s = _row_tensor(gate, "gate", param, mods, device)
+    scale_p, scale_s = _row_tensor(scale, "scale", param, mods, device)
+    f32, row = torch.float32, (channels,)
+    a = _ResidualNormGrads(
+        rows, group, channels, _dtype_code(dx.dtype, "dx"), DTYPE_BF16 if branch is None else _dtype_code(branch, "dh"),
+        DTYPE_F32 if param is None else _dtype_code(param, "weights"), norm, y_norm, residual_scale, r_p, y_p, dr_p,
+        dh_p, dx_p, dy_p, r_s, y_s, dr_s, dh_s, dx_s, dy_s, _exact(stats, "stats", f32, (rows, 2), device),
+        _exact(y_stats, "y_stats", f32, (rows, 2), device), gate_p, scale_p, gate_s, scale_s, _exact(weight, "weight", param, row, device),
+        _exact(bias, "bias", param, row, device), _exact(y_weight, "y_weight", param, row, device), _exact(dgate, "dgate", f32, mods, device),
+        _exact(dscale, "dscale", f32, mods, device), _exact(dshift, "dshift", f32, mods, device), _exact(dweight, "dweight", f32, row, device),
+        _exact(dbias, "dbias", f32, row, device), _exact(dy_weight, "dy_weight", f32, row, device))
+    lib, need, args = load(), ctypes.c_int64(), ctypes.byref(a)
+    _check(lib.bss_residual_norm_backward_workspace(args, ctypes.byref(need)))
     workspace = _workspace(workspace, need.value, stream)
     if workspace is not None:
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.bss_residual_norm_backward(ctypes.byref(a), _stream(stream)))
+    _check(lib.bss_residual_norm_backward(args, _stream(stream)))
     return dx, dy

@@ -20,8 +20,8 @@
 // of its rotary pairs, is the same for all the heads of Q and K that the lane
 // holds, a token's coordinates are the same for the warp, and the norm's sums need
 // no barrier.  Every lane copies its own pieces of the next token into its own
-// slots of shared memory (cp.async, two stages) while it works on this one: loads
-// stay in flight without holding registers, and the pieces are walked in a loop.
+// slots of shared memory (cp.async, two stages) while it works on this one, and V
+// goes straight through: loads stay in flight without holding registers, and the pieces are walked in a loop.
 // Wide tokens are shared by several warps when the norm is over the token, else
 // their heads go to several grid columns.
 #include <cstring>
@@ -55,6 +55,7 @@ struct HeadsArgs {
     uint32_t N, F, S, H;
     int32_t pieces;               // 16-byte pieces of a head: 8 or 16
     int32_t heads_per_block;      // heads of a token that a block's grid column covers
+    uint32_t span;                // tokens that a block walks over, one after the other
     float* partial;               // backward: [blocks][2][width], or NULL
 };
 
@@ -77,9 +78,17 @@ __device__ __forceinline__ Lane lane_of(const HeadsArgs& a, int warp) {
     l.step = W * per;
     l.count = l.head0 < last ? min(VPT, (last - l.head0 + l.step - 1) / l.step) : 0;
     l.temporal = 0;
-    if (a.flags != nullptr)
-        for (int i = 0; i < l.count; ++i) l.temporal |= (a.flags[l.head0 + i * l.step] != 0 ? 1u : 0u) << i;
     return l;
+}
+
+template <int VPT>
+__device__ __forceinline__ uint32_t temporal_heads(const HeadsArgs& a, const Lane& l) {
+    uint32_t r = 0;
+    if (a.flags != nullptr)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (j < l.count) r |= (a.flags[l.head0 + j * l.step] != 0 ? 1u : 0u) << j;
+    return r;
 }
 
 struct Token {
@@ -139,25 +148,46 @@ __device__ __forceinline__ Pairs<HALVES> pairs_of(const HeadsArgs& a, int piece)
     return r;
 }
 
-// One token's angles for a lane's pairs; the identity where nothing turns.
+// One token's angles for a lane's pairs.
 template <bool HALVES>
 struct Turn {
     float2 c[HALVES ? 4 : 2], s[HALVES ? 4 : 2];
 };
 
+// A lane's angle slots, [pair][32 lanes] of 8 bytes: those of pairs that do not
+// turn hold the identity throughout, the others are copied token by token.
 template <bool HALVES>
-__device__ __forceinline__ Turn<HALVES> load_turn(const Pairs<HALVES>& pr, const Token& t) {
-    Turn<HALVES> r;
+__device__ __forceinline__ void clear_turn(const Pairs<HALVES>& pr, uint32_t at) {
+#pragma unroll
+    for (int j = 0; j < Pairs<HALVES>::kCount; ++j)
+        if ((pr.axes >> (2 * j) & 3u) == 3)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + j * 256), "f"(1.0f), "f"(0.0f) : "memory");
+}
+
+template <bool HALVES>
+__device__ __forceinline__ void fetch_turn(const Pairs<HALVES>& pr, const Token& t, uint32_t at) {
 #pragma unroll
     for (int j = 0; j < Pairs<HALVES>::kCount; ++j) {
         const uint32_t axis = pr.axes >> (2 * j) & 3u;
-        float2 v = make_float2(1.0f, 0.0f);
-        const uint32_t at = axis == 0 ? t.f : axis == 1 ? t.h : t.w;
-        if (axis != 3) v = __ldg(pr.entry[j] + static_cast<int64_t>(at) * pr.stride[j]);
+        const uint32_t row = axis == 0 ? t.f : axis == 1 ? t.h : t.w;
+        if (axis != 3)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + j * 256),
+                         "l"(pr.entry[j] + static_cast<int64_t>(row) * pr.stride[j])
+                         : "memory");
+    }
+}
+
+template <bool HALVES>
+__device__ __forceinline__ Turn<HALVES> read_turn(uint32_t at) {
+    Turn<HALVES> r;
+#pragma unroll
+    for (int j = 0; j < Pairs<HALVES>::kCount; ++j) {
+        float c, s;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(c), "=f"(s) : "r"(at + j * 256));
         if (j & 1)
-            r.c[j / 2].y = v.x, r.s[j / 2].y = v.y;
+            r.c[j / 2].y = c, r.s[j / 2].y = s;
         else
-            r.c[j / 2].x = v.x, r.s[j / 2].x = v.y;
+            r.c[j / 2].x = c, r.s[j / 2].x = s;
     }
     return r;
 }
@@ -258,23 +288,29 @@ template <bool EO>
 __device__ __forceinline__ void stage_weights(const HeadsArgs& a, uint32_t at) {
     const int all = a.H * a.pieces;
     for (int i = 0; i < 2; ++i)
+#pragma unroll 4
         for (int e = threadIdx.x; e < all; e += blockDim.x)
             planes_store(at + (i * 2 * all + e) * 16, all * 16,
                          weights_of<EO>(a.weight[i], static_cast<int64_t>(e) * 8, a.weight_dtype));
 }
 
-// A warp's slots: two stages of [tensor][VPT][32 lanes] pieces.  Those of pieces
-// that do not exist hold zeros throughout.
-template <int TENSORS, int VPT>
+// A warp's slots: two stages of [tensor][VPT][32 lanes] pieces and the angles.
+// Those of pieces that do not exist hold zeros throughout.
+__host__ __device__ constexpr uint32_t stage_bytes(int tensors, int vpt, bool halves) {
+    return tensors * vpt * 512 + (halves ? 2048 : 1024);
+}
+
+template <int TENSORS, int VPT, bool HALVES>
 __device__ __forceinline__ uint32_t slots_of(uint32_t at, int count) {
-    at += ((threadIdx.x >> 5) * (2 * TENSORS * VPT * 32) + (threadIdx.x & 31)) * 16;
+    constexpr uint32_t kStage = stage_bytes(TENSORS, VPT, HALVES);
+    at += (threadIdx.x >> 5) * 2 * kStage + (threadIdx.x & 31) * 16;
     for (int e = 0; e < 2 * TENSORS * VPT; ++e)
-        if (e % VPT >= count) sts128(at + e * 512, make_uint4(0, 0, 0, 0));
+        if (e % VPT >= count) sts128(at + e / (TENSORS * VPT) * kStage + e % (TENSORS * VPT) * 512, make_uint4(0, 0, 0, 0));
     return at;
 }
 
 // Blocks of 4 warps an SM shall hold at least, by the registers a thread needs.
-__host__ __device__ constexpr int forward_blocks(int vpt) { return vpt <= 2 ? 5 : vpt <= 5 ? 4 : 3; }
+__host__ __device__ constexpr int forward_blocks(int vpt) { return vpt <= 2 ? 4 : 3; }
 __host__ __device__ constexpr int backward_blocks(int vpt) { return vpt <= 2 ? 4 : 3; }
 
 // W warps share a token, a lane holds up to VPT pieces of a tensor.
@@ -283,17 +319,18 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
     extern __shared__ __align__(16) float4 planes[];  // weights of a norm over a token, then the slots
     __shared__ float buf[2][4 * 2];
     constexpr int kTokens = 4 / W;
-    constexpr uint32_t kStage = 3 * VPT * 512;
+    constexpr uint32_t kStage = stage_bytes(2, VPT, HALVES), kTurn = 2 * VPT * 512;
     const int warp = threadIdx.x / 32 % W, group = threadIdx.x / 32 / W;
-    const Lane me = lane_of<W, VPT>(a, warp);
+    Lane me = lane_of<W, VPT>(a, warp);
     const bool rotary = a.rot.first[3] > 0;
     const Pairs<HALVES> pr = pairs_of<HALVES>(a, me.piece);
     const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
     const uint32_t base = smem_u32(planes);
     const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
-    const uint32_t slots = slots_of<3, VPT>(base + (NORM == BSS_HEAD_NORM_TOKEN ? 4 * all16 : 0), me.count);
-    const uint32_t step = gridDim.x * kTokens;
-    uint32_t n = blockIdx.x * kTokens + group;
+    const uint32_t slots = slots_of<2, VPT, HALVES>(base + (NORM == BSS_HEAD_NORM_TOKEN ? 4 * all16 : 0), me.count);
+    constexpr uint32_t step = kTokens;
+    uint32_t n = blockIdx.x * a.span + group;
+    const uint32_t end = a.N - blockIdx.x * a.span > a.span ? (blockIdx.x + 1) * a.span : a.N;
     // running addresses of the token to fetch, and the steps to the next piece and token
     const char* src[3];
     int64_t apart[3], ahead[3];
@@ -303,10 +340,16 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
         apart[i] = me.step * a.hs[i] * 2;
         ahead[i] = step * a.ts[i] * 2;
     }
-    auto fetch = [&](bool exists, uint32_t to) {
+    const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 8;  // from a lane's slots to its angles
+    if (rotary) clear_turn<HALVES>(pr, slots + turn_at), clear_turn<HALVES>(pr, slots + kStage + turn_at);
+    uint32_t next_row = 0;  // of the fetched token in temporal heads
+    auto fetch = [&](uint32_t m, bool exists, uint32_t to) {
         if (exists) {
+            const Token tok = token_of(a, m);
+            next_row = tok.temporal_row;
+            if (rotary) fetch_turn<HALVES>(pr, tok, to + turn_at);
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 if (a.in[i] == nullptr) continue;
                 const char* p = src[i];
 #pragma unroll
@@ -317,7 +360,8 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
         }
         cp_async_commit();
     };
-    fetch(n < a.N, slots);
+    fetch(n, n < end, slots);
+    me.temporal = temporal_heads<VPT>(a, me);
     V8 w[2];
     if (NORM == BSS_HEAD_NORM_TOKEN) {
         stage_weights<!HALVES>(a, base);
@@ -331,12 +375,20 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
     const int64_t dst = me.head0 * head_bytes + me.piece * 16;
     uint32_t now = slots, other = slots + kStage;
     int turn_buf = 0;
-    for (; n < a.N; n += step, turn_buf ^= 1) {
-        fetch(a.N - n > step, other);
-        const Token tok = token_of(a, n);
-        Turn<HALVES> turn;
-        if (rotary) turn = load_turn<HALVES>(pr, tok);
+    for (; n < end; n += step, turn_buf ^= 1) {
+        const uint32_t temporal_row = next_row;
+        uint4 v_raw[VPT];  // V goes straight through, its loads under Q and K's arithmetic
+        if (a.in[2] != nullptr) {
+            const char* p = src[2];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j, p += apart[2])
+                if (j < me.count) v_raw[j] = ld_row(p);
+            src[2] += ahead[2];
+        }
+        fetch(n + step, end - n > step, other);
         cp_async_wait_group<1>();
+        Turn<HALVES> turn;
+        if (rotary) turn = read_turn<HALVES>(now + turn_at);
         float r[2] = {0.0f, 0.0f};
         if (NORM == BSS_HEAD_NORM_TOKEN) {
 #pragma unroll
@@ -355,22 +407,19 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
 #pragma unroll
         for (int j = 0; j < VPT; ++j, at += head_step) {
             const bool live = j < me.count;
-            const int64_t to = at + static_cast<int64_t>(me.temporal >> j & 1u ? tok.temporal_row : n) * row_bytes;
+            const int64_t to = at + static_cast<int64_t>(me.temporal >> j & 1u ? temporal_row : n) * row_bytes;
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 if (a.in[i] == nullptr) continue;
-                uint4 o = lds128(now + (i * VPT + j) * 512);
-                if (i < 2) {
-                    V8 v = unpack_bf16<!HALVES>(o);
-                    if (NORM == BSS_HEAD_NORM_HEAD)
-                        v = mul(v, mul(w[i < 2 ? i : 0], rsqrtf(head_sum(dot(v, v), a.pieces) * a.inv_width + a.eps)));
-                    if (NORM == BSS_HEAD_NORM_TOKEN && live)
-                        v = mul(v, mul(planes_load(weights + i * 2 * all16 + j * (W * 512), all16), r[i < 2 ? i : 0]));
-                    if (rotary) rotate8<HALVES, false>(v, turn, pr);
-                    o = pack_bf16<!HALVES>(v);
-                }
-                if (live) st_row(reinterpret_cast<char*>(a.out[i]) + to, o);
+                V8 v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
+                if (NORM == BSS_HEAD_NORM_HEAD)
+                    v = mul(v, mul(w[i], rsqrtf(head_sum(dot(v, v), a.pieces) * a.inv_width + a.eps)));
+                if (NORM == BSS_HEAD_NORM_TOKEN && live)
+                    v = mul(v, mul(planes_load(weights + i * 2 * all16 + j * (W * 512), all16), r[i]));
+                if (rotary) rotate8<HALVES, false>(v, turn, pr);
+                if (live) st_row(reinterpret_cast<char*>(a.out[i]) + to, pack_bf16<!HALVES>(v));
             }
+            if (a.in[2] != nullptr && live) st_row(reinterpret_cast<char*>(a.out[2]) + to, v_raw[j]);
         }
         const uint32_t t = now;
         now = other, other = t;
@@ -384,21 +433,24 @@ template <bool HALVES, int NORM, int W, int VPT>
 __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blocks(VPT))
     heads_backward_kernel(const __grid_constant__ HeadsArgs a) {
     constexpr bool kToken = NORM == BSS_HEAD_NORM_TOKEN;
+    constexpr bool kStaged = kToken && W < 8;  // the widest tokens' weights do not fit beside their slots
     constexpr int kWarps = W > 4 ? W : 4, kTokens = kWarps / W;
-    constexpr int kTensors = NORM == BSS_HEAD_NORM_NONE ? 3 : 5;  // dQ, dK, dV, q, k
-    constexpr uint32_t kStage = kTensors * VPT * 512;
+    constexpr int kTensors = NORM == BSS_HEAD_NORM_NONE ? 2 : 4;  // dQ, dK, q, k
+    constexpr uint32_t kStage = stage_bytes(kTensors, VPT, HALVES), kTurn = kTensors * VPT * 512;
     extern __shared__ __align__(16) float4 planes[];
     __shared__ float4 buf4[2][kWarps];
     const int warp = threadIdx.x / 32 % W, group = threadIdx.x / 32 / W;
-    const Lane me = lane_of<W, VPT>(a, warp);
+    Lane me = lane_of<W, VPT>(a, warp);
+    me.temporal = temporal_heads<VPT>(a, me);
     const bool rotary = a.rot.first[3] > 0;
     const Pairs<HALVES> pr = pairs_of<HALVES>(a, me.piece);
     const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
     const uint32_t base = smem_u32(planes);
     const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
-    const uint32_t slots = slots_of<kTensors, VPT>(base + (kToken ? 4 * all16 : 0), me.count);
-    const uint32_t step = gridDim.x * kTokens;
-    uint32_t n = blockIdx.x * kTokens + group;
+    const uint32_t slots = slots_of<kTensors, VPT, HALVES>(base + (kStaged ? 4 * all16 : 0), me.count);
+    constexpr uint32_t step = kTokens;
+    uint32_t n = blockIdx.x * a.span + group;
+    const uint32_t end = a.N - blockIdx.x * a.span > a.span ? (blockIdx.x + 1) * a.span : a.N;
     const int64_t head_bytes = static_cast<int64_t>(a.N) * row_bytes;
     const int64_t head_step = me.step * head_bytes;
     const int64_t grad0 = me.head0 * head_bytes + me.piece * 16;
@@ -416,16 +468,19 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
             xahead[i] = step * a.xts[i] * 2;
         }
     }
+    const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 8;  // from a lane's slots to its angles
+    if (rotary) clear_turn<HALVES>(pr, slots + turn_at), clear_turn<HALVES>(pr, slots + kStage + turn_at);
     auto fetch = [&](uint32_t m, bool exists, uint32_t to) {
         if (exists) {
             const Token tok = token_of(a, m);
+            if (rotary) fetch_turn<HALVES>(pr, tok, to + turn_at);
             int64_t at = grad0;
 #pragma unroll
             for (int j = 0; j < VPT; ++j, at += head_step) {
                 const int64_t from = at + static_cast<int64_t>(me.temporal >> j & 1u ? tok.temporal_row : m) * row_bytes;
                 if (j < me.count)
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
+                    for (int i = 0; i < 2; ++i)
                         if (a.in[i] != nullptr)
                             cp_async_16(to + (i * VPT + j) * 512, reinterpret_cast<const char*>(a.in[i]) + from);
             }
@@ -436,19 +491,24 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
                     const char* p = src[i];
 #pragma unroll
                     for (int j = 0; j < VPT; ++j, p += xapart[i])
-                        if (j < me.count) cp_async_16(to + ((3 + i) * VPT + j) * 512, p);
+                        if (j < me.count) cp_async_16(to + ((2 + i) * VPT + j) * 512, p);
                     src[i] += xahead[i];
                 }
         }
         cp_async_commit();
     };
-    fetch(n, n < a.N, slots);
+    fetch(n, n < end, slots);
     constexpr int kHeld = kToken ? VPT : 1;
     V8 w[2], dw[2][kHeld];
-    if (kToken) {
+    if (kStaged) {
         stage_weights<!HALVES>(a, base);
         __syncthreads();
     }
+    auto weight = [&](int i, int j) {
+        if (kStaged) return planes_load(weights + i * 2 * all16 + j * (W * 512), all16);
+        return weights_of<!HALVES>(a.weight[i], static_cast<int64_t>(me.head0 + j * me.step) * (a.pieces * 8) + me.piece * 8,
+                                   a.weight_dtype);
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         if (NORM == BSS_HEAD_NORM_HEAD) w[i] = weights_of<!HALVES>(a.weight[i], me.piece * 8, a.weight_dtype);
@@ -457,11 +517,21 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
     }
     uint32_t now = slots, other = slots + kStage;
     int turn_buf = 0;
-    for (; n < a.N; n += step, turn_buf ^= 1) {
-        fetch(n + step, a.N - n > step, other);
-        Turn<HALVES> turn;
-        if (rotary) turn = load_turn<HALVES>(pr, token_of(a, n));
+    for (; n < end; n += step, turn_buf ^= 1) {
+        uint4 v_raw[VPT];  // dV goes straight through, its loads under the others' arithmetic
+        if (a.in[2] != nullptr) {
+            const uint32_t temporal_row = token_of(a, n).temporal_row;
+            int64_t at = grad0;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j, at += head_step)
+                if (j < me.count)
+                    v_raw[j] = ld_row(reinterpret_cast<const char*>(a.in[2]) + at +
+                                      static_cast<int64_t>(me.temporal >> j & 1u ? temporal_row : n) * row_bytes);
+        }
+        fetch(n + step, end - n > step, other);
         cp_async_wait_group<1>();
+        Turn<HALVES> turn;
+        if (rotary) turn = read_turn<HALVES>(now + turn_at);
         float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // x^2 and g w x of Q, then of K
         if (kToken) {
 #pragma unroll
@@ -472,50 +542,52 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
                     V8 v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
                     if (rotary) rotate8<HALVES, true>(v, turn, pr);
                     if (j >= me.count) continue;
-                    const V8 x = unpack_bf16<!HALVES>(lds128(now + ((3 + i) * VPT + j) * 512));
+                    const V8 x = unpack_bf16<!HALVES>(lds128(now + ((2 + i) * VPT + j) * 512));
                     sums[2 * i] += dot(x, x);
-                    sums[2 * i + 1] += dot(mul(v, planes_load(weights + i * 2 * all16 + j * (W * 512), all16)), x);
+                    sums[2 * i + 1] += dot(mul(v, weight(i, j)), x);
                 }
             }
             token_sum<4, W>(sums, reinterpret_cast<float*>(buf4[turn_buf] + W * group), group, warp);
         }
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             if (a.in[i] == nullptr) continue;
             char* to = dst[i];
             dst[i] += ahead[i];
-            const int k = i < 2 ? i : 0;
             float r = 0.0f, m = 0.0f;
-            if (kToken && i < 2) {
-                r = rsqrtf(sums[2 * k] * a.inv_width + a.eps);
-                m = -r * r * (sums[2 * k + 1] * a.inv_width);
+            if (kToken) {
+                r = rsqrtf(sums[2 * i] * a.inv_width + a.eps);
+                m = -r * r * (sums[2 * i + 1] * a.inv_width);
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j, to += apart[i]) {
                 const bool live = j < me.count;
-                uint4 o = lds128(now + (i * VPT + j) * 512);
-                if (i < 2) {
-                    V8 v = unpack_bf16<!HALVES>(o);
-                    if (rotary) rotate8<HALVES, true>(v, turn, pr);
-                    if (NORM != BSS_HEAD_NORM_NONE) {
-                        const V8 x = unpack_bf16<!HALVES>(lds128(now + ((3 + k) * VPT + j) * 512));
-                        V8 gw = v;
-                        if (kToken) {
-                            if (live) gw = mul(v, planes_load(weights + k * 2 * all16 + j * (W * 512), all16));
-                        } else {
-                            gw = mul(v, w[k]);
-                            r = rsqrtf(head_sum(dot(x, x), a.pieces) * a.inv_width + a.eps);
-                            m = -r * r * (head_sum(dot(gw, x), a.pieces) * a.inv_width);
-                        }
-                        const V8 xr = mul(x, r);
-                        V8& d = dw[k][kToken ? j : 0];
-                        d = fma8(v, xr, d);  // zeros where there is no piece
-                        v = fma8(xr, m, mul(gw, r));
+                V8 v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
+                if (rotary) rotate8<HALVES, true>(v, turn, pr);
+                if (NORM != BSS_HEAD_NORM_NONE) {
+                    const V8 x = unpack_bf16<!HALVES>(lds128(now + ((2 + i) * VPT + j) * 512));
+                    V8 gw = v;
+                    if (kToken) {
+                        if (live) gw = mul(v, weight(i, j));
+                    } else {
+                        gw = mul(v, w[i]);
+                        r = rsqrtf(head_sum(dot(x, x), a.pieces) * a.inv_width + a.eps);
+                        m = -r * r * (head_sum(dot(gw, x), a.pieces) * a.inv_width);
                     }
-                    o = pack_bf16<!HALVES>(v);
+                    const V8 xr = mul(x, r);
+                    V8& d = dw[i][kToken ? j : 0];
+                    d = fma8(v, xr, d);  // zeros where there is no piece
+                    v = fma8(xr, m, mul(gw, r));
                 }
-                if (live) st_row(to, o);
+                if (live) st_row(to, pack_bf16<!HALVES>(v));
             }
+        }
+        if (a.in[2] != nullptr) {
+            char* to = dst[2];
+            dst[2] += ahead[2];
+#pragma unroll
+            for (int j = 0; j < VPT; ++j, to += apart[2])
+                if (j < me.count) st_row(to, v_raw[j]);
         }
         const uint32_t t = now;
         now = other, other = t;
@@ -598,6 +670,8 @@ __global__ void rotary_table_kernel(const double* positions, int32_t length, int
 // ---------------------------------------------------------------- host side
 
 // How a token's heads are dealt to warps and grid columns.
+constexpr int kWaves = 4;  // of the forward pass's blocks
+
 struct Shape {
     int warps, vpt, heads_per_block, threads, smem;
     uint32_t grid_x, grid_y;
@@ -610,7 +684,7 @@ int warps_of(bool backward, int chunks) {
     return chunks <= 3 ? 1 : chunks <= 6 ? 2 : chunks <= 12 ? 4 : 8;
 }
 
-Shape shape_of(int32_t H, int pieces, int32_t norm, uint32_t N, bool backward) {
+Shape shape_of(int32_t H, int pieces, int32_t norm, bool halves, uint32_t N, bool backward) {
     Shape s;
     const int per = 32 / pieces, total = (H + per - 1) / per;  // warp-wide rows of pieces
     const bool token = norm == BSS_HEAD_NORM_TOKEN;
@@ -624,11 +698,11 @@ Shape shape_of(int32_t H, int pieces, int32_t norm, uint32_t N, bool backward) {
     s.grid_y = static_cast<uint32_t>((H + s.heads_per_block - 1) / s.heads_per_block);
     const int block_warps = s.warps > 4 ? s.warps : 4, tokens = block_warps / s.warps;
     s.threads = 32 * block_warps;
-    // shared memory: two stages of every piece, the weights of the norm over a
+    // shared memory: two stages of every piece but V's, the weights of the norm over a
     // token; at the end of the backward pass the weight gradients
     const int all = H * pieces * 64;
-    const int tensors = backward && norm != BSS_HEAD_NORM_NONE ? 5 : 3;
-    s.smem = (token ? all : 0) + block_warps * 2 * tensors * s.vpt * 512;
+    const int tensors = backward && norm != BSS_HEAD_NORM_NONE ? 4 : 2;
+    s.smem = (token && s.warps < 8 ? all : 0) + block_warps * 2 * static_cast<int>(stage_bytes(tensors, s.vpt, halves));
     const int grads = token ? all * tokens : s.threads * 64;
     if (backward && norm != BSS_HEAD_NORM_NONE && s.smem < grads) s.smem = grads;
     // as many blocks as an SM holds, each walking over tokens
@@ -766,16 +840,25 @@ Kernel pick(bool backward, int32_t norm, const Shape& s) {
     return backward ? pick_backward<HALVES, BSS_HEAD_NORM_NONE>(s) : pick_forward<HALVES, BSS_HEAD_NORM_NONE>(s);
 }
 
-// Launches at most the blocks of the shape, and no more than the GPU holds at
-// once; *blocks: how many.
-bss_status launch(bool backward, int pairing, int32_t norm, const HeadsArgs& a, const Shape& s, cudaStream_t stream,
+// Launches as many blocks as the GPU holds at once (never more than the shape's
+// in the backward pass), times the waves; *blocks: how many.
+bss_status launch(bool backward, int pairing, int32_t norm, const HeadsArgs& args, const Shape& s, cudaStream_t stream,
                   const char* what, int* blocks) {
     const Kernel k = pairing == BSS_PAIR_HALVES ? pick<true>(backward, norm, s) : pick<false>(backward, norm, s);
     int resident = 1;
     const bss_status st = resident_blocks(reinterpret_cast<const void*>(k), s.threads, s.smem, &resident);
     if (st != BSS_OK) return st;
     const uint32_t fill = static_cast<uint32_t>(resident * num_sms()) / s.grid_y;
-    const uint32_t grid_x = s.grid_x < fill ? s.grid_x : (fill < 1 ? 1 : fill);
+    uint32_t grid_x = s.grid_x < fill ? s.grid_x : (fill < 1 ? 1 : fill);
+    const uint32_t tokens = s.threads / 32 / s.warps;
+    HeadsArgs a = args;
+    // forward four waves of blocks, so that SMs that finish early take more; backward
+    // one, since every block leaves a partial sum (75,600 tokens x 10 heads: 193 us
+    // against 203 in one wave; backward 291 in one wave, 301 in two)
+    const uint32_t many = grid_x * (backward ? 1 : kWaves);
+    a.span = (a.N + many - 1) / many;
+    a.span = (a.span + tokens - 1) / tokens * tokens;
+    grid_x = (a.N + a.span - 1) / a.span;
     *blocks = static_cast<int>(grid_x * s.grid_y);
     k<<<dim3(grid_x, s.grid_y), s.threads, s.smem, stream>>>(a);
     return cuda_check(cudaGetLastError(), what);
@@ -858,7 +941,7 @@ bss_status bss_heads_from_tokens(const bss_token_tensor* q, const bss_token_tens
             if (j < i && a.out[i] != nullptr && a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
                 return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
         }
-    const Shape s = shape_of(H, d / 8, options->norm, a.N, false);
+    const Shape s = shape_of(H, d / 8, options->norm, pairing == BSS_PAIR_HALVES, a.N, false);
     set_shape(s, options->norm, d, &a);
     int blocks = 0;
     return launch(false, pairing, options->norm, a, s, stream, "heads launch", &blocks);
@@ -874,7 +957,7 @@ bss_status bss_heads_from_tokens_backward_workspace(int32_t H, const bss_mask_pa
     if (st != BSS_OK) return st;
     if ((st = check_norm(norm, H, params->head_dim)) != BSS_OK) return st;
     if (norm == BSS_HEAD_NORM_NONE) return BSS_OK;
-    const Shape s = shape_of(H, params->head_dim / 8, norm, static_cast<uint32_t>(params->F) * params->Hs * params->Ws, true);
+    const Shape s = shape_of(H, params->head_dim / 8, norm, false, static_cast<uint32_t>(params->F) * params->Hs * params->Ws, true);
     const int64_t width = norm == BSS_HEAD_NORM_TOKEN ? static_cast<int64_t>(H) * params->head_dim : params->head_dim;
     *bytes = static_cast<int64_t>(s.grid_x) * s.grid_y * 2 * width * 4;
     return BSS_OK;
@@ -942,7 +1025,7 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
             if (a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
                 return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
     }
-    const Shape s = shape_of(H, d / 8, norm, a.N, true);
+    const Shape s = shape_of(H, d / 8, norm, pairing == BSS_PAIR_HALVES, a.N, true);
     set_shape(s, norm, d, &a);
     const bool want = dq_weight != nullptr || dk_weight != nullptr;
     const int width = norm == BSS_HEAD_NORM_TOKEN ? H * d : d;
