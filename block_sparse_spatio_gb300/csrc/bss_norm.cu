@@ -16,7 +16,9 @@
 // HBM-bound: each row's tensors are read once and written once (bf16: 8 bytes a
 // channel forward, 12 backward), everything else stays on chip.  Statistics and
 // sums are 32-bit; a variance is taken about the mean, not as a difference of
-// squares.
+// squares.  Every thread copies its own vectors of the next rows into its own
+// slots of shared memory (cp.async) while it works on this one, so loads stay in
+// flight without holding registers.
 #include <cstring>
 
 #include "bss_rows.cuh"
@@ -27,157 +29,277 @@ namespace {
 constexpr int kMaxChannels = 8192;
 constexpr int kMinChunkRows = 16;  // rows a block of the backward pass reduces at least
 
-// Sum over the W warps that share a row (W = 1: the warp); every thread gets it.
-// `buf` holds W floats and is used once between two barriers.
+// ---------------------------------------------------------------- shared memory
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// A vector of 8 channels from 16-byte pieces `apart` bytes apart (one of bf16,
+// two of float).
+__device__ __forceinline__ V8 floats_of(const uint4& a, const uint4& b) {
+    V8 v;
+    v.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
+    v.p[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
+    v.p[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
+    v.p[3] = make_float2(__uint_as_float(b.z), __uint_as_float(b.w));
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ V8 lds_vector(uint32_t at, uint32_t apart) {
+    if constexpr (sizeof(T) == 2)
+        return unpack_bf16<false>(lds128(at));
+    else
+        return floats_of(lds128(at), lds128(at + apart));
+}
+
+template <typename T>
+__device__ __forceinline__ void fetch_vector(uint32_t to, uint32_t apart, const T* from) {
+    cp_async_16(to, from);
+    if (sizeof(T) == 4) cp_async_16(to + apart, from + 4);
+}
+
+__device__ __forceinline__ V8 zeros() { return floats_of(make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)); }
+
+template <typename T>
+__device__ __forceinline__ void store_vector(T* to, const V8& v) {
+    if constexpr (sizeof(T) == 2) {
+        st_row(to, pack_bf16<false>(v));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            st_row(to + 2 * i, make_uint4(__float_as_uint(v.p[i].x), __float_as_uint(v.p[i].y),
+                                          __float_as_uint(v.p[i + 1].x), __float_as_uint(v.p[i + 1].y)));
+    }
+}
+
+__device__ __forceinline__ V8 param_vector(const void* p, int64_t at, int dtype) {
+    float f[8];
+    load_param8(p, at, dtype, f);
+    return arrange<false>(f);
+}
+
+__device__ __forceinline__ V8 add8(const V8& a, const V8& b) {
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __fadd2_rn(a.p[i], b.p[i]);
+    return r;
+}
+
+__device__ __forceinline__ V8 add8(const V8& a, float b) {
+    V8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.p[i] = __fadd2_rn(a.p[i], f2(b));
+    return r;
+}
+
+__device__ __forceinline__ float sum8(const V8& a) {
+    const float2 s = __fadd2_rn(__fadd2_rn(a.p[0], a.p[1]), __fadd2_rn(a.p[2], a.p[3]));
+    return s.x + s.y;
+}
+
+// ---------------------------------------------------------------- forward
+// What multiplies and is added to the normed values of a group, folded:
+//   0  gate * y_weight      1  weight * (1 + scale)      2  bias * (1 + scale) + shift
+struct Folded {
+    bool has[3];
+};
+
+struct ForwardArgs {
+    bss_residual_norm_args a;
+    Folded folded;
+    int32_t folds;          // how many of them there are
+    int64_t groups;         // of rows that share them
+    int64_t chunks, chunk_rows;
+};
+
+__device__ __forceinline__ V8 fold(const bss_residual_norm_args& a, int which, int64_t group, int c) {
+    V8 v = zeros();
+    if (which == 0) {
+        v = a.gate != nullptr ? param_vector(a.gate, group * a.gate_stride + c, a.param_dtype) : add8(v, 1.0f);
+        if (a.y_weight != nullptr) v = mul(v, param_vector(a.y_weight, c, a.param_dtype));
+        return v;
+    }
+    V8 m = add8(v, 1.0f);
+    if (a.scale != nullptr) m = add8(param_vector(a.scale, group * a.scale_stride + c, a.param_dtype), 1.0f);
+    if (which == 1) return a.weight != nullptr ? mul(m, param_vector(a.weight, c, a.param_dtype)) : m;
+    if (a.bias != nullptr) v = mul(m, param_vector(a.bias, c, a.param_dtype));
+    return a.shift != nullptr ? add8(v, param_vector(a.shift, group * a.shift_stride + c, a.param_dtype)) : v;
+}
+
+// Sum over the W warps that share a row; every thread gets it.  Each use between
+// two barriers has W floats of its own.
 template <int W>
 __device__ __forceinline__ float row_sum(float v, float* buf) {
     v = lane_sum<32>(v);
     if (W == 1) return v;
     if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.0f;
+    v = buf[0];
 #pragma unroll
-    for (int i = 0; i < W; ++i) v += buf[i];
+    for (int i = 1; i < W; ++i) v += buf[i];
     return v;
 }
 
-// ---------------------------------------------------------------- forward
-// W warps share a row, each thread holding up to VPT vectors of it in registers.
-// With W = 1 a block of 8 warps takes 8 rows; else one.
-template <typename TS, typename TB, int W, int VPT>
-__global__ void __launch_bounds__(W == 1 ? 256 : 32 * W) norm_forward_kernel(const __grid_constant__ bss_residual_norm_args a) {
-    __shared__ float buf[4][W];
-    constexpr int kRows = W == 1 ? 8 : 1;
-    const int lane = W == 1 ? threadIdx.x & 31 : threadIdx.x;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + (W == 1 ? threadIdx.x >> 5 : 0);
-    if (row >= a.rows) return;  // whole warps (W = 1) or never
+template <typename TS, typename TB>
+__host__ __device__ constexpr uint32_t forward_stage(int vpt) {
+    return vpt * (sizeof(TS) + sizeof(TB)) * 8 * 32;
+}
+
+// W warps share a row, each thread holding up to VPT vectors of it in registers;
+// with W = 1 a block takes 4 rows side by side.  A block covers one chunk of one
+// group's rows, whose folded parameters it keeps in shared memory (STAGED); with
+// few rows a group it reads them row by row.
+template <typename TS, typename TB, int W, int VPT, bool STAGED>
+__global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(const __grid_constant__ ForwardArgs g) {
+    extern __shared__ __align__(16) float4 folded[];
+    __shared__ float buf[2][4][W];
+    const bss_residual_norm_args& a = g.a;
+    constexpr int kWarps = W > 4 ? W : 4, kRows = kWarps / W;
+    constexpr uint32_t kStage = forward_stage<TS, TB>(VPT), kY = VPT * sizeof(TS) * 256;
+    const int lane = (threadIdx.x & 31) + 32 * (W == 1 ? 0 : threadIdx.x >> 5);
     const int vecs = a.channels / 8;
     const float inv = 1.0f / a.channels;
-    const int64_t group = row / a.rows_per_group;
-    float r[VPT][8];
-    {
-        Raw8<TS> xr[VPT];
-        Raw8<TB> yr[VPT];
-        const TS* x = static_cast<const TS*>(a.x) + row * a.x_stride;
-        const TB* y = static_cast<const TB*>(a.y) + row * a.y_stride;
+    const int64_t first_group = blockIdx.x / g.chunks, chunk = blockIdx.x - first_group * g.chunks;
+    const int64_t group_rows = STAGED ? a.rows_per_group : a.rows;
+    int64_t row = first_group * group_rows + chunk * g.chunk_rows;
+    int64_t last = row + g.chunk_rows;
+    if (last > (first_group + 1) * group_rows) last = (first_group + 1) * group_rows;
+    if (last > a.rows) last = a.rows;
+    row += threadIdx.x / 32 / W;
+
+    const uint32_t base = smem_u32(folded);
+    const uint32_t slots = base + (STAGED ? g.folds * a.channels * 4 : 0) + (threadIdx.x >> 5) * 2 * kStage +
+                           (threadIdx.x & 31) * 16;
+    const TS* x = static_cast<const TS*>(a.x) + row * a.x_stride + lane * 8;
+    const TB* y = static_cast<const TB*>(a.y) + row * a.y_stride + lane * 8;
+    auto fetch = [&](bool exists, uint32_t to) {
+        if (exists) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = lane + i * 32 * W;
-            xr[i] = zero_raw<TS>();
-            yr[i] = zero_raw<TB>();
-            if (v < vecs) xr[i] = load_raw(x + v * 8);
-            if (v < vecs && a.y != nullptr) yr[i] = load_raw(y + v * 8);
+            for (int i = 0; i < VPT; ++i) {
+                if (lane + i * 32 * W >= vecs) continue;
+                fetch_vector(to + i * sizeof(TS) * 256, 512, x + i * 256 * W);
+                if (a.y != nullptr) fetch_vector(to + kY + i * sizeof(TB) * 256, 512, y + i * 256 * W);
+            }
+            x += kRows * a.x_stride;
+            y += kRows * a.y_stride;
         }
+        cp_async_commit();
+    };
+    fetch(row < last, slots);
+    if (STAGED && g.folds > 0) {
+        int k = 0;
+#pragma unroll
+        for (int which = 0; which < 3; ++which) {
+            if (!g.folded.has[which]) continue;
+#pragma unroll 2
+            for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
+                const V8 f = fold(a, which, first_group, v * 8);
+                const uint32_t at = base + k * a.channels * 4 + v * 16;
+                sts128(at, make_uint4(__float_as_uint(f.p[0].x), __float_as_uint(f.p[0].y), __float_as_uint(f.p[1].x),
+                                      __float_as_uint(f.p[1].y)));
+                sts128(at + vecs * 16, make_uint4(__float_as_uint(f.p[2].x), __float_as_uint(f.p[2].y),
+                                                  __float_as_uint(f.p[3].x), __float_as_uint(f.p[3].y)));
+            }
+            ++k;
+        }
+        __syncthreads();
+    }
+    const uint32_t fold1 = base + (g.folded.has[0] ? a.channels * 4 : 0);
+    const uint32_t fold2 = fold1 + (g.folded.has[1] ? a.channels * 4 : 0);
+    const uint32_t plane = vecs * 16;
+    auto folded_at = [&](int which, int64_t group, int v) {
+        if (!STAGED) return fold(a, which, group, v * 8);
+        const uint32_t at = (which == 0 ? base : which == 1 ? fold1 : fold2) + v * 16;
+        return floats_of(lds128(at), lds128(at + plane));
+    };
+    uint32_t now = slots, other = slots + kStage;
+    int parity = 0;
+    for (; row < last; row += kRows, parity ^= 1) {
+        fetch(row + kRows < last, other);
+        cp_async_wait_group<1>();
+        const int64_t group = STAGED ? first_group : row / a.rows_per_group;
+        V8 r[VPT];
         float ym = 0.0f, yrstd = 1.0f;
         if (a.y != nullptr && a.y_norm != BSS_NORM_NONE) {
             float s = 0.0f;
             if (a.y_norm == BSS_NORM_LAYER) {
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) {
-                    float v[8];
-                    unpack(yr[i], v);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) s += v[j];
-                }
-                ym = row_sum<W>(s, buf[0]) * inv;
+                for (int i = 0; i < VPT; ++i)
+                    if (lane + i * 32 * W < vecs) s += sum8(lds_vector<TB>(now + kY + i * sizeof(TB) * 256, 512));
+                ym = row_sum<W>(s, buf[parity][0]) * inv;
             }
             s = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 if (lane + i * 32 * W >= vecs) continue;
-                float v[8];
-                unpack(yr[i], v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s = fmaf(v[j] - ym, v[j] - ym, s);
+                const V8 v = add8(lds_vector<TB>(now + kY + i * sizeof(TB) * 256, 512), -ym);
+                s += dot(v, v);
             }
-            yrstd = rsqrtf(row_sum<W>(s, buf[1]) * inv + a.eps);
+            yrstd = rsqrtf(row_sum<W>(s, buf[parity][1]) * inv + a.eps);
             if (a.y_stats != nullptr && lane == 0)
                 *reinterpret_cast<float2*>(a.y_stats + 2 * row) = make_float2(ym, yrstd);
+        }
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = lane + i * 32 * W;
+            r[i] = zeros();
+            if (v >= vecs) continue;
+            r[i] = lds_vector<TS>(now + i * sizeof(TS) * 256, 512);
+            if (a.y != nullptr) {
+                V8 t = lds_vector<TB>(now + kY + i * sizeof(TB) * 256, 512);
+                if (a.y_norm != BSS_NORM_NONE) t = mul(add8(t, -ym), yrstd);
+                if (g.folded.has[0]) t = mul(t, folded_at(0, group, v));
+                r[i] = fma8(r[i], a.residual_scale, t);
+                if (a.r != nullptr) store_vector(static_cast<TS*>(a.r) + row * a.r_stride + v * 8, r[i]);
+            }
+            s += sum8(r[i]);
+        }
+        const uint32_t t = now;
+        now = other, other = t;
+        if (a.h == nullptr) continue;
+        float mean = 0.0f, rstd = 1.0f;
+        if (a.norm != BSS_NORM_NONE) {
+            if (a.norm == BSS_NORM_LAYER) mean = row_sum<W>(s, buf[parity][2]) * inv;
+            s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                if (lane + i * 32 * W >= vecs) continue;
+                r[i] = add8(r[i], -mean);
+                s += dot(r[i], r[i]);
+            }
+            rstd = rsqrtf(row_sum<W>(s, buf[parity][3]) * inv + a.eps);
+            if (a.stats != nullptr && lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = lane + i * 32 * W;
-            unpack(xr[i], r[i]);
-            if (v >= vecs || a.y == nullptr) continue;
-            float yv[8], p[8];
-            unpack(yr[i], yv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) yv[j] = (yv[j] - ym) * yrstd;
-            if (a.y_weight != nullptr) {
-                load_param8(a.y_weight, v * 8, a.param_dtype, p);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) yv[j] *= p[j];
-            }
-            if (a.gate != nullptr) {
-                load_param8(a.gate, group * a.gate_stride + v * 8, a.param_dtype, p);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) yv[j] *= p[j];
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[i][j] = fmaf(a.residual_scale, r[i][j], yv[j]);
-            if (a.r != nullptr) store8(static_cast<TS*>(a.r) + row * a.r_stride + v * 8, r[i]);
+            if (v >= vecs) continue;
+            V8 n = mul(r[i], rstd);
+            if (g.folded.has[1]) n = mul(n, folded_at(1, group, v));
+            if (g.folded.has[2]) n = add8(n, folded_at(2, group, v));
+            store_vector(static_cast<TB*>(a.h) + row * a.h_stride + v * 8, n);
         }
     }
-    if (a.h == nullptr) return;
-    float mean = 0.0f, rstd = 1.0f;
-    if (a.norm != BSS_NORM_NONE) {
-        float s = 0.0f;
-        if (a.norm == BSS_NORM_LAYER) {
-#pragma unroll
-            for (int i = 0; i < VPT; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s += r[i][j];  // vectors past the row hold zeros
-            mean = row_sum<W>(s, buf[2]) * inv;
-        }
-        s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if (lane + i * 32 * W >= vecs) continue;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s = fmaf(r[i][j] - mean, r[i][j] - mean, s);
-        }
-        rstd = rsqrtf(row_sum<W>(s, buf[3]) * inv + a.eps);
-        if (a.stats != nullptr && lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
-    }
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int v = lane + i * 32 * W;
-        if (v >= vecs) continue;
-        float p[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = (r[i][j] - mean) * rstd;
-        if (a.weight != nullptr) {
-            load_param8(a.weight, v * 8, a.param_dtype, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[i][j] *= p[j];
-        }
-        if (a.bias != nullptr) {
-            load_param8(a.bias, v * 8, a.param_dtype, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[i][j] += p[j];
-        }
-        if (a.scale != nullptr) {
-            load_param8(a.scale, group * a.scale_stride + v * 8, a.param_dtype, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[i][j] = fmaf(r[i][j], p[j], r[i][j]);
-        }
-        if (a.shift != nullptr) {
-            load_param8(a.shift, group * a.shift_stride + v * 8, a.param_dtype, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) r[i][j] += p[j];
-        }
-        store8(static_cast<TB*>(a.h) + row * a.h_stride + v * 8, r[i]);
-    }
+    cp_async_wait_group<0>();
 }
 
 // ---------------------------------------------------------------- backward
-// A thread owns 8 channels and walks over rows, so the three column sums stay in
-// its registers; `lanes` warps share a row, several rows go side by side in a
-// block when a row is short.  A block covers one chunk of one group's rows.
+// A thread owns 8 channels and walks over rows, T at a time, so the three column
+// sums stay in its registers; `warps` warps share a row, several rows go side by
+// side in a block when a row is short.  A block covers one chunk of one group's
+// rows.
 struct GradShape {
     int warps;        // per row
     int side;         // rows side by side
-    int threads;
+    int threads, T, stages, smem;
     int64_t groups, chunks, chunk_rows;  // chunks per group
 };
 
@@ -188,190 +310,187 @@ struct GradArgs {
     int want_sums;
 };
 
-// Sums of N values over the row's warps.
-template <int N>
-__device__ __forceinline__ void shared_sums(float (&v)[N], int warps, int warp0, float* buf) {
+// A thread's slots of one stage: T rows of r, dh, dr, y and the statistics.
+template <typename TS, typename TB>
+__host__ __device__ constexpr int grad_pieces(int T) {
+    return T * static_cast<int>(sizeof(TS) + sizeof(TB) + 1);
+}
+
+// Sums of NV values over the row's warps; `buf` holds NV floats a warp of the block.
+template <int NV>
+__device__ __forceinline__ void shared_sums(float (&v)[NV], int warps, int warp0, float* buf) {
+    const float s = scatter_sum<NV, 32>(v);
+    if (scattered_writer<NV, 32>()) buf[(threadIdx.x >> 5) * NV + scattered_index<NV, 32>()] = s;
+    if (warps == 1)
+        __syncwarp();
+    else
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = lane_sum<32>(v[i]);
-    if (warps == 1) return;
-    if ((threadIdx.x & 31) == 0) {
+    for (int i = 0; i < NV; ++i) v[i] = buf[warp0 * NV + i];
+    for (int w = warp0 + 1; w < warp0 + warps; ++w) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) buf[(threadIdx.x >> 5) * N + i] = v[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.0f;
-    for (int w = warp0; w < warp0 + warps; ++w) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += buf[w * N + i];
+        for (int i = 0; i < NV; ++i) v[i] += buf[w * NV + i];
     }
 }
 
-template <typename TS, typename TB, int T>
-__global__ void __launch_bounds__(T == 1 ? 1024 : 512) norm_backward_kernel(const __grid_constant__ GradArgs g) {
-    extern __shared__ __align__(16) float shared[];  // sums of the row's warps; column sums of the rows side by side
-    __shared__ float buf[4][32 * 2 * T];
+template <typename TS, typename TB, int T, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_constant__ GradArgs g) {
+    extern __shared__ __align__(16) float shared[];  // slots; at the end the column sums of the rows side by side
+    __shared__ __align__(16) float buf[4][32 * 2 * T];
     const bss_residual_norm_grads& a = g.a;
+    constexpr int kPieces = grad_pieces<TS, TB>(T), kS = sizeof(TS) / 2, kB = sizeof(TB) / 2;
     const int per = g.s.warps * 32;
     const int side = threadIdx.x / per;
-    const int v = threadIdx.x - side * per;
+    const int vec = threadIdx.x - side * per;
     const int warp0 = side * g.s.warps;
-    const bool active = v * 8 < a.channels;
-    const int c = active ? v * 8 : 0;
+    const bool active = vec * 8 < a.channels;
+    const int c = active ? vec * 8 : 0;
     const float inv = 1.0f / a.channels;
     const int64_t group = blockIdx.x / g.s.chunks, chunk = blockIdx.x - group * g.s.chunks;
     const int64_t first = group * a.rows_per_group + chunk * g.s.chunk_rows;
     int64_t last = first + g.s.chunk_rows;
     if (last > (group + 1) * a.rows_per_group) last = (group + 1) * a.rows_per_group;
     if (last > a.rows) last = a.rows;
-
-    float m1[8], m2[8];  // (1 + scale) weight, gate y_weight
-    {
-        float p[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m1[j] = m2[j] = 1.0f;
-        if (a.scale != nullptr) {
-            load_param8(a.scale, group * a.scale_stride + c, a.param_dtype, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m1[j] += p[j];
-        }
-        if (a.weight != nullptr) {
-            load_param8(a.weight, c, a.param_dtype, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m1[j] *= p[j];
-        }
-        if (a.gate != nullptr) load_param8(a.gate, group * a.gate_stride + c, a.param_dtype, m2);
-        if (a.y_weight != nullptr) {
-            load_param8(a.y_weight, c, a.param_dtype, p);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m2[j] *= p[j];
-        }
-        if (!active) {  // lanes past the row: u there is -mean(t), keep it out of the sums over z
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m2[j] = 0.0f;
-        }
-    }
-    float sa[8], sb[8], sc[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sa[j] = sb[j] = sc[j] = 0.0f;
     const bool stats = a.dh != nullptr && a.norm != BSS_NORM_NONE;
     const bool ystats = a.y != nullptr && a.y_norm != BSS_NORM_NONE;
-    int turn = 0;
-    for (int64_t row0 = first; row0 < last; row0 += g.s.side * T, turn ^= 2) {
-        const int64_t mine = row0 + side * T;
-        Raw8<TS> rr[T], drr[T];
-        Raw8<TB> yr[T], dhr[T];
-        float2 st[T], yst[T];
+
+    // slot of piece k: a column of `threads` 16-byte pieces
+    const uint32_t apart = blockDim.x * 16;
+    const uint32_t slots = smem_u32(shared) + threadIdx.x * 16;
+    const TS* r_in = static_cast<const TS*>(a.r) + c;
+    const TS* dr_in = static_cast<const TS*>(a.dr) + c;
+    const TB* dh_in = static_cast<const TB*>(a.dh) + c;
+    const TB* y_in = static_cast<const TB*>(a.y) + c;
+    auto fetch = [&](int64_t row0, uint32_t to) {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const int64_t row = mine + t;
-            const bool live = active && row < last;
-            rr[t] = zero_raw<TS>();
-            drr[t] = zero_raw<TS>();
-            yr[t] = zero_raw<TB>();
-            dhr[t] = zero_raw<TB>();
-            st[t] = yst[t] = make_float2(0.0f, 1.0f);
-            if (!live) continue;
+            const int64_t row = row0 + t;
+            if (!active || row >= last) continue;
+            const uint32_t at = to + t * (kPieces / T) * apart;
             if (a.dh != nullptr) {
-                rr[t] = load_raw(static_cast<const TS*>(a.r) + row * a.r_stride + c);
-                dhr[t] = load_raw(static_cast<const TB*>(a.dh) + row * a.dh_stride + c);
+                fetch_vector(at, apart, r_in + row * a.r_stride);
+                fetch_vector(at + (2 * kS) * apart, apart, dh_in + row * a.dh_stride);
             }
-            if (a.dr != nullptr) drr[t] = load_raw(static_cast<const TS*>(a.dr) + row * a.dr_stride + c);
-            if (a.y != nullptr) yr[t] = load_raw(static_cast<const TB*>(a.y) + row * a.y_stride + c);
-            if (stats) st[t] = __ldg(reinterpret_cast<const float2*>(a.stats) + row);
-            if (ystats) yst[t] = __ldg(reinterpret_cast<const float2*>(a.y_stats) + row);
+            if (a.dr != nullptr) fetch_vector(at + kS * apart, apart, dr_in + row * a.dr_stride);
+            if (a.y != nullptr) fetch_vector(at + (2 * kS + kB) * apart, apart, y_in + row * a.y_stride);
+            const uint32_t st = at + (2 * kS + 2 * kB) * apart;
+            if (stats)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st), "l"(a.stats + 2 * row) : "memory");
+            if (ystats)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + 8), "l"(a.y_stats + 2 * row)
+                             : "memory");
         }
+        cp_async_commit();
+    };
+    const int64_t step = g.s.side * T;
+    int64_t mine = first + side * T;
+    const bool ahead = g.s.stages > 1;  // the widest float rows have room for one stage only
+    if (ahead) fetch(mine, slots);
+
+    // (1 + scale) weight, gate y_weight; zeros past the row keep its lanes out of
+    // the sums
+    V8 m1 = zeros(), m2 = zeros();
+    if (active) {
+        m1 = add8(m1, 1.0f), m2 = add8(m2, 1.0f);
+        if (a.scale != nullptr) m1 = add8(m1, param_vector(a.scale, group * a.scale_stride + c, a.param_dtype));
+        if (a.weight != nullptr) m1 = mul(m1, param_vector(a.weight, c, a.param_dtype));
+        if (a.gate != nullptr) m2 = param_vector(a.gate, group * a.gate_stride + c, a.param_dtype);
+        if (a.y_weight != nullptr) m2 = mul(m2, param_vector(a.y_weight, c, a.param_dtype));
+    }
+    V8 sa = zeros(), sb = zeros(), sc = zeros();
+    int stage = 0, turn = 0;
+    for (int64_t row0 = first; row0 < last; row0 += step, mine += step, turn ^= 2) {
+        if (ahead) {
+            fetch(mine + step, slots + (stage ^ 1) * kPieces * apart);
+            cp_async_wait_group<1>();
+        } else {
+            fetch(mine, slots);
+            cp_async_wait_group<0>();
+        }
+        const uint32_t now = slots + stage * kPieces * apart;
+        stage ^= ahead ? 1 : 0;
+        V8 xh[T], tt[T];
+        float2 st[T], yst[T];
         float sums[2 * T];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            float rv[8], dhv[8], s1 = 0.0f, s2 = 0.0f;
-            unpack(rr[t], rv);
-            unpack(dhr[t], dhv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xh = (rv[j] - st[t].x) * st[t].y;
-                const float tt = dhv[j] * m1[j];
-                s1 += tt;
-                s2 = fmaf(tt, xh, s2);
-                sa[j] = fmaf(dhv[j], xh, sa[j]);
-                sb[j] += dhv[j];
+            const uint32_t at = now + t * (kPieces / T) * apart;
+            const bool live = active && mine + t < last;
+            xh[t] = tt[t] = zeros();
+            st[t] = yst[t] = make_float2(0.0f, 1.0f);
+            if (live) {
+                const uint4 q = lds128(at + (2 * kS + 2 * kB) * apart);
+                if (stats) st[t] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+                if (ystats) yst[t] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
             }
-            sums[2 * t] = s1;
-            sums[2 * t + 1] = s2;
+            if (live && a.dh != nullptr) {
+                xh[t] = mul(add8(lds_vector<TS>(at, apart), -st[t].x), st[t].y);
+                const V8 dh = lds_vector<TB>(at + (2 * kS) * apart, apart);
+                tt[t] = mul(dh, m1);
+                sa = fma8(dh, xh[t], sa);
+                sb = add8(sb, dh);
+            }
+            sums[2 * t] = sum8(tt[t]);
+            sums[2 * t + 1] = dot(tt[t], xh[t]);
         }
         if (stats) shared_sums<2 * T>(sums, g.s.warps, warp0, buf[turn]);
-        float u[T][8], zs[2 * T];
+        float zs[2 * T];
+        V8 z[T];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            float rv[8], dhv[8], yv[8], out[8];
-            unpack(rr[t], rv);
-            unpack(dhr[t], dhv);
-            unpack(drr[t], u[t]);
-            unpack(yr[t], yv);
+            const uint32_t at = now + t * (kPieces / T) * apart;
+            const bool live = active && mine + t < last;
             const float mean1 = a.norm == BSS_NORM_LAYER ? sums[2 * t] * inv : 0.0f;
             const float mean2 = a.norm != BSS_NORM_NONE ? sums[2 * t + 1] * inv : 0.0f;
-            float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float xh = (rv[j] - st[t].x) * st[t].y;
-                const float tt = dhv[j] * m1[j];
-                u[t][j] += st[t].y * (tt - mean1 - xh * mean2);
-                out[j] = u[t][j] * a.residual_scale;
-                const float yh = (yv[j] - yst[t].x) * yst[t].y;
-                sc[j] = fmaf(u[t][j], yh, sc[j]);
-                const float z = u[t][j] * m2[j];
-                s1 += z;
-                s2 = fmaf(z, yh, s2);
-                u[t][j] = z;
-            }
-            zs[2 * t] = s1;
-            zs[2 * t + 1] = s2;
-            if (active && mine + t < last) store8(static_cast<TS*>(a.dx) + (mine + t) * a.dx_stride + c, out);
+            V8 u = zeros();
+            if (live && a.dr != nullptr) u = lds_vector<TS>(at + kS * apart, apart);
+            u = fma8(fma8(xh[t], -mean2, add8(tt[t], -mean1)), st[t].y, u);
+            if (live) store_vector(static_cast<TS*>(a.dx) + (mine + t) * a.dx_stride + c, mul(u, a.residual_scale));
+            z[t] = zeros();
+            zs[2 * t] = zs[2 * t + 1] = 0.0f;
+            if (a.dy == nullptr || !live) continue;
+            const V8 yh = mul(add8(lds_vector<TB>(at + (2 * kS + kB) * apart, apart), -yst[t].x), yst[t].y);
+            sc = fma8(u, yh, sc);
+            z[t] = mul(u, m2);
+            zs[2 * t] = sum8(z[t]);
+            zs[2 * t + 1] = dot(z[t], yh);
         }
         if (a.dy == nullptr) continue;
         if (ystats) shared_sums<2 * T>(zs, g.s.warps, warp0, buf[turn + 1]);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
+            if (!active || mine + t >= last) continue;
             if (ystats) {
-                float yv[8];
-                unpack(yr[t], yv);
+                const uint32_t at = now + t * (kPieces / T) * apart;
                 const float mean1 = a.y_norm == BSS_NORM_LAYER ? zs[2 * t] * inv : 0.0f;
-                const float mean2 = zs[2 * t + 1] * inv;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float yh = (yv[j] - yst[t].x) * yst[t].y;
-                    u[t][j] = yst[t].y * (u[t][j] - mean1 - yh * mean2);
-                }
+                const V8 yh = mul(add8(lds_vector<TB>(at + (2 * kS + kB) * apart, apart), -yst[t].x), yst[t].y);
+                z[t] = mul(fma8(yh, -zs[2 * t + 1] * inv, add8(z[t], -mean1)), yst[t].y);
             }
-            if (active && mine + t < last) store8(static_cast<TB*>(a.dy) + (mine + t) * a.dy_stride + c, u[t]);
+            store_vector(static_cast<TB*>(a.dy) + (mine + t) * a.dy_stride + c, z[t]);
         }
     }
+    cp_async_wait_group<0>();
     if (!g.want_sums) return;
     // the rows side by side, in order
     const int C = a.channels;
     float* dst = g.partial + static_cast<int64_t>(blockIdx.x) * 3 * C;
-    if (g.s.side > 1) {
-        if (active) {
+    const V8* sums3[3] = {&sa, &sb, &sc};
+    if (g.s.side > 1) __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                shared[(side * 3 + 0) * C + c + j] = sa[j];
-                shared[(side * 3 + 1) * C + c + j] = sb[j];
-                shared[(side * 3 + 2) * C + c + j] = sc[j];
-            }
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < 3 * C; e += blockDim.x) {
-            float s = 0.0f;
-            for (int k = 0; k < g.s.side; ++k) s += shared[k * 3 * C + e];
-            dst[e] = s;
-        }
-    } else if (active) {
+    for (int q = 0; q < 3; ++q) {
+        if (!active) continue;
+        float* at = g.s.side > 1 ? shared + (side * 3 + q) * C + c : dst + q * C + c;
 #pragma unroll
-        for (int j = 0; j < 8; j += 4) {
-            *reinterpret_cast<float4*>(dst + c + j) = make_float4(sa[j], sa[j + 1], sa[j + 2], sa[j + 3]);
-            *reinterpret_cast<float4*>(dst + C + c + j) = make_float4(sb[j], sb[j + 1], sb[j + 2], sb[j + 3]);
-            *reinterpret_cast<float4*>(dst + 2 * C + c + j) = make_float4(sc[j], sc[j + 1], sc[j + 2], sc[j + 3]);
-        }
+        for (int j = 0; j < 4; j += 2)
+            *reinterpret_cast<float4*>(at + 2 * j) =
+                make_float4(sums3[q]->p[j].x, sums3[q]->p[j].y, sums3[q]->p[j + 1].x, sums3[q]->p[j + 1].y);
+    }
+    if (g.s.side == 1) return;
+    __syncthreads();
+    for (int e = threadIdx.x; e < 3 * C; e += blockDim.x) {
+        float s = 0.0f;
+        for (int k = 0; k < g.s.side; ++k) s += shared[k * 3 * C + e];
+        dst[e] = s;
     }
 }
 
@@ -386,10 +505,12 @@ __global__ void __launch_bounds__(256) norm_groups_kernel(const __grid_constant_
     for (int64_t group = blockIdx.y; group < g.s.groups; group += gridDim.y) {
         float* base = g.partial + group * g.s.chunks * 3 * C;
         float s[3] = {0.0f, 0.0f, 0.0f};
-        if (c < C)
+        if (c < C) {
+#pragma unroll 4
             for (int64_t k = lane; k < g.s.chunks; k += 8)
 #pragma unroll
                 for (int q = 0; q < 3; ++q) s[q] += base[(k * 3 + q) * C + c];
+        }
 #pragma unroll
         for (int q = 0; q < 3; ++q) part[q][lane][col] = s[q];
         __syncthreads();
@@ -505,23 +626,60 @@ bss_status check_overlaps(const Named* t, int n) {
     return BSS_OK;
 }
 
-template <typename TS, typename TB, int W, int VPT>
-bss_status launch_forward(const bss_residual_norm_args& a, cudaStream_t stream) {
-    const int64_t blocks = W == 1 ? (a.rows + 7) / 8 : a.rows;
-    norm_forward_kernel<TS, TB, W, VPT><<<static_cast<unsigned>(blocks), W == 1 ? 256 : 32 * W, 0, stream>>>(a);
+// Rows a group must have for its folded parameters to be staged.
+constexpr int64_t kStagedRows = 64;
+constexpr int kForwardWaves = 4;
+
+template <typename TS, typename TB, int W, int VPT, bool STAGED>
+bss_status launch_forward(ForwardArgs g, cudaStream_t stream) {
+    constexpr int kWarps = W > 4 ? W : 4, kRows = kWarps / W;
+    const void* kernel = reinterpret_cast<const void*>(norm_forward_kernel<TS, TB, W, VPT, STAGED>);
+    const int smem = (STAGED ? g.folds * g.a.channels * 4 : 0) +
+                     kWarps * 2 * static_cast<int>(forward_stage<TS, TB>(VPT));
+    int resident = 1;
+    const bss_status st = resident_blocks(kernel, 32 * kWarps, smem, &resident);
+    if (st != BSS_OK) return st;
+    // a few waves of blocks, so that SMs that finish early take more; a block keeps
+    // to one group
+    const int64_t group_rows = STAGED ? g.a.rows_per_group : g.a.rows;
+    g.groups = (g.a.rows + group_rows - 1) / group_rows;
+    int64_t blocks = static_cast<int64_t>(kForwardWaves) * resident * num_sms() / g.groups;
+    if (blocks < 1) blocks = 1;
+    g.chunk_rows = (group_rows + blocks - 1) / blocks;
+    g.chunk_rows = (g.chunk_rows + kRows - 1) / kRows * kRows;
+    g.chunks = (group_rows + g.chunk_rows - 1) / g.chunk_rows;
+    norm_forward_kernel<TS, TB, W, VPT, STAGED>
+        <<<static_cast<unsigned>(g.groups * g.chunks), 32 * kWarps, smem, stream>>>(g);
     return cuda_check(cudaGetLastError(), "residual norm launch");
 }
 
-// Warps per row by the row's vectors: a warp alone needs no barrier and holds up
-// to 5 vectors a lane (1280 channels); longer rows take 8 warps.
+template <typename TS, typename TB, bool STAGED>
+bss_status forward_width(const ForwardArgs& g, cudaStream_t stream) {
+    // a warp alone needs no barrier and holds up to 5 vectors a lane (1280
+    // channels); longer rows take 4 or 8 warps
+    const int vecs = g.a.channels / 8;
+    if (vecs <= 32) return launch_forward<TS, TB, 1, 1, STAGED>(g, stream);
+    if (vecs <= 64) return launch_forward<TS, TB, 1, 2, STAGED>(g, stream);
+    if (vecs <= 96) return launch_forward<TS, TB, 1, 3, STAGED>(g, stream);
+    if (vecs <= 160) return launch_forward<TS, TB, 1, 5, STAGED>(g, stream);
+    if (vecs <= 384) return launch_forward<TS, TB, 4, 3, STAGED>(g, stream);
+    return launch_forward<TS, TB, 8, 4, STAGED>(g, stream);
+}
+
 template <typename TS, typename TB>
 bss_status forward_of(const bss_residual_norm_args& a, cudaStream_t stream) {
-    const int vecs = a.channels / 8;
-    if (vecs <= 32) return launch_forward<TS, TB, 1, 1>(a, stream);
-    if (vecs <= 64) return launch_forward<TS, TB, 1, 2>(a, stream);
-    if (vecs <= 160) return launch_forward<TS, TB, 1, 5>(a, stream);
-    if (vecs <= 512) return launch_forward<TS, TB, 8, 2>(a, stream);
-    return launch_forward<TS, TB, 8, 4>(a, stream);
+    ForwardArgs g;
+    memset(&g, 0, sizeof(g));
+    g.a = a;
+    if (g.a.rows_per_group > a.rows) g.a.rows_per_group = a.rows;
+    // nothing that differs between groups: one group holds the rows
+    if (a.gate == nullptr && a.scale == nullptr && a.shift == nullptr) g.a.rows_per_group = a.rows;
+    g.folded.has[0] = a.gate != nullptr || a.y_weight != nullptr;
+    g.folded.has[1] = a.scale != nullptr || a.weight != nullptr;
+    g.folded.has[2] = a.shift != nullptr || a.bias != nullptr;
+    for (bool has : g.folded.has) g.folds += has;
+    return g.a.rows_per_group >= kStagedRows || g.a.rows_per_group == a.rows ? forward_width<TS, TB, true>(g, stream)
+                                                                             : forward_width<TS, TB, false>(g, stream);
 }
 
 bool wants_sums(const bss_residual_norm_grads& a) {
@@ -538,10 +696,25 @@ GradShape grad_shape(const bss_residual_norm_grads& a) {
     s.warps = (a.channels / 8 + 31) / 32;
     s.side = s.warps >= 4 ? 1 : 4 / s.warps;
     s.threads = s.warps * s.side * 32;
+#ifndef GT
+#define GT 2
+#endif
+    s.T = s.threads <= 512 ? GT : 1;
+    const int pieces = s.T * (esize(a.stream_dtype) + esize(a.branch_dtype) + 1);
+    s.stages = 2 * pieces * s.threads * 16 <= 224 * 1024 ? 2 : 1;
+    s.smem = s.stages * pieces * s.threads * 16;
+    if (s.side > 1 && s.smem < s.side * 3 * a.channels * 4) s.smem = s.side * 3 * a.channels * 4;
     const int64_t per_group = !grouped(a) || a.rows_per_group > a.rows ? a.rows : a.rows_per_group;
     s.groups = (a.rows + per_group - 1) / per_group;
-    const int64_t per_sm = s.threads >= 512 ? 1 : 512 / s.threads;
-    const int64_t most = (per_sm * num_sms() + s.groups - 1) / s.groups;
+    // one wave of blocks: 16 warps an SM at 128 registers a thread, or what the
+    // slots leave room for
+#ifndef GW
+#define GW 16
+#endif
+    int per_sm = GW * 32 / s.threads, by_smem = 224 * 1024 / (s.smem + 3072);
+    per_sm = per_sm < by_smem ? per_sm : by_smem;
+    int64_t most = (per_sm < 1 ? 1 : per_sm) * static_cast<int64_t>(num_sms()) / s.groups;
+    if (most < 1) most = 1;
     s.chunks = (per_group + kMinChunkRows - 1) / kMinChunkRows;
     if (s.chunks > most) s.chunks = most;
     s.chunk_rows = (per_group + s.chunks - 1) / s.chunks;
@@ -553,15 +726,21 @@ int64_t grad_workspace(const bss_residual_norm_grads& a, const GradShape& s) {
     return wants_sums(a) ? s.groups * s.chunks * 3 * a.channels * 4 : 0;
 }
 
+template <typename TS, typename TB, int T, int THREADS>
+bss_status launch_backward_rows(const GradArgs& g, cudaStream_t stream) {
+    int resident = 1;  // asked for the shared memory limit it sets
+    const bss_status st = resident_blocks(reinterpret_cast<const void*>(norm_backward_kernel<TS, TB, T, THREADS>),
+                                          g.s.threads, g.s.smem, &resident);
+    if (st != BSS_OK) return st;
+    norm_backward_kernel<TS, TB, T, THREADS>
+        <<<static_cast<unsigned>(g.s.groups * g.s.chunks), g.s.threads, g.s.smem, stream>>>(g);
+    return cuda_check(cudaGetLastError(), "residual norm backward launch");
+}
+
 template <typename TS, typename TB>
 bss_status launch_backward(const GradArgs& g, cudaStream_t stream) {
-    const int smem = g.s.side > 1 && g.want_sums ? g.s.side * 3 * g.a.channels * 4 : 0;
-    const unsigned grid = static_cast<unsigned>(g.s.groups * g.s.chunks);
-    if (g.s.threads <= 512)
-        norm_backward_kernel<TS, TB, 2><<<grid, g.s.threads, smem, stream>>>(g);
-    else
-        norm_backward_kernel<TS, TB, 1><<<grid, g.s.threads, smem, stream>>>(g);
-    return cuda_check(cudaGetLastError(), "residual norm backward launch");
+    if (g.s.threads > 512) return launch_backward_rows<TS, TB, 1, 1024>(g, stream);
+    return launch_backward_rows<TS, TB, GT, 512>(g, stream);
 }
 
 bss_status check_grads(const bss_residual_norm_grads* args) {
