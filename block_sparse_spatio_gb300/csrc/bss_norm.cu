@@ -40,8 +40,12 @@ __device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// A vector of 8 channels from 16-byte pieces `apart` bytes apart (one of bf16,
-// two of float).
+__device__ __forceinline__ uint2 lds64(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+
 __device__ __forceinline__ V8 floats_of(const uint4& a, const uint4& b) {
     V8 v;
     v.p[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
@@ -51,38 +55,95 @@ __device__ __forceinline__ V8 floats_of(const uint4& a, const uint4& b) {
     return v;
 }
 
-template <typename T>
-__device__ __forceinline__ V8 lds_vector(uint32_t at, uint32_t apart) {
-    if constexpr (sizeof(T) == 2)
-        return unpack_bf16<false>(lds128(at));
-    else
-        return floats_of(lds128(at), lds128(at + apart));
+__device__ __forceinline__ uint4 bits_of(const float2& a, const float2& b) {
+    return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
 }
 
-template <typename T>
-__device__ __forceinline__ void fetch_vector(uint32_t to, uint32_t apart, const T* from) {
-    cp_async_16(to, from);
-    if (sizeof(T) == 4) cp_async_16(to + apart, from + 4);
+// The 8 channels of a thread's vector.  Rows of bf16 alone: 8 neighbouring
+// channels, 16 bytes.  With a float stream (SPLIT): two runs of 4, 128 channels
+// apart, so that 32 lanes read and write whole sectors of every tensor: 16 bytes
+// a lane of float, 8 of bf16 (8 neighbouring float channels would be two loads of
+// 16 bytes at a stride of 32, each sector asked for twice).
+template <bool SPLIT>
+__device__ __forceinline__ int channel_at(int warp_of_row, int half) {
+    const int lane = threadIdx.x & 31;
+    return SPLIT ? warp_of_row * 256 + half * 128 + lane * 4 : (warp_of_row * 32 + lane) * 8 + half * 4;
+}
+
+// A vector in shared memory: `lanes` threads' pieces side by side, a piece of
+// 16 (or 8) bytes of thread `idx` at region + idx * size, its second half after
+// all the first ones.
+template <typename T, bool SPLIT>
+__device__ __forceinline__ void fetch_vector(uint32_t region, int idx, int lanes, const T* from, bool live0, bool live1) {
+    if constexpr (!SPLIT) {
+        if (live0) cp_async_16(region + idx * 16, from);
+    } else if constexpr (sizeof(T) == 4) {
+        if (live0) cp_async_16(region + idx * 16, from);
+        if (live1) cp_async_16(region + (lanes + idx) * 16, from + 128);
+    } else {
+        if (live0)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(region + idx * 8), "l"(from) : "memory");
+        if (live1)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(region + (lanes + idx) * 8), "l"(from + 128)
+                         : "memory");
+    }
+}
+
+template <typename T, bool SPLIT>
+__device__ __forceinline__ V8 lds_vector(uint32_t region, int idx, int lanes) {
+    if constexpr (!SPLIT) {
+        return unpack_bf16<false>(lds128(region + idx * 16));
+    } else if constexpr (sizeof(T) == 4) {
+        return floats_of(lds128(region + idx * 16), lds128(region + (lanes + idx) * 16));
+    } else {
+        const uint2 a = lds64(region + idx * 8), b = lds64(region + (lanes + idx) * 8);
+        return unpack_bf16<false>(make_uint4(a.x, a.y, b.x, b.y));
+    }
+}
+
+__device__ __forceinline__ void st_row8(void* p, uint32_t a, uint32_t b) {
+    asm volatile("st.global.cs.v2.u32 [%0], {%1,%2};" ::"l"(p), "r"(a), "r"(b) : "memory");
+}
+
+template <typename T, bool SPLIT>
+__device__ __forceinline__ void store_vector(T* to, const V8& v, bool live0, bool live1) {
+    if constexpr (!SPLIT) {
+        if (live0) st_row(to, pack_bf16<false>(v));
+    } else if constexpr (sizeof(T) == 4) {
+        if (live0) st_row(to, bits_of(v.p[0], v.p[1]));
+        if (live1) st_row(to + 128, bits_of(v.p[2], v.p[3]));
+    } else {
+        if (live0) st_row8(to, pack2(v.p[0].x, v.p[0].y), pack2(v.p[1].x, v.p[1].y));
+        if (live1) st_row8(to + 128, pack2(v.p[2].x, v.p[2].y), pack2(v.p[3].x, v.p[3].y));
+    }
 }
 
 __device__ __forceinline__ V8 zeros() { return floats_of(make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)); }
 
-template <typename T>
-__device__ __forceinline__ void store_vector(T* to, const V8& v) {
-    if constexpr (sizeof(T) == 2) {
-        st_row(to, pack_bf16<false>(v));
+// Zeros in the half that lies past the row.
+__device__ __forceinline__ void keep_live(V8& v, bool live0, bool live1) {
+    if (!live0) v.p[0] = v.p[1] = f2(0.0f);
+    if (!live1) v.p[2] = v.p[3] = f2(0.0f);
+}
+
+// Four parameters.
+__device__ __forceinline__ void param4(const void* p, int64_t at, int dtype, float2& a, float2& b) {
+    if (dtype == BSS_DTYPE_F32) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at));
+        a = make_float2(v.x, v.y), b = make_float2(v.z, v.w);
     } else {
-#pragma unroll
-        for (int i = 0; i < 4; i += 2)
-            st_row(to + 2 * i, make_uint4(__float_as_uint(v.p[i].x), __float_as_uint(v.p[i].y),
-                                          __float_as_uint(v.p[i + 1].x), __float_as_uint(v.p[i + 1].y)));
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p) + at));
+        a = make_float2(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u));
+        b = make_float2(__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u));
     }
 }
 
-__device__ __forceinline__ V8 param_vector(const void* p, int64_t at, int dtype) {
-    float f[8];
-    load_param8(p, at, dtype, f);
-    return arrange<false>(f);
+// Those of the channels c0 .. c0 + 3 and c1 .. c1 + 3.
+__device__ __forceinline__ V8 param_vector(const void* p, int64_t row, int c0, int c1, int dtype) {
+    V8 v;
+    param4(p, row + c0, dtype, v.p[0], v.p[1]);
+    param4(p, row + c1, dtype, v.p[2], v.p[3]);
+    return v;
 }
 
 __device__ __forceinline__ V8 add8(const V8& a, const V8& b) {
@@ -119,18 +180,19 @@ struct ForwardArgs {
     int64_t chunks, chunk_rows;
 };
 
-__device__ __forceinline__ V8 fold(const bss_residual_norm_args& a, int which, int64_t group, int c) {
+__device__ __forceinline__ V8 fold(const bss_residual_norm_args& a, int which, int64_t group, int c0, int c1) {
     V8 v = zeros();
+    const int dt = a.param_dtype;
     if (which == 0) {
-        v = a.gate != nullptr ? param_vector(a.gate, group * a.gate_stride + c, a.param_dtype) : add8(v, 1.0f);
-        if (a.y_weight != nullptr) v = mul(v, param_vector(a.y_weight, c, a.param_dtype));
+        v = a.gate != nullptr ? param_vector(a.gate, group * a.gate_stride, c0, c1, dt) : add8(v, 1.0f);
+        if (a.y_weight != nullptr) v = mul(v, param_vector(a.y_weight, 0, c0, c1, dt));
         return v;
     }
     V8 m = add8(v, 1.0f);
-    if (a.scale != nullptr) m = add8(param_vector(a.scale, group * a.scale_stride + c, a.param_dtype), 1.0f);
-    if (which == 1) return a.weight != nullptr ? mul(m, param_vector(a.weight, c, a.param_dtype)) : m;
-    if (a.bias != nullptr) v = mul(m, param_vector(a.bias, c, a.param_dtype));
-    return a.shift != nullptr ? add8(v, param_vector(a.shift, group * a.shift_stride + c, a.param_dtype)) : v;
+    if (a.scale != nullptr) m = add8(param_vector(a.scale, group * a.scale_stride, c0, c1, dt), 1.0f);
+    if (which == 1) return a.weight != nullptr ? mul(m, param_vector(a.weight, 0, c0, c1, dt)) : m;
+    if (a.bias != nullptr) v = mul(m, param_vector(a.bias, 0, c0, c1, dt));
+    return a.shift != nullptr ? add8(v, param_vector(a.shift, group * a.shift_stride, c0, c1, dt)) : v;
 }
 
 // Sum over the W warps that share a row; every thread gets it.  Each use between
@@ -161,11 +223,12 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
     extern __shared__ __align__(16) float4 folded[];
     __shared__ float buf[2][4][W];
     const bss_residual_norm_args& a = g.a;
+    constexpr bool kSplit = sizeof(TS) == 4;
     constexpr int kWarps = W > 4 ? W : 4, kRows = kWarps / W;
     constexpr uint32_t kStage = forward_stage<TS, TB>(VPT), kY = VPT * sizeof(TS) * 256;
-    const int lane = (threadIdx.x & 31) + 32 * (W == 1 ? 0 : threadIdx.x >> 5);
-    const int vecs = a.channels / 8;
-    const float inv = 1.0f / a.channels;
+    const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
+    const int C = a.channels;
+    const float inv = 1.0f / C;
     const int64_t first_group = blockIdx.x / g.chunks, chunk = blockIdx.x - first_group * g.chunks;
     const int64_t group_rows = STAGED ? a.rows_per_group : a.rows;
     int64_t row = first_group * group_rows + chunk * g.chunk_rows;
@@ -174,18 +237,21 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
     if (last > a.rows) last = a.rows;
     row += threadIdx.x / 32 / W;
 
+    // channels of vector i: c0 + i * 256 W and c1 + i * 256 W, four each
+    const int c0 = channel_at<kSplit>(warp, 0), c1 = channel_at<kSplit>(warp, 1);
+    auto live0 = [&](int i) { return c0 + i * 256 * W < C; };
+    auto live1 = [&](int i) { return (kSplit ? c1 : c0) + i * 256 * W < C; };
     const uint32_t base = smem_u32(folded);
-    const uint32_t slots = base + (STAGED ? g.folds * a.channels * 4 : 0) + (threadIdx.x >> 5) * 2 * kStage +
-                           (threadIdx.x & 31) * 16;
-    const TS* x = static_cast<const TS*>(a.x) + row * a.x_stride + lane * 8;
-    const TB* y = static_cast<const TB*>(a.y) + row * a.y_stride + lane * 8;
+    const uint32_t slots = base + (STAGED ? g.folds * C * 4 : 0) + (threadIdx.x >> 5) * 2 * kStage;
+    const TS* x = static_cast<const TS*>(a.x) + row * a.x_stride + c0;
+    const TB* y = static_cast<const TB*>(a.y) + row * a.y_stride + c0;
     auto fetch = [&](bool exists, uint32_t to) {
         if (exists) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                if (lane + i * 32 * W >= vecs) continue;
-                fetch_vector(to + i * sizeof(TS) * 256, 512, x + i * 256 * W);
-                if (a.y != nullptr) fetch_vector(to + kY + i * sizeof(TB) * 256, 512, y + i * 256 * W);
+                fetch_vector<TS, kSplit>(to + i * sizeof(TS) * 256, lane, 32, x + i * 256 * W, live0(i), live1(i));
+                if (a.y != nullptr)
+                    fetch_vector<TB, kSplit>(to + kY + i * sizeof(TB) * 256, lane, 32, y + i * 256 * W, live0(i), live1(i));
             }
             x += kRows * a.x_stride;
             y += kRows * a.y_stride;
@@ -193,31 +259,32 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
         cp_async_commit();
     };
     fetch(row < last, slots);
+    // folded parameters: by channel, or for neighbouring channels in two planes, so
+    // that lanes read them without bank conflicts
+    const uint32_t fold1 = base + (g.folded.has[0] ? C * 4 : 0);
+    const uint32_t fold2 = fold1 + (g.folded.has[1] ? C * 4 : 0);
+    auto fold_at = [&](int which, int c) -> uint32_t {
+        const uint32_t at = which == 0 ? base : which == 1 ? fold1 : fold2;
+        return kSplit ? at + c * 4 : at + (c & 4) * (C / 2) + (c >> 3) * 16;
+    };
     if (STAGED && g.folds > 0) {
-        int k = 0;
 #pragma unroll
         for (int which = 0; which < 3; ++which) {
             if (!g.folded.has[which]) continue;
 #pragma unroll 2
-            for (int v = threadIdx.x; v < vecs; v += blockDim.x) {
-                const V8 f = fold(a, which, first_group, v * 8);
-                const uint32_t at = base + k * a.channels * 4 + v * 16;
-                sts128(at, make_uint4(__float_as_uint(f.p[0].x), __float_as_uint(f.p[0].y), __float_as_uint(f.p[1].x),
-                                      __float_as_uint(f.p[1].y)));
-                sts128(at + vecs * 16, make_uint4(__float_as_uint(f.p[2].x), __float_as_uint(f.p[2].y),
-                                                  __float_as_uint(f.p[3].x), __float_as_uint(f.p[3].y)));
+            for (int c = threadIdx.x * 8; c < C; c += blockDim.x * 8) {
+                const V8 f = fold(a, which, first_group, c, c + 4);
+                sts128(fold_at(which, c), bits_of(f.p[0], f.p[1]));
+                sts128(fold_at(which, c + 4), bits_of(f.p[2], f.p[3]));
             }
-            ++k;
         }
         __syncthreads();
     }
-    const uint32_t fold1 = base + (g.folded.has[0] ? a.channels * 4 : 0);
-    const uint32_t fold2 = fold1 + (g.folded.has[1] ? a.channels * 4 : 0);
-    const uint32_t plane = vecs * 16;
-    auto folded_at = [&](int which, int64_t group, int v) {
-        if (!STAGED) return fold(a, which, group, v * 8);
-        const uint32_t at = (which == 0 ? base : which == 1 ? fold1 : fold2) + v * 16;
-        return floats_of(lds128(at), lds128(at + plane));
+    // those of vector i; only called where it is live, a dead half takes the other's
+    auto folded_of = [&](int which, int64_t group, int i) {
+        const int lo = c0 + i * 256 * W, hi = live1(i) ? c1 + i * 256 * W : lo;
+        if (!STAGED) return fold(a, which, group, lo, hi);
+        return floats_of(lds128(fold_at(which, lo)), lds128(fold_at(which, hi)));
     };
     uint32_t now = slots, other = slots + kStage;
     int parity = 0;
@@ -232,34 +299,40 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
             if (a.y_norm == BSS_NORM_LAYER) {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
-                    if (lane + i * 32 * W < vecs) s += sum8(lds_vector<TB>(now + kY + i * sizeof(TB) * 256, 512));
+                    if (live0(i)) {
+                        V8 v = lds_vector<TB, kSplit>(now + kY + i * sizeof(TB) * 256, lane, 32);
+                        keep_live(v, true, live1(i));
+                        s += sum8(v);
+                    }
                 ym = row_sum<W>(s, buf[parity][0]) * inv;
             }
             s = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                if (lane + i * 32 * W >= vecs) continue;
-                const V8 v = add8(lds_vector<TB>(now + kY + i * sizeof(TB) * 256, 512), -ym);
+                if (!live0(i)) continue;
+                V8 v = add8(lds_vector<TB, kSplit>(now + kY + i * sizeof(TB) * 256, lane, 32), -ym);
+                keep_live(v, true, live1(i));
                 s += dot(v, v);
             }
             yrstd = rsqrtf(row_sum<W>(s, buf[parity][1]) * inv + a.eps);
-            if (a.y_stats != nullptr && lane == 0)
+            if (a.y_stats != nullptr && lane == 0 && warp == 0)
                 *reinterpret_cast<float2*>(a.y_stats + 2 * row) = make_float2(ym, yrstd);
         }
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = lane + i * 32 * W;
             r[i] = zeros();
-            if (v >= vecs) continue;
-            r[i] = lds_vector<TS>(now + i * sizeof(TS) * 256, 512);
+            if (!live0(i)) continue;
+            r[i] = lds_vector<TS, kSplit>(now + i * sizeof(TS) * 256, lane, 32);
             if (a.y != nullptr) {
-                V8 t = lds_vector<TB>(now + kY + i * sizeof(TB) * 256, 512);
+                V8 t = lds_vector<TB, kSplit>(now + kY + i * sizeof(TB) * 256, lane, 32);
                 if (a.y_norm != BSS_NORM_NONE) t = mul(add8(t, -ym), yrstd);
-                if (g.folded.has[0]) t = mul(t, folded_at(0, group, v));
+                if (g.folded.has[0]) t = mul(t, folded_of(0, group, i));
                 r[i] = fma8(r[i], a.residual_scale, t);
-                if (a.r != nullptr) store_vector(static_cast<TS*>(a.r) + row * a.r_stride + v * 8, r[i]);
+                if (a.r != nullptr)
+                    store_vector<TS, kSplit>(static_cast<TS*>(a.r) + row * a.r_stride + c0 + i * 256 * W, r[i], true, live1(i));
             }
+            keep_live(r[i], true, live1(i));
             s += sum8(r[i]);
         }
         const uint32_t t = now;
@@ -271,21 +344,22 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
             s = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                if (lane + i * 32 * W >= vecs) continue;
+                if (!live0(i)) continue;
                 r[i] = add8(r[i], -mean);
+                keep_live(r[i], true, live1(i));
                 s += dot(r[i], r[i]);
             }
             rstd = rsqrtf(row_sum<W>(s, buf[parity][3]) * inv + a.eps);
-            if (a.stats != nullptr && lane == 0) *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
+            if (a.stats != nullptr && lane == 0 && warp == 0)
+                *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int v = lane + i * 32 * W;
-            if (v >= vecs) continue;
+            if (!live0(i)) continue;
             V8 n = mul(r[i], rstd);
-            if (g.folded.has[1]) n = mul(n, folded_at(1, group, v));
-            if (g.folded.has[2]) n = add8(n, folded_at(2, group, v));
-            store_vector(static_cast<TB*>(a.h) + row * a.h_stride + v * 8, n);
+            if (g.folded.has[1]) n = mul(n, folded_of(1, group, i));
+            if (g.folded.has[2]) n = add8(n, folded_of(2, group, i));
+            store_vector<TB, kSplit>(static_cast<TB*>(a.h) + row * a.h_stride + c0 + i * 256 * W, n, true, live1(i));
         }
     }
     cp_async_wait_group<0>();
@@ -334,17 +408,25 @@ __device__ __forceinline__ void shared_sums(float (&v)[NV], int warps, int warp0
 }
 
 template <typename TS, typename TB, int T, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_constant__ GradArgs g) {
+#ifdef MR
+__global__ void __maxnreg__(THREADS > 512 ? 64 : MR) norm_backward_kernel
+#else
+__global__ void __launch_bounds__(THREADS) norm_backward_kernel
+#endif
+    (const __grid_constant__ GradArgs g) {
     extern __shared__ __align__(16) float shared[];  // slots; at the end the column sums of the rows side by side
     __shared__ __align__(16) float buf[4][32 * 2 * T];
     const bss_residual_norm_grads& a = g.a;
+    constexpr bool kSplit = sizeof(TS) == 4;
     constexpr int kPieces = grad_pieces<TS, TB>(T), kS = sizeof(TS) / 2, kB = sizeof(TB) / 2;
-    const int per = g.s.warps * 32;
-    const int side = threadIdx.x / per;
-    const int vec = threadIdx.x - side * per;
+    const int side = (threadIdx.x >> 5) / g.s.warps;
     const int warp0 = side * g.s.warps;
-    const bool active = vec * 8 < a.channels;
-    const int c = active ? vec * 8 : 0;
+    const int warp = (threadIdx.x >> 5) - warp0;
+    const bool active = channel_at<kSplit>(warp, 0) < a.channels;
+    const bool whole = kSplit ? channel_at<kSplit>(warp, 1) < a.channels : active;  // the second half too
+    const int c = active ? channel_at<kSplit>(warp, 0) : 0;
+    const int c1 = whole ? channel_at<kSplit>(warp, 1) : c;
+    const int idx = threadIdx.x, lanes = blockDim.x;
     const float inv = 1.0f / a.channels;
     const int64_t group = blockIdx.x / g.s.chunks, chunk = blockIdx.x - group * g.s.chunks;
     const int64_t first = group * a.rows_per_group + chunk * g.s.chunk_rows;
@@ -356,7 +438,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
 
     // slot of piece k: a column of `threads` 16-byte pieces
     const uint32_t apart = blockDim.x * 16;
-    const uint32_t slots = smem_u32(shared) + threadIdx.x * 16;
+    const uint32_t slots = smem_u32(shared);
     const TS* r_in = static_cast<const TS*>(a.r) + c;
     const TS* dr_in = static_cast<const TS*>(a.dr) + c;
     const TB* dh_in = static_cast<const TB*>(a.dh) + c;
@@ -368,12 +450,14 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             if (!active || row >= last) continue;
             const uint32_t at = to + t * (kPieces / T) * apart;
             if (a.dh != nullptr) {
-                fetch_vector(at, apart, r_in + row * a.r_stride);
-                fetch_vector(at + (2 * kS) * apart, apart, dh_in + row * a.dh_stride);
+                fetch_vector<TS, kSplit>(at, idx, lanes, r_in + row * a.r_stride, true, whole);
+                fetch_vector<TB, kSplit>(at + (2 * kS) * apart, idx, lanes, dh_in + row * a.dh_stride, true, whole);
             }
-            if (a.dr != nullptr) fetch_vector(at + kS * apart, apart, dr_in + row * a.dr_stride);
-            if (a.y != nullptr) fetch_vector(at + (2 * kS + kB) * apart, apart, y_in + row * a.y_stride);
-            const uint32_t st = at + (2 * kS + 2 * kB) * apart;
+            if (a.dr != nullptr)
+                fetch_vector<TS, kSplit>(at + kS * apart, idx, lanes, dr_in + row * a.dr_stride, true, whole);
+            if (a.y != nullptr)
+                fetch_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes, y_in + row * a.y_stride, true, whole);
+            const uint32_t st = at + (2 * kS + 2 * kB) * apart + idx * 16;
             if (stats)
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st), "l"(a.stats + 2 * row) : "memory");
             if (ystats)
@@ -392,10 +476,13 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
     V8 m1 = zeros(), m2 = zeros();
     if (active) {
         m1 = add8(m1, 1.0f), m2 = add8(m2, 1.0f);
-        if (a.scale != nullptr) m1 = add8(m1, param_vector(a.scale, group * a.scale_stride + c, a.param_dtype));
-        if (a.weight != nullptr) m1 = mul(m1, param_vector(a.weight, c, a.param_dtype));
-        if (a.gate != nullptr) m2 = param_vector(a.gate, group * a.gate_stride + c, a.param_dtype);
-        if (a.y_weight != nullptr) m2 = mul(m2, param_vector(a.y_weight, c, a.param_dtype));
+        const int dt = a.param_dtype;
+        if (a.scale != nullptr) m1 = add8(m1, param_vector(a.scale, group * a.scale_stride, c, c1, dt));
+        if (a.weight != nullptr) m1 = mul(m1, param_vector(a.weight, 0, c, c1, dt));
+        if (a.gate != nullptr) m2 = param_vector(a.gate, group * a.gate_stride, c, c1, dt);
+        if (a.y_weight != nullptr) m2 = mul(m2, param_vector(a.y_weight, 0, c, c1, dt));
+        keep_live(m1, true, whole);
+        keep_live(m2, true, whole);
     }
     V8 sa = zeros(), sb = zeros(), sc = zeros();
     int stage = 0, turn = 0;
@@ -419,13 +506,14 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             xh[t] = tt[t] = zeros();
             st[t] = yst[t] = make_float2(0.0f, 1.0f);
             if (live) {
-                const uint4 q = lds128(at + (2 * kS + 2 * kB) * apart);
+                const uint4 q = lds128(at + (2 * kS + 2 * kB) * apart + idx * 16);
                 if (stats) st[t] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
                 if (ystats) yst[t] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
             }
             if (live && a.dh != nullptr) {
-                xh[t] = mul(add8(lds_vector<TS>(at, apart), -st[t].x), st[t].y);
-                const V8 dh = lds_vector<TB>(at + (2 * kS) * apart, apart);
+                xh[t] = mul(add8(lds_vector<TS, kSplit>(at, idx, lanes), -st[t].x), st[t].y);
+                V8 dh = lds_vector<TB, kSplit>(at + (2 * kS) * apart, idx, lanes);
+                if (kSplit) keep_live(xh[t], true, whole), keep_live(dh, true, whole);
                 tt[t] = mul(dh, m1);
                 sa = fma8(dh, xh[t], sa);
                 sb = add8(sb, dh);
@@ -443,13 +531,16 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             const float mean1 = a.norm == BSS_NORM_LAYER ? sums[2 * t] * inv : 0.0f;
             const float mean2 = a.norm != BSS_NORM_NONE ? sums[2 * t + 1] * inv : 0.0f;
             V8 u = zeros();
-            if (live && a.dr != nullptr) u = lds_vector<TS>(at + kS * apart, apart);
+            if (live && a.dr != nullptr) u = lds_vector<TS, kSplit>(at + kS * apart, idx, lanes);
             u = fma8(fma8(xh[t], -mean2, add8(tt[t], -mean1)), st[t].y, u);
-            if (live) store_vector(static_cast<TS*>(a.dx) + (mine + t) * a.dx_stride + c, mul(u, a.residual_scale));
+            if (live)
+                store_vector<TS, kSplit>(static_cast<TS*>(a.dx) + (mine + t) * a.dx_stride + c, mul(u, a.residual_scale), true,
+                                         whole);
             z[t] = zeros();
             zs[2 * t] = zs[2 * t + 1] = 0.0f;
             if (a.dy == nullptr || !live) continue;
-            const V8 yh = mul(add8(lds_vector<TB>(at + (2 * kS + kB) * apart, apart), -yst[t].x), yst[t].y);
+            V8 yh = mul(add8(lds_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes), -yst[t].x), yst[t].y);
+            if (kSplit) keep_live(u, true, whole), keep_live(yh, true, whole);
             sc = fma8(u, yh, sc);
             z[t] = mul(u, m2);
             zs[2 * t] = sum8(z[t]);
@@ -463,10 +554,10 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             if (ystats) {
                 const uint32_t at = now + t * (kPieces / T) * apart;
                 const float mean1 = a.y_norm == BSS_NORM_LAYER ? zs[2 * t] * inv : 0.0f;
-                const V8 yh = mul(add8(lds_vector<TB>(at + (2 * kS + kB) * apart, apart), -yst[t].x), yst[t].y);
+                const V8 yh = mul(add8(lds_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes), -yst[t].x), yst[t].y);
                 z[t] = mul(fma8(yh, -zs[2 * t + 1] * inv, add8(z[t], -mean1)), yst[t].y);
             }
-            store_vector(static_cast<TB*>(a.dy) + (mine + t) * a.dy_stride + c, z[t]);
+            store_vector<TB, kSplit>(static_cast<TB*>(a.dy) + (mine + t) * a.dy_stride + c, z[t], true, whole);
         }
     }
     cp_async_wait_group<0>();
@@ -479,11 +570,9 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
 #pragma unroll
     for (int q = 0; q < 3; ++q) {
         if (!active) continue;
-        float* at = g.s.side > 1 ? shared + (side * 3 + q) * C + c : dst + q * C + c;
-#pragma unroll
-        for (int j = 0; j < 4; j += 2)
-            *reinterpret_cast<float4*>(at + 2 * j) =
-                make_float4(sums3[q]->p[j].x, sums3[q]->p[j].y, sums3[q]->p[j + 1].x, sums3[q]->p[j + 1].y);
+        float* at = g.s.side > 1 ? shared + (side * 3 + q) * C : dst + q * C;
+        *reinterpret_cast<uint4*>(at + c) = bits_of(sums3[q]->p[0], sums3[q]->p[1]);
+        if (whole) *reinterpret_cast<uint4*>(at + c1) = bits_of(sums3[q]->p[2], sums3[q]->p[3]);
     }
     if (g.s.side == 1) return;
     __syncthreads();
