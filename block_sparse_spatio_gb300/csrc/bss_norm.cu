@@ -390,6 +390,14 @@ __host__ __device__ constexpr int grad_pieces(int T) {
     return T * static_cast<int>(sizeof(TS) + sizeof(TB) + 1);
 }
 
+// What is behind the two gradients:
+//   PLAIN  no norm of y, one round of sums (mean t, mean t xh)
+//   RMS2   both norms RMS: one round too, since z = u f with f = gate y_weight is
+//          linear in mean(t xh):
+//            sum z yh = sum f yh (dr + rstd t) - rstd mean(t xh) sum f yh xh
+//   BOTH   any other norm of y: a second round for z
+enum { PLAIN = 0, RMS2 = 1, BOTH = 2 };
+
 // Sums of NV values over the row's warps; `buf` holds NV floats a warp of the block.
 template <int NV>
 __device__ __forceinline__ void shared_sums(float (&v)[NV], int warps, int warp0, float* buf) {
@@ -407,15 +415,10 @@ __device__ __forceinline__ void shared_sums(float (&v)[NV], int warps, int warp0
     }
 }
 
-template <typename TS, typename TB, int T, int THREADS>
-#ifdef MR
-__global__ void __maxnreg__(THREADS > 512 ? 64 : MR) norm_backward_kernel
-#else
-__global__ void __launch_bounds__(THREADS) norm_backward_kernel
-#endif
-    (const __grid_constant__ GradArgs g) {
+template <typename TS, typename TB, int MODE, int T, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_constant__ GradArgs g) {
     extern __shared__ __align__(16) float shared[];  // slots; at the end the column sums of the rows side by side
-    __shared__ __align__(16) float buf[4][32 * 2 * T];
+    __shared__ __align__(16) float buf[4][32 * (MODE == RMS2 ? 4 : 2) * T];
     const bss_residual_norm_grads& a = g.a;
     constexpr bool kSplit = sizeof(TS) == 4;
     constexpr int kPieces = grad_pieces<TS, TB>(T), kS = sizeof(TS) / 2, kB = sizeof(TB) / 2;
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel
     if (last > (group + 1) * a.rows_per_group) last = (group + 1) * a.rows_per_group;
     if (last > a.rows) last = a.rows;
     const bool stats = a.dh != nullptr && a.norm != BSS_NORM_NONE;
-    const bool ystats = a.y != nullptr && a.y_norm != BSS_NORM_NONE;
+    constexpr bool ystats = MODE != PLAIN;
 
     // slot of piece k: a column of `threads` 16-byte pieces
     const uint32_t apart = blockDim.x * 16;
@@ -498,7 +501,8 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel
         stage ^= ahead ? 1 : 0;
         V8 xh[T], tt[T];
         float2 st[T], yst[T];
-        float sums[2 * T];
+        constexpr int NV = MODE == RMS2 ? 4 : 2;
+        float sums[NV * T];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             const uint32_t at = now + t * (kPieces / T) * apart;
@@ -518,18 +522,29 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel
                 sa = fma8(dh, xh[t], sa);
                 sb = add8(sb, dh);
             }
-            sums[2 * t] = sum8(tt[t]);
-            sums[2 * t + 1] = dot(tt[t], xh[t]);
+            sums[NV * t] = MODE == RMS2 ? 0.0f : sum8(tt[t]);
+            sums[NV * t + 1] = dot(tt[t], xh[t]);
+            if constexpr (MODE == RMS2) {
+                sums[NV * t + 2] = sums[NV * t + 3] = 0.0f;
+                if (!live) continue;
+                V8 w = zeros();
+                if (a.dr != nullptr) w = lds_vector<TS, kSplit>(at + kS * apart, idx, lanes);
+                w = fma8(tt[t], st[t].y, w);
+                V8 f = mul(mul(lds_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes), yst[t].y), m2);
+                if (kSplit) keep_live(w, true, whole), keep_live(f, true, whole);
+                sums[NV * t + 2] = dot(f, w);
+                sums[NV * t + 3] = dot(f, xh[t]);
+            }
         }
-        if (stats) shared_sums<2 * T>(sums, g.s.warps, warp0, buf[turn]);
+        if (stats) shared_sums<NV * T>(sums, g.s.warps, warp0, buf[turn]);
         float zs[2 * T];
         V8 z[T];
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             const uint32_t at = now + t * (kPieces / T) * apart;
             const bool live = active && mine + t < last;
-            const float mean1 = a.norm == BSS_NORM_LAYER ? sums[2 * t] * inv : 0.0f;
-            const float mean2 = a.norm != BSS_NORM_NONE ? sums[2 * t + 1] * inv : 0.0f;
+            const float mean1 = a.norm == BSS_NORM_LAYER ? sums[NV * t] * inv : 0.0f;
+            const float mean2 = a.norm != BSS_NORM_NONE ? sums[NV * t + 1] * inv : 0.0f;
             V8 u = zeros();
             if (live && a.dr != nullptr) u = lds_vector<TS, kSplit>(at + kS * apart, idx, lanes);
             u = fma8(fma8(xh[t], -mean2, add8(tt[t], -mean1)), st[t].y, u);
@@ -543,15 +558,21 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel
             if (kSplit) keep_live(u, true, whole), keep_live(yh, true, whole);
             sc = fma8(u, yh, sc);
             z[t] = mul(u, m2);
-            zs[2 * t] = sum8(z[t]);
-            zs[2 * t + 1] = dot(z[t], yh);
+            if constexpr (MODE == BOTH) {
+                zs[2 * t] = sum8(z[t]);
+                zs[2 * t + 1] = dot(z[t], yh);
+            } else {
+                if constexpr (MODE == RMS2)
+                    z[t] = mul(fma8(yh, -inv * (sums[NV * t + 2] - st[t].y * mean2 * sums[NV * t + 3]), z[t]), yst[t].y);
+                store_vector<TB, kSplit>(static_cast<TB*>(a.dy) + (mine + t) * a.dy_stride + c, z[t], true, whole);
+            }
         }
-        if (a.dy == nullptr) continue;
-        if (ystats) shared_sums<2 * T>(zs, g.s.warps, warp0, buf[turn + 1]);
+        if constexpr (MODE != BOTH) continue;
+        if (MODE == BOTH) shared_sums<2 * T>(zs, g.s.warps, warp0, buf[turn + 1]);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
             if (!active || mine + t >= last) continue;
-            if (ystats) {
+            {
                 const uint32_t at = now + t * (kPieces / T) * apart;
                 const float mean1 = a.y_norm == BSS_NORM_LAYER ? zs[2 * t] * inv : 0.0f;
                 const V8 yh = mul(add8(lds_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes), -yst[t].x), yst[t].y);
@@ -815,21 +836,29 @@ int64_t grad_workspace(const bss_residual_norm_grads& a, const GradShape& s) {
     return wants_sums(a) ? s.groups * s.chunks * 3 * a.channels * 4 : 0;
 }
 
-template <typename TS, typename TB, int T, int THREADS>
+template <typename TS, typename TB, int MODE, int T, int THREADS>
 bss_status launch_backward_rows(const GradArgs& g, cudaStream_t stream) {
     int resident = 1;  // asked for the shared memory limit it sets
-    const bss_status st = resident_blocks(reinterpret_cast<const void*>(norm_backward_kernel<TS, TB, T, THREADS>),
+    const bss_status st = resident_blocks(reinterpret_cast<const void*>(norm_backward_kernel<TS, TB, MODE, T, THREADS>),
                                           g.s.threads, g.s.smem, &resident);
     if (st != BSS_OK) return st;
-    norm_backward_kernel<TS, TB, T, THREADS>
+    norm_backward_kernel<TS, TB, MODE, T, THREADS>
         <<<static_cast<unsigned>(g.s.groups * g.s.chunks), g.s.threads, g.s.smem, stream>>>(g);
     return cuda_check(cudaGetLastError(), "residual norm backward launch");
 }
 
+template <typename TS, typename TB, int MODE>
+bss_status launch_backward_mode(const GradArgs& g, cudaStream_t stream) {
+    if (g.s.threads > 512) return launch_backward_rows<TS, TB, MODE, 1, 1024>(g, stream);
+    return launch_backward_rows<TS, TB, MODE, GT, 512>(g, stream);
+}
+
 template <typename TS, typename TB>
 bss_status launch_backward(const GradArgs& g, cudaStream_t stream) {
-    if (g.s.threads > 512) return launch_backward_rows<TS, TB, 1, 1024>(g, stream);
-    return launch_backward_rows<TS, TB, GT, 512>(g, stream);
+    if (g.a.y == nullptr || g.a.y_norm == BSS_NORM_NONE) return launch_backward_mode<TS, TB, PLAIN>(g, stream);
+    if (g.a.dh != nullptr && g.a.norm == BSS_NORM_RMS && g.a.y_norm == BSS_NORM_RMS)
+        return launch_backward_mode<TS, TB, RMS2>(g, stream);
+    return launch_backward_mode<TS, TB, BOTH>(g, stream);
 }
 
 bss_status check_grads(const bss_residual_norm_grads* args) {
