@@ -20,6 +20,7 @@
 // slots of shared memory (cp.async) while it works on this one, so loads stay in
 // flight without holding registers.
 #include <cstring>
+#include <type_traits>
 
 #include "bss_rows.cuh"
 
@@ -27,6 +28,7 @@ namespace bss {
 namespace {
 
 constexpr int kMaxChannels = 8192;
+constexpr int64_t kMaxStride = int64_t(1) << 28;  // elements between rows: a row's offset is one 32 x 32 bit product
 constexpr int kMinChunkRows = 16;  // rows a block of the backward pass reduces at least
 
 // ---------------------------------------------------------------- shared memory
@@ -118,6 +120,17 @@ __device__ __forceinline__ void store_vector(T* to, const V8& v, bool live0, boo
     }
 }
 
+template <typename T>
+__device__ __forceinline__ T* at_row(T* base, uint32_t row, uint32_t stride_bytes) {
+    using Byte = std::conditional_t<std::is_const_v<T>, const char, char>;
+    return reinterpret_cast<T*>(reinterpret_cast<Byte*>(base) + static_cast<uint64_t>(row) * stride_bytes);
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t bytes_of(int64_t stride) {
+    return static_cast<uint32_t>(stride * static_cast<int64_t>(sizeof(T)));
+}
+
 __device__ __forceinline__ V8 zeros() { return floats_of(make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)); }
 
 // Zeros in the half that lies past the row.
@@ -178,6 +191,7 @@ struct ForwardArgs {
     int32_t folds;          // how many of them there are
     int64_t groups;         // of rows that share them
     int64_t chunks, chunk_rows;
+    FastDiv by_rows;        // rows of a group
 };
 
 __device__ __forceinline__ V8 fold(const bss_residual_norm_args& a, int which, int64_t group, int c0, int c1) {
@@ -229,13 +243,15 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
     const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
     const int C = a.channels;
     const float inv = 1.0f / C;
-    const int64_t first_group = blockIdx.x / g.chunks, chunk = blockIdx.x - first_group * g.chunks;
+    const int64_t first_group = blockIdx.x / static_cast<uint32_t>(g.chunks), chunk = blockIdx.x - first_group * g.chunks;
     const int64_t group_rows = STAGED ? a.rows_per_group : a.rows;
-    int64_t row = first_group * group_rows + chunk * g.chunk_rows;
-    int64_t last = row + g.chunk_rows;
-    if (last > (first_group + 1) * group_rows) last = (first_group + 1) * group_rows;
-    if (last > a.rows) last = a.rows;
-    row += threadIdx.x / 32 / W;
+    const int64_t begin = first_group * group_rows + chunk * g.chunk_rows;
+    int64_t end = begin + g.chunk_rows;
+    if (end > (first_group + 1) * group_rows) end = (first_group + 1) * group_rows;
+    if (end > a.rows) end = a.rows;
+    const uint32_t last = static_cast<uint32_t>(end);
+    uint32_t row = static_cast<uint32_t>(begin) + threadIdx.x / 32 / W;
+    const uint32_t r_bytes = bytes_of<TS>(a.r_stride), h_bytes = bytes_of<TB>(a.h_stride);
 
     // channels of vector i: c0 + i * 256 W and c1 + i * 256 W, four each
     const int c0 = channel_at<kSplit>(warp, 0), c1 = channel_at<kSplit>(warp, 1);
@@ -243,8 +259,8 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
     auto live1 = [&](int i) { return (kSplit ? c1 : c0) + i * 256 * W < C; };
     const uint32_t base = smem_u32(folded);
     const uint32_t slots = base + (STAGED ? g.folds * C * 4 : 0) + (threadIdx.x >> 5) * 2 * kStage;
-    const TS* x = static_cast<const TS*>(a.x) + row * a.x_stride + c0;
-    const TB* y = static_cast<const TB*>(a.y) + row * a.y_stride + c0;
+    const TS* x = at_row(static_cast<const TS*>(a.x), row, bytes_of<TS>(a.x_stride)) + c0;
+    const TB* y = at_row(static_cast<const TB*>(a.y), row, bytes_of<TB>(a.y_stride)) + c0;
     auto fetch = [&](bool exists, uint32_t to) {
         if (exists) {
 #pragma unroll
@@ -289,9 +305,9 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
     uint32_t now = slots, other = slots + kStage;
     int parity = 0;
     for (; row < last; row += kRows, parity ^= 1) {
-        fetch(row + kRows < last, other);
+        fetch(last - row > kRows, other);
         cp_async_wait_group<1>();
-        const int64_t group = STAGED ? first_group : row / a.rows_per_group;
+        const int64_t group = STAGED ? first_group : g.by_rows.div(row);
         V8 r[VPT];
         float ym = 0.0f, yrstd = 1.0f;
         if (a.y != nullptr && a.y_norm != BSS_NORM_NONE) {
@@ -316,7 +332,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
             }
             yrstd = rsqrtf(row_sum<W>(s, buf[parity][1]) * inv + a.eps);
             if (a.y_stats != nullptr && lane == 0 && warp == 0)
-                *reinterpret_cast<float2*>(a.y_stats + 2 * row) = make_float2(ym, yrstd);
+                *reinterpret_cast<float2*>(a.y_stats + 2 * static_cast<int64_t>(row)) = make_float2(ym, yrstd);
         }
         float s = 0.0f;
 #pragma unroll
@@ -330,7 +346,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
                 if (g.folded.has[0]) t = mul(t, folded_of(0, group, i));
                 r[i] = fma8(r[i], a.residual_scale, t);
                 if (a.r != nullptr)
-                    store_vector<TS, kSplit>(static_cast<TS*>(a.r) + row * a.r_stride + c0 + i * 256 * W, r[i], true, live1(i));
+                    store_vector<TS, kSplit>(at_row(static_cast<TS*>(a.r), row, r_bytes) + c0 + i * 256 * W, r[i], true, live1(i));
             }
             keep_live(r[i], true, live1(i));
             s += sum8(r[i]);
@@ -351,7 +367,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
             }
             rstd = rsqrtf(row_sum<W>(s, buf[parity][3]) * inv + a.eps);
             if (a.stats != nullptr && lane == 0 && warp == 0)
-                *reinterpret_cast<float2*>(a.stats + 2 * row) = make_float2(mean, rstd);
+                *reinterpret_cast<float2*>(a.stats + 2 * static_cast<int64_t>(row)) = make_float2(mean, rstd);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -359,7 +375,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128) norm_forward_kernel(cons
             V8 n = mul(r[i], rstd);
             if (g.folded.has[1]) n = mul(n, folded_of(1, group, i));
             if (g.folded.has[2]) n = add8(n, folded_of(2, group, i));
-            store_vector<TB, kSplit>(static_cast<TB*>(a.h) + row * a.h_stride + c0 + i * 256 * W, n, true, live1(i));
+            store_vector<TB, kSplit>(at_row(static_cast<TB*>(a.h), row, h_bytes) + c0 + i * 256 * W, n, true, live1(i));
         }
     }
     cp_async_wait_group<0>();
@@ -431,11 +447,16 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
     const int c1 = whole ? channel_at<kSplit>(warp, 1) : c;
     const int idx = threadIdx.x, lanes = blockDim.x;
     const float inv = 1.0f / a.channels;
-    const int64_t group = blockIdx.x / g.s.chunks, chunk = blockIdx.x - group * g.s.chunks;
-    const int64_t first = group * a.rows_per_group + chunk * g.s.chunk_rows;
-    int64_t last = first + g.s.chunk_rows;
-    if (last > (group + 1) * a.rows_per_group) last = (group + 1) * a.rows_per_group;
-    if (last > a.rows) last = a.rows;
+    const int64_t group = blockIdx.x / static_cast<uint32_t>(g.s.chunks), chunk = blockIdx.x - group * g.s.chunks;
+    const int64_t begin = group * a.rows_per_group + chunk * g.s.chunk_rows;
+    int64_t end = begin + g.s.chunk_rows;
+    if (end > (group + 1) * a.rows_per_group) end = (group + 1) * a.rows_per_group;
+    if (end > a.rows) end = a.rows;
+    // a chunk past its group's rows is empty
+    const uint32_t first = static_cast<uint32_t>(begin < end ? begin : end), last = static_cast<uint32_t>(end);
+    const uint32_t r_bytes = bytes_of<TS>(a.r_stride), dr_bytes = bytes_of<TS>(a.dr_stride);
+    const uint32_t dh_bytes = bytes_of<TB>(a.dh_stride), y_bytes = bytes_of<TB>(a.y_stride);
+    const uint32_t dx_bytes = bytes_of<TS>(a.dx_stride), dy_bytes = bytes_of<TB>(a.dy_stride);
     const bool stats = a.dh != nullptr && a.norm != BSS_NORM_NONE;
     constexpr bool ystats = MODE != PLAIN;
 
@@ -446,31 +467,31 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
     const TS* dr_in = static_cast<const TS*>(a.dr) + c;
     const TB* dh_in = static_cast<const TB*>(a.dh) + c;
     const TB* y_in = static_cast<const TB*>(a.y) + c;
-    auto fetch = [&](int64_t row0, uint32_t to) {
+    auto fetch = [&](uint32_t row0, uint32_t to) {
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            const int64_t row = row0 + t;
+            const uint32_t row = row0 + t;
             if (!active || row >= last) continue;
             const uint32_t at = to + t * (kPieces / T) * apart;
             if (a.dh != nullptr) {
-                fetch_vector<TS, kSplit>(at, idx, lanes, r_in + row * a.r_stride, true, whole);
-                fetch_vector<TB, kSplit>(at + (2 * kS) * apart, idx, lanes, dh_in + row * a.dh_stride, true, whole);
+                fetch_vector<TS, kSplit>(at, idx, lanes, at_row(r_in, row, r_bytes), true, whole);
+                fetch_vector<TB, kSplit>(at + (2 * kS) * apart, idx, lanes, at_row(dh_in, row, dh_bytes), true, whole);
             }
             if (a.dr != nullptr)
-                fetch_vector<TS, kSplit>(at + kS * apart, idx, lanes, dr_in + row * a.dr_stride, true, whole);
+                fetch_vector<TS, kSplit>(at + kS * apart, idx, lanes, at_row(dr_in, row, dr_bytes), true, whole);
             if (a.y != nullptr)
-                fetch_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes, y_in + row * a.y_stride, true, whole);
+                fetch_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes, at_row(y_in, row, y_bytes), true, whole);
             const uint32_t st = at + (2 * kS + 2 * kB) * apart + idx * 16;
             if (stats)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st), "l"(a.stats + 2 * row) : "memory");
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st), "l"(at_row(a.stats, row, 8)) : "memory");
             if (ystats)
-                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + 8), "l"(a.y_stats + 2 * row)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(st + 8), "l"(at_row(a.y_stats, row, 8))
                              : "memory");
         }
         cp_async_commit();
     };
-    const int64_t step = g.s.side * T;
-    int64_t mine = first + side * T;
+    const uint32_t step = g.s.side * T;
+    uint32_t mine = first + side * T;
     const bool ahead = g.s.stages > 1;  // the widest float rows have room for one stage only
     if (ahead) fetch(mine, slots);
 
@@ -489,7 +510,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
     }
     V8 sa = zeros(), sb = zeros(), sc = zeros();
     int stage = 0, turn = 0;
-    for (int64_t row0 = first; row0 < last; row0 += step, mine += step, turn ^= 2) {
+    for (uint32_t row0 = first; row0 < last; row0 += step, mine += step, turn ^= 2) {
         if (ahead) {
             fetch(mine + step, slots + (stage ^ 1) * kPieces * apart);
             cp_async_wait_group<1>();
@@ -499,7 +520,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
         }
         const uint32_t now = slots + stage * kPieces * apart;
         stage ^= ahead ? 1 : 0;
-        V8 xh[T], tt[T];
+        V8 xh[T], w[T];  // the normed stream; dr + rstd t
         float2 st[T], yst[T];
         constexpr int NV = MODE == RMS2 ? 4 : 2;
         float sums[NV * T];
@@ -507,32 +528,31 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
         for (int t = 0; t < T; ++t) {
             const uint32_t at = now + t * (kPieces / T) * apart;
             const bool live = active && mine + t < last;
-            xh[t] = tt[t] = zeros();
+            xh[t] = w[t] = zeros();
             st[t] = yst[t] = make_float2(0.0f, 1.0f);
-            if (live) {
-                const uint4 q = lds128(at + (2 * kS + 2 * kB) * apart + idx * 16);
-                if (stats) st[t] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
-                if (ystats) yst[t] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
-            }
-            if (live && a.dh != nullptr) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) sums[NV * t + k] = 0.0f;
+            if (!live) continue;
+            const uint4 q = lds128(at + (2 * kS + 2 * kB) * apart + idx * 16);
+            if (stats) st[t] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+            if (ystats) yst[t] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
+            if (a.dr != nullptr) w[t] = lds_vector<TS, kSplit>(at + kS * apart, idx, lanes);
+            if (a.dh != nullptr) {
                 xh[t] = mul(add8(lds_vector<TS, kSplit>(at, idx, lanes), -st[t].x), st[t].y);
                 V8 dh = lds_vector<TB, kSplit>(at + (2 * kS) * apart, idx, lanes);
                 if (kSplit) keep_live(xh[t], true, whole), keep_live(dh, true, whole);
-                tt[t] = mul(dh, m1);
+                const V8 tt = mul(dh, m1);
                 sa = fma8(dh, xh[t], sa);
                 sb = add8(sb, dh);
+                w[t] = fma8(tt, st[t].y, w[t]);
+                if (MODE != RMS2) sums[NV * t] = sum8(tt);
+                sums[NV * t + 1] = dot(tt, xh[t]);
             }
-            sums[NV * t] = MODE == RMS2 ? 0.0f : sum8(tt[t]);
-            sums[NV * t + 1] = dot(tt[t], xh[t]);
+            if (kSplit) keep_live(w[t], true, whole);
             if constexpr (MODE == RMS2) {
-                sums[NV * t + 2] = sums[NV * t + 3] = 0.0f;
-                if (!live) continue;
-                V8 w = zeros();
-                if (a.dr != nullptr) w = lds_vector<TS, kSplit>(at + kS * apart, idx, lanes);
-                w = fma8(tt[t], st[t].y, w);
                 V8 f = mul(mul(lds_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes), yst[t].y), m2);
-                if (kSplit) keep_live(w, true, whole), keep_live(f, true, whole);
-                sums[NV * t + 2] = dot(f, w);
+                if (kSplit) keep_live(f, true, whole);
+                sums[NV * t + 2] = dot(f, w[t]);
                 sums[NV * t + 3] = dot(f, xh[t]);
             }
         }
@@ -545,11 +565,10 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             const bool live = active && mine + t < last;
             const float mean1 = a.norm == BSS_NORM_LAYER ? sums[NV * t] * inv : 0.0f;
             const float mean2 = a.norm != BSS_NORM_NONE ? sums[NV * t + 1] * inv : 0.0f;
-            V8 u = zeros();
-            if (live && a.dr != nullptr) u = lds_vector<TS, kSplit>(at + kS * apart, idx, lanes);
-            u = fma8(fma8(xh[t], -mean2, add8(tt[t], -mean1)), st[t].y, u);
+            V8 u = fma8(xh[t], -st[t].y * mean2, w[t]);
+            if (a.norm == BSS_NORM_LAYER) u = add8(u, -st[t].y * mean1);
             if (live)
-                store_vector<TS, kSplit>(static_cast<TS*>(a.dx) + (mine + t) * a.dx_stride + c, mul(u, a.residual_scale), true,
+                store_vector<TS, kSplit>(at_row(static_cast<TS*>(a.dx) + c, mine + t, dx_bytes), mul(u, a.residual_scale), true,
                                          whole);
             z[t] = zeros();
             zs[2 * t] = zs[2 * t + 1] = 0.0f;
@@ -564,7 +583,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             } else {
                 if constexpr (MODE == RMS2)
                     z[t] = mul(fma8(yh, -inv * (sums[NV * t + 2] - st[t].y * mean2 * sums[NV * t + 3]), z[t]), yst[t].y);
-                store_vector<TB, kSplit>(static_cast<TB*>(a.dy) + (mine + t) * a.dy_stride + c, z[t], true, whole);
+                store_vector<TB, kSplit>(at_row(static_cast<TB*>(a.dy) + c, mine + t, dy_bytes), z[t], true, whole);
             }
         }
         if constexpr (MODE != BOTH) continue;
@@ -578,7 +597,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
                 const V8 yh = mul(add8(lds_vector<TB, kSplit>(at + (2 * kS + kB) * apart, idx, lanes), -yst[t].x), yst[t].y);
                 z[t] = mul(fma8(yh, -zs[2 * t + 1] * inv, add8(z[t], -mean1)), yst[t].y);
             }
-            store_vector<TB, kSplit>(static_cast<TB*>(a.dy) + (mine + t) * a.dy_stride + c, z[t], true, whole);
+            store_vector<TB, kSplit>(at_row(static_cast<TB*>(a.dy) + c, mine + t, dy_bytes), z[t], true, whole);
         }
     }
     cp_async_wait_group<0>();
@@ -701,8 +720,8 @@ bss_status check_rows(const void* p, const char* name, int64_t rows, int64_t str
                       bool output, Region* r) {
     if (p == nullptr) return BSS_OK;
     if (!is_aligned(p, 16)) return set_error(BSS_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
-    if (rows > 1 && (stride % 8 != 0 || stride < 0 || stride > (int64_t(1) << 31)))
-        return set_error(BSS_ERR_INVALID_ARG, "%s: the row stride must be a multiple of 8 elements, 0 .. 2^31", name);
+    if (rows > 1 && (stride % 8 != 0 || stride < 0 || stride > kMaxStride))
+        return set_error(BSS_ERR_INVALID_ARG, "%s: the row stride must be a multiple of 8 elements, 0 .. 2^28", name);
     *r = region_2d(p, rows, stride, channels, esize(dtype));
     if (output && r->self_overlap) return set_error(BSS_ERR_INVALID_ARG, "%s: rows overlap", name);
     return BSS_OK;
@@ -784,6 +803,7 @@ bss_status forward_of(const bss_residual_norm_args& a, cudaStream_t stream) {
     if (g.a.rows_per_group > a.rows) g.a.rows_per_group = a.rows;
     // nothing that differs between groups: one group holds the rows
     if (a.gate == nullptr && a.scale == nullptr && a.shift == nullptr) g.a.rows_per_group = a.rows;
+    g.by_rows = FastDiv(static_cast<uint32_t>(g.a.rows_per_group));
     g.folded.has[0] = a.gate != nullptr || a.y_weight != nullptr;
     g.folded.has[1] = a.scale != nullptr || a.weight != nullptr;
     g.folded.has[2] = a.shift != nullptr || a.bias != nullptr;

@@ -201,8 +201,8 @@ enum {
  *               1 / deviation) of norm and y_norm (mean 0 for RMS), which the
  *               backward pass reads.
  * (stream_dtype, branch_dtype): (BF16, BF16), (F32, BF16) or (F32, F32).
- * Tensors are 16-byte aligned and their strides multiples of 8 elements; stats
- * are 8-byte aligned. */
+ * Tensors are 16-byte aligned, their strides multiples of 8 elements of at most
+ * 2^28; stats are 8-byte aligned. */
 typedef struct {
     int64_t rows;
     int64_t rows_per_group;
