@@ -32,6 +32,7 @@ namespace bss {
 namespace {
 
 constexpr int kMaxTokenWidth = 8192;  // H * head_dim of the norm over a token
+constexpr int64_t kMaxTokenStride = int64_t(1) << 28;  // elements: a token's offset is one 32 x 32 bit product
 
 struct RotaryDev {
     const float2* table[3];
@@ -44,8 +45,8 @@ struct HeadsArgs {
     const __nv_bfloat16* in[3];   // token-major q, k, v (forward), head-major dQh, dKh, dVh (backward)
     __nv_bfloat16* out[3];        // head-major (forward), token-major (backward)
     const __nv_bfloat16* x[2];    // backward: token-major q, k
-    int64_t ts[3], hs[3];         // strides of the token-major tensors in / out
-    int64_t xts[2], xhs[2];       // strides of x
+    uint32_t ts[3], xts[2];       // bytes from token to token of the token-major tensors: in / out, x
+    int64_t hs[3], xhs[2];        // elements from head to head
     const void* weight[2];
     int32_t weight_dtype;
     float eps, inv_width;         // 1 / channels of the norm's mean
@@ -294,24 +295,33 @@ __device__ __forceinline__ void stage_weights(const HeadsArgs& a, uint32_t at) {
                          weights_of<EO>(a.weight[i], static_cast<int64_t>(e) * 8, a.weight_dtype));
 }
 
-// A warp's slots: two stages of [tensor][VPT][32 lanes] pieces and the angles.
-// Those of pieces that do not exist hold zeros throughout.
+// A warp's slots: stages of [tensor][VPT][32 lanes] pieces and the angles.  Those
+// of pieces that do not exist hold zeros throughout.
 __host__ __device__ constexpr uint32_t stage_bytes(int tensors, int vpt, bool halves) {
     return tensors * vpt * 512 + (halves ? 2048 : 1024);
 }
 
-template <int TENSORS, int VPT, bool HALVES>
+template <int TENSORS, int VPT, bool HALVES, int STAGES>
 __device__ __forceinline__ uint32_t slots_of(uint32_t at, int count) {
     constexpr uint32_t kStage = stage_bytes(TENSORS, VPT, HALVES);
-    at += (threadIdx.x >> 5) * 2 * kStage + (threadIdx.x & 31) * 16;
-    for (int e = 0; e < 2 * TENSORS * VPT; ++e)
-        if (e % VPT >= count) sts128(at + e / (TENSORS * VPT) * kStage + e % (TENSORS * VPT) * 512, make_uint4(0, 0, 0, 0));
+    constexpr int kPieces = TENSORS * VPT;
+    at += (threadIdx.x >> 5) * STAGES * kStage + (threadIdx.x & 31) * 16;
+    for (int e = 0; e < STAGES * kPieces; ++e)
+        if (e % VPT >= count) sts128(at + e / kPieces * kStage + e % kPieces * 512, make_uint4(0, 0, 0, 0));
     return at;
 }
 
 // Blocks of 4 warps an SM shall hold at least, by the registers a thread needs.
 __host__ __device__ constexpr int forward_blocks(int vpt) { return vpt <= 2 ? 4 : 3; }
-__host__ __device__ constexpr int backward_blocks(int vpt) { return vpt <= 2 ? 4 : 3; }
+
+// The backward pass's block: warps, tokens a lane's pieces are fetched ahead plus
+// one, and how many blocks an SM shall hold.
+__host__ __device__ constexpr int backward_warps(int W) { return W <= 2 ? 4 : W; }
+__host__ __device__ constexpr int backward_stages(bool token, int vpt) { return token && vpt == 1 ? 3 : 2; }
+__host__ __device__ constexpr int backward_tensors(int norm) { return norm == BSS_HEAD_NORM_NONE ? 3 : 5; }
+__host__ __device__ constexpr int backward_blocks(int W, int vpt) {
+    return vpt > 2 && W == 8 ? 1 : vpt > 2 ? 12 / backward_warps(W) : 16 / backward_warps(W);
+}
 
 // W warps share a token, a lane holds up to VPT pieces of a tensor.
 template <bool HALVES, int NORM, int W, int VPT>
@@ -327,18 +337,17 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
     const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
     const uint32_t base = smem_u32(planes);
     const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
-    const uint32_t slots = slots_of<2, VPT, HALVES>(base + (NORM == BSS_HEAD_NORM_TOKEN ? 4 * all16 : 0), me.count);
+    const uint32_t slots = slots_of<2, VPT, HALVES, 2>(base + (NORM == BSS_HEAD_NORM_TOKEN ? 4 * all16 : 0), me.count);
     constexpr uint32_t step = kTokens;
     uint32_t n = blockIdx.x * a.span + group;
     const uint32_t end = a.N - blockIdx.x * a.span > a.span ? (blockIdx.x + 1) * a.span : a.N;
-    // running addresses of the token to fetch, and the steps to the next piece and token
+    // the lane's first piece in token 0, and the step to its next piece
     const char* src[3];
-    int64_t apart[3], ahead[3];
+    int64_t apart[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        src[i] = reinterpret_cast<const char*>(a.in[i] + n * a.ts[i] + me.head0 * a.hs[i] + me.piece * 8);
+        src[i] = reinterpret_cast<const char*>(a.in[i] + me.head0 * a.hs[i] + me.piece * 8);
         apart[i] = me.step * a.hs[i] * 2;
-        ahead[i] = step * a.ts[i] * 2;
     }
     const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 8;  // from a lane's slots to its angles
     if (rotary) clear_turn<HALVES>(pr, slots + turn_at), clear_turn<HALVES>(pr, slots + kStage + turn_at);
@@ -351,11 +360,10 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (a.in[i] == nullptr) continue;
-                const char* p = src[i];
+                const char* p = src[i] + static_cast<uint64_t>(m) * a.ts[i];
 #pragma unroll
                 for (int j = 0; j < VPT; ++j, p += apart[i])
                     if (j < me.count) cp_async_16(to + (i * VPT + j) * 512, p);
-                src[i] += ahead[i];
             }
         }
         cp_async_commit();
@@ -379,11 +387,10 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
         const uint32_t temporal_row = next_row;
         uint4 v_raw[VPT];  // V goes straight through, its loads under Q and K's arithmetic
         if (a.in[2] != nullptr) {
-            const char* p = src[2];
+            const char* p = src[2] + static_cast<uint64_t>(n) * a.ts[2];
 #pragma unroll
             for (int j = 0; j < VPT; ++j, p += apart[2])
                 if (j < me.count) v_raw[j] = ld_row(p);
-            src[2] += ahead[2];
         }
         fetch(n + step, end - n > step, other);
         cp_async_wait_group<1>();
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
 #pragma unroll
         for (int j = 0; j < VPT; ++j, at += head_step) {
             const bool live = j < me.count;
-            const int64_t to = at + static_cast<int64_t>(me.temporal >> j & 1u ? temporal_row : n) * row_bytes;
+            const int64_t to = at + static_cast<uint64_t>(me.temporal >> j & 1u ? temporal_row : n) * row_bytes;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (a.in[i] == nullptr) continue;
@@ -427,15 +434,16 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
     cp_async_wait_group<0>();
 }
 
-// The norm over a token: W warps share one.  Its weight gradients stay in the
-// registers of the lane that holds the piece; those of a norm over a head too.
+// The norm over a token: W warps share one, each lane one piece of a tensor where
+// it can (VPT = 1, up to 8 warps: the piece's weights, weight gradients and both
+// passes' values stay in registers); wider tokens take several pieces a lane and 8
+// warps.  Otherwise one warp a token.
 template <bool HALVES, int NORM, int W, int VPT>
-__global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blocks(VPT))
+__global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT))
     heads_backward_kernel(const __grid_constant__ HeadsArgs a) {
-    constexpr bool kToken = NORM == BSS_HEAD_NORM_TOKEN;
-    constexpr bool kStaged = kToken && W < 8;  // the widest tokens' weights do not fit beside their slots
-    constexpr int kWarps = W > 4 ? W : 4, kTokens = kWarps / W;
-    constexpr int kTensors = NORM == BSS_HEAD_NORM_NONE ? 2 : 4;  // dQ, dK, q, k
+    constexpr bool kToken = NORM == BSS_HEAD_NORM_TOKEN, kOne = kToken && VPT == 1;
+    constexpr int kWarps = backward_warps(W), kTokens = kWarps / W;
+    constexpr int kTensors = backward_tensors(NORM), kStages = backward_stages(kToken, VPT);  // dQ, dK, dV, q, k
     constexpr uint32_t kStage = stage_bytes(kTensors, VPT, HALVES), kTurn = kTensors * VPT * 512;
     extern __shared__ __align__(16) float4 planes[];
     __shared__ float4 buf4[2][kWarps];
@@ -447,7 +455,7 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
     const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
     const uint32_t base = smem_u32(planes);
     const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
-    const uint32_t slots = slots_of<kTensors, VPT, HALVES>(base + (kStaged ? 4 * all16 : 0), me.count);
+    const uint32_t slots = slots_of<kTensors, VPT, HALVES, kStages>(base, me.count);
     constexpr uint32_t step = kTokens;
     uint32_t n = blockIdx.x * a.span + group;
     const uint32_t end = a.N - blockIdx.x * a.span > a.span ? (blockIdx.x + 1) * a.span : a.N;
@@ -456,20 +464,19 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
     const int64_t grad0 = me.head0 * head_bytes + me.piece * 16;
     const char* src[2];
     char* dst[3];
-    int64_t xapart[2], xahead[2], apart[3], ahead[3];
+    int64_t xapart[2], apart[3];
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-        dst[i] = reinterpret_cast<char*>(a.out[i] + n * a.ts[i] + me.head0 * a.hs[i] + me.piece * 8);
+        dst[i] = reinterpret_cast<char*>(a.out[i] + me.head0 * a.hs[i] + me.piece * 8);
         apart[i] = me.step * a.hs[i] * 2;
-        ahead[i] = step * a.ts[i] * 2;
         if (i < 2) {
-            src[i] = reinterpret_cast<const char*>(a.x[i] + n * a.xts[i] + me.head0 * a.xhs[i] + me.piece * 8);
+            src[i] = reinterpret_cast<const char*>(a.x[i] + me.head0 * a.xhs[i] + me.piece * 8);
             xapart[i] = me.step * a.xhs[i] * 2;
-            xahead[i] = step * a.xts[i] * 2;
         }
     }
     const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 8;  // from a lane's slots to its angles
-    if (rotary) clear_turn<HALVES>(pr, slots + turn_at), clear_turn<HALVES>(pr, slots + kStage + turn_at);
+    if (rotary)
+        for (int k = 0; k < kStages; ++k) clear_turn<HALVES>(pr, slots + k * kStage + turn_at);
     auto fetch = [&](uint32_t m, bool exists, uint32_t to) {
         if (exists) {
             const Token tok = token_of(a, m);
@@ -477,10 +484,10 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
             int64_t at = grad0;
 #pragma unroll
             for (int j = 0; j < VPT; ++j, at += head_step) {
-                const int64_t from = at + static_cast<int64_t>(me.temporal >> j & 1u ? tok.temporal_row : m) * row_bytes;
+                const int64_t from = at + static_cast<uint64_t>(me.temporal >> j & 1u ? tok.temporal_row : m) * row_bytes;
                 if (j < me.count)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int i = 0; i < 3; ++i)
                         if (a.in[i] != nullptr)
                             cp_async_16(to + (i * VPT + j) * 512, reinterpret_cast<const char*>(a.in[i]) + from);
             }
@@ -488,51 +495,41 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     if (a.in[i] == nullptr) continue;
-                    const char* p = src[i];
+                    const char* p = src[i] + static_cast<uint64_t>(m) * a.xts[i];
 #pragma unroll
                     for (int j = 0; j < VPT; ++j, p += xapart[i])
-                        if (j < me.count) cp_async_16(to + ((2 + i) * VPT + j) * 512, p);
-                    src[i] += xahead[i];
+                        if (j < me.count) cp_async_16(to + ((3 + i) * VPT + j) * 512, p);
                 }
         }
         cp_async_commit();
     };
-    fetch(n, n < end, slots);
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) fetch(n + k * step, n < end && end - n > k * step, slots + k * kStage);
     constexpr int kHeld = kToken ? VPT : 1;
+    constexpr bool kInRegisters = NORM == BSS_HEAD_NORM_HEAD || kOne;  // the weights
     V8 w[2], dw[2][kHeld];
-    if (kStaged) {
-        stage_weights<!HALVES>(a, base);
-        __syncthreads();
-    }
+    // elsewhere they are read again for every token (from L1: beside the slots of a
+    // wide token there is no shared memory for them)
     auto weight = [&](int i, int j) {
-        if (kStaged) return planes_load(weights + i * 2 * all16 + j * (W * 512), all16);
-        return weights_of<!HALVES>(a.weight[i], static_cast<int64_t>(me.head0 + j * me.step) * (a.pieces * 8) + me.piece * 8,
-                                   a.weight_dtype);
+        return weights_of<!HALVES>(
+            a.weight[i], kToken ? static_cast<int64_t>(me.head0 + j * me.step) * (a.pieces * 8) + me.piece * 8 : me.piece * 8,
+            a.weight_dtype);
     };
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        if (NORM == BSS_HEAD_NORM_HEAD) w[i] = weights_of<!HALVES>(a.weight[i], me.piece * 8, a.weight_dtype);
+        if (kInRegisters) w[i] = kToken && me.count == 0 ? unpack_bf16<!HALVES>(make_uint4(0, 0, 0, 0)) : weight(i, 0);
 #pragma unroll
         for (int j = 0; j < kHeld; ++j) dw[i][j] = unpack_bf16<!HALVES>(make_uint4(0, 0, 0, 0));
     }
-    uint32_t now = slots, other = slots + kStage;
+    uint32_t now = slots, ahead_at = slots + (kStages - 1) * kStage;
     int turn_buf = 0;
     for (; n < end; n += step, turn_buf ^= 1) {
-        uint4 v_raw[VPT];  // dV goes straight through, its loads under the others' arithmetic
-        if (a.in[2] != nullptr) {
-            const uint32_t temporal_row = token_of(a, n).temporal_row;
-            int64_t at = grad0;
-#pragma unroll
-            for (int j = 0; j < VPT; ++j, at += head_step)
-                if (j < me.count)
-                    v_raw[j] = ld_row(reinterpret_cast<const char*>(a.in[2]) + at +
-                                      static_cast<int64_t>(me.temporal >> j & 1u ? temporal_row : n) * row_bytes);
-        }
-        fetch(n + step, end - n > step, other);
-        cp_async_wait_group<1>();
+        fetch(n + (kStages - 1) * step, end - n > (kStages - 1) * step, ahead_at);
+        cp_async_wait_group<kStages - 1>();
         Turn<HALVES> turn;
         if (rotary) turn = read_turn<HALVES>(now + turn_at);
         float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // x^2 and g w x of Q, then of K
+        V8 gv[2], xv[2];                           // of one piece, for both passes
         if (kToken) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -541,56 +538,60 @@ __global__ void __launch_bounds__(W > 4 ? 32 * W : 128, W > 4 ? 1 : backward_blo
                 for (int j = 0; j < VPT; ++j) {
                     V8 v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
                     if (rotary) rotate8<HALVES, true>(v, turn, pr);
-                    if (j >= me.count) continue;
-                    const V8 x = unpack_bf16<!HALVES>(lds128(now + ((2 + i) * VPT + j) * 512));
+                    if (!kOne && j >= me.count) continue;
+                    const V8 x = unpack_bf16<!HALVES>(lds128(now + ((3 + i) * VPT + j) * 512));
                     sums[2 * i] += dot(x, x);
-                    sums[2 * i + 1] += dot(mul(v, weight(i, j)), x);
+                    sums[2 * i + 1] += dot(mul(v, kOne ? w[i] : weight(i, j)), x);
+                    if (kOne) gv[i] = v, xv[i] = x;
                 }
             }
             token_sum<4, W>(sums, reinterpret_cast<float*>(buf4[turn_buf] + W * group), group, warp);
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 3; ++i) {
             if (a.in[i] == nullptr) continue;
-            char* to = dst[i];
-            dst[i] += ahead[i];
+            char* to = dst[i] + static_cast<uint64_t>(n) * a.ts[i];
+            const int k = i < 2 ? i : 0;
             float r = 0.0f, m = 0.0f;
-            if (kToken) {
-                r = rsqrtf(sums[2 * i] * a.inv_width + a.eps);
-                m = -r * r * (sums[2 * i + 1] * a.inv_width);
+            if (kToken && i < 2) {
+                r = rsqrtf(sums[2 * k] * a.inv_width + a.eps);
+                m = -r * r * (sums[2 * k + 1] * a.inv_width);
             }
 #pragma unroll
             for (int j = 0; j < VPT; ++j, to += apart[i]) {
                 const bool live = j < me.count;
-                V8 v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
-                if (rotary) rotate8<HALVES, true>(v, turn, pr);
+                if (i == 2) {
+                    if (live) st_row(to, lds128(now + (i * VPT + j) * 512));
+                    continue;
+                }
+                V8 v;
+                if (kOne) {
+                    v = gv[k];
+                } else {
+                    v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
+                    if (rotary) rotate8<HALVES, true>(v, turn, pr);
+                }
                 if (NORM != BSS_HEAD_NORM_NONE) {
-                    const V8 x = unpack_bf16<!HALVES>(lds128(now + ((2 + i) * VPT + j) * 512));
+                    const V8 x = kOne ? xv[k] : unpack_bf16<!HALVES>(lds128(now + ((3 + k) * VPT + j) * 512));
                     V8 gw = v;
-                    if (kToken) {
-                        if (live) gw = mul(v, weight(i, j));
-                    } else {
-                        gw = mul(v, w[i]);
+                    if (kInRegisters)
+                        gw = mul(v, w[k]);
+                    else if (live)
+                        gw = mul(v, weight(k, j));
+                    if (!kToken) {
                         r = rsqrtf(head_sum(dot(x, x), a.pieces) * a.inv_width + a.eps);
                         m = -r * r * (head_sum(dot(gw, x), a.pieces) * a.inv_width);
                     }
                     const V8 xr = mul(x, r);
-                    V8& d = dw[i][kToken ? j : 0];
+                    V8& d = dw[k][kToken ? j : 0];
                     d = fma8(v, xr, d);  // zeros where there is no piece
                     v = fma8(xr, m, mul(gw, r));
                 }
                 if (live) st_row(to, pack_bf16<!HALVES>(v));
             }
         }
-        if (a.in[2] != nullptr) {
-            char* to = dst[2];
-            dst[2] += ahead[2];
-#pragma unroll
-            for (int j = 0; j < VPT; ++j, to += apart[2])
-                if (j < me.count) st_row(to, v_raw[j]);
-        }
-        const uint32_t t = now;
-        now = other, other = t;
+        now = now == slots + (kStages - 1) * kStage ? slots : now + kStage;
+        ahead_at = ahead_at == slots + (kStages - 1) * kStage ? slots : ahead_at + kStage;
     }
     cp_async_wait_group<0>();
     if (NORM == BSS_HEAD_NORM_NONE || a.partial == nullptr) return;
@@ -678,10 +679,10 @@ struct Shape {
 };
 
 // Warps that share a token under the norm over a token.  Forward: one up to 2048
-// channels.  Backward: as many as leave a lane at most 3 pieces (4 of the widest).
+// channels.  Backward: one for each warp-wide row of pieces, up to 8.
 int warps_of(bool backward, int chunks) {
     if (!backward) return chunks <= 8 ? 1 : 4;
-    return chunks <= 3 ? 1 : chunks <= 6 ? 2 : chunks <= 12 ? 4 : 8;
+    return chunks <= 6 ? chunks : 8;
 }
 
 Shape shape_of(int32_t H, int pieces, int32_t norm, bool halves, uint32_t N, bool backward) {
@@ -691,18 +692,19 @@ Shape shape_of(int32_t H, int pieces, int32_t norm, bool halves, uint32_t N, boo
     s.warps = token ? warps_of(backward, total) : 1;
     const int columns = token ? 1 : (total + 4) / 5;  // up to 5 pieces a lane and column
     const int held = (total + s.warps * columns - 1) / (s.warps * columns);
-    // the instances there are: 1, 2, 3, 5 and, for the norm over a token, 8 forward
-    // (the only one of 4 warps) and 4 backward (of 8 warps)
-    s.vpt = backward && s.warps == 8 ? held : !backward && s.warps == 4 ? 8 : held == 4 ? 5 : held > 5 ? 8 : held;
+    // the instances there are: 1, 2, 3, 5; for the norm over a token forward 8 too
+    // (the only one of 4 warps), backward 1 .. 4 (8 warps)
+    s.vpt = backward && token ? held : !backward && s.warps == 4 ? 8 : held == 4 ? 5 : held > 5 ? 8 : held;
     s.heads_per_block = columns == 1 ? H : held * per;
     s.grid_y = static_cast<uint32_t>((H + s.heads_per_block - 1) / s.heads_per_block);
-    const int block_warps = s.warps > 4 ? s.warps : 4, tokens = block_warps / s.warps;
+    const int block_warps = backward ? backward_warps(s.warps) : 4, tokens = block_warps / s.warps;
     s.threads = 32 * block_warps;
-    // shared memory: two stages of every piece but V's, the weights of the norm over a
-    // token; at the end of the backward pass the weight gradients
+    // shared memory: the stages of every piece (V's only backward) and, forward, the
+    // weights of the norm over a token; at the end of the backward pass the weight
+    // gradients
     const int all = H * pieces * 64;
-    const int tensors = backward && norm != BSS_HEAD_NORM_NONE ? 4 : 2;
-    s.smem = (token && s.warps < 8 ? all : 0) + block_warps * 2 * static_cast<int>(stage_bytes(tensors, s.vpt, halves));
+    const int tensors = backward ? backward_tensors(norm) : 2, stages = backward ? backward_stages(token, s.vpt) : 2;
+    s.smem = (token && !backward ? all : 0) + block_warps * stages * static_cast<int>(stage_bytes(tensors, s.vpt, halves));
     const int grads = token ? all * tokens : s.threads * 64;
     if (backward && norm != BSS_HEAD_NORM_NONE && s.smem < grads) s.smem = grads;
     // as many blocks as an SM holds, each walking over tokens
@@ -737,8 +739,9 @@ bool span_ok(int64_t n, int64_t stride) { return stride >= 0 && (n <= 1 || strid
 bss_status check_tokens(const bss_token_tensor* t, const char* name, uint32_t N, int32_t H, int32_t d, Region* r) {
     if (!is_aligned(t->data, 16)) return set_error(BSS_ERR_INVALID_ARG, "%s must be 16-byte aligned", name);
     const int64_t ts = N > 1 ? t->token_stride : 0, hs = H > 1 ? t->head_stride : 0;
-    if (!span_ok(N, ts) || !span_ok(H, hs) || ts % 8 != 0 || hs % 8 != 0)
-        return set_error(BSS_ERR_INVALID_ARG, "%s: strides must be multiples of 8 elements, not negative", name);
+    if (!span_ok(N, ts) || !span_ok(H, hs) || ts % 8 != 0 || hs % 8 != 0 || ts > kMaxTokenStride)
+        return set_error(BSS_ERR_INVALID_ARG,
+                         "%s: strides must be multiples of 8 elements, not negative, a token's at most 2^28", name);
     *r = region_3d(t->data, N, ts, H, hs, d, 2);
     return BSS_OK;
 }
@@ -819,12 +822,12 @@ template <bool HALVES>
 Kernel pick_backward_token(const Shape& s) {
     switch (s.warps * 10 + s.vpt) {
         case 11: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 1, 1>;
-        case 12: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 1, 2>;
-        case 13: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 1, 3>;
-        case 22: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 2, 2>;
-        case 23: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 2, 3>;
-        case 42: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 4, 2>;
-        case 43: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 4, 3>;
+        case 21: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 2, 1>;
+        case 31: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 3, 1>;
+        case 41: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 4, 1>;
+        case 51: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 5, 1>;
+        case 61: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 6, 1>;
+        case 81: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 8, 1>;
         case 82: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 8, 2>;
         case 83: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 8, 3>;
         default: return heads_backward_kernel<HALVES, BSS_HEAD_NORM_TOKEN, 8, 4>;
@@ -930,7 +933,7 @@ bss_status bss_heads_from_tokens(const bss_token_tensor* q, const bss_token_tens
         rout[i] = region_2d(out[i], 1, 0, static_cast<int64_t>(H) * a.N * d, 2);
         a.in[i] = static_cast<const __nv_bfloat16*>(in[i]->data);
         a.out[i] = static_cast<__nv_bfloat16*>(out[i]);
-        a.ts[i] = a.N > 1 ? in[i]->token_stride : 0;
+        a.ts[i] = a.N > 1 ? static_cast<uint32_t>(in[i]->token_stride * 2) : 0;
         a.hs[i] = H > 1 ? in[i]->head_stride : 0;
     }
     if (given == 0) return set_error(BSS_ERR_INVALID_ARG, "no tensor given");
@@ -1004,7 +1007,7 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
         if (rout[i].self_overlap) return set_error(BSS_ERR_INVALID_ARG, "%s overlaps itself", names[i]);
         a.in[i] = static_cast<const __nv_bfloat16*>(grad[i]);
         a.out[i] = static_cast<__nv_bfloat16*>(out[i]->data);
-        a.ts[i] = a.N > 1 ? out[i]->token_stride : 0;
+        a.ts[i] = a.N > 1 ? static_cast<uint32_t>(out[i]->token_stride * 2) : 0;
         a.hs[i] = H > 1 ? out[i]->head_stride : 0;
         if (i == 2 || norm == BSS_HEAD_NORM_NONE) continue;
         if (x[i] == nullptr || x[i]->data == nullptr)
@@ -1012,7 +1015,7 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
         if ((st = check_tokens(x[i], xnames[i], a.N, H, d, &rin[3 + i])) != BSS_OK) return st;
         has_x[i] = true;
         a.x[i] = static_cast<const __nv_bfloat16*>(x[i]->data);
-        a.xts[i] = a.N > 1 ? x[i]->token_stride : 0;
+        a.xts[i] = a.N > 1 ? static_cast<uint32_t>(x[i]->token_stride * 2) : 0;
         a.xhs[i] = H > 1 ? x[i]->head_stride : 0;
     }
     if (given == 0) return set_error(BSS_ERR_INVALID_ARG, "no tensor given");

@@ -755,8 +755,12 @@ bss_status check_overlaps(const Named* t, int n) {
     return BSS_OK;
 }
 
-// Rows a group must have for its folded parameters to be staged.
-constexpr int64_t kStagedRows = 64;
+// Rows a group must have for its folded parameters to be staged (75,600 x 1,280:
+// groups of 8 rows 172 us staged, 286 read row by row; 302,400 x 256: groups of 4
+// 200 and 181, of 16 111 and 139).
+constexpr int64_t kStagedRows = 8;
+// Waves of blocks (75,600 x 1,280, modulations a frame / RMS on both sides: one
+// wave 142 / 197 us, two 131 / 189, four 128 / 182, eight 130 / 181).
 constexpr int kForwardWaves = 4;
 
 template <typename TS, typename TB, int W, int VPT, bool STAGED>
@@ -826,10 +830,7 @@ GradShape grad_shape(const bss_residual_norm_grads& a) {
     s.warps = (a.channels / 8 + 31) / 32;
     s.side = s.warps >= 4 ? 1 : 4 / s.warps;
     s.threads = s.warps * s.side * 32;
-#ifndef GT
-#define GT 2
-#endif
-    s.T = s.threads <= 512 ? GT : 1;
+    s.T = s.threads <= 512 ? 2 : 1;
     const int pieces = s.T * (esize(a.stream_dtype) + esize(a.branch_dtype) + 1);
     s.stages = 2 * pieces * s.threads * 16 <= 224 * 1024 ? 2 : 1;
     s.smem = s.stages * pieces * s.threads * 16;
@@ -838,10 +839,7 @@ GradShape grad_shape(const bss_residual_norm_grads& a) {
     s.groups = (a.rows + per_group - 1) / per_group;
     // one wave of blocks: 16 warps an SM at 128 registers a thread, or what the
     // slots leave room for
-#ifndef GW
-#define GW 16
-#endif
-    int per_sm = GW * 32 / s.threads, by_smem = 224 * 1024 / (s.smem + 3072);
+    int per_sm = 512 / s.threads, by_smem = 224 * 1024 / (s.smem + 3072);
     per_sm = per_sm < by_smem ? per_sm : by_smem;
     int64_t most = (per_sm < 1 ? 1 : per_sm) * static_cast<int64_t>(num_sms()) / s.groups;
     if (most < 1) most = 1;
@@ -870,7 +868,7 @@ bss_status launch_backward_rows(const GradArgs& g, cudaStream_t stream) {
 template <typename TS, typename TB, int MODE>
 bss_status launch_backward_mode(const GradArgs& g, cudaStream_t stream) {
     if (g.s.threads > 512) return launch_backward_rows<TS, TB, MODE, 1, 1024>(g, stream);
-    return launch_backward_rows<TS, TB, MODE, GT, 512>(g, stream);
+    return launch_backward_rows<TS, TB, MODE, 2, 512>(g, stream);
 }
 
 template <typename TS, typename TB>
