@@ -236,9 +236,6 @@ def _ptr(t):
 def _stream(stream):
     import torch
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:  # the address alone: a Stream object costs 3 us
-            return ctypes.c_void_p(raw(torch.cuda.current_device()))
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
@@ -624,6 +621,17 @@ def _current_device():
     return torch.cuda.current_device()
 
 
+def _stream_on(stream, device):
+    """The address of a stream (None: the current one of the device)."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:  # the address alone: a Stream object costs 3 us
+        return raw(device)
+    return torch.cuda.current_stream().cuda_stream
+
+
 def _on_device(t, name, device):
     """A tensor on the current device, where kernels are launched."""
     try:
@@ -639,8 +647,8 @@ def _exact(t, name, dtype, shape, device):
     """The address of a given contiguous tensor of this type and shape (None: None)."""
     if t is None:
         return None
-    _on_device(t, name, device)
-    if t.dtype != dtype:
+    if getattr(t, "dtype", None) != dtype or t.get_device() != device:
+        _on_device(t, name, device)
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape}")
@@ -704,7 +712,7 @@ def rotary_table(length: int, pairs: int, base: float = 10000.0, dim: int | None
     device = _current_device()
     _check(load().bss_rotary_table(_exact(positions, "positions", torch.float64, (length,), device), length, pairs,
                                    2 * pairs if dim is None else dim, float(base),
-                                   _exact(out, "out", torch.float32, (length, pairs, 2), device), _stream(stream)))
+                                   _exact(out, "out", torch.float32, (length, pairs, 2), device), _stream_on(stream, device)))
     return out
 
 
@@ -720,25 +728,25 @@ class Rotary:
 
     def __init__(self, time=None, height=None, width=None, offset=(0, 0, 0), pairing: int = PAIR_INTERLEAVED):
         import torch
-        self.time, self.height, self.width, self.offset, self.pairing = time, height, width, tuple(offset), pairing
-        address, length, pairs, device = [], [], [], None
-        for t, n in ((time, "time"), (height, "height"), (width, "width")):
+        self.time, self.height, self.width, self.offset, self.pairing = time, height, width, offset, pairing
+        if len(offset) != 3:
+            raise ValueError("offset must have three entries")
+        device, address, shapes = None, [], []
+        for t in (time, height, width):
             if t is None:
                 address.append(None)
-                length.append(0)
-                pairs.append(0)
+                shapes.append((0, 0, 2))
                 continue
             if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != 2:
-                raise ValueError(f"rotary table {n} must be a tensor [positions][pairs][2]")
+                raise ValueError("a rotary table must be a tensor [positions][pairs][2]")
             if device is None:
                 device = t.get_device()
-            address.append(_exact(t, f"rotary table {n}", torch.float32, t.shape, max(device, 0)))
-            length.append(t.shape[0])
-            pairs.append(t.shape[1])
-        if len(self.offset) != 3:
-            raise ValueError("offset must have three entries")
+            shape = t.shape
+            address.append(_exact(t, "a rotary table", torch.float32, shape, device if device >= 0 else 0))
+            shapes.append(shape)
         self.device = device
-        self._pointer = ctypes.pointer(_Rotary(tuple(address), tuple(length), tuple(pairs), self.offset, pairing))
+        (t0, p0, _), (t1, p1, _), (t2, p2, _) = shapes
+        self._pointer = ctypes.pointer(_Rotary(tuple(address), (t0, t1, t2), (p0, p1, p2), tuple(offset), pairing))
 
 
 def _token_tensor(t, name, shape, device):
@@ -746,8 +754,8 @@ def _token_tensor(t, name, shape, device):
     import torch
     if t is None:
         return None
-    _on_device(t, name, device)
-    if t.dtype != torch.bfloat16:
+    if t.dtype != torch.bfloat16 or t.get_device() != device:
+        _on_device(t, name, device)
         raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape} (tokens, heads, channels)")
@@ -802,7 +810,7 @@ def heads_from_tokens(q, k, v, Qh, Kh, Vh, params: MaskParams, head_is_temporal=
         _token_tensor(q, "q", shape, device), _token_tensor(k, "k", shape, device), _token_tensor(v, "v", shape, device),
         _exact(Qh, "Qh", torch.bfloat16, heads, device), _exact(Kh, "Kh", torch.bfloat16, heads, device),
         _exact(Vh, "Vh", torch.bfloat16, heads, device), _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,), device), H,
-        ctypes.byref(params.c()), ctypes.byref(options), _stream(stream)))
+        ctypes.byref(params.c()), ctypes.byref(options), _stream_on(stream, device)))
     return Qh, Kh, Vh
 
 
@@ -837,7 +845,7 @@ def heads_from_tokens_backward(dQh, dKh, dVh, dq, dk, dv, params: MaskParams, he
         _token_tensor(dq, "dq", shape, device), _token_tensor(dk, "dk", shape, device), _token_tensor(dv, "dv", shape, device),
         _exact(dq_weight, "dq_weight", torch.float32, (width,), device), _exact(dk_weight, "dk_weight", torch.float32, (width,), device),
         _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,), device), H, mp, ctypes.byref(options),
-        None if workspace is None else workspace.data_ptr(), nbytes, _stream(stream)))
+        None if workspace is None else workspace.data_ptr(), nbytes, _stream_on(stream, device)))
     return dq, dk, dv
 
 
@@ -863,7 +871,7 @@ def attention_step_tokens(q, k, v, O, tile_map: TileMap, head_is_temporal, Qh, K
         _token_tensor(q, "q", shape, device), _token_tensor(k, "k", shape, device), _token_tensor(v, "v", shape, device), O_p,
         _exact(lse, "lse", torch.float32, (H, N), device), tile_map.handle,
         _exact(head_is_temporal, "head_is_temporal", torch.uint8, (H,), device), H, ctypes.byref(options), Q_p, K_p, V_p,
-        _stream(stream)))
+        _stream_on(stream, device)))
     return O
 
 
@@ -871,7 +879,8 @@ def _row_tensor(t, name, dtype, shape, device):
     """(address, row stride) of a given [rows][channels] tensor with any row stride."""
     if t is None:
         return None, 0
-    _on_device(t, name, device)
+    if t.get_device() != device:
+        _on_device(t, name, device)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {shape}")
     if t.dtype != dtype:
@@ -935,7 +944,7 @@ def residual_norm(x, y=None, r=None, h=None, gate=None, scale=None, shift=None, 
         _exact(weight, "weight", param, (channels,), device), _exact(bias, "bias", param, (channels,), device),
         _exact(y_weight, "y_weight", param, (channels,), device), _exact(stats, "stats", torch.float32, (rows, 2), device),
         _exact(y_stats, "y_stats", torch.float32, (rows, 2), device))
-    _check(load().bss_residual_norm(ctypes.byref(a), _stream(stream)))
+    _check(load().bss_residual_norm(ctypes.byref(a), _stream_on(stream, device)))
     return r, h
 
 
@@ -980,5 +989,5 @@ def residual_norm_backward(r, y=None, dr=None, dh=None, dx=None, dy=None, stats=
     workspace = _workspace(workspace, need.value, stream)
     if workspace is not None:
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _check(lib.bss_residual_norm_backward(args, _stream(stream)))
+    _check(lib.bss_residual_norm_backward(args, _stream_on(stream, device)))
     return dx, dy
