@@ -638,6 +638,7 @@ __global__ void __launch_bounds__(1024) heads_reduce_kernel(const float* __restr
     __shared__ float part[32][33];
     const int col = threadIdx.x % 32, lane = threadIdx.x / 32, c = blockIdx.x * 32 + col;
     float s = 0.0f;
+    cudaGridDependencySynchronize();
     if (c < 2 * width) {
 #pragma unroll 4
         for (int b = lane; b < blocks; b += 32) s += partial[static_cast<int64_t>(b) * 2 * width + c];
@@ -1044,8 +1045,8 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
     int blocks = 0;
     st = launch(true, pairing, norm, a, s, stream, "heads backward launch", &blocks);
     if (st != BSS_OK || !want) return st;
-    heads_reduce_kernel<<<(2 * width + 31) / 32, 1024, 0, stream>>>(a.partial, blocks, width, dq_weight, dk_weight);
-    return cuda_check(cudaGetLastError(), "weight gradient launch");
+    return launch_behind(heads_reduce_kernel, dim3((2 * width + 31) / 32), 1024, stream, "weight gradient launch",
+                         a.partial, blocks, width, dq_weight, dk_weight);
 }
 
 bss_status bss_attention_step_tokens(const bss_token_tensor* q, const bss_token_tensor* k,

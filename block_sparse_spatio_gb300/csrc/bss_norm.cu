@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kMaxChannels = 8192;
 constexpr int64_t kMaxStride = int64_t(1) << 28;  // elements between rows: a row's offset is one 32 x 32 bit product
-constexpr int kMinChunkRows = 16;  // rows a block of the backward pass reduces at least
+constexpr int kMinChunkRows = 4;  // rows a block of the backward pass reduces at least
 
 // ---------------------------------------------------------------- shared memory
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
@@ -623,20 +623,22 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
     }
 }
 
-// One group's column sums over its chunks (in order within 8 lanes, then the
-// lanes), the modulations' gradients, and the sums kept in the group's first
-// chunk for the weights' gradients.
-__global__ void __launch_bounds__(256) norm_groups_kernel(const __grid_constant__ GradArgs g) {
-    __shared__ float part[3][8][33];
+// One group's column sums over its chunks (in order within a lane, then the lanes
+// in order; a block is 32 columns wide and has a lane per warp) and the
+// modulations' gradients.  With one group the weights' gradients too; else the
+// sums are kept in the group's first chunk for norm_weights_kernel.
+__global__ void __launch_bounds__(1024) norm_groups_kernel(const __grid_constant__ GradArgs g) {
+    __shared__ float part[3][32][33];
     const bss_residual_norm_grads& a = g.a;
-    const int C = a.channels, col = threadIdx.x % 32, lane = threadIdx.x / 32;
+    const int C = a.channels, col = threadIdx.x % 32, lane = threadIdx.x / 32, lanes = blockDim.x / 32;
     const int c = blockIdx.x * 32 + col;
+    cudaGridDependencySynchronize();
     for (int64_t group = blockIdx.y; group < g.s.groups; group += gridDim.y) {
         float* base = g.partial + group * g.s.chunks * 3 * C;
         float s[3] = {0.0f, 0.0f, 0.0f};
         if (c < C) {
 #pragma unroll 4
-            for (int64_t k = lane; k < g.s.chunks; k += 8)
+            for (int64_t k = lane; k < g.s.chunks; k += lanes)
 #pragma unroll
                 for (int q = 0; q < 3; ++q) s[q] += base[(k * 3 + q) * C + c];
         }
@@ -647,9 +649,7 @@ __global__ void __launch_bounds__(256) norm_groups_kernel(const __grid_constant_
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
                 s[q] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) s[q] += part[q][k][col];
-                base[q * C + c] = s[q];
+                for (int k = 0; k < lanes; ++k) s[q] += part[q][k][col];
             }
             const float w = a.weight != nullptr ? load_param(a.weight, c, a.param_dtype) : 1.0f;
             const float b = a.bias != nullptr ? load_param(a.bias, c, a.param_dtype) : 0.0f;
@@ -657,6 +657,16 @@ __global__ void __launch_bounds__(256) norm_groups_kernel(const __grid_constant_
             if (a.dscale != nullptr) a.dscale[group * C + c] = fmaf(w, s[0], b * s[1]);
             if (a.dshift != nullptr) a.dshift[group * C + c] = s[1];
             if (a.dgate != nullptr) a.dgate[group * C + c] = wy * s[2];
+            if (g.s.groups > 1) {
+#pragma unroll
+                for (int q = 0; q < 3; ++q) base[q * C + c] = s[q];
+            } else {
+                const float m = a.scale != nullptr ? 1.0f + load_param(a.scale, c, a.param_dtype) : 1.0f;
+                const float gt = a.gate != nullptr ? load_param(a.gate, c, a.param_dtype) : 1.0f;
+                if (a.dweight != nullptr) a.dweight[c] = m * s[0];
+                if (a.dbias != nullptr) a.dbias[c] = m * s[1];
+                if (a.dy_weight != nullptr) a.dy_weight[c] = gt * s[2];
+            }
         }
         __syncthreads();
     }
@@ -669,7 +679,9 @@ __global__ void __launch_bounds__(256) norm_weights_kernel(const __grid_constant
     const int C = a.channels, col = threadIdx.x % 32, lane = threadIdx.x / 32;
     const int c = blockIdx.x * 32 + col;
     float s[3] = {0.0f, 0.0f, 0.0f};
-    if (c < C)
+    cudaGridDependencySynchronize();
+    if (c < C) {
+#pragma unroll 2
         for (int64_t group = lane; group < g.s.groups; group += 8) {
             const float* base = g.partial + group * g.s.chunks * 3 * C;
             const float m = a.scale != nullptr ? 1.0f + load_param(a.scale, group * a.scale_stride + c, a.param_dtype) : 1.0f;
@@ -678,6 +690,7 @@ __global__ void __launch_bounds__(256) norm_weights_kernel(const __grid_constant
             s[1] = fmaf(m, base[C + c], s[1]);
             s[2] = fmaf(gt, base[2 * C + c], s[2]);
         }
+    }
 #pragma unroll
     for (int q = 0; q < 3; ++q) part[q][lane][col] = s[q];
     __syncthreads();
@@ -1018,11 +1031,10 @@ bss_status bss_residual_norm_backward(const bss_residual_norm_grads* args, cudaS
     else st = launch_backward<float, float>(g, stream);
     if (st != BSS_OK || !g.want_sums) return st;
     const unsigned cols = (a.channels + 31) / 32;
-    norm_groups_kernel<<<dim3(cols, static_cast<unsigned>(g.s.groups < 4096 ? g.s.groups : 4096)), 256, 0, stream>>>(g);
-    if ((st = cuda_check(cudaGetLastError(), "modulation gradient launch")) != BSS_OK) return st;
-    if (a.dweight == nullptr && a.dbias == nullptr && a.dy_weight == nullptr) return BSS_OK;
-    norm_weights_kernel<<<cols, 256, 0, stream>>>(g);
-    return cuda_check(cudaGetLastError(), "weight gradient launch");
+    const dim3 grid(cols, static_cast<unsigned>(g.s.groups < 4096 ? g.s.groups : 4096));
+    st = launch_behind(norm_groups_kernel, grid, g.s.chunks > 64 ? 1024 : 256, stream, "modulation gradient launch", g);
+    if (st != BSS_OK || g.s.groups == 1 || (a.dweight == nullptr && a.dbias == nullptr && a.dy_weight == nullptr)) return st;
+    return launch_behind(norm_weights_kernel, dim3(cols), 256, stream, "weight gradient launch", g);
 }
 
 }  // extern "C"

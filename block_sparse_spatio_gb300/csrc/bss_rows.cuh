@@ -286,6 +286,24 @@ inline bss_status resident_blocks(const void* kernel, int threads, int smem, int
     return BSS_OK;
 }
 
+// A kernel launched behind another one of the same stream, its launch overlapping
+// that one's end: it calls cudaGridDependencySynchronize() before it reads what
+// the other wrote.
+template <typename... Params, typename... Args>
+bss_status launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, const char* what,
+                         Args... args) {
+    cudaLaunchConfig_t config = {};
+    config.gridDim = grid;
+    config.blockDim = dim3(static_cast<unsigned>(threads));
+    config.stream = stream;
+    cudaLaunchAttribute attribute = {};
+    attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attribute.val.programmaticStreamSerializationAllowed = 1;
+    config.attrs = &attribute;
+    config.numAttrs = 1;
+    return cuda_check(cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...), what);
+}
+
 // The bytes that a strided tensor touches: `n` runs of `extent` bytes, `stride`
 // bytes apart.
 struct Region {
