@@ -807,6 +807,59 @@ def variants(bss, torch, W, w, H, Q, K, V, dev, peaks, flags):
                               "frac_of_hbm_peak": 3 * hbytes / qkv_ms / 1e6 / peaks["hbm_gbs"]},
                           "timing": "20 launches back to back between one pair of CUDA events"}
     out["p1440_step"] = p1440_step(bss, torch, W, dev, peaks)
+    out["block_operators"] = block_operators(bss, torch, w, H, Q, K, V, dev, peaks, flags)
+    return out
+
+
+def block_operators(bss, torch, w, H, Q, K, V, dev, peaks, flags):
+    """The operators on either side of the attention step on the step's tokens:
+    time, and the bytes each cannot do without (inputs read once, outputs written
+    once) against the measured copy bandwidth."""
+    N, d, C, S = w.N, w.d, H * w.d, w.Hs * w.Ws
+    g = torch.Generator(device=dev).manual_seed(w.index)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=dev, dtype=torch.float32)  # noqa: E731
+    p = bss.MaskParams(w.F, w.Hs, w.Ws, d, w.wf, w.ws)
+    fl = torch.tensor(flags, dtype=torch.uint8, device=dev)
+    qkv = torch.empty(N, 3, H, d, dtype=torch.bfloat16, device=dev)
+    for i, t in enumerate((Q, K, V)):
+        qkv[:, i] = t.transpose(0, 1)
+    q, k, v = qkv.unbind(1)
+    third = d // 6
+    rot = bss.Rotary(bss.rotary_table(w.F, d // 2 - 2 * third), bss.rotary_table(w.Hs, third),
+                     bss.rotary_table(w.Ws, third))
+    wq, wk = 1 + 0.1 * rnd(C), 1 + 0.1 * rnd(C)
+    kw = dict(rotary=rot, q_weight=wq, k_weight=wk, norm=bss.HEAD_NORM_TOKEN)
+    heads = [torch.empty_like(Q) for _ in range(3)]
+    grads = torch.empty_like(qkv)
+    dw = [torch.empty(C, device=dev) for _ in range(2)]
+    x, y = rnd(N, C).to(torch.bfloat16), rnd(N, C).to(torch.bfloat16)
+    mod = rnd(w.F, 3, C) * 0.3
+    r, h, stats = torch.empty_like(x), torch.empty_like(x), torch.empty(N, 2, device=dev)
+    dx, dy = torch.empty_like(x), torch.empty_like(x)
+    dmod = [torch.empty(w.F, C, device=dev) for _ in range(3)]
+    e = 2.0 * N * C  # bytes of one tensor
+    ops = {
+        "residual_norm": (4 * e, lambda: bss.residual_norm(
+            x, y, r, h, gate=mod[:, 0], scale=mod[:, 1], shift=mod[:, 2], rows_per_group=S, stats=stats)),
+        "residual_norm_backward": (6 * e, lambda: bss.residual_norm_backward(
+            r, y, dr=x, dh=h, dx=dx, dy=dy, stats=stats, gate=mod[:, 0], scale=mod[:, 1], dgate=dmod[0], dscale=dmod[1],
+            dshift=dmod[2], rows_per_group=S)),
+        "heads_from_tokens": (6 * e, lambda: bss.heads_from_tokens(q, k, v, *heads, p, fl, **kw)),
+        "heads_from_tokens_backward": (8 * e, lambda: bss.heads_from_tokens_backward(
+            *heads, *grads.unbind(1), p, fl, q=q, k=k, dq_weight=dw[0], dk_weight=dw[1], **kw))}
+    out = {}
+    for name, (nbytes, fn) in ops.items():
+        ms = _time_batched(torch, fn)
+        out[name] = {"ms": ms, "gbs": nbytes / ms / 1e6, "frac_of_hbm_peak": nbytes / ms / 1e6 / peaks["hbm_gbs"]}
+    O, Qp, Kp, Vp = (torch.empty_like(Q) for _ in range(4))
+    with bss.build_tile_map(p) as tm:
+        out["step"] = _time_interleaved(torch, {
+            "from_tokens_ms": lambda: bss.attention_step_tokens(q, k, v, O, tm, fl, *heads, **kw),
+            "from_heads_ms": lambda: bss.attention_step(Q, K, V, O, tm, fl, Qp, Kp, Vp)}, rounds=5)
+    status = bss.get_device_status()
+    if status != 0:
+        raise RuntimeError(f"device status {bss.status_string(status)} in the block operators")
+    out["timing"] = "20 calls back to back between one pair of CUDA events; inputs larger than L2"
     return out
 
 
