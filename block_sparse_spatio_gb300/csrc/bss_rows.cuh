@@ -8,7 +8,6 @@
 
 #include <cstdint>
 #include <mutex>
-#include <vector>
 
 #include "bss_block.h"
 #include "bss_internal.h"
@@ -254,27 +253,31 @@ struct FastDiv {
 inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Blocks of a kernel that an SM holds at once, and the kernel allowed its dynamic
-// shared memory.  Asked of the runtime once per kernel, size and device.
+// shared memory.  Asked of the runtime once per kernel, size and device (up to as
+// many as are kept).
 inline bss_status resident_blocks(const void* kernel, int threads, int smem, int* blocks) {
     struct Known {
         const void* kernel;
         int device, threads, smem, blocks;
     };
+    constexpr int kKept = 512;
     static std::mutex mutex;
-    static std::vector<Known> known;
+    static Known known[kKept];
+    static int count = 0;
     int device = 0;
     bss_status st = cuda_check(cudaGetDevice(&device), "current device");
     if (st != BSS_OK) return st;
     std::lock_guard<std::mutex> lock(mutex);
-    for (const Known& k : known)
-        if (k.kernel == kernel && k.device == device && k.threads == threads && k.smem == smem) {
+    int most = smem;  // the limit only grows: another size of the kernel may be in use
+    for (int i = 0; i < count; ++i) {
+        const Known& k = known[i];
+        if (k.kernel != kernel || k.device != device) continue;
+        if (k.threads == threads && k.smem == smem) {
             *blocks = k.blocks;
             return BSS_OK;
         }
-    // the limit of a kernel only grows: another size of it may be in use
-    int most = smem;
-    for (const Known& k : known)
-        if (k.kernel == kernel && k.device == device && k.smem > most) most = k.smem;
+        if (k.smem > most) most = k.smem;
+    }
     if (most > 48 * 1024)
         st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "shared memory size");
     int n = 0;
@@ -282,7 +285,7 @@ inline bss_status resident_blocks(const void* kernel, int threads, int smem, int
         st = cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem), "occupancy");
     if (st != BSS_OK) return st;
     *blocks = n < 1 ? 1 : n;
-    known.push_back({kernel, device, threads, smem, *blocks});
+    if (count < kKept) known[count++] = {kernel, device, threads, smem, *blocks};
     return BSS_OK;
 }
 

@@ -88,8 +88,9 @@ enum {
 /* One token-major tensor: element (token n, head h, channel c) at
  * data[n * token_stride + h * head_stride + c] (strides in elements, multiples
  * of 8, >= 0, the token stride at most 2^28; the stride of a dimension of size
- * 1 is not used).  [N][H][d] outputs, views of a packed [N][3][H][d] projection and head-major [H][N][d]
- * tensors are all of this form; inputs may also broadcast (stride 0). */
+ * 1 is not used).  [N][H][d] outputs, views of a packed [N][3][H][d] projection
+ * and head-major [H][N][d] tensors are all of this form; inputs may also
+ * broadcast (stride 0). */
 typedef struct {
     void* data;           /* bf16, 16-byte aligned; NULL: this tensor is left out */
     int64_t token_stride;

@@ -243,3 +243,12 @@ def test_binding_refuses_cpu_tensors_and_bad_shapes():
         bss.heads_from_tokens(None, None, None, None, None, None, bss.MaskParams(1, 1, 1, 64, 0, 0))
     with pytest.raises(ValueError):
         bss.rotary_table(0, 4)
+
+
+def test_step_from_tokens_refuses_before_the_first_launch(lib):
+    """With a map that is never dereferenced on the device: a stale one only, on the CPU."""
+    o = bss._HeadsOptions(0, 1e-6, 1, None, None, None)
+    t = ctypes.byref(tokens(0))
+    for m in (None, ctypes.c_void_p(0x40)):
+        assert lib.bss_attention_step_tokens(t, t, t, ptr(5), None, m, None, 4, ctypes.byref(o), ptr(6), ptr(7), ptr(8),
+                                             None) == INVALID

@@ -208,6 +208,24 @@ def test_nonfinite_values_stay_in_their_token(bss):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("name,rotated", [("no_weights", 14), ("head_norm_halves", 48)])
+def test_channels_that_pass_keep_their_bits(bss, name, rotated):
+    """Unrotated channels next to infinities and of zeros of both signs."""
+    c = Case(bss, name)
+    q = c.dev[0].clone()
+    q[1, :, rotated] = float("inf")
+    q[2, :, -1] = float("-inf")
+    q[3, :, rotated:] = -0.0
+    out = c.outputs()[0]
+    bss.heads_from_tokens(q, None, None, out, None, None, c.p, None, rotary=c.rotary)
+    bits = lambda t: t.contiguous().view(torch.int16)  # noqa: E731
+    assert torch.equal(bits(out[:, :, rotated:]), bits(q.transpose(0, 1)[:, :, rotated:]))
+    back = torch.empty_like(q)
+    bss.heads_from_tokens_backward(out, None, None, back, None, None, c.p, None, rotary=c.rotary)
+    assert torch.equal(bits(back[:, :, rotated:]), bits(q[:, :, rotated:]))
+
+
+@pytest.mark.gpu
 def test_zero_tokens_stay_zero(bss):
     """A token of zeros (padding): finite, zero heads, and no part in the gradients."""
     c = Case(bss, "token_norm")
@@ -340,3 +358,29 @@ def test_offsets_past_32_bits(bss):
     x = q[rows].cpu().double()
     ref, mag = R.heads(x, w.cpu(), 1, 1e-6, None, False, [0] * H, 5, 1)
     R.check(out[:H - 1, rows], ref[:H - 1], mag[:H - 1], K_HEADS)
+
+
+@pytest.mark.gpu
+def test_step_refusals_launch_nothing(bss):
+    """What the attention call would refuse is refused before Q, K and V are touched."""
+    p = bss.MaskParams(2, 3, 5, 64, 1, 2)
+    H, N, d = 2, p.N, 64
+    q = torch.randn(N, H, d, device=DEV).to(torch.bfloat16)
+    make = lambda: torch.full((H, N, d), -7.0, dtype=torch.bfloat16, device=DEV)  # noqa: E731
+    ws, O = [make() for _ in range(3)], make()
+    with bss.build_tile_map(p, BQ=64, BKV=64) as tm:  # a tile the attention kernel does not run
+        with pytest.raises(bss.BssError) as e:
+            bss.attention_step_tokens(q, q, q, O, tm, None, *ws)
+        assert e.value.status == 2
+    with bss.build_tile_map(p) as tm:
+        for bad in (ws[0], ws[2]):
+            with pytest.raises(bss.BssError):
+                bss.attention_step_tokens(q, q, q, bad, tm, None, *ws)
+        with pytest.raises(bss.BssError):
+            bss.attention_step_tokens(q, None, q, O, tm, None, *ws)
+        with pytest.raises(ValueError):
+            bss.attention_step_tokens(q, q, q, O[:, :-1], tm, None, *ws)
+        with pytest.raises(ValueError):
+            bss.attention_step_tokens(q, q, q, O, tm, torch.ones(H + 1, dtype=torch.uint8, device=DEV), *ws)
+    torch.cuda.synchronize()
+    assert all(torch.all(t == -7.0) for t in ws + [O])
