@@ -110,126 +110,151 @@ __device__ __forceinline__ Token token_of(const HeadsArgs& a, uint32_t n) {
     return t;
 }
 
-// A lane's rotary pairs: 4 interleaved ones, or for halves the 8 whose other
-// channels another lane holds.  Per pair the table entry of position 0, the
-// table's row length and the axis.
+// Shared memory by 32-bit address, so that a piece's place is an offset in the
+// instruction.
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The angles of a token, one (cos, sin) a pair of a head, lie in the warp's slots:
+// lane l copies those of pairs l and l + 32 (per pair the table entry of position
+// 0, the table's row length and the axis), every lane reads those of its channels.
+// Pairs past the rotated ones hold the identity throughout.
+struct Angles {
+    const float2* entry[2];
+    uint32_t stride[2];
+    uint32_t axes;   // 2 bits a pair; 3: not copied
+};
+
+__device__ __forceinline__ Angles angles_of(const HeadsArgs& a) {
+    Angles r;
+    r.axes = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int p = (threadIdx.x & 31) + 32 * j;
+        const int axis = p >= a.rot.first[3] ? 3 : p < a.rot.first[1] ? 0 : p < a.rot.first[2] ? 1 : 2;
+        r.axes |= static_cast<uint32_t>(axis) << (2 * j);
+        r.entry[j] = axis == 3 ? nullptr
+                               : a.rot.table[axis] + static_cast<int64_t>(a.rot.offset[axis]) * a.rot.pairs[axis] +
+                                     (p - a.rot.first[axis]);
+        r.stride[j] = axis == 3 ? 0 : a.rot.pairs[axis] * 8;
+    }
+    return r;
+}
+
+constexpr uint32_t kAngleBytes = 64 * 8;  // of a warp's slots: 64 pairs at most
+
+// `at`: the warp's angle slots, here and below.
+__device__ __forceinline__ void clear_angles(const Angles& r, uint32_t at) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        if ((r.axes >> (2 * j) & 3u) == 3)
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + ((threadIdx.x & 31) + 32 * j) * 8), "f"(1.0f),
+                         "f"(0.0f)
+                         : "memory");
+}
+
+__device__ __forceinline__ void fetch_angles(const Angles& r, const Token& t, uint32_t at) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const uint32_t axis = r.axes >> (2 * j) & 3u;
+        const uint32_t row = axis == 0 ? t.f : axis == 1 ? t.h : t.w;
+        if (axis != 3)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + ((threadIdx.x & 31) + 32 * j) * 8),
+                         "l"(reinterpret_cast<const char*>(r.entry[j]) + static_cast<uint64_t>(row) * r.stride[j])
+                         : "memory");
+    }
+}
+
+// How a lane's channels pair up: 4 interleaved pairs, or for halves 8 pairs whose
+// other channels lane `other` holds.
 template <bool HALVES>
 struct Pairs {
-    static constexpr int kCount = HALVES ? 8 : 4;
-    const float2* entry[kCount];
-    int32_t stride[kCount];
-    uint32_t axes;   // 2 bits a pair; 3: not rotated
-    bool partial;    // some channels of the head pass unrotated (the same for all lanes)
-    int other;       // lane of the paired piece
+    uint32_t at;     // byte of the first one's angles
+    int other;
     float sign;      // of the sine there
+    uint32_t keep;   // bit j: pair j is not rotated (halves: none or all)
+    bool partial;    // some channels of the head are not (the same for all lanes)
 };
 
 template <bool HALVES>
 __device__ __forceinline__ Pairs<HALVES> pairs_of(const HeadsArgs& a, int piece) {
     Pairs<HALVES> r;
-    int pair = piece * 4;
-    bool in = true;
-    r.other = threadIdx.x & 31;
+    r.partial = a.rot.first[3] < a.pieces * 4;
     r.sign = 1.0f;
+    r.other = threadIdx.x & 31;
+    r.keep = 0;
     if (HALVES) {
         const int half = a.rot.first[3] / 8;  // pieces per half
-        const bool lower = piece < half;
-        in = piece < 2 * half;
+        const bool lower = piece < half, in = piece < 2 * half;
         const int other = in ? (lower ? piece + half : piece - half) : piece;
         r.other = (threadIdx.x & 31 & ~(a.pieces - 1)) | other;
         r.sign = lower ? -1.0f : 1.0f;
-        pair = (lower ? piece : other) * 8;
-    }
-    r.axes = 0;
-    r.partial = a.rot.first[3] < a.pieces * 4;
+        r.at = in ? (lower ? piece : other) * 64 : 0;
+        r.keep = in ? 0 : 0xFu;
+    } else {
+        r.at = piece * 32;
 #pragma unroll
-    for (int j = 0; j < Pairs<HALVES>::kCount; ++j) {
-        const int p = pair + j;
-        const int axis = !in || p >= a.rot.first[3] ? 3 : p < a.rot.first[1] ? 0 : p < a.rot.first[2] ? 1 : 2;
-        r.axes |= static_cast<uint32_t>(axis) << (2 * j);
-        r.entry[j] = axis == 3 ? nullptr
-                               : a.rot.table[axis] + static_cast<int64_t>(a.rot.offset[axis]) * a.rot.pairs[axis] +
-                                     (p - a.rot.first[axis]);
-        r.stride[j] = axis == 3 ? 0 : a.rot.pairs[axis];
+        for (int j = 0; j < 4; ++j) r.keep |= (piece * 4 + j >= a.rot.first[3] ? 1u : 0u) << j;
     }
     return r;
 }
 
-// One token's angles for a lane's pairs.
+// One token's cosines and (signed, for halves and BACK) sines of a lane's pairs.
 template <bool HALVES>
 struct Turn {
     float2 c[HALVES ? 4 : 2], s[HALVES ? 4 : 2];
 };
 
-// A lane's angle slots, [pair][32 lanes] of 8 bytes: those of pairs that do not
-// turn hold the identity throughout, the others are copied token by token.
-template <bool HALVES>
-__device__ __forceinline__ void clear_turn(const Pairs<HALVES>& pr, uint32_t at) {
-#pragma unroll
-    for (int j = 0; j < Pairs<HALVES>::kCount; ++j)
-        if ((pr.axes >> (2 * j) & 3u) == 3)
-            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at + j * 256), "f"(1.0f), "f"(0.0f) : "memory");
-}
-
-template <bool HALVES>
-__device__ __forceinline__ void fetch_turn(const Pairs<HALVES>& pr, const Token& t, uint32_t at) {
-#pragma unroll
-    for (int j = 0; j < Pairs<HALVES>::kCount; ++j) {
-        const uint32_t axis = pr.axes >> (2 * j) & 3u;
-        const uint32_t row = axis == 0 ? t.f : axis == 1 ? t.h : t.w;
-        if (axis != 3)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at + j * 256),
-                         "l"(pr.entry[j] + static_cast<int64_t>(row) * pr.stride[j])
-                         : "memory");
-    }
-}
-
-template <bool HALVES>
-__device__ __forceinline__ Turn<HALVES> read_turn(uint32_t at) {
+template <bool HALVES, bool BACK>
+__device__ __forceinline__ Turn<HALVES> read_turn(const Pairs<HALVES>& pr, uint32_t at) {
     Turn<HALVES> r;
+    const float sg = (HALVES ? pr.sign : 1.0f) * (BACK ? -1.0f : 1.0f);
 #pragma unroll
-    for (int j = 0; j < Pairs<HALVES>::kCount; ++j) {
-        float c, s;
-        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(c), "=f"(s) : "r"(at + j * 256));
-        if (j & 1)
-            r.c[j / 2].y = c, r.s[j / 2].y = s;
-        else
-            r.c[j / 2].x = c, r.s[j / 2].x = s;
+    for (int j = 0; j < (HALVES ? 4 : 2); ++j) {
+        const uint4 q = lds128(at + pr.at + 16 * j);
+        r.c[j] = make_float2(__uint_as_float(q.x), __uint_as_float(q.z));
+        r.s[j] = make_float2(__uint_as_float(q.y) * sg, __uint_as_float(q.w) * sg);
     }
     return r;
 }
 
-// Turn 8 channels by their angles, or back (BACK).  Interleaved pairs lie in the
-// thread (even channels apart from odd ones), those of halves in two lanes.
-// Channels that are not rotated keep their values (also next to an infinity, which
-// the identity's zero sine would turn into NaN).
-template <bool HALVES, bool BACK>
+// Turn 8 channels by their angles.  Interleaved pairs lie in the thread (even
+// channels apart from odd ones), those of halves in two lanes.  Channels that are
+// not rotated keep their values (also next to an infinity, which the identity's
+// zero sine would turn into NaN).
+template <bool HALVES>
 __device__ __forceinline__ void rotate8(V8& v, const Turn<HALVES>& t, const Pairs<HALVES>& pr) {
     const V8 old = v;
     if (!HALVES) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float2 minus = make_float2(-t.s[i].x, -t.s[i].y);
             const float2 a = v.p[2 * i], b = v.p[2 * i + 1];
-            v.p[2 * i] = __ffma2_rn(b, BACK ? t.s[i] : minus, __fmul2_rn(a, t.c[i]));
-            v.p[2 * i + 1] = __ffma2_rn(a, BACK ? minus : t.s[i], __fmul2_rn(b, t.c[i]));
+            const float2 minus = make_float2(-t.s[i].x, -t.s[i].y);
+            v.p[2 * i] = __ffma2_rn(b, minus, __fmul2_rn(a, t.c[i]));
+            v.p[2 * i + 1] = __ffma2_rn(a, t.s[i], __fmul2_rn(b, t.c[i]));
         }
         if (pr.partial) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {  // pairs 2 (i / 2) and the next
-                if ((pr.axes >> (4 * (i / 2)) & 3u) == 3) v.p[i].x = old.p[i].x;
-                if ((pr.axes >> (4 * (i / 2) + 2) & 3u) == 3) v.p[i].y = old.p[i].y;
+                if (pr.keep >> (2 * (i / 2)) & 1u) v.p[i].x = old.p[i].x;
+                if (pr.keep >> (2 * (i / 2) + 1) & 1u) v.p[i].y = old.p[i].y;
             }
         }
     } else {
-        const float2 sg = f2(BACK ? -pr.sign : pr.sign);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 o = make_float2(__shfl_sync(0xFFFFFFFFu, v.p[i].x, pr.other),
                                          __shfl_sync(0xFFFFFFFFu, v.p[i].y, pr.other));
-            v.p[i] = __ffma2_rn(o, __fmul2_rn(t.s[i], sg), __fmul2_rn(v.p[i], t.c[i]));
+            v.p[i] = __ffma2_rn(o, t.s[i], __fmul2_rn(v.p[i], t.c[i]));
         }
-        if (pr.partial && (pr.axes & 3u) == 3) v = old;  // a piece of halves is rotated whole or not
+        if (pr.partial && pr.keep != 0) v = old;
     }
 }
 
@@ -257,18 +282,6 @@ __device__ __forceinline__ void token_sum(float (&v)[NV], float* buf, int group,
 #pragma unroll
         for (int k = 1; k < W; ++k) v[i] += buf[k * NV + i];
     }
-}
-
-// Shared memory by 32-bit address, so that a piece's place is an offset in the
-// instruction.
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
-}
-
-__device__ __forceinline__ void sts128(uint32_t at, const uint4& v) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
 // Eight floats a piece as two 16-byte planes `plane` bytes apart, pieces side by
@@ -314,13 +327,13 @@ __device__ __forceinline__ void stage_weights(const HeadsArgs& a, uint32_t at) {
 
 // A warp's slots: stages of [tensor][VPT][32 lanes] pieces and the angles.  Those
 // of pieces that do not exist hold zeros throughout.
-__host__ __device__ constexpr uint32_t stage_bytes(int tensors, int vpt, bool halves) {
-    return tensors * vpt * 512 + (halves ? 2048 : 1024);
+__host__ __device__ constexpr uint32_t stage_bytes(int tensors, int vpt) {
+    return tensors * vpt * 512 + kAngleBytes;
 }
 
-template <int TENSORS, int VPT, bool HALVES, int STAGES>
+template <int TENSORS, int VPT, int STAGES>
 __device__ __forceinline__ uint32_t slots_of(uint32_t at, int count) {
-    constexpr uint32_t kStage = stage_bytes(TENSORS, VPT, HALVES);
+    constexpr uint32_t kStage = stage_bytes(TENSORS, VPT);
     constexpr int kPieces = TENSORS * VPT;
     at += (threadIdx.x >> 5) * STAGES * kStage + (threadIdx.x & 31) * 16;
     for (int e = 0; e < STAGES * kPieces; ++e)
@@ -346,15 +359,16 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
     extern __shared__ __align__(16) float4 planes[];  // weights of a norm over a token, then the slots
     __shared__ float buf[2][4 * 2];
     constexpr int kTokens = 4 / W;
-    constexpr uint32_t kStage = stage_bytes(2, VPT, HALVES), kTurn = 2 * VPT * 512;
+    constexpr uint32_t kStage = stage_bytes(2, VPT), kTurn = 2 * VPT * 512;
     const int warp = threadIdx.x / 32 % W, group = threadIdx.x / 32 / W;
     Lane me = lane_of<W, VPT>(a, warp);
     const bool rotary = a.rot.first[3] > 0;
     const Pairs<HALVES> pr = pairs_of<HALVES>(a, me.piece);
+    const Angles angles = angles_of(a);
     const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
     const uint32_t base = smem_u32(planes);
     const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
-    const uint32_t slots = slots_of<2, VPT, HALVES, 2>(base + (NORM == BSS_HEAD_NORM_TOKEN ? 4 * all16 : 0), me.count);
+    const uint32_t slots = slots_of<2, VPT, 2>(base + (NORM == BSS_HEAD_NORM_TOKEN ? 4 * all16 : 0), me.count);
     constexpr uint32_t step = kTokens;
     uint32_t n = blockIdx.x * a.span + group;
     const uint32_t end = a.N - blockIdx.x * a.span > a.span ? (blockIdx.x + 1) * a.span : a.N;
@@ -366,14 +380,14 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
         src[i] = reinterpret_cast<const char*>(a.in[i] + me.head0 * a.hs[i] + me.piece * 8);
         apart[i] = me.step * a.hs[i] * 2;
     }
-    const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 8;  // from a lane's slots to its angles
-    if (rotary) clear_turn<HALVES>(pr, slots + turn_at), clear_turn<HALVES>(pr, slots + kStage + turn_at);
+    const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 16;  // from a lane's slots to the warp's angles
+    if (rotary) clear_angles(angles, slots + turn_at), clear_angles(angles, slots + kStage + turn_at);
     uint32_t next_row = 0;  // of the fetched token in temporal heads
     auto fetch = [&](uint32_t m, bool exists, uint32_t to) {
         if (exists) {
             const Token tok = token_of(a, m);
             next_row = tok.temporal_row;
-            if (rotary) fetch_turn<HALVES>(pr, tok, to + turn_at);
+            if (rotary) fetch_angles(angles, tok, to + turn_at);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (a.in[i] == nullptr) continue;
@@ -409,10 +423,14 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
             for (int j = 0; j < VPT; ++j, p += apart[2])
                 if (j < me.count) v_raw[j] = ld_row(p);
         }
+        __syncwarp();  // every lane has read the angles in the slots to be filled
         fetch(n + step, end - n > step, other);
         cp_async_wait_group<1>();
         Turn<HALVES> turn;
-        if (rotary) turn = read_turn<HALVES>(now + turn_at);
+        if (rotary) {
+            __syncwarp();  // the other lanes' copies
+            turn = read_turn<HALVES, false>(pr, now + turn_at);
+        }
         float r[2] = {0.0f, 0.0f};
         if (NORM == BSS_HEAD_NORM_TOKEN) {
 #pragma unroll
@@ -440,7 +458,7 @@ __global__ void __launch_bounds__(128, forward_blocks(VPT)) heads_forward_kernel
                     v = mul(v, mul(w[i], rsqrtf(head_sum(dot(v, v), a.pieces) * a.inv_width + a.eps)));
                 if (NORM == BSS_HEAD_NORM_TOKEN && live)
                     v = mul(v, mul(planes_load(weights + i * 2 * all16 + j * (W * 512), all16), r[i]));
-                if (rotary) rotate8<HALVES, false>(v, turn, pr);
+                if (rotary) rotate8<HALVES>(v, turn, pr);
                 if (live) st_row(reinterpret_cast<char*>(a.out[i]) + to, pack_bf16<!HALVES>(v));
             }
             if (a.in[2] != nullptr && live) st_row(reinterpret_cast<char*>(a.out[2]) + to, v_raw[j]);
@@ -461,7 +479,7 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
     constexpr bool kToken = NORM == BSS_HEAD_NORM_TOKEN, kOne = kToken && VPT == 1;
     constexpr int kWarps = backward_warps(W), kTokens = kWarps / W;
     constexpr int kTensors = backward_tensors(NORM), kStages = backward_stages(kToken, VPT);  // dQ, dK, dV, q, k
-    constexpr uint32_t kStage = stage_bytes(kTensors, VPT, HALVES), kTurn = kTensors * VPT * 512;
+    constexpr uint32_t kStage = stage_bytes(kTensors, VPT), kTurn = kTensors * VPT * 512;
     extern __shared__ __align__(16) float4 planes[];
     __shared__ float4 buf4[2][kWarps];
     const int warp = threadIdx.x / 32 % W, group = threadIdx.x / 32 / W;
@@ -469,10 +487,11 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
     me.temporal = temporal_heads<VPT>(a, me);
     const bool rotary = a.rot.first[3] > 0;
     const Pairs<HALVES> pr = pairs_of<HALVES>(a, me.piece);
+    const Angles angles = angles_of(a);
     const uint32_t all16 = a.H * a.pieces * 16, row_bytes = a.pieces * 16;
     const uint32_t base = smem_u32(planes);
     const uint32_t weights = base + (me.head0 * a.pieces + me.piece) * 16;
-    const uint32_t slots = slots_of<kTensors, VPT, HALVES, kStages>(base, me.count);
+    const uint32_t slots = slots_of<kTensors, VPT, kStages>(base, me.count);
     constexpr uint32_t step = kTokens;
     uint32_t n = blockIdx.x * a.span + group;
     const uint32_t end = a.N - blockIdx.x * a.span > a.span ? (blockIdx.x + 1) * a.span : a.N;
@@ -491,13 +510,13 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
             xapart[i] = me.step * a.xhs[i] * 2;
         }
     }
-    const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 8;  // from a lane's slots to its angles
+    const uint32_t turn_at = kTurn - (threadIdx.x & 31) * 16;  // from a lane's slots to the warp's angles
     if (rotary)
-        for (int k = 0; k < kStages; ++k) clear_turn<HALVES>(pr, slots + k * kStage + turn_at);
+        for (int k = 0; k < kStages; ++k) clear_angles(angles, slots + k * kStage + turn_at);
     auto fetch = [&](uint32_t m, bool exists, uint32_t to) {
         if (exists) {
             const Token tok = token_of(a, m);
-            if (rotary) fetch_turn<HALVES>(pr, tok, to + turn_at);
+            if (rotary) fetch_angles(angles, tok, to + turn_at);
             int64_t at = grad0;
 #pragma unroll
             for (int j = 0; j < VPT; ++j, at += head_step) {
@@ -541,10 +560,14 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
     uint32_t now = slots, ahead_at = slots + (kStages - 1) * kStage;
     int turn_buf = 0;
     for (; n < end; n += step, turn_buf ^= 1) {
+        __syncwarp();  // every lane has read the angles in the slots to be filled
         fetch(n + (kStages - 1) * step, end - n > (kStages - 1) * step, ahead_at);
         cp_async_wait_group<kStages - 1>();
         Turn<HALVES> turn;
-        if (rotary) turn = read_turn<HALVES>(now + turn_at);
+        if (rotary) {
+            __syncwarp();  // the other lanes' copies
+            turn = read_turn<HALVES, true>(pr, now + turn_at);
+        }
         float sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // x^2 and g w x of Q, then of K
         V8 gv[2], xv[2];                           // of one piece, for both passes
         if (kToken) {
@@ -554,7 +577,7 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
 #pragma unroll
                 for (int j = 0; j < VPT; ++j) {
                     V8 v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
-                    if (rotary) rotate8<HALVES, true>(v, turn, pr);
+                    if (rotary) rotate8<HALVES>(v, turn, pr);
                     if (!kOne && j >= me.count) continue;
                     const V8 x = unpack_bf16<!HALVES>(lds128(now + ((3 + i) * VPT + j) * 512));
                     sums[2 * i] += dot(x, x);
@@ -586,7 +609,7 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
                     v = gv[k];
                 } else {
                     v = unpack_bf16<!HALVES>(lds128(now + (i * VPT + j) * 512));
-                    if (rotary) rotate8<HALVES, true>(v, turn, pr);
+                    if (rotary) rotate8<HALVES>(v, turn, pr);
                 }
                 if (NORM != BSS_HEAD_NORM_NONE) {
                     const V8 x = kOne ? xv[k] : unpack_bf16<!HALVES>(lds128(now + ((3 + k) * VPT + j) * 512));
@@ -703,7 +726,7 @@ int warps_of(bool backward, int chunks) {
     return chunks <= 6 ? chunks : 8;
 }
 
-Shape shape_of(int32_t H, int pieces, int32_t norm, bool halves, uint32_t N, bool backward) {
+Shape shape_of(int32_t H, int pieces, int32_t norm, uint32_t N, bool backward) {
     Shape s;
     const int per = 32 / pieces, total = (H + per - 1) / per;  // warp-wide rows of pieces
     const bool token = norm == BSS_HEAD_NORM_TOKEN;
@@ -722,7 +745,7 @@ Shape shape_of(int32_t H, int pieces, int32_t norm, bool halves, uint32_t N, boo
     // gradients
     const int all = H * pieces * 64;
     const int tensors = backward ? backward_tensors(norm) : 2, stages = backward ? backward_stages(token, s.vpt) : 2;
-    s.smem = (token && !backward ? all : 0) + block_warps * stages * static_cast<int>(stage_bytes(tensors, s.vpt, halves));
+    s.smem = (token && !backward ? all : 0) + block_warps * stages * static_cast<int>(stage_bytes(tensors, s.vpt));
     const int grads = token ? all * tokens : s.threads * 64;
     if (backward && norm != BSS_HEAD_NORM_NONE && s.smem < grads) s.smem = grads;
     // as many blocks as an SM holds, each walking over tokens
@@ -962,7 +985,7 @@ bss_status bss_heads_from_tokens(const bss_token_tensor* q, const bss_token_tens
             if (j < i && a.out[i] != nullptr && a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
                 return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
         }
-    const Shape s = shape_of(H, d / 8, options->norm, pairing == BSS_PAIR_HALVES, a.N, false);
+    const Shape s = shape_of(H, d / 8, options->norm, a.N, false);
     set_shape(s, options->norm, d, &a);
     int blocks = 0;
     return launch(false, pairing, options->norm, a, s, stream, "heads launch", &blocks);
@@ -978,7 +1001,7 @@ bss_status bss_heads_from_tokens_backward_workspace(int32_t H, const bss_mask_pa
     if (st != BSS_OK) return st;
     if ((st = check_norm(norm, H, params->head_dim)) != BSS_OK) return st;
     if (norm == BSS_HEAD_NORM_NONE) return BSS_OK;
-    const Shape s = shape_of(H, params->head_dim / 8, norm, false, static_cast<uint32_t>(params->F) * params->Hs * params->Ws, true);
+    const Shape s = shape_of(H, params->head_dim / 8, norm, static_cast<uint32_t>(params->F) * params->Hs * params->Ws, true);
     const int64_t width = norm == BSS_HEAD_NORM_TOKEN ? static_cast<int64_t>(H) * params->head_dim : params->head_dim;
     *bytes = static_cast<int64_t>(s.grid_x) * s.grid_y * 2 * width * 4;
     return BSS_OK;
@@ -1046,7 +1069,7 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
             if (a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
                 return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
     }
-    const Shape s = shape_of(H, d / 8, norm, pairing == BSS_PAIR_HALVES, a.N, true);
+    const Shape s = shape_of(H, d / 8, norm, a.N, true);
     set_shape(s, norm, d, &a);
     const bool want = dq_weight != nullptr || dk_weight != nullptr;
     const int width = norm == BSS_HEAD_NORM_TOKEN ? H * d : d;
