@@ -25,9 +25,8 @@
 // the norm is over the token, else their heads go to several grid columns.
 //
 // Measured (75,600 tokens x 10 heads x 128, norm over the token, GB300): forward
-// 192 us, 89% of the measured copy bandwidth; backward 270 us, 84%.  What is left
-// forward is the ends of the launch (302,400 tokens: 90%); backward the five warps'
-// barrier a token and 500 instructions a warp between two of them.
+// 189 us, backward 250 us, both 91% of the measured copy bandwidth; what is left is
+// mostly the ends of the launch (302,400 tokens: 92 to 93% and 94 to 96%).
 #include <cstring>
 
 #include "bss_rows.cuh"
@@ -897,8 +896,9 @@ bss_status launch(bool backward, int pairing, int32_t norm, const HeadsArgs& arg
     const uint32_t tokens = s.threads / 32 / s.warps;
     HeadsArgs a = args;
     // forward four waves of blocks, so that SMs that finish early take more; backward
-    // one, since every block leaves a partial sum (75,600 tokens x 10 heads: 193 us
-    // against 203 in one wave; backward 291 in one wave, 301 in two)
+    // one, since every block leaves a partial sum (75,600 tokens x 10 heads, measured
+    // on earlier forms of the kernels: forward 193 us in four waves, 203 in one;
+    // backward 291 in one, 301 in two)
     const uint32_t many = grid_x * (backward ? 1 : kWaves);
     a.span = (a.N + many - 1) / many;
     a.span = (a.span + tokens - 1) / tokens * tokens;
