@@ -580,7 +580,8 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             const bool live = active && mine + t < last;
             const float mean1 = a.norm == BSS_NORM_LAYER ? sums[NV * t] * inv : 0.0f;
             const float mean2 = a.norm != BSS_NORM_NONE ? sums[NV * t + 1] * inv : 0.0f;
-            V8 u = fma8(xh[t], -st[t].y * mean2, w[t]);
+            V8 u = w[t];  // without a norm it is that: not 0 times an infinity of r more
+            if (a.norm != BSS_NORM_NONE) u = fma8(xh[t], -st[t].y * mean2, u);
             if (a.norm == BSS_NORM_LAYER) u = add8(u, -st[t].y * mean1);
             if (live)
                 store_vector<TS, kSplit>(at_row(static_cast<TS*>(a.dx) + c, mine + t, dx_bytes), mul(u, a.residual_scale), true,

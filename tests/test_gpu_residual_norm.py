@@ -30,6 +30,10 @@ CASES = {
     "long_row": (9, 5000, 4, F32, F32, F32, 1, 1, "y gate scale shift weight bias y_weight"),
     "longest_row": (5, 8192, 2, BF, BF, BF, 1, 2, "y gate scale shift weight bias y_weight"),
     "smallest_row": (300, 8, 100, BF, BF, F32, 2, 0, "y gate scale shift"),
+    # the shapes whose slots fill shared memory furthest
+    "wide_stream": (11, 4096, 4, F32, BF, F32, 1, 0, "y gate scale shift"),
+    "widest_stream": (5, 8192, 2, F32, BF, F32, 1, 0, "y gate scale shift weight bias"),
+    "widest_float": (9, 8192, 9, F32, F32, F32, 1, 1, "y gate scale shift weight bias y_weight"),
     "many_rows": (2011, 512, 301, BF, BF, F32, 1, 0, "y gate scale shift weight bias"),
 }
 
@@ -238,6 +242,28 @@ def test_nonfinite_rows_and_constant_rows(bss):
     assert torch.isnan(h[8]).all() and not torch.isfinite(h[3]).all()
     for row in (5, 6):
         assert torch.equal(h[row], c.dev["shift"][0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("stream", [BF, F32])
+@pytest.mark.parametrize("y_norm", [0, 2])
+def test_infinite_stream_without_a_norm(bss, stream, y_norm):
+    """Without a norm dx and dy do not depend on r: they stay what they are next to its infinities."""
+    rows, C = 9, 264
+    g = torch.Generator().manual_seed(5)
+    v = {k: torch.randn(rows, C, generator=g).to(BF).to(DEV) for k in ("y", "dh")}
+    r, dr = (torch.randn(rows, C, generator=g).to(stream).to(DEV) for _ in range(2))
+    ys = torch.stack((torch.zeros(rows), torch.rand(rows, generator=g) + 0.5), 1).to(DEV) if y_norm else None
+    got = []
+    for value in (1.0, float("inf"), float("-inf"), float("nan")):
+        r[2, 5], r[7, 263] = value, value
+        dx, dy = torch.empty_like(r), torch.empty_like(v["y"])
+        bss.residual_norm_backward(r, dr=dr, dx=dx, dy=dy, y_stats=ys, norm=0, y_norm=y_norm, **v)
+        got.append((dx.clone(), dy.clone()))
+    torch.cuda.synchronize()
+    assert torch.isfinite(got[0][0]).all() and torch.isfinite(got[0][1]).all()
+    for dx, dy in got[1:]:
+        assert torch.equal(dx, got[0][0]) and torch.equal(dy, got[0][1])
 
 
 @pytest.mark.gpu
