@@ -25,8 +25,8 @@
 // the norm is over the token, else their heads go to several grid columns.
 //
 // Measured (75,600 tokens x 10 heads x 128, norm over the token, GB300): forward
-// 189 us, backward 250 us, both 91% of the measured copy bandwidth; what is left is
-// mostly the ends of the launch (302,400 tokens: 92 to 93% and 94 to 96%).
+// 188 us, backward 250 to 255 us, 91 and 89 to 91% of the measured copy bandwidth;
+// what is left is mostly the ends of the launch (302,400 tokens: 92 to 93% and 94 to 96%).
 #include <cstring>
 
 #include "bss_rows.cuh"

@@ -21,8 +21,8 @@
 // flight without holding registers.
 //
 // Measured (75,600 x 1,280, GB300, share of the measured copy bandwidth): forward
-// bf16 128 us (89%; 302,400 rows 92 to 93%), float stream with both norms 181 us (94%);
-// backward bf16 181 us (94%), 302,400 rows with both norms RMS 712 us (96%).
+// bf16 128 us (89%; 302,400 rows 92 to 93%), float stream with both norms 181 us (95%);
+// backward bf16 182 us (94%), 302,400 rows with both norms RMS 713 us (96%).
 #include <cstring>
 #include <type_traits>
 
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const __grid_con
             const float mean1 = a.norm == BSS_NORM_LAYER ? sums[NV * t] * inv : 0.0f;
             const float mean2 = a.norm != BSS_NORM_NONE ? sums[NV * t + 1] * inv : 0.0f;
             V8 u = w[t];  // without a norm it is that: not 0 times an infinity of r more
-            if (a.norm != BSS_NORM_NONE) u = fma8(xh[t], -st[t].y * mean2, u);
+            if (MODE == RMS2 || a.norm != BSS_NORM_NONE) u = fma8(xh[t], -st[t].y * mean2, u);
             if (a.norm == BSS_NORM_LAYER) u = add8(u, -st[t].y * mean1);
             if (live)
                 store_vector<TS, kSplit>(at_row(static_cast<TS*>(a.dx) + c, mine + t, dx_bytes), mul(u, a.residual_scale), true,
