@@ -278,8 +278,8 @@ inline bss_status resident_blocks(const void* kernel, int threads, int smem, int
         }
         if (k.smem > most) most = k.smem;
     }
-    if (most > 48 * 1024)
-        st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "shared memory size");
+    // below 48 KiB too: what a kernel may use unasked includes its static memory
+    st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "shared memory size");
     int n = 0;
     if (st == BSS_OK)
         st = cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem), "occupancy");

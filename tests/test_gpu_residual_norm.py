@@ -1,4 +1,8 @@
 """residual_norm and its gradient against 64-bit references."""
+import subprocess
+import sys
+from pathlib import Path
+
 import pytest
 import torch
 
@@ -264,6 +268,34 @@ def test_infinite_stream_without_a_norm(bss, stream, y_norm):
     assert torch.isfinite(got[0][0]).all() and torch.isfinite(got[0][1]).all()
     for dx, dy in got[1:]:
         assert torch.equal(dx, got[0][0]) and torch.equal(dy, got[0][1])
+
+
+FIRST_CALL = """
+import torch
+import block_sparse_spatio_gb300 as bss
+x = torch.randn(16, {channels}, device="cuda").to(torch.{stream})
+mods = dict(zip(("scale", "shift", "gate"), torch.zeros(3, 1, {channels}, device="cuda")[:{folds}]))
+y = torch.zeros({channels}, device="cuda").to(torch.{branch}).expand(16, -1) if {folds} > 2 else None
+h = torch.empty(16, {channels}, device="cuda", dtype=torch.{branch})
+bss.residual_norm(x, y=y, h=h, **mods)
+ref = torch.nn.functional.layer_norm(x.double(), ({channels},), eps=1e-6)
+assert (h.double() - ref).abs().max() <= 2.0 ** -8 * ref.abs().max() + 1e-4
+print("ran")
+"""
+# Calls whose dynamic shared memory alone just fits 48 KiB, with static memory no
+# longer.  Each is its process's first: a larger call before it would have raised
+# the kernel's limit.  channels, stream, branch, vectors folded
+FIRST_CALLS = [(2048, "float32", "float32", 0), (1536, "float32", "bfloat16", 2), (2048, "bfloat16", "bfloat16", 3),
+               (1024, "bfloat16", "bfloat16", 2)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("channels,stream,branch,folds", FIRST_CALLS)
+def test_first_call_of_a_process(channels, stream, branch, folds):
+    code = FIRST_CALL.format(channels=channels, stream=stream, branch=branch, folds=folds)
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True,
+                         timeout=300, cwd=Path(__file__).resolve().parents[1])
+    assert out.returncode == 0 and "ran" in out.stdout, out.stderr[-600:]
 
 
 @pytest.mark.gpu
