@@ -871,7 +871,7 @@ GradShape grad_shape(const bss_residual_norm_grads& a) {
     s.groups = (a.rows + per_group - 1) / per_group;
     // one wave of blocks: 16 warps an SM at 128 registers a thread, or what the
     // slots leave room for
-    int per_sm = 512 / s.threads, by_smem = 224 * 1024 / (s.smem + 3072);
+    int per_sm = 512 / s.threads, by_smem = 224 * 1024 / (s.smem + 3 * 1024);
     per_sm = per_sm < by_smem ? per_sm : by_smem;
     int64_t most = (per_sm < 1 ? 1 : per_sm) * static_cast<int64_t>(num_sms()) / s.groups;
     if (most < 1) most = 1;
