@@ -623,7 +623,9 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
                     }
                     const V8 xr = mul(x, r);
                     V8& d = dw[k][kToken ? j : 0];
-                    d = fma8(v, xr, d);  // zeros where there is no piece
+                    // the norm over a head keeps one sum for all of a lane's pieces: those that do not
+                    // exist stay out (with eps = 0 their r is infinite, and 0 times it no zero)
+                    if (kToken || live) d = fma8(v, xr, d);
                     v = fma8(xr, m, mul(gw, r));
                 }
                 if (live) st_row(to, pack_bf16<!HALVES>(v));
