@@ -776,7 +776,7 @@ bss_status check_overlaps(const Named* t, int n) {
         for (int j = 0; j < n; ++j) {
             if (j == i || t[j].p == nullptr || (t[j].output && j < i)) continue;
             if (!t[j].output && t[i].same != nullptr && t[j].p == t[i].same && t[i].p == t[j].p &&
-                t[i].r.stride == t[j].r.stride && t[i].r.extent == t[j].r.extent && !t[j].r.self_overlap)
+                t[i].r.s0 == t[j].r.s0 && t[i].r.width == t[j].r.width && !t[j].r.self_overlap)
                 continue;
             if (!disjoint(t[i].r, t[j].r)) return set_error(BSS_ERR_INVALID_ARG, "an output overlaps another tensor");
         }

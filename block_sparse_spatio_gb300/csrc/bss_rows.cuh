@@ -1,15 +1,14 @@
 // bss_rows.cuh -- what the row operators around the attention step share:
-// 8-channel vectors of bf16 or float rows, sums over parts of a block, the
-// fixed-order sum of per-block partial results, and host-side overlap checks of
-// strided tensors.
+// 8-channel vectors of bf16 or float rows, sums over parts of a block and the
+// launch of a kernel behind another (the rest of the host side: bss_host.h).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
-#include <mutex>
 
 #include "bss_block.h"
+#include "bss_host.h"
 #include "bss_internal.h"
 #include "bss_ptx.cuh"
 
@@ -250,45 +249,6 @@ struct FastDiv {
 };
 
 // ---------------------------------------------------------------- host side
-inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
-// Blocks of a kernel that an SM holds at once, and the kernel allowed its dynamic
-// shared memory.  Asked of the runtime once per kernel, size and device (up to as
-// many as are kept).
-inline bss_status resident_blocks(const void* kernel, int threads, int smem, int* blocks) {
-    struct Known {
-        const void* kernel;
-        int device, threads, smem, blocks;
-    };
-    constexpr int kKept = 512;
-    static std::mutex mutex;
-    static Known known[kKept];
-    static int count = 0;
-    int device = 0;
-    bss_status st = cuda_check(cudaGetDevice(&device), "current device");
-    if (st != BSS_OK) return st;
-    std::lock_guard<std::mutex> lock(mutex);
-    int most = smem;  // the limit only grows: another size of the kernel may be in use
-    for (int i = 0; i < count; ++i) {
-        const Known& k = known[i];
-        if (k.kernel != kernel || k.device != device) continue;
-        if (k.threads == threads && k.smem == smem) {
-            *blocks = k.blocks;
-            return BSS_OK;
-        }
-        if (k.smem > most) most = k.smem;
-    }
-    // below 48 KiB too: what a kernel may use unasked includes its static memory
-    st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "shared memory size");
-    int n = 0;
-    if (st == BSS_OK)
-        st = cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem), "occupancy");
-    if (st != BSS_OK) return st;
-    *blocks = n < 1 ? 1 : n;
-    if (count < kKept) known[count++] = {kernel, device, threads, smem, *blocks};
-    return BSS_OK;
-}
-
 // A kernel launched behind another one of the same stream, its launch overlapping
 // that one's end: it calls cudaGridDependencySynchronize() before it reads what
 // the other wrote.
@@ -305,62 +265,6 @@ bss_status launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cuda
     config.attrs = &attribute;
     config.numAttrs = 1;
     return cuda_check(cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...), what);
-}
-
-// The bytes that a strided tensor touches: `n` runs of `extent` bytes, `stride`
-// bytes apart.
-struct Region {
-    uintptr_t lo = 0;
-    int64_t n = 0, stride = 0, extent = 0;
-    bool self_overlap = false;
-    uintptr_t hi() const { return lo + static_cast<uintptr_t>((n - 1) * stride + extent); }
-};
-
-// rows x width elements
-inline Region region_2d(const void* p, int64_t rows, int64_t stride, int64_t width, int64_t esize) {
-    Region r;
-    r.lo = reinterpret_cast<uintptr_t>(p);
-    r.n = rows;
-    r.stride = rows > 1 ? stride * esize : 0;
-    r.extent = width * esize;
-    r.self_overlap = rows > 1 && stride < width;
-    return r;
-}
-
-// [n0][n1][width] elements with strides s0, s1: runs over the larger stride
-inline Region region_3d(const void* p, int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t width, int64_t esize) {
-    if (n0 <= 1) s0 = 0;
-    if (n1 <= 1) s1 = 0;
-    if (n1 > 1 && (n0 <= 1 || s1 > s0)) {
-        int64_t t = n0;
-        n0 = n1, n1 = t;
-        t = s0, s0 = s1, s1 = t;
-    }
-    Region r;
-    r.lo = reinterpret_cast<uintptr_t>(p);
-    const int64_t inner = (n1 - 1) * s1 + width;
-    r.self_overlap = (n1 > 1 && s1 < width) || (n0 > 1 && s0 < inner);
-    if (n0 > 1 && s0 < inner) {  // interleaved or broadcast: one run over everything
-        r.n = 1;
-        r.extent = ((n0 - 1) * s0 + inner) * esize;
-        return r;
-    }
-    r.n = n0;
-    r.stride = s0 * esize;
-    r.extent = inner * esize;
-    return r;
-}
-
-// Whether two tensors certainly share no byte (views of one tensor that differ
-// in a column range are told apart when their runs have the same stride).
-inline bool disjoint(const Region& a, const Region& b) {
-    if (a.hi() <= b.lo || b.hi() <= a.lo) return true;
-    if (a.n <= 1 || b.n <= 1 || a.stride != b.stride || a.stride == 0) return false;
-    const int64_t s = a.stride;
-    int64_t d = static_cast<int64_t>(b.lo) - static_cast<int64_t>(a.lo);
-    d %= s;
-    if (d < 0) d += s;
-    return d >= a.extent && s - d >= b.extent;
 }
 
 }  // namespace bss

@@ -1,0 +1,60 @@
+"""The host side of the operators around the attention step, by a host program
+that compiles it alone (``host_checks.cpp``), and through the C ABI on the CPU."""
+import os
+import subprocess
+
+import pytest
+
+import block_sparse_spatio_gb300 as bss
+from block_sparse_spatio_gb300 import build as nb
+from test_block_args import INVALID, backward, tokens
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+NO_DEVICE = 3  # BSS_ERR_CUDA: every check passed, there is nothing to launch on
+
+
+@pytest.fixture(scope="module")
+def lib():
+    nb.build()
+    return bss.load()
+
+
+@pytest.fixture(scope="module")
+def program(tmp_path_factory):
+    out = str(tmp_path_factory.mktemp("host") / "host_checks")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nb.nvcc()))), "include")
+    for name in (cuda, "/usr/local/cuda/include"):
+        if os.path.exists(os.path.join(name, "cuda_runtime_api.h")):
+            cuda = name
+    res = subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", nb.INCLUDE, "-I", nb.CSRC, "-I", cuda,
+                          os.path.join(HERE, "host_checks.cpp"), "-o", out], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-2000:]
+    return out
+
+
+def run(program, what):
+    res = subprocess.run([program, what], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout[-1000:]
+
+
+def test_overlap_of_strided_tensors(program):
+    run(program, "regions")
+
+
+@pytest.fixture
+def no_gpu():
+    """Calls that pass every check on made-up addresses: only where nothing can be launched."""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("made-up addresses, never on a machine with a GPU")
+
+
+@pytest.mark.parametrize("H,d", [(1, 128), (2, 128), (10, 64)])
+def test_gradients_packed_head_by_head(lib, no_gpu, H, d):
+    """dq, dk and dv as views of one [N][H][3][d] or [H][N][3][d] tensor share no byte."""
+    p = bss.MaskParams(3, 4, 5, d, 1, 1)
+    for ts, hs in ((3 * H * d, 3 * d), (3 * d, p.N * 3 * d), (3 * H * d + 8, 3 * d)):
+        views = [tokens(0, data=(1 << 32) + 2 * i * d, token_stride=ts, head_stride=hs) for i in range(3)]
+        assert backward(lib, H=H, params=p, outs=views) == NO_DEVICE
+        views[1] = tokens(0, data=(1 << 32) + 2 * d - 16, token_stride=ts, head_stride=hs)  # 8 channels into dq
+        assert backward(lib, H=H, params=p, outs=views) == INVALID
