@@ -762,22 +762,26 @@ bss_status check_param(const void* p, const char* name, int64_t groups, int64_t 
 }
 
 // Inputs may be named twice; an output must share no byte with any other tensor,
-// but for the pairs that may be the same tensor.
+// but for the input that it may be written over (`over`, its place in the list; -1:
+// none), and further row tensors that name the very same bytes as that one: a row is
+// in its threads' hands before any of it is stored.  Parameters never are: other rows
+// read them later.
 struct Named {
     const void* p;
     Region r;
     bool output;
-    const void* same;  // the input this output may equal
+    int over;
 };
 
-bss_status check_overlaps(const Named* t, int n) {
+// `rows`: the first so many are the call's row inputs.
+bss_status check_overlaps(const Named* t, int n, int rows) {
     for (int i = 0; i < n; ++i) {
         if (t[i].p == nullptr || !t[i].output) continue;
+        const Named* over = t[i].over < 0 ? nullptr : &t[t[i].over];
+        const bool in_place = over != nullptr && over->p != nullptr && over->r.same_bytes(t[i].r) && !t[i].r.self_overlap;
         for (int j = 0; j < n; ++j) {
             if (j == i || t[j].p == nullptr || (t[j].output && j < i)) continue;
-            if (!t[j].output && t[i].same != nullptr && t[j].p == t[i].same && t[i].p == t[j].p &&
-                t[i].r.s0 == t[j].r.s0 && t[i].r.width == t[j].r.width && !t[j].r.self_overlap)
-                continue;
+            if (in_place && j < rows && t[j].r.same_bytes(t[i].r) && !t[j].r.self_overlap) continue;
             if (!disjoint(t[i].r, t[j].r)) return set_error(BSS_ERR_INVALID_ARG, "an output overlaps another tensor");
         }
     }
@@ -945,10 +949,10 @@ bss_status bss_residual_norm(const bss_residual_norm_args* args, cudaStream_t st
     if (!is_aligned(a.stats, 8) || !is_aligned(a.y_stats, 8))
         return set_error(BSS_ERR_INVALID_ARG, "statistics must be 8-byte aligned");
     const int64_t groups = (a.rows + a.rows_per_group - 1) / a.rows_per_group;
-    Named t[12] = {{a.x, {}, false, nullptr},     {a.y, {}, false, nullptr},        {a.gate, {}, false, nullptr},
-                   {a.scale, {}, false, nullptr}, {a.shift, {}, false, nullptr},    {a.weight, {}, false, nullptr},
-                   {a.bias, {}, false, nullptr},  {a.y_weight, {}, false, nullptr}, {a.r, {}, true, a.x},
-                   {a.h, {}, true, a.y},          {a.stats, {}, true, nullptr},     {a.y_stats, {}, true, nullptr}};
+    Named t[12] = {{a.x, {}, false, -1},     {a.y, {}, false, -1},        {a.gate, {}, false, -1},
+                   {a.scale, {}, false, -1}, {a.shift, {}, false, -1},    {a.weight, {}, false, -1},
+                   {a.bias, {}, false, -1},  {a.y_weight, {}, false, -1}, {a.r, {}, true, 0},
+                   {a.h, {}, true, 1},       {a.stats, {}, true, -1},     {a.y_stats, {}, true, -1}};
     if ((st = check_rows(a.x, "x", a.rows, a.x_stride, a.channels, a.stream_dtype, false, &t[0].r)) != BSS_OK ||
         (st = check_rows(a.y, "y", a.rows, a.y_stride, a.channels, a.branch_dtype, false, &t[1].r)) != BSS_OK ||
         (st = check_param(a.gate, "gate", groups, a.gate_stride, a.channels, a.param_dtype, &t[2].r)) != BSS_OK ||
@@ -962,7 +966,7 @@ bss_status bss_residual_norm(const bss_residual_norm_args* args, cudaStream_t st
         return st;
     t[10].r = region_2d(a.stats, 1, 0, 2 * a.rows, 4);
     t[11].r = region_2d(a.y_stats, 1, 0, 2 * a.rows, 4);
-    if ((st = check_overlaps(t, 12)) != BSS_OK) return st;
+    if ((st = check_overlaps(t, 12, 2)) != BSS_OK) return st;
     if (groups == 1) a.gate_stride = a.scale_stride = a.shift_stride = 0;
     if (a.stream_dtype == BSS_DTYPE_BF16) return forward_of<__nv_bfloat16, __nv_bfloat16>(a, stream);
     if (a.branch_dtype == BSS_DTYPE_BF16) return forward_of<float, __nv_bfloat16>(a, stream);
@@ -1016,13 +1020,13 @@ bss_status bss_residual_norm_backward(const bss_residual_norm_grads* args, cudaS
     const void* r = a.dh != nullptr ? a.r : nullptr;
     const void* stats = a.dh != nullptr && a.norm != BSS_NORM_NONE ? a.stats : nullptr;
     const void* ystats = a.y_norm != BSS_NORM_NONE ? a.y_stats : nullptr;
-    Named t[20] = {{r, {}, false, nullptr},          {a.y, {}, false, nullptr},      {a.dr, {}, false, nullptr},
-                   {a.dh, {}, false, nullptr},       {a.gate, {}, false, nullptr},   {a.scale, {}, false, nullptr},
-                   {a.weight, {}, false, nullptr},   {a.bias, {}, false, nullptr},   {a.y_weight, {}, false, nullptr},
-                   {stats, {}, false, nullptr},      {ystats, {}, false, nullptr},   {a.dx, {}, true, a.dr},
-                   {a.dy, {}, true, a.dh},           {a.dgate, {}, true, nullptr},   {a.dscale, {}, true, nullptr},
-                   {a.dshift, {}, true, nullptr},    {a.dweight, {}, true, nullptr}, {a.dbias, {}, true, nullptr},
-                   {a.dy_weight, {}, true, nullptr}, {need > 0 ? a.workspace : nullptr, {}, true, nullptr}};
+    Named t[20] = {{r, {}, false, -1},          {a.y, {}, false, -1},      {a.dr, {}, false, -1},
+                   {a.dh, {}, false, -1},       {a.gate, {}, false, -1},   {a.scale, {}, false, -1},
+                   {a.weight, {}, false, -1},   {a.bias, {}, false, -1},   {a.y_weight, {}, false, -1},
+                   {stats, {}, false, -1},      {ystats, {}, false, -1},   {a.dx, {}, true, 2},
+                   {a.dy, {}, true, 3},         {a.dgate, {}, true, -1},   {a.dscale, {}, true, -1},
+                   {a.dshift, {}, true, -1},    {a.dweight, {}, true, -1}, {a.dbias, {}, true, -1},
+                   {a.dy_weight, {}, true, -1}, {need > 0 ? a.workspace : nullptr, {}, true, -1}};
     if ((st = check_rows(r, "r", a.rows, a.r_stride, a.channels, a.stream_dtype, false, &t[0].r)) != BSS_OK ||
         (st = check_rows(a.y, "y", a.rows, a.y_stride, a.channels, a.branch_dtype, false, &t[1].r)) != BSS_OK ||
         (st = check_rows(a.dr, "dr", a.rows, a.dr_stride, a.channels, a.stream_dtype, false, &t[2].r)) != BSS_OK ||
@@ -1039,7 +1043,7 @@ bss_status bss_residual_norm_backward(const bss_residual_norm_grads* args, cudaS
     t[10].r = region_2d(ystats, 1, 0, 2 * a.rows, 4);
     for (int i = 13; i < 19; ++i) t[i].r = region_2d(t[i].p, 1, 0, (i < 16 ? groups : 1) * a.channels, 4);
     t[19].r = region_2d(a.workspace, 1, 0, need, 1);
-    if ((st = check_overlaps(t, 20)) != BSS_OK) return st;
+    if ((st = check_overlaps(t, 20, 4)) != BSS_OK) return st;
     if (groups == 1) a.gate_stride = a.scale_stride = 0;
     if (a.dh == nullptr) a.norm = BSS_NORM_NONE;
     a.rows_per_group = g.s.groups == 1 ? a.rows : a.rows_per_group;

@@ -7,7 +7,7 @@ import pytest
 
 import block_sparse_spatio_gb300 as bss
 from block_sparse_spatio_gb300 import build as nb
-from test_block_args import INVALID, backward, tokens
+from test_block_args import INVALID, backward, norm_args, ptr, tokens
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 NO_DEVICE = 3  # BSS_ERR_CUDA: every check passed, there is nothing to launch on
@@ -58,3 +58,37 @@ def test_gradients_packed_head_by_head(lib, no_gpu, H, d):
         assert backward(lib, H=H, params=p, outs=views) == NO_DEVICE
         views[1] = tokens(0, data=(1 << 32) + 2 * d - 16, token_stride=ts, head_stride=hs)  # 8 channels into dq
         assert backward(lib, H=H, params=p, outs=views) == INVALID
+
+
+# Outputs written over their input, with a parameter at the same address: rows would
+# read modulations that other rows have overwritten.  bf16 parameters, 64 channels.
+OVER_FORWARD = [dict(r=ptr(0), **{k: ptr(0), k + "_stride": 64}) for k in ("gate", "scale", "shift")] + [
+    dict(h=ptr(1), **{k: ptr(1), k + "_stride": 64}) for k in ("gate", "scale", "shift")] + [
+    dict(r=ptr(0), scale=ptr(0), scale_stride=64, rows_per_group=1), dict(r=ptr(0), weight=ptr(0), rows=1),
+    dict(h=ptr(1), y_weight=ptr(1), rows=1), dict(h=ptr(1), bias=ptr(1), rows=1),
+    dict(r=ptr(0), h=None, gate=ptr(0), gate_stride=64)]
+OVER_BACKWARD = [dict(dx=ptr(2), **{k: ptr(2), k + "_stride": 64}) for k in ("gate", "scale")] + [
+    dict(dy=ptr(3), **{k: ptr(3), k + "_stride": 64}) for k in ("gate", "scale")] + [
+    dict(dx=ptr(2), weight=ptr(2), rows=1), dict(dy=ptr(3), y_weight=ptr(3), rows=1),
+    dict(dx=ptr(2), scale=ptr(2), scale_stride=64, rows_per_group=1), dict(dx=ptr(2), stats=ptr(2)),
+    dict(dx=ptr(3), dr=None), dict(dy=ptr(2), dx=ptr(5))]
+
+
+@pytest.mark.parametrize("kw", OVER_FORWARD)
+def test_norm_in_place_refuses_parameters_there(lib, no_gpu, kw):
+    assert lib.bss_residual_norm(norm_args(bss._ResidualNormArgs, param_dtype=0, **kw), None) == INVALID
+
+
+@pytest.mark.parametrize("kw", OVER_BACKWARD)
+def test_norm_backward_in_place_refuses_parameters_there(lib, no_gpu, kw):
+    assert lib.bss_residual_norm_backward(norm_args(bss._ResidualNormGrads, param_dtype=0, **kw), None) == INVALID
+
+
+def test_norm_in_place_still_taken(lib, no_gpu):
+    """Over the paired input, also where another row input is that same tensor."""
+    for kw in (dict(r=ptr(0)), dict(h=ptr(1)), dict(r=ptr(0), h=ptr(1)), dict(y=ptr(0), r=ptr(0)),
+               dict(y=ptr(0), h=ptr(0)), dict(r=ptr(0), rows=1, x_stride=8, r_stride=24)):
+        assert lib.bss_residual_norm(norm_args(bss._ResidualNormArgs, **kw), None) == NO_DEVICE
+    for kw in (dict(dx=ptr(2)), dict(dy=ptr(3)), dict(dx=ptr(2), dy=ptr(3)), dict(r=ptr(2), dx=ptr(2)),
+               dict(y=ptr(3), dy=ptr(3)), dict(dr=ptr(3), dx=ptr(3))):
+        assert lib.bss_residual_norm_backward(norm_args(bss._ResidualNormGrads, **kw), None) == NO_DEVICE
