@@ -836,6 +836,39 @@ bss_status set_options(const bss_heads_options* o, const bss_mask_params* p, int
     return BSS_OK;
 }
 
+// What a call reads and what it writes: no byte is both, nor written twice.
+struct Touched {
+    Region in[16], out[6];
+    int ins = 0, outs = 0;
+    void read(const Region& r) { in[ins++] = r; }
+    void write(const Region& r) { out[outs++] = r; }
+    void read(const void* p, int64_t bytes) {
+        if (p != nullptr && bytes > 0) read(region_2d(p, 1, 0, bytes, 1));
+    }
+    void write(const void* p, int64_t bytes) {
+        if (p != nullptr && bytes > 0) write(region_2d(p, 1, 0, bytes, 1));
+    }
+    // weights, rotary tables and flags
+    void read_options(const HeadsArgs& a, const bss_heads_options* o, int32_t d) {
+        if (o->norm != BSS_HEAD_NORM_NONE) {
+            const int64_t width = o->norm == BSS_HEAD_NORM_TOKEN ? static_cast<int64_t>(a.H) * d : d;
+            for (const void* w : a.weight) read(w, width * (a.weight_dtype == BSS_DTYPE_F32 ? 4 : 2));
+        }
+        for (int i = 0; i < 3; ++i)
+            if (a.rot.pairs[i] > 0) read(a.rot.table[i], static_cast<int64_t>(o->rotary->length[i]) * a.rot.pairs[i] * 8);
+        read(a.flags, a.H);
+    }
+    bss_status check() const {
+        for (int i = 0; i < outs; ++i) {
+            for (int j = 0; j < ins; ++j)
+                if (!disjoint(out[i], in[j])) return set_error(BSS_ERR_INVALID_ARG, "an output overlaps an input");
+            for (int j = 0; j < i; ++j)
+                if (!disjoint(out[i], out[j])) return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
+        }
+        return BSS_OK;
+    }
+};
+
 using Kernel = void (*)(const HeadsArgs);
 
 template <bool HALVES, int NORM>
@@ -963,7 +996,8 @@ bss_status bss_heads_from_tokens(const bss_token_tensor* q, const bss_token_tens
     const bss_token_tensor* in[3] = {q, k, v};
     void* out[3] = {Qh, Kh, Vh};
     const char* names[3] = {"q", "k", "v"};
-    Region rin[3], rout[3];
+    Touched touched;
+    Region r;
     int given = 0;
     for (int i = 0; i < 3; ++i) {
         const bool has = in[i] != nullptr && in[i]->data != nullptr;
@@ -971,22 +1005,18 @@ bss_status bss_heads_from_tokens(const bss_token_tensor* q, const bss_token_tens
             return set_error(BSS_ERR_INVALID_ARG, "%s and its output must be given together", names[i]);
         if (!has) continue;
         ++given;
-        if ((st = check_tokens(in[i], names[i], a.N, H, d, &rin[i])) != BSS_OK) return st;
+        if ((st = check_tokens(in[i], names[i], a.N, H, d, &r)) != BSS_OK) return st;
         if (!is_aligned(out[i], 16)) return set_error(BSS_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
-        rout[i] = region_2d(out[i], 1, 0, static_cast<int64_t>(H) * a.N * d, 2);
+        touched.read(r);
+        touched.write(out[i], static_cast<int64_t>(H) * a.N * d * 2);
         a.in[i] = static_cast<const __nv_bfloat16*>(in[i]->data);
         a.out[i] = static_cast<__nv_bfloat16*>(out[i]);
         a.ts[i] = a.N > 1 ? static_cast<uint32_t>(in[i]->token_stride * 2) : 0;
         a.hs[i] = H > 1 ? in[i]->head_stride : 0;
     }
     if (given == 0) return set_error(BSS_ERR_INVALID_ARG, "no tensor given");
-    for (int i = 0; i < 3; ++i)
-        for (int j = 0; j < 3; ++j) {
-            if (a.out[i] != nullptr && a.in[j] != nullptr && !disjoint(rout[i], rin[j]))
-                return set_error(BSS_ERR_INVALID_ARG, "an output overlaps an input");
-            if (j < i && a.out[i] != nullptr && a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
-                return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
-        }
+    touched.read_options(a, options, d);
+    if ((st = touched.check()) != BSS_OK) return st;
     const Shape s = shape_of(H, d / 8, options->norm, a.N, false);
     set_shape(s, options->norm, d, &a);
     int blocks = 0;
@@ -1033,8 +1063,8 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
     float* dweight[2] = {dq_weight, dk_weight};
     const char* names[3] = {"dq", "dk", "dv"};
     const char* xnames[2] = {"q", "k"};
-    Region rin[5], rout[3];
-    bool has_x[2] = {false, false};
+    Touched touched;
+    Region r;
     int given = 0;
     for (int i = 0; i < 3; ++i) {
         const bool has = grad[i] != nullptr;
@@ -1045,9 +1075,10 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
         if (!has) continue;
         ++given;
         if (!is_aligned(grad[i], 16)) return set_error(BSS_ERR_INVALID_ARG, "gradients must be 16-byte aligned");
-        rin[i] = region_2d(grad[i], 1, 0, static_cast<int64_t>(H) * a.N * d, 2);
-        if ((st = check_tokens(out[i], names[i], a.N, H, d, &rout[i])) != BSS_OK) return st;
-        if (rout[i].self_overlap) return set_error(BSS_ERR_INVALID_ARG, "%s overlaps itself", names[i]);
+        touched.read(grad[i], static_cast<int64_t>(H) * a.N * d * 2);
+        if ((st = check_tokens(out[i], names[i], a.N, H, d, &r)) != BSS_OK) return st;
+        if (r.self_overlap) return set_error(BSS_ERR_INVALID_ARG, "%s overlaps itself", names[i]);
+        touched.write(r);
         a.in[i] = static_cast<const __nv_bfloat16*>(grad[i]);
         a.out[i] = static_cast<__nv_bfloat16*>(out[i]->data);
         a.ts[i] = a.N > 1 ? static_cast<uint32_t>(out[i]->token_stride * 2) : 0;
@@ -1055,22 +1086,13 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
         if (i == 2 || norm == BSS_HEAD_NORM_NONE) continue;
         if (x[i] == nullptr || x[i]->data == nullptr)
             return set_error(BSS_ERR_INVALID_ARG, "the norm's gradient needs %s", xnames[i]);
-        if ((st = check_tokens(x[i], xnames[i], a.N, H, d, &rin[3 + i])) != BSS_OK) return st;
-        has_x[i] = true;
+        if ((st = check_tokens(x[i], xnames[i], a.N, H, d, &r)) != BSS_OK) return st;
+        touched.read(r);
         a.x[i] = static_cast<const __nv_bfloat16*>(x[i]->data);
         a.xts[i] = a.N > 1 ? static_cast<uint32_t>(x[i]->token_stride * 2) : 0;
         a.xhs[i] = H > 1 ? x[i]->head_stride : 0;
     }
     if (given == 0) return set_error(BSS_ERR_INVALID_ARG, "no tensor given");
-    for (int i = 0; i < 3; ++i) {
-        if (a.out[i] == nullptr) continue;
-        for (int j = 0; j < 5; ++j)
-            if ((j < 3 ? a.in[j] != nullptr : has_x[j - 3]) && !disjoint(rout[i], rin[j]))
-                return set_error(BSS_ERR_INVALID_ARG, "an output overlaps an input");
-        for (int j = 0; j < i; ++j)
-            if (a.out[j] != nullptr && !disjoint(rout[i], rout[j]))
-                return set_error(BSS_ERR_INVALID_ARG, "outputs overlap");
-    }
     const Shape s = shape_of(H, d / 8, norm, a.N, true);
     set_shape(s, norm, d, &a);
     const bool want = dq_weight != nullptr || dk_weight != nullptr;
@@ -1083,7 +1105,12 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
             return set_error(BSS_ERR_INVALID_ARG, "the workspace must be 16-byte aligned and hold %lld bytes",
                              static_cast<long long>(need));
         a.partial = static_cast<float*>(workspace);
+        touched.write(dq_weight, 4 * width);
+        touched.write(dk_weight, 4 * width);
+        touched.write(workspace, need);
     }
+    touched.read_options(a, options, d);
+    if ((st = touched.check()) != BSS_OK) return st;
     int blocks = 0;
     st = launch(true, pairing, norm, a, s, stream, "heads backward launch", &blocks);
     if (st != BSS_OK || !want) return st;
@@ -1108,13 +1135,17 @@ bss_status bss_attention_step_tokens(const bss_token_tensor* q, const bss_token_
     int device = 0;
     cudaGetDevice(&device);
     if (device != map->device) return set_error(BSS_ERR_INVALID_ARG, "tile map belongs to device %d", map->device);
-    if (H <= 0) return set_error(BSS_ERR_INVALID_ARG, "H must be positive");
-    const int64_t elements = static_cast<int64_t>(H) * map->g.N * map->p.head_dim;
-    for (const void* p : {Qh, Kh, Vh})
-        if (!disjoint(region_2d(O, 1, 0, elements, 2), region_2d(p, 1, 0, elements, 2)))
-            return set_error(BSS_ERR_INVALID_ARG, "O overlaps a workspace");
+    bss_status st = check_geometry(&map->p, H);
+    if (st != BSS_OK) return st;
+    // of both launches; the heads call checks its inputs against the workspaces
+    const int64_t bytes = static_cast<int64_t>(H) * map->g.N * map->p.head_dim * 2;
+    Touched touched;
+    touched.read(head_is_temporal, H);
+    for (const void* p : {O, Qh, Kh, Vh}) touched.write(p, bytes);
+    touched.write(lse, static_cast<int64_t>(H) * map->g.N * 4);
+    if ((st = touched.check()) != BSS_OK) return st;
     const uint8_t* permuted = map->p.temporal_permuted ? head_is_temporal : nullptr;
-    const bss_status st = bss_heads_from_tokens(q, k, v, Qh, Kh, Vh, permuted, H, &map->p, options, stream);
+    st = bss_heads_from_tokens(q, k, v, Qh, Kh, Vh, permuted, H, &map->p, options, stream);
     if (st != BSS_OK) return st;
     if (permuted == nullptr)
         return bss_sparse_attention(Qh, Kh, Vh, O, lse, map, head_is_temporal, H, 0.0f, stream);

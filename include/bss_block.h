@@ -117,7 +117,8 @@ typedef struct {
  *   q, k, v     token-major inputs; any may be left out (data NULL) together
  *               with its output.  They are not written.
  *   Qh, Kh, Vh  device [H][N][d] bf16 outputs, 16-byte aligned, overlapping
- *               neither an input nor each other.
+ *               neither each other nor anything the call reads (weights, rotary
+ *               tables and flags too).
  *   head_is_temporal  device uint8[H], NULL = no head permuted.
  * The results are what bss_sparse_attention takes for a map built with
  * temporal_permuted = 1.  Only F, Hs, Ws and head_dim of params are used.
@@ -137,15 +138,17 @@ bss_status bss_heads_from_tokens_backward_workspace(int32_t H, const bss_mask_pa
  *                  the layout it was written in; any may be NULL together with
  *                  its dq, dk or dv (data NULL).
  *   q, k           the forward inputs; read only with a norm (else may be NULL).
- *   dq, dk, dv     token-major outputs, any strides that do not make a tensor
- *                  overlap itself; they may be views of one packed tensor.  They
- *                  must overlap no input.
+ *   dq, dk, dv     token-major outputs: all heads of a token lie within the token
+ *                  stride, or all tokens of a head within the head stride.  They
+ *                  may be views of one tensor, packed token by token ([N][3][H][d])
+ *                  or head by head ([N][H][3][d]).
  *   dq_weight, dk_weight  device float [head_dim] or [H * head_dim] (by the norm)
  *                  gradients of the weights, overwritten; NULL = not wanted.
  *   workspace      device memory of at least the size that
  *                  bss_heads_from_tokens_backward_workspace gives, 16-byte
  *                  aligned, used by this call only until its work is done; NULL
  *                  when no weight gradient is wanted.
+ * No output, nor the workspace, may overlap another or anything the call reads.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, const void* dVh,
                                           const bss_token_tensor* q, const bss_token_tensor* k,
@@ -161,7 +164,8 @@ bss_status bss_heads_from_tokens_backward(const void* dQh, const void* dKh, cons
  * order.  With a map built with temporal_permuted = 0, or head_is_temporal =
  * NULL, no head is permuted.  The same result as bss_heads_from_tokens without
  * flags followed by bss_attention_step, with one pass over Q, K, V less.  q, k
- * and v must all be given.  Two launches.  lse as in bss_attention_step.
+ * and v must all be given.  Two launches.  lse as in bss_attention_step.  O, lse,
+ * Qh, Kh, Vh and the flags must not overlap one another.
  * Errors: those of the calls it makes. */
 bss_status bss_attention_step_tokens(const bss_token_tensor* q, const bss_token_tensor* k,
                                      const bss_token_tensor* v, void* O, float* lse, bss_tile_map map,

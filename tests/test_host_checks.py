@@ -7,7 +7,7 @@ import pytest
 
 import block_sparse_spatio_gb300 as bss
 from block_sparse_spatio_gb300 import build as nb
-from test_block_args import INVALID, backward, norm_args, ptr, tokens
+from test_block_args import INVALID, backward, forward, norm_args, ptr, rotary, tokens
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 NO_DEVICE = 3  # BSS_ERR_CUDA: every check passed, there is nothing to launch on
@@ -92,3 +92,30 @@ def test_norm_in_place_still_taken(lib, no_gpu):
     for kw in (dict(dx=ptr(2)), dict(dy=ptr(3)), dict(dx=ptr(2), dy=ptr(3)), dict(r=ptr(2), dx=ptr(2)),
                dict(y=ptr(3), dy=ptr(3)), dict(dr=ptr(3), dx=ptr(3))):
         assert lib.bss_residual_norm_backward(norm_args(bss._ResidualNormGrads, **kw), None) == NO_DEVICE
+
+
+# heads: addresses 0 .. 2 are the token-major tensors, 3 .. 5 the head-major ones
+@pytest.mark.parametrize("norm", [1, 2])
+def test_heads_refuse_outputs_over_what_is_read(lib, no_gpu, norm):
+    x = (tokens(6), tokens(7))
+    near = lambda i: ptr(i) + 64  # noqa: E731  inside the tensor
+    rot = lambda a, i: dict(rotary=rotary(tables=[near(i) if k == a else ptr(10 + k) for k in range(3)]))  # noqa: E731
+    for i in (3, 4, 5):  # outputs forward
+        for kw in (dict(qw=near(i)), dict(kw=near(i)), dict(flags=near(i)), rot(0, i), rot(1, i), rot(2, i)):
+            assert forward(lib, norm=norm, **kw) == INVALID
+    for i in (0, 1, 2):  # and back
+        for kw in (dict(qw=near(i)), dict(kw=near(i)), dict(flags=near(i)), rot(0, i), rot(2, i)):
+            assert backward(lib, norm=norm, x=x, **kw) == INVALID
+    good = dict(norm=norm, x=x, ws=ptr(22), ws_bytes=1 << 26, qw=ptr(23), kw=ptr(24), flags=ptr(25), rotary=rotary())
+    assert backward(lib, dw=(ptr(20), ptr(21)), **good) == NO_DEVICE
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 10, 22, 23, 24, 25):  # weight gradients over anything
+        assert backward(lib, dw=(ptr(i), ptr(21)), **good) == INVALID
+        assert backward(lib, dw=(ptr(20), ptr(i)), **good) == INVALID
+    assert backward(lib, dw=(ptr(20), ptr(20) + 16), **good) == INVALID
+    for i in (0, 1, 2, 3, 4, 5, 6, 7, 10, 20, 21, 23, 24, 25):  # the workspace too
+        assert backward(lib, dw=(ptr(20), ptr(21)), **{**good, "ws": ptr(i)}) == INVALID
+    # what is not read or written may lie anywhere: no weight gradient, no norm, an axis without pairs
+    assert backward(lib, **{**good, "ws": ptr(0)}) == NO_DEVICE
+    assert forward(lib, norm=0, qw=near(3)) == NO_DEVICE
+    r = rotary(pairs=(22, 0, 21), tables=(ptr(10), near(3), ptr(12)))
+    assert forward(lib, norm=norm, rotary=r) == NO_DEVICE
