@@ -13,9 +13,13 @@ namespace bss {
 
 inline bool is_aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Blocks of a kernel that an SM holds at once, and the kernel allowed its dynamic
-// shared memory.  Asked of the runtime once per kernel, size and device (up to as
-// many as are kept).
+// Blocks of a kernel that an SM holds at once with this much dynamic shared memory;
+// the kernel may use it afterwards.  A kernel's limit is always set to all that a
+// block may have beside the kernel's static memory, never to the size at hand: calls
+// of other sizes, also in other threads, then leave it as it is.  (Below 48 KiB too:
+// what a kernel may use unasked includes its static memory.)  The runtime is asked
+// once per kernel, size and device, as long as the answer is among those kept: the
+// last so many.
 inline bss_status resident_blocks(const void* kernel, int threads, int smem, int* blocks) {
     struct Known {
         const void* kernel;
@@ -24,29 +28,36 @@ inline bss_status resident_blocks(const void* kernel, int threads, int smem, int
     constexpr int kKept = 512;
     static std::mutex mutex;
     static Known known[kKept];
-    static int count = 0;
+    static int count = 0, next = 0;
     int device = 0;
     bss_status st = cuda_check(cudaGetDevice(&device), "current device");
     if (st != BSS_OK) return st;
-    std::lock_guard<std::mutex> lock(mutex);
-    int most = smem;  // the limit only grows: another size of the kernel may be in use
-    for (int i = 0; i < count; ++i) {
-        const Known& k = known[i];
-        if (k.kernel != kernel || k.device != device) continue;
-        if (k.threads == threads && k.smem == smem) {
-            *blocks = k.blocks;
-            return BSS_OK;
+    {
+        std::lock_guard<std::mutex> lock(mutex);
+        for (int i = 0; i < count; ++i) {
+            const Known& k = known[i];
+            if (k.kernel == kernel && k.device == device && k.threads == threads && k.smem == smem) {
+                *blocks = k.blocks;
+                return BSS_OK;
+            }
         }
-        if (k.smem > most) most = k.smem;
     }
-    // below 48 KiB too: what a kernel may use unasked includes its static memory
-    st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "shared memory size");
-    int n = 0;
+    cudaFuncAttributes attributes = {};
+    st = cuda_check(cudaFuncGetAttributes(&attributes, kernel), "kernel attributes");
+    int most = 0, n = 0;
+    if (st == BSS_OK)
+        st = cuda_check(cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, device), "shared memory of a block");
+    most -= static_cast<int>(attributes.sharedSizeBytes);
+    if (st == BSS_OK && attributes.maxDynamicSharedSizeBytes != most)
+        st = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "shared memory size");
     if (st == BSS_OK)
         st = cuda_check(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem), "occupancy");
     if (st != BSS_OK) return st;
     *blocks = n < 1 ? 1 : n;
-    if (count < kKept) known[count++] = {kernel, device, threads, smem, *blocks};
+    std::lock_guard<std::mutex> lock(mutex);
+    known[next] = {kernel, device, threads, smem, *blocks};
+    next = (next + 1) % kKept;
+    if (count < kKept) ++count;
     return BSS_OK;
 }
 

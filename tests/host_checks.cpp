@@ -1,9 +1,11 @@
 // Host program of the checks in bss_host.h: disjoint() against the bytes of small
-// strided tensors.
+// strided tensors, and launch sizes against a runtime that keeps each kernel's limit.
+#include <atomic>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <set>
+#include <thread>
 #include <vector>
 
 #include "bss_host.h"
@@ -13,12 +15,37 @@ bss_status set_error(bss_status st, const char*, ...) { return st; }
 bss_status cuda_check(cudaError_t e, const char*) { return e == cudaSuccess ? BSS_OK : BSS_ERR_CUDA; }
 }  // namespace bss
 
-// The runtime, as far as it is asked.
+// The runtime, as far as it is asked: kernels with their static memory and limit.
+namespace {
+constexpr int kOptin = 232448, kKernels = 4;
+struct Kernel {
+    std::atomic<int> limit{48 * 1024};
+    std::atomic<int> asked{0};
+    int fixed = 0;
+} kernels[kKernels];
+Kernel& of(const void* k) { return kernels[reinterpret_cast<uintptr_t>(k) - 1]; }
+}  // namespace
 extern "C" {
 cudaError_t cudaGetDevice(int* device) { return *device = 0, cudaSuccess; }
-cudaError_t cudaFuncSetAttribute(const void*, cudaFuncAttribute, int) { return cudaSuccess; }
-cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessor(int* n, const void*, int, size_t) {
-    return *n = 1, cudaSuccess;
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr a, int) {
+    *v = kOptin;
+    return a == cudaDevAttrMaxSharedMemoryPerBlockOptin ? cudaSuccess : cudaErrorInvalidValue;
+}
+cudaError_t cudaFuncGetAttributes(cudaFuncAttributes* a, const void* k) {
+    *a = {};
+    a->sharedSizeBytes = of(k).fixed;
+    a->maxDynamicSharedSizeBytes = of(k).limit;
+    return cudaSuccess;
+}
+cudaError_t cudaFuncSetAttribute(const void* k, cudaFuncAttribute a, int v) {
+    if (a != cudaFuncAttributeMaxDynamicSharedMemorySize || v + of(k).fixed > kOptin) return cudaErrorInvalidValue;
+    of(k).limit = v;
+    return cudaSuccess;
+}
+cudaError_t cudaOccupancyMaxActiveBlocksPerMultiprocessor(int* n, const void* k, int, size_t smem) {
+    ++of(k).asked;
+    *n = (kOptin + 1024) / (static_cast<int>(smem) + of(k).fixed + 1024);
+    return cudaSuccess;
 }
 }
 
@@ -96,9 +123,54 @@ int regions(int rounds) {
     return apart > rounds / 10 && touching > rounds / 10 ? 0 : 1;
 }
 
+bool may_launch(int kernel, int smem) {
+    int blocks = 0;
+    const void* k = reinterpret_cast<const void*>(static_cast<uintptr_t>(kernel + 1));
+    return bss::resident_blocks(k, 128, smem, &blocks) == BSS_OK && blocks >= 1;
+}
+
+// More sizes than are kept, large ones followed by small ones: a kernel's limit covers
+// its static memory and never falls below a size that was allowed (another thread may
+// be about to launch it).
+int limits() {
+    for (int k = 0; k < kKernels; ++k) kernels[k].fixed = k * 700;
+    for (int k = 0; k < kKernels; ++k) {
+        for (int i = 0; i < 600; ++i)
+            if (!may_launch(k, 64 + 32 * i)) return 1;
+        const int large = kOptin - kernels[k].fixed;
+        if (!may_launch(k, large) || kernels[k].limit < large) return 2;
+        for (int i = 0; i < 600; ++i) {
+            if (!may_launch(k, 96 + 16 * i)) return 3;
+            if (kernels[k].limit < large) return 4;
+        }
+    }
+    // a size in use is asked for once, whatever came before it
+    const int before = kernels[0].asked;
+    for (int i = 0; i < 100; ++i)
+        if (!may_launch(0, 100000)) return 5;
+    if (kernels[0].asked != before + 1) return 6;
+    // threads with sizes of their own
+    std::atomic<int> bad{0};
+    std::vector<std::thread> threads;
+    for (int t = 0; t < 4; ++t)
+        threads.emplace_back([&bad, t] {
+            for (int i = 0; i < 20000; ++i) {
+                const int smem = t == 0 ? 200000 : 64 + (i * 4 + t) % 9001;
+                if (!may_launch(1, smem) || kernels[1].limit < smem) ++bad;
+            }
+        });
+    for (std::thread& t : threads) t.join();
+    return bad == 0 ? 0 : 7;
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
     if (argc > 1 && !std::strcmp(argv[1], "regions")) return regions(200000);
+    if (argc > 1 && !std::strcmp(argv[1], "limits")) {
+        const int bad = limits();
+        std::printf("limits: check %d\n", bad);
+        return bad;
+    }
     return 2;
 }

@@ -41,6 +41,11 @@ def test_overlap_of_strided_tensors(program):
     run(program, "regions")
 
 
+def test_limits_of_many_launch_sizes(program):
+    """More sizes than the library keeps, also from several threads."""
+    run(program, "limits")
+
+
 @pytest.fixture
 def no_gpu():
     """Calls that pass every check on made-up addresses: only where nothing can be launched."""
