@@ -685,35 +685,39 @@ def _one_dtype(*named):
     return dtype
 
 
+def _empty_on(stream, *shape, dtype):
+    """Memory from torch's allocator that belongs to the stream the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    with torch.cuda.stream(stream):
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+
+
 def _workspace(workspace, nbytes, stream):
-    """The caller's workspace, or one from torch's allocator that belongs to the
-    stream the call runs on."""
+    """The caller's workspace, or one that belongs to the stream of the call."""
     import torch
     if workspace is not None:
         _on_device(workspace, "workspace", _current_device())
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         return workspace
-    if nbytes == 0:
-        return None
-    if stream is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    with torch.cuda.stream(stream):
-        return torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    return None if nbytes == 0 else _empty_on(stream, nbytes, dtype=torch.uint8)
 
 
 def rotary_table(length: int, pairs: int, base: float = 10000.0, dim: int | None = None, positions=None, out=None,
                  stream=None):
     """(cos, sin) of one rotary axis, float32 [length][pairs][2] (``bss_rotary_table``):
     position i (or positions[i], a float64 CUDA tensor) times base^(-2 j / dim) for
-    pair j; dim defaults to 2 * pairs.  Angles are taken in 64 bits."""
+    pair j; dim defaults to 2 * pairs.  Angles are taken in 64 bits.  A table that
+    the call makes (out None) belongs to its stream, like a tensor made there."""
     import torch
     if length <= 0 or pairs <= 0:
         raise ValueError("length and pairs must be positive")
     if out is None:
-        out = torch.empty(length, pairs, 2, dtype=torch.float32, device="cuda")
+        out = _empty_on(stream, length, pairs, 2, dtype=torch.float32)
     device = _current_device()
     _check(load().bss_rotary_table(_exact(positions, "positions", torch.float64, (length,), device), length, pairs,
                                    2 * pairs if dim is None else dim, float(base),
