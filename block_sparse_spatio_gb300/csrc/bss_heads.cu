@@ -618,14 +618,14 @@ __global__ void __launch_bounds__(32 * backward_warps(W), backward_blocks(W, VPT
                     else if (live)
                         gw = mul(v, weight(k, j));
                     if (!kToken) {
+                        // a piece that does not exist: zeros, whose root with eps = 0 is infinite
                         r = rsqrtf(head_sum(dot(x, x), a.pieces) * a.inv_width + a.eps);
+                        r = live ? r : 0.0f;
                         m = -r * r * (head_sum(dot(gw, x), a.pieces) * a.inv_width);
                     }
                     const V8 xr = mul(x, r);
                     V8& d = dw[k][kToken ? j : 0];
-                    // the norm over a head keeps one sum for all of a lane's pieces: those that do not
-                    // exist stay out (with eps = 0 their r is infinite, and 0 times it no zero)
-                    if (kToken || live) d = fma8(v, xr, d);
+                    d = fma8(v, xr, d);  // zeros where there is no piece
                     v = fma8(xr, m, mul(gw, r));
                 }
                 if (live) st_row(to, pack_bf16<!HALVES>(v));
