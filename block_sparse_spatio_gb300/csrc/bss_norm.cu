@@ -33,7 +33,9 @@ namespace {
 
 constexpr int kMaxChannels = 8192;
 constexpr int64_t kMaxStride = int64_t(1) << 28;  // elements between rows: a row's offset is one 32 x 32 bit product
-constexpr int kMinChunkRows = 4;  // rows a block of the backward pass reduces at least
+// A group's rows are shared by at most one block for every so many of them (5 rows: two
+// blocks of 3 and 2; groups of fewer rows: a block each).
+constexpr int kRowsPerChunk = 4;
 
 // ---------------------------------------------------------------- shared memory
 __device__ __forceinline__ uint4 lds128(uint32_t at) {
@@ -879,7 +881,7 @@ GradShape grad_shape(const bss_residual_norm_grads& a) {
     per_sm = per_sm < by_smem ? per_sm : by_smem;
     int64_t most = (per_sm < 1 ? 1 : per_sm) * static_cast<int64_t>(num_sms()) / s.groups;
     if (most < 1) most = 1;
-    s.chunks = (per_group + kMinChunkRows - 1) / kMinChunkRows;
+    s.chunks = (per_group + kRowsPerChunk - 1) / kRowsPerChunk;
     if (s.chunks > most) s.chunks = most;
     s.chunk_rows = (per_group + s.chunks - 1) / s.chunks;
     s.chunks = (per_group + s.chunk_rows - 1) / s.chunk_rows;

@@ -1,5 +1,5 @@
 // bss_rows.cuh -- what the row operators around the attention step share:
-// 8-channel vectors of bf16 or float rows, sums over parts of a block and the
+// 8-channel vectors and packed arithmetic, sums over parts of a block and the
 // launch of a kernel behind another (the rest of the host side: bss_host.h).
 #pragma once
 #include <cuda_bf16.h>
@@ -15,14 +15,7 @@
 namespace bss {
 
 // ---------------------------------------------------------------- vectors
-// Rows move in vectors of 8 channels: 16 bytes of bf16, 32 of float.
-template <typename T>
-struct Raw8 {
-    uint4 q[sizeof(T) / 2];
-};
-
-// Row data is read once: keep it out of L1.  Not the read-only path, since an
-// output may alias its input exactly (a thread reads before it writes).
+// Row data is read once: keep it out of L1.
 __device__ __forceinline__ uint4 ld_row(const void* p) {
     uint4 v;
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -37,55 +30,9 @@ __device__ __forceinline__ void st_row(void* p, const uint4& v) {
                  : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ Raw8<T> load_raw(const T* p) {
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.q[i] = ld_row(reinterpret_cast<const uint4*>(p) + i);
-    return r;
-}
-
-template <typename T>
-__device__ __forceinline__ Raw8<T> zero_raw() {
-    Raw8<T> r;
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.q[i] = make_uint4(0, 0, 0, 0);
-    return r;
-}
-
-__device__ __forceinline__ void unpack(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
-    const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-}
-
-__device__ __forceinline__ void unpack(const Raw8<float>& r, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        v[4 * i] = __uint_as_float(r.q[i].x);
-        v[4 * i + 1] = __uint_as_float(r.q[i].y);
-        v[4 * i + 2] = __uint_as_float(r.q[i].z);
-        v[4 * i + 3] = __uint_as_float(r.q[i].w);
-    }
-}
-
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-    st_row(p, make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])));
-}
-
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        st_row(p + 4 * i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                     __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
 }
 
 // Parameters (weights, modulations) are shared by many rows: read through L1.
@@ -95,9 +42,13 @@ __device__ __forceinline__ void load_param8(const void* base, int64_t index, int
         const float4 a = __ldg(p), b = __ldg(p + 1);
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     } else {
-        Raw8<__nv_bfloat16> r;
-        r.q[0] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + index));
-        unpack(r, v);
+        const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + index));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
     }
 }
 
