@@ -187,7 +187,8 @@ __device__ __forceinline__ bool scattered_writer() {
 }
 
 // ---------------------------------------------------------------- integer division
-// n / d for n < 2^31 by a multiplication: with 2^(L-1) < d <= 2^L and
+// n / d for n < 2^31 by a multiplication (division by an invariant integer after
+// Granlund and Montgomery, 1994): with 2^(L-1) < d <= 2^L and
 // m = floor(2^32 (2^L - d) / d) + 1, n / d = (n m / 2^32 + n) / 2^L.
 struct FastDiv {
     uint32_t d, m, shift;

@@ -98,8 +98,9 @@ typedef struct {
 } bss_token_tensor;
 
 /* Shared description of the two passes.
- *   norm, eps, weight_dtype, q_weight, k_weight   weights of BSS_DTYPE_*, 16-byte
- *              aligned, NULL = ones; both unused without a norm.
+ *   norm, eps, weight_dtype, q_weight, k_weight   eps >= 0; weights of BSS_DTYPE_*,
+ *              16-byte aligned, NULL = ones; all unused without a norm.  With
+ *              eps = 0 a head (or token) of zeros gives NaN, as the formula does.
  *   rotary     NULL = no rotation. */
 typedef struct {
     int32_t norm;
@@ -133,7 +134,8 @@ bss_status bss_heads_from_tokens(const bss_token_tensor* q, const bss_token_tens
 bss_status bss_heads_from_tokens_backward_workspace(int32_t H, const bss_mask_params* params, int32_t norm,
                                                     int64_t* bytes);
 
-/* Gradients of bss_heads_from_tokens.
+/* Gradients of bss_heads_from_tokens.  The library has no backward pass of the
+ * attention: dQh, dKh and dVh are the caller's.
  *   dQh, dKh, dVh  device [H][N][d] bf16 gradients of its outputs, each head in
  *                  the layout it was written in; any may be NULL together with
  *                  its dq, dk or dv (data NULL).
@@ -194,7 +196,8 @@ enum {
  *               (updated in place, same stride).
  *   y, h        branch_dtype, likewise; h may be NULL when only r is wanted, or
  *               equal y (same stride).  Otherwise outputs overlap no input and
- *               no other output.
+ *               no other output.  (x and y may be one tensor, then also with r or
+ *               h over it.)
  *   gate, scale, shift   param_dtype [groups][channels], groups gate_stride ...
  *               elements apart (not used with one group); row i belongs to group
  *               i / rows_per_group, groups = ceil(rows / rows_per_group): one
@@ -286,7 +289,8 @@ typedef struct {
 } bss_residual_norm_grads;
 
 /* Bytes of workspace that bss_residual_norm_backward needs for these arguments
- * on the current device (its workspace fields are not looked at). */
+ * on the current device (its workspace fields are not looked at).  Where a
+ * parameter's gradient is wanted every group takes at least 12 bytes a channel. */
 bss_status bss_residual_norm_backward_workspace(const bss_residual_norm_grads* args, int64_t* bytes);
 
 /* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
