@@ -839,7 +839,6 @@ bss_status forward_of(const bss_residual_norm_args& a, cudaStream_t stream) {
     ForwardArgs g;
     memset(&g, 0, sizeof(g));
     g.a = a;
-    if (g.a.rows_per_group > a.rows) g.a.rows_per_group = a.rows;
     // nothing that differs between groups: one group holds the rows
     if (a.gate == nullptr && a.scale == nullptr && a.shift == nullptr) g.a.rows_per_group = a.rows;
     g.by_rows = FastDiv(static_cast<uint32_t>(g.a.rows_per_group));
@@ -950,6 +949,7 @@ bss_status bss_residual_norm(const bss_residual_norm_args* args, cudaStream_t st
         return set_error(BSS_ERR_INVALID_ARG, "statistics are only written by a norm");
     if (!is_aligned(a.stats, 8) || !is_aligned(a.y_stats, 8))
         return set_error(BSS_ERR_INVALID_ARG, "statistics must be 8-byte aligned");
+    if (a.rows_per_group > a.rows) a.rows_per_group = a.rows;
     const int64_t groups = (a.rows + a.rows_per_group - 1) / a.rows_per_group;
     Named t[12] = {{a.x, {}, false, -1},     {a.y, {}, false, -1},        {a.gate, {}, false, -1},
                    {a.scale, {}, false, -1}, {a.shift, {}, false, -1},    {a.weight, {}, false, -1},
@@ -1012,6 +1012,7 @@ bss_status bss_residual_norm_backward(const bss_residual_norm_grads* args, cudaS
         return set_error(BSS_ERR_INVALID_ARG, "statistics must be 8-byte aligned");
     for (const float* p : {a.dgate, a.dscale, a.dshift, a.dweight, a.dbias, a.dy_weight})
         if (!is_aligned(p, 16)) return set_error(BSS_ERR_INVALID_ARG, "parameter gradients must be 16-byte aligned");
+    if (a.rows_per_group > a.rows) a.rows_per_group = a.rows;
     const int64_t groups = (a.rows + a.rows_per_group - 1) / a.rows_per_group;
     g.s = grad_shape(a);
     const int64_t need = grad_workspace(a, g.s);

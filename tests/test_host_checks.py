@@ -124,3 +124,17 @@ def test_heads_refuse_outputs_over_what_is_read(lib, no_gpu, norm):
     assert forward(lib, norm=0, qw=near(3)) == NO_DEVICE
     r = rotary(pairs=(22, 0, 21), tables=(ptr(10), near(3), ptr(12)))
     assert forward(lib, norm=norm, rotary=r) == NO_DEVICE
+
+
+@pytest.mark.parametrize("group", [7, 1 << 40, (1 << 63) - 1])
+def test_norm_groups_longer_than_the_rows(lib, no_gpu, group):
+    """One group, however many rows it could hold: its overlaps are still seen."""
+    many = dict(rows_per_group=group)
+    assert lib.bss_residual_norm(norm_args(bss._ResidualNormArgs, gate=ptr(8), gate_stride=4, **many), None) == NO_DEVICE
+    assert lib.bss_residual_norm(norm_args(bss._ResidualNormArgs, gate=ptr(3) + 256, **many), None) == INVALID
+    ws = dict(workspace=ptr(10), workspace_bytes=1 << 24)
+    back = lambda **kw: lib.bss_residual_norm_backward(norm_args(bss._ResidualNormGrads, **many, **ws, **kw), None)  # noqa: E731
+    assert back(dshift=ptr(9)) == NO_DEVICE
+    for over in (ptr(3), ptr(4) + 64, ptr(10)):
+        assert back(dshift=over) == INVALID
+        assert back(dgate=over) == INVALID
