@@ -32,6 +32,7 @@ TILE_INDEX_MASK = (1 << 30) - 1
 DTYPE_BF16, DTYPE_F32 = 0, 1
 NORM_NONE, NORM_LAYER, NORM_RMS = 0, 1, 2                      # residual_norm
 HEAD_NORM_NONE, HEAD_NORM_HEAD, HEAD_NORM_TOKEN = 0, 1, 2      # heads_from_tokens: Q/K norm over a head or a token
+ACT_NONE, ACT_GELU_TANH, ACT_GELU, ACT_SILU = 0, 1, 2, 3       # linear
 PAIR_INTERLEAVED, PAIR_HALVES = 0, 1                           # rotary pairs: channels (2p, 2p + 1) or (p, p + R/2)
 STAT_NAMES = ("full", "boundary", "pad", "skip", "retained_pairs", "exact_retained_pairs", "columns")
 STATUS_NAMES = {0: "BSS_OK", 1: "BSS_ERR_INVALID_ARG", 2: "BSS_ERR_UNSUPPORTED", 3: "BSS_ERR_CUDA",
@@ -131,6 +132,26 @@ class _ResidualNormGrads(ctypes.Structure):
                 + [("workspace_bytes", ctypes.c_int64)])
 
 
+class _LinearArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "rows_per_group")]
+                + [(n, ctypes.c_int32) for n in ("in_channels", "out_channels", "out_dtype", "param_dtype", "activation")]
+                + [("residual_scale", ctypes.c_float)]
+                + [(n, ctypes.c_void_p) for n in ("x", "weight", "bias", "gate", "residual", "out", "pre")]
+                + [(n, ctypes.c_int64) for n in ("x_stride", "weight_stride", "gate_stride", "residual_stride",
+                                                 "out_stride", "pre_stride")]
+                + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)])
+
+
+class _LinearGrads(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "rows_per_group")]
+                + [(n, ctypes.c_int32) for n in ("in_channels", "out_channels", "dout_dtype", "param_dtype",
+                                                 "dweight_dtype", "activation")]
+                + [(n, ctypes.c_void_p) for n in ("dout", "x", "weight", "pre", "gate", "dx", "dweight", "dbias", "dgate")]
+                + [(n, ctypes.c_int64) for n in ("dout_stride", "x_stride", "weight_stride", "pre_stride", "gate_stride",
+                                                 "dx_stride", "dweight_stride")]
+                + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)])
+
+
 EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bss_tile_map_copy_csr",
             "bss_destroy_tile_map", "bss_permute", "bss_sparse_attention", "bss_dense_attention",
             "bss_get_device_status", "bss_status_string", "bss_last_error_message", "bss_version",
@@ -141,7 +162,8 @@ EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bs
             "bss_permute_flagged_multi", "bss_rotary_table", "bss_heads_from_tokens",
             "bss_heads_from_tokens_backward_workspace", "bss_heads_from_tokens_backward",
             "bss_attention_step_tokens", "bss_residual_norm", "bss_residual_norm_backward_workspace",
-            "bss_residual_norm_backward")
+            "bss_residual_norm_backward", "bss_linear_workspace", "bss_linear", "bss_linear_backward_workspace",
+            "bss_linear_backward")
 
 
 def load(path: str | None = None):
@@ -223,6 +245,10 @@ def load(path: str | None = None):
     lib.bss_residual_norm_backward_workspace.restype = st
     lib.bss_residual_norm_backward.argtypes = [ctypes.POINTER(_ResidualNormGrads), p]
     lib.bss_residual_norm_backward.restype = st
+    for name, args in (("linear", _LinearArgs), ("linear_backward", _LinearGrads)):
+        getattr(lib, f"bss_{name}").argtypes = [ctypes.POINTER(args), p]
+        getattr(lib, f"bss_{name}_workspace").argtypes = [ctypes.POINTER(args), i64p]
+        getattr(lib, f"bss_{name}").restype = getattr(lib, f"bss_{name}_workspace").restype = st
     _lib = lib
     return lib
 
@@ -1006,3 +1032,103 @@ def residual_norm_backward(r, y=None, dr=None, dh=None, dx=None, dy=None, stats=
         a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(lib.bss_residual_norm_backward(args, _stream_on(stream, device)))
     return dx, dy
+
+
+# ---------------------------------------------------------------- matrix products
+
+def _matrix(t, name):
+    """(rows, width) of a given CUDA matrix."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor of two dimensions")
+    return t.shape
+
+
+def _with_workspace(args, need, call, workspace, stream, device):
+    """Makes a call whose workspace `need` tells the size of."""
+    ref = ctypes.byref(args)
+    nbytes = ctypes.c_int64()
+    _check(need(ref, ctypes.byref(nbytes)))
+    if nbytes.value or workspace is not None:
+        workspace = _workspace(workspace, nbytes.value, stream)
+        args.workspace, args.workspace_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(call(ref, _stream_on(stream, device)))
+
+
+def linear(x, weight, out, bias=None, activation: int = ACT_NONE, gate=None, residual=None,
+           rows_per_group: int | None = None, residual_scale: float = 1.0, pre=None, workspace=None, stream=None):
+    """A linear layer with what follows it (``bss_linear``)::
+
+        z   = x weight^T + bias
+        out = residual_scale * residual + gate * activation(z)
+
+    x: bf16 [rows][in]; weight: bf16 [out][in]; out, residual: bf16 or float32
+    [rows][out] (out may be residual); bias [out] and gate [groups][out], row i in
+    group i // rows_per_group (default: one group), both float32 or both bf16;
+    activation: ACT_*.  pre: optional bf16 [rows][out] output, z for the backward
+    pass.  Rows may be strided.  workspace: memory for partial sums where the call
+    needs some (taken from torch's allocator when None).  Returns out."""
+    import torch
+    rows, inner = _matrix(x, "x")
+    outer = _matrix(weight, "weight")[0]
+    device = _current_device()
+    group, mods = _groups(rows, rows_per_group, outer)
+    dtype = _one_dtype((out, "out"), (residual, "residual"))
+    if dtype is None:
+        raise ValueError("out must be a CUDA tensor")
+    param = _one_dtype((bias, "bias"), (gate, "gate"))
+    bf16, shape = torch.bfloat16, (rows, outer)
+    x_p, x_s = _row_tensor(x, "x", bf16, (rows, inner), device)
+    w_p, w_s = _row_tensor(weight, "weight", bf16, (outer, inner), device)
+    g_p, g_s = _row_tensor(gate, "gate", param, mods, device)
+    r_p, r_s = _row_tensor(residual, "residual", dtype, shape, device)
+    o_p, o_s = _row_tensor(out, "out", dtype, shape, device)
+    p_p, p_s = _row_tensor(pre, "pre", bf16, shape, device)
+    a = _LinearArgs(rows, group, inner, outer, _dtype_code(dtype, "out"),
+                    DTYPE_F32 if param is None else _dtype_code(param, "bias"), activation, residual_scale, x_p, w_p,
+                    _exact(bias, "bias", param, (outer,), device), g_p, r_p, o_p, p_p, x_s, w_s, g_s, r_s, o_s, p_s)
+    lib = load()
+    _with_workspace(a, lib.bss_linear_workspace, lib.bss_linear, workspace, stream, device)
+    return out
+
+
+def linear_backward(dout, x=None, weight=None, dx=None, dweight=None, dbias=None, dgate=None, activation: int = ACT_NONE,
+                    pre=None, gate=None, rows_per_group: int | None = None, workspace=None, stream=None):
+    """Gradients of ``linear`` (``bss_linear_backward``)::
+
+        dz = gate * dout * activation'(pre)
+        dx = dz weight      dweight = dz^T x      dbias = sum of dz
+        dgate = sum over a group's rows of dout * activation(pre)
+
+    dout: bf16 or float32 [rows][out]; x, weight, gate: the forward inputs (x for
+    dweight, weight for dx); pre: the z that ``linear`` kept, with an activation or
+    for dgate.  Outputs, each optional, overwritten: dx bf16 [rows][in], dweight
+    bf16 or float32 [out][in], dbias float32 [out], dgate float32 [groups][out].
+    (The residual's gradient is residual_scale * dout.)  Sums over rows are taken in
+    a fixed order.  workspace: taken from torch's allocator when None."""
+    import torch
+    rows, outer = _matrix(dout, "dout")
+    inner = None
+    for t, n, axis in ((x, "x", 1), (weight, "weight", 1), (dx, "dx", 1), (dweight, "dweight", 1)):
+        if t is not None and inner is None:
+            inner = _matrix(t, n)[axis]
+    device = _current_device()
+    group, mods = _groups(rows, rows_per_group, outer)
+    bf16, f32 = torch.bfloat16, torch.float32
+    param = _one_dtype((gate, "gate"))
+    dw = _one_dtype((dweight, "dweight"))
+    d_p, d_s = _row_tensor(dout, "dout", dout.dtype, (rows, outer), device)
+    x_p, x_s = _row_tensor(x, "x", bf16, (rows, inner), device)
+    w_p, w_s = _row_tensor(weight, "weight", bf16, (outer, inner), device)
+    p_p, p_s = _row_tensor(pre, "pre", bf16, (rows, outer), device)
+    g_p, g_s = _row_tensor(gate, "gate", param, mods, device)
+    dx_p, dx_s = _row_tensor(dx, "dx", bf16, (rows, inner), device)
+    dw_p, dw_s = _row_tensor(dweight, "dweight", dw, (outer, inner), device)
+    a = _LinearGrads(rows, group, 8 if inner is None else inner, outer, _dtype_code(dout.dtype, "dout"),
+                     DTYPE_F32 if param is None else _dtype_code(param, "gate"),
+                     DTYPE_F32 if dw is None else _dtype_code(dw, "dweight"), activation, d_p, x_p, w_p, p_p, g_p, dx_p, dw_p,
+                     _exact(dbias, "dbias", f32, (outer,), device), _exact(dgate, "dgate", f32, mods, device),
+                     d_s, x_s, w_s, p_s, g_s, dx_s, dw_s)
+    lib = load()
+    _with_workspace(a, lib.bss_linear_backward_workspace, lib.bss_linear_backward, workspace, stream, device)
+    return dx, dweight

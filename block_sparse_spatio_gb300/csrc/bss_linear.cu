@@ -1,0 +1,744 @@
+// bss_linear.cu -- linear layers: a matrix product with bias, activation, gate and
+// residual in its epilogue, and its gradients.
+//
+//   z = x W^T + b,  out = a residual + gate * act(z)
+//   dz = gate * dout * act'(z),  dx = dz W,  dW = dz^T x,  db = sum dz,
+//   dgate = sum over a group's rows of dout * act(z)
+//
+// All three products are D[m][n] = sum over k of A[m][k] B[n][k]; an operand whose
+// k is contiguous is K-major in shared memory, one whose m (or n) is contiguous
+// MN-major, so nothing is transposed in memory:
+//   z   A = x [rows][in]     K-major   B = W [out][in]  K-major
+//   dx  A = dz [rows][out]   K-major   B = W [out][in]  MN-major
+//   dW  A = dz [rows][out]   MN-major  B = x [rows][in] MN-major
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "bss_args.h"
+#include "bss_rows.cuh"
+
+namespace bss {
+namespace {
+
+constexpr int kMaxWidth = 65536;
+
+// ---------------------------------------------------------------- activations
+// sigmoid(x) = 1 / (1 + exp(-x)); exp past the float range gives 0 or infinity and
+// the quotient its limit.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+
+// tanh form: (1 + tanh u) / 2 = sigmoid(2 u), which keeps the small values of
+// negative z exact to a few roundings (1 + tanh u does not).
+constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kTanhD = 0.044715f;
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) {
+    if constexpr (ACT == BSS_ACT_GELU_TANH) {
+        // z sigmoid(u), not z / (1 + exp(-u)): with exp at infinity the quotient would
+        // still be right, a fast division's would not
+        return z * sigmoid(kTanhC * z * fmaf(kTanhD * z, z, 1.0f));
+    } else if constexpr (ACT == BSS_ACT_GELU) {
+        return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    } else if constexpr (ACT == BSS_ACT_SILU) {
+        return z * sigmoid(z);
+    } else {
+        return z;
+    }
+}
+
+// Value and slope.  Beyond |z| = 20 (SiLU: 110) a slope is 0 or 1 to the last bit of
+// a float's range; held there, no product of an overflowed factor and a zero can
+// arise (NaN stays).
+template <int ACT>
+__device__ __forceinline__ void activate_both(float z, float& value, float& slope) {
+    if constexpr (ACT == BSS_ACT_NONE) {
+        value = z, slope = 1.0f;
+        return;
+    }
+    value = activate<ACT>(z);
+    constexpr float kEnd = ACT == BSS_ACT_SILU ? 110.0f : 20.0f;
+    const float t = z > kEnd ? kEnd : (z < -kEnd ? -kEnd : z);
+    if constexpr (ACT == BSS_ACT_GELU_TANH) {
+        const float s = sigmoid(kTanhC * t * fmaf(kTanhD * t, t, 1.0f));
+        slope = fmaf(t * s * (1.0f - s), kTanhC * fmaf(3.0f * kTanhD * t, t, 1.0f), s);
+    } else if constexpr (ACT == BSS_ACT_GELU) {
+        slope = fmaf(t, 0.39894228040143268f * __expf(-0.5f * t * t), 0.5f * erfcf(-0.70710678118654752f * t));
+    } else if constexpr (ACT == BSS_ACT_SILU) {
+        const float s = sigmoid(t);
+        slope = s * fmaf(t, 1.0f - s, 1.0f);
+    }
+}
+
+// ---------------------------------------------------------------- tile product
+// A tile of 128 CG rows and columns is made by CG CTAs (a pair's MMA takes half of
+// A and of B from each): warp 0 loads, warp 1 of the first CTA issues the MMAs,
+// warps 4 to 7 of each bring the accumulators of its 128 rows from TMEM to memory.
+// Two accumulators a CTA: the MMAs of the next tile run during this one's stores.
+constexpr int kTileK = 64;  // 128 bytes of bf16: one swizzle row
+constexpr int kOperand = 128 * kTileK * 2;
+constexpr int kStages = 6;
+constexpr int kThreads = 256;
+constexpr int kEpilogueWarp = 4;
+
+struct Epilogue {
+    const void* bias;
+    const void* gate;
+    const void* residual;
+    void* out;
+    void* pre;
+    int64_t gate_stride, residual_stride, out_stride, pre_stride;
+    int32_t param_dtype, out_dtype, activation;
+    float residual_scale;
+    FastDiv by_rows;
+};
+
+struct GemmArgs {
+    CUtensorMap a, b;
+    int32_t m, n, kblocks;
+    int32_t tiles_n, tiles;
+    int* status;
+    Epilogue e;
+};
+
+struct GemmSmem {
+    static constexpr uint32_t kBars = kStages * 2 * kOperand;
+    static constexpr uint32_t kBytes = kBars + (2 * kStages + 4) * 8 + 16;
+    static constexpr uint32_t kAlloc = kBytes + 1024;  // the operands start on 1024 bytes
+};
+
+// 8 values of a row -> bf16 or float memory
+__device__ __forceinline__ void store8(void* base, int64_t at, int dtype, const float (&v)[8]) {
+    if (dtype == BSS_DTYPE_F32) {
+        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+        p[0] = make_float4(v[0], v[1], v[2], v[3]);
+        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) =
+            make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+    }
+}
+
+// 8 values that another thread of this call may write afterwards: not through the
+// read-only path.
+__device__ __forceinline__ void load8(const void* base, int64_t at, int dtype, float (&v)[8]) {
+    if (dtype == BSS_DTYPE_F32) {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+        const float4 a = p[0], b = p[1];
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+        const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <int ACT>
+__device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t group, int col, float (&v)[8]) {
+    float w[8];
+    if (e.bias != nullptr) {
+        load_param8(e.bias, col, e.param_dtype, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += w[i];
+    }
+    if (e.pre != nullptr) store8(e.pre, row * e.pre_stride + col, BSS_DTYPE_BF16, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
+    if (e.gate != nullptr) {
+        load_param8(e.gate, group * e.gate_stride + col, e.param_dtype, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= w[i];
+    }
+    if (e.residual != nullptr) {
+        load8(e.residual, row * e.residual_stride + col, e.out_dtype, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(e.residual_scale, w[i], v[i]);
+    }
+    store8(e.out, row * e.out_stride + col, e.out_dtype, v);
+}
+
+template <int CG, bool A_MN, bool B_MN, int ACT>
+__global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
+    using L = GemmSmem;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+    uint64_t* empty = full + kStages;
+    uint64_t* acc_full = empty + kStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    constexpr int kTile = 128 * CG;
+    constexpr uint32_t kAccCols = 128 * CG;  // a CTA's accumulator: its 128 rows, the tile's columns
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 4 * CG);
+        }
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        if constexpr (CG == 2) tmem_alloc_pair(tmem_slot, 2 * kAccCols);
+        else tmem_alloc(tmem_slot, 2 * kAccCols);
+    }
+    tc_fence_before();
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            tma_prefetch_desc(&g.a);
+            tma_prefetch_desc(&g.b);
+            auto load = [&](uint8_t* to, const CUtensorMap* map, int c0, int c1, uint64_t* bar) {
+                if constexpr (CG == 2) tma_load_3d_pair(to, map, c0, c1, 0, map_to_rank(bar, 0));
+                else tma_load_3d(to, map, c0, c1, 0, bar);
+            };
+            uint32_t fill = 0;
+            bool ok = true;
+            for (int t = first; ok && t < g.tiles; t += step) {
+                const int mt = t / g.tiles_n, nt = t - mt * g.tiles_n;
+                const int row_a = mt * kTile + static_cast<int>(rank) * 128, row_b = nt * kTile + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < g.kblocks; ++kb, ++fill) {
+                    const uint32_t s = fill % kStages;
+                    if (fill >= kStages) ok = mbar_wait(empty + s, (fill / kStages - 1) & 1, g.status);
+                    if (!ok) break;
+                    uint8_t* sa = smem + s * 2 * kOperand;
+                    uint8_t* sb = sa + kOperand;
+                    if (rank == 0) mbar_arrive_expect_tx(full + s, 2 * kOperand * CG);
+                    if constexpr (A_MN) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) load(sa + c * kOperand / 2, &g.a, row_a + c * 64, kb * kTileK, full + s);
+                    } else {
+                        load(sa, &g.a, kb * kTileK, row_a, full + s);
+                    }
+                    if constexpr (B_MN) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) load(sb + c * kOperand / 2, &g.b, row_b + c * 64, kb * kTileK, full + s);
+                    } else {
+                        load(sb, &g.b, kb * kTileK, row_b, full + s);
+                    }
+                }
+            }
+            // no copy may still be landing when the CTAs end
+            if (rank == 0)
+                for (uint32_t f = fill > kStages ? fill - kStages : 0; f < fill; ++f)
+                    mbar_wait(full + f % kStages, (f / kStages) & 1, g.status);
+        }
+    } else if (warp == 1) {
+        if (rank == 0) {
+            constexpr uint32_t idesc = idesc_bf16_f32(kTile, kTile, B_MN, A_MN);
+            const bool leader = elect_one();
+            const uint32_t base = smem_u32(smem);
+            const uint64_t da0 = A_MN ? desc_mnmajor_sw128(base, 0, kOperand / 2) : desc_kmajor_sw128(base, 0);
+            const uint64_t db0 = B_MN ? desc_mnmajor_sw128(base + kOperand, 0, kOperand / 2)
+                                      : desc_kmajor_sw128(base + kOperand, 0);
+            constexpr uint64_t kStepA = A_MN ? 128 : 2, kStepB = B_MN ? 128 : 2;  // 16 of k, in 16-byte units
+            uint32_t fill = 0, n_tile = 0;
+            bool ok = true;
+            auto commit = [&](uint64_t* bar) {
+                if (leader) {
+                    if constexpr (CG == 2) tc_commit_pair(bar);
+                    else tc_commit(bar);
+                }
+            };
+            for (int t = first; ok && t < g.tiles; t += step, ++n_tile) {
+                const uint32_t buf = n_tile & 1;
+                if (n_tile >= 2)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_empty + buf, (n_tile / 2 - 1) & 1, g.status));
+                if (!ok) break;
+                tc_fence_after();
+                for (int kb = 0; kb < g.kblocks; ++kb, ++fill) {
+                    const uint32_t s = fill % kStages;
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, (fill / kStages) & 1, g.status));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        const uint64_t at = static_cast<uint64_t>(s) * (2 * kOperand >> 4);
+#pragma unroll
+                        for (int kk = 0; kk < kTileK / 16; ++kk) {
+                            const uint32_t acc = kb > 0 || kk > 0 ? 1u : 0u;
+                            if constexpr (CG == 2)
+                                umma_ss_pair(tmem + buf * kAccCols, da0 + at + kk * kStepA, db0 + at + kk * kStepB, idesc, acc);
+                            else
+                                umma_ss(tmem + buf * kAccCols, da0 + at + kk * kStepA, db0 + at + kk * kStepB, idesc, acc);
+                        }
+                    }
+                    commit(empty + s);
+                }
+                if (ok) commit(acc_full + buf);
+            }
+        }
+    } else if (warp >= kEpilogueWarp) {
+        const int quarter = warp & 3;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        uint32_t n_tile = 0;
+        for (int t = first; t < g.tiles; t += step, ++n_tile) {
+            const int mt = t / g.tiles_n, nt = t - mt * g.tiles_n;
+            const uint32_t buf = n_tile & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + buf, (n_tile / 2) & 1, g.status))) break;
+            tc_fence_after();
+            const int row = mt * kTile + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+            const int64_t group = g.e.gate != nullptr && row < g.m ? g.e.by_rows.div(row) : 0;
+#pragma unroll 1
+            for (int c = 0; c < static_cast<int>(kAccCols); c += 32) {
+                const int col = nt * kTile + c;
+                if (col >= g.n) break;
+                uint32_t r[32];
+                BSS_TMEM_LD32(tmem + lanes + buf * kAccCols + c, r);
+                tmem_wait_ld();
+                if (row < g.m) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        if (col + 8 * u < g.n) {
+                            float v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * u + i]);
+                            finish8<ACT>(g.e, row, group, col + 8 * u, v);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2) mbar_arrive_cluster(map_to_rank(acc_empty + buf, 0));
+                else mbar_arrive(acc_empty + buf);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncwarp();
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        if constexpr (CG == 2) tmem_dealloc_pair(tmem, 2 * kAccCols);
+        else tmem_dealloc(tmem, 2 * kAccCols);
+    }
+}
+
+// ---------------------------------------------------------------- dz and its sums over rows
+// A thread has 8 channels, a warp walks over rows; a block covers `unit` rows that
+// share a gate, or (small groups) whole groups, one a warp at a time.
+struct DzArgs {
+    const void* dout;
+    const __nv_bfloat16* pre;
+    const void* gate;
+    __nv_bfloat16* dz;  // NULL: only the sums are wanted
+    float *dbias, *dgate;  // partial sums, or (small groups) dgate itself
+    int64_t rows, group_rows, dout_stride, pre_stride, gate_stride;
+    int64_t units;      // rows of a block's chunk; of small groups: groups of a block
+    int32_t chunks;     // blocks a group; 0: small groups
+    int32_t n, dout_dtype, param_dtype;
+};
+
+constexpr int kDzWarps = 8;
+
+template <int ACT>
+__global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const __grid_constant__ DzArgs a) {
+    __shared__ float sums[kDzWarps][2][32 * 9];  // a lane's 8 values 9 apart
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = (blockIdx.x * 32 + lane) * 8;
+    const bool live = c < a.n;
+    const bool small = a.chunks == 0;
+    int64_t group, begin, end;
+    if (small) {
+        group = blockIdx.y * a.units + warp;
+        begin = end = 0;
+    } else {
+        group = blockIdx.y / a.chunks;
+        begin = group * a.group_rows + (blockIdx.y - group * a.chunks) * a.units;
+        end = begin + a.units;
+        const int64_t group_end = (group + 1) * a.group_rows;
+        if (end > group_end) end = group_end;
+        if (end > a.rows) end = a.rows;
+    }
+    const int64_t last_group = (blockIdx.y + 1) * a.units;  // small groups
+    float db[8] = {}, dg[8] = {}, gate[8];
+    while (true) {
+        if (small) {
+            begin = group * a.group_rows;
+            end = begin + a.group_rows;
+            if (end > a.rows) end = a.rows;
+            if (group >= last_group || begin >= a.rows) break;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gate[i] = 1.0f;
+        if (a.gate != nullptr && live) load_param8(a.gate, group * a.gate_stride + c, a.param_dtype, gate);
+        for (int64_t row = begin + (small ? 0 : warp); live && row < end; row += small ? 1 : kDzWarps) {
+            float d[8], z[8] = {}, v, s;
+            load8(a.dout, row * a.dout_stride + c, a.dout_dtype, d);
+            if (a.pre != nullptr) load8(a.pre, row * a.pre_stride + c, BSS_DTYPE_BF16, z);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                activate_both<ACT>(z[i], v, s);
+                dg[i] = fmaf(d[i], v, dg[i]);
+                d[i] *= gate[i] * s;
+                db[i] += d[i];
+            }
+            if (a.dz != nullptr) store8(a.dz, row * a.n + c, BSS_DTYPE_BF16, d);
+        }
+        if (!small) break;
+        if (a.dgate != nullptr && live) store8(a.dgate, group * a.n + c, BSS_DTYPE_F32, dg);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dg[i] = 0.0f;
+        group += kDzWarps;
+    }
+    const bool want_gate = a.dgate != nullptr && !small;
+    if (a.dbias == nullptr && !want_gate) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        sums[warp][0][lane * 9 + i] = db[i];
+        sums[warp][1][lane * 9 + i] = dg[i];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += 32 * kDzWarps) {
+        const int col = blockIdx.x * 256 + i, at = (i >> 3) * 9 + (i & 7);
+        if (col >= a.n) continue;
+        float b = 0.0f, g = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDzWarps; ++w) {
+            b += sums[w][0][at];
+            g += sums[w][1][at];
+        }
+        if (a.dbias != nullptr) a.dbias[static_cast<int64_t>(blockIdx.y) * a.n + col] = b;
+        if (want_gate) a.dgate[static_cast<int64_t>(blockIdx.y) * a.n + col] = g;
+    }
+}
+
+// out[j][c] = sum over i of partial[j * parts + i][c], in a fixed order: a block's
+// eight warps take every eighth part each.
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float* partial, float* out, int64_t parts, int32_t n) {
+    __shared__ float sums[8][32];
+    cudaGridDependencySynchronize();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < n)
+        for (int64_t i = warp; i < parts; i += 8) s += partial[(blockIdx.y * parts + i) * n + c];
+    sums[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0 && c < n) {
+#pragma unroll
+        for (int w = 1; w < 8; ++w) s += sums[w][lane];
+        out[static_cast<int64_t>(blockIdx.y) * n + c] = s;
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// Operand [rows][width] whose k (K-major) or m / n (MN-major) is its width.
+bss_status operand_map(CUtensorMap* map, const void* p, int64_t rows, int64_t stride, int64_t width, bool mn_major) {
+    const uint64_t bytes = static_cast<uint64_t>(rows > 1 ? stride : (width + 7) / 8 * 8) * 2;
+    return encode_tmap_3d(map, p, width, rows, 1, bytes, bytes, 64, mn_major ? kTileK : 128);
+}
+
+template <int CG, bool A_MN, bool B_MN, int ACT>
+bss_status launch_gemm(GemmArgs& g, cudaStream_t stream) {
+    constexpr int kTile = 128 * CG;
+    const int64_t tiles_m = (static_cast<int64_t>(g.m) + kTile - 1) / kTile;
+    g.tiles_n = (g.n + kTile - 1) / kTile;
+    if (tiles_m * g.tiles_n > 0x7FFFFFFF) return set_error(BSS_ERR_UNSUPPORTED, "too many tiles");
+    g.tiles = static_cast<int32_t>(tiles_m * g.tiles_n);
+    auto kernel = gemm_kernel<CG, A_MN, B_MN, ACT>;
+    int blocks;
+    const bss_status st = resident_blocks(reinterpret_cast<const void*>(kernel), kThreads, GemmSmem::kAlloc, &blocks);
+    if (st != BSS_OK) return st;
+    int units = num_sms() / CG;
+    if (units > g.tiles) units = g.tiles;
+    cudaLaunchConfig_t config = {};
+    config.gridDim = dim3(static_cast<unsigned>(units * CG));
+    config.blockDim = dim3(kThreads);
+    config.dynamicSmemBytes = GemmSmem::kAlloc;
+    config.stream = stream;
+    cudaLaunchAttribute attribute = {};
+    attribute.id = cudaLaunchAttributeClusterDimension;
+    attribute.val.clusterDim.x = CG;
+    attribute.val.clusterDim.y = attribute.val.clusterDim.z = 1;
+    config.attrs = &attribute;
+    config.numAttrs = CG == 2 ? 1 : 0;
+    return cuda_check(cudaLaunchKernelEx(&config, kernel, g), "matrix product launch");
+}
+
+// D[m][n] = A B^T of k, then the epilogue.
+template <bool A_MN, bool B_MN>
+bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t m, int64_t n, int64_t k,
+                const Epilogue& e, cudaStream_t stream) {
+    GemmArgs g;
+    memset(&g, 0, sizeof(g));
+    g.status = device_status_ptr();
+    if (g.status == nullptr) return set_error(BSS_ERR_CUDA, "cannot resolve the device status word");
+    bss_status st = A_MN ? operand_map(&g.a, a, k, a_stride, m, true) : operand_map(&g.a, a, m, a_stride, k, false);
+    if (st != BSS_OK) return st;
+    st = B_MN ? operand_map(&g.b, b, k, b_stride, n, true) : operand_map(&g.b, b, n, b_stride, k, false);
+    if (st != BSS_OK) return st;
+    g.m = static_cast<int32_t>(m);
+    g.n = static_cast<int32_t>(n);
+    g.kblocks = static_cast<int32_t>((k + kTileK - 1) / kTileK);
+    g.e = e;
+    if constexpr (A_MN || B_MN) {
+        return launch_gemm<1, A_MN, B_MN, BSS_ACT_NONE>(g, stream);
+    } else {
+        switch (e.activation) {
+            case BSS_ACT_GELU_TANH: return launch_gemm<1, false, false, BSS_ACT_GELU_TANH>(g, stream);
+            case BSS_ACT_GELU: return launch_gemm<1, false, false, BSS_ACT_GELU>(g, stream);
+            case BSS_ACT_SILU: return launch_gemm<1, false, false, BSS_ACT_SILU>(g, stream);
+            default: return launch_gemm<1, false, false, BSS_ACT_NONE>(g, stream);
+        }
+    }
+}
+
+bss_status check_sizes(int64_t rows, int64_t* rows_per_group, int32_t in, int32_t out, int32_t activation) {
+    if (rows <= 0 || *rows_per_group <= 0) return set_error(BSS_ERR_INVALID_ARG, "rows and rows_per_group must be positive");
+    if (rows > 0x7FFFFFFF) return set_error(BSS_ERR_UNSUPPORTED, "rows must be below 2^31");
+    if (in <= 0 || out <= 0 || in % 8 != 0 || out % 8 != 0)
+        return set_error(BSS_ERR_INVALID_ARG, "channels must be positive multiples of 8 (got %d, %d)", in, out);
+    if (in > kMaxWidth || out > kMaxWidth) return set_error(BSS_ERR_UNSUPPORTED, "more than %d channels", kMaxWidth);
+    if (activation < BSS_ACT_NONE || activation > BSS_ACT_SILU) return set_error(BSS_ERR_INVALID_ARG, "unknown activation %d", activation);
+    if (*rows_per_group > rows) *rows_per_group = rows;
+    return BSS_OK;
+}
+
+bss_status check_linear(bss_linear_args& a) {
+    bss_status st = check_sizes(a.rows, &a.rows_per_group, a.in_channels, a.out_channels, a.activation);
+    if (st != BSS_OK) return st;
+    if (!known_dtype(a.out_dtype) || !known_dtype(a.param_dtype)) return set_error(BSS_ERR_INVALID_ARG, "unknown dtype");
+    if (a.x == nullptr || a.weight == nullptr || a.out == nullptr) return set_error(BSS_ERR_INVALID_ARG, "x, weight or out is NULL");
+    if (!std::isfinite(a.residual_scale)) return set_error(BSS_ERR_INVALID_ARG, "residual_scale must be finite");
+    if (a.residual == nullptr && a.residual_scale != 1.0f)
+        return set_error(BSS_ERR_INVALID_ARG, "residual_scale is given without a residual");
+    return BSS_OK;
+}
+
+int64_t linear_need(const bss_linear_args&) { return 0; }
+
+int64_t groups_of(int64_t rows, int64_t per) { return (rows + per - 1) / per; }
+
+// How the rows are dealt to blocks for dz and its sums, and the workspace.
+struct GradPlan {
+    bool makes_dz, sums;
+    int64_t groups, units, blocks, parts;  // parts: partial sums a group (of dgate), of dbias: blocks
+    int32_t chunks;
+    int64_t dz_at, dbias_at, dgate_at, bytes;
+};
+
+int64_t aligned_up(int64_t v) { return (v + 255) / 256 * 256; }
+
+GradPlan plan_of(const bss_linear_grads& a) {
+    GradPlan p = {};
+    const int64_t n = a.out_channels;
+    p.makes_dz = a.activation != BSS_ACT_NONE || a.gate != nullptr || a.dout_dtype == BSS_DTYPE_F32;
+    p.makes_dz = p.makes_dz && (a.dx != nullptr || a.dweight != nullptr);
+    p.sums = a.dbias != nullptr || a.dgate != nullptr;
+    // without a gate all rows are one group here
+    const int64_t per = a.gate != nullptr ? a.rows_per_group : a.rows;
+    p.groups = groups_of(a.rows, per);
+    // about 16 blocks an SM over all columns, of 32 rows at least
+    const int64_t columns = (n + 255) / 256;
+    int64_t want = 16ll * num_sms() / columns;
+    if (want < 1) want = 1;
+    int64_t rows = (a.rows + want - 1) / want;
+    if (rows < 32) rows = 32;
+    if (per >= rows || p.groups == 1) {
+        int64_t chunks = (per + rows - 1) / rows;
+        if (chunks > 32768) chunks = 32768;
+        p.units = (per + chunks - 1) / chunks;
+        p.chunks = static_cast<int32_t>((per + p.units - 1) / p.units);
+        p.blocks = p.groups * p.chunks;
+    } else {
+        p.units = (rows + per - 1) / per;
+        p.chunks = 0;
+        p.blocks = (p.groups + p.units - 1) / p.units;
+    }
+    p.bytes = 0;
+    if (p.makes_dz) {
+        p.dz_at = 0;
+        p.bytes = aligned_up(a.rows * n * 2);
+    }
+    if (a.dbias != nullptr) {
+        p.dbias_at = p.bytes;
+        p.bytes += aligned_up(p.blocks * n * 4);
+    }
+    if (a.dgate != nullptr && p.chunks > 0) {
+        p.dgate_at = p.bytes;
+        p.bytes += aligned_up(p.blocks * n * 4);
+    }
+    return p;
+}
+
+bss_status check_grads(bss_linear_grads& a) {
+    bss_status st = check_sizes(a.rows, &a.rows_per_group, a.in_channels, a.out_channels, a.activation);
+    if (st != BSS_OK) return st;
+    if (!known_dtype(a.dout_dtype) || !known_dtype(a.param_dtype) || !known_dtype(a.dweight_dtype))
+        return set_error(BSS_ERR_INVALID_ARG, "unknown dtype");
+    if (a.dout == nullptr) return set_error(BSS_ERR_INVALID_ARG, "dout is NULL");
+    if (a.dx == nullptr && a.dweight == nullptr && a.dbias == nullptr && a.dgate == nullptr)
+        return set_error(BSS_ERR_INVALID_ARG, "no gradient is wanted");
+    if (a.dx != nullptr && a.weight == nullptr) return set_error(BSS_ERR_INVALID_ARG, "dx needs weight");
+    if (a.dweight != nullptr && a.x == nullptr) return set_error(BSS_ERR_INVALID_ARG, "dweight needs x");
+    if (a.dgate != nullptr && a.gate == nullptr) return set_error(BSS_ERR_INVALID_ARG, "dgate needs gate");
+    if ((a.dgate != nullptr || a.activation != BSS_ACT_NONE) && a.pre == nullptr)
+        return set_error(BSS_ERR_INVALID_ARG, "an activation's slope and dgate need pre");
+    return BSS_OK;
+}
+
+template <int ACT>
+bss_status launch_dz(const DzArgs& d, int64_t blocks, cudaStream_t stream) {
+    const unsigned columns = static_cast<unsigned>((d.n + 255) / 256);
+    dz_kernel<ACT><<<dim3(columns, static_cast<unsigned>(blocks)), 32 * kDzWarps, 0, stream>>>(d);
+    return cuda_check(cudaGetLastError(), "dz launch");
+}
+
+}  // namespace
+}  // namespace bss
+
+extern "C" {
+
+bss_status bss_linear_workspace(const bss_linear_args* args, int64_t* bytes) {
+    using namespace bss;
+    clear_error();
+    if (bytes == nullptr) return set_error(BSS_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    if (args == nullptr) return set_error(BSS_ERR_INVALID_ARG, "args is NULL");
+    bss_linear_args a = *args;
+    const bss_status st = check_linear(a);
+    if (st != BSS_OK) return st;
+    *bytes = linear_need(a);
+    return BSS_OK;
+}
+
+bss_status bss_linear(const bss_linear_args* args, cudaStream_t stream) {
+    using namespace bss;
+    clear_error();
+    if (args == nullptr) return set_error(BSS_ERR_INVALID_ARG, "args is NULL");
+    bss_linear_args a = *args;
+    bss_status st = check_linear(a);
+    if (st != BSS_OK) return st;
+    const int64_t groups = groups_of(a.rows, a.rows_per_group), need = linear_need(a);
+    Operand t[8];
+    if ((st = check_matrix(&t[0], a.x, "x", a.rows, a.x_stride, a.in_channels, BSS_DTYPE_BF16, false)) != BSS_OK ||
+        (st = check_matrix(&t[1], a.weight, "weight", a.out_channels, a.weight_stride, a.in_channels, BSS_DTYPE_BF16, false)) != BSS_OK ||
+        (st = check_matrix(&t[2], a.bias, "bias", 1, 0, a.out_channels, a.param_dtype, false)) != BSS_OK ||
+        (st = check_matrix(&t[3], a.gate, "gate", groups, a.gate_stride, a.out_channels, a.param_dtype, false)) != BSS_OK ||
+        (st = check_matrix(&t[4], a.residual, "residual", a.rows, a.residual_stride, a.out_channels, a.out_dtype, false)) != BSS_OK ||
+        (st = check_matrix(&t[5], a.out, "out", a.rows, a.out_stride, a.out_channels, a.out_dtype, true)) != BSS_OK ||
+        (st = check_matrix(&t[6], a.pre, "pre", a.rows, a.pre_stride, a.out_channels, BSS_DTYPE_BF16, true)) != BSS_OK ||
+        (st = check_run(&t[7], need > 0 ? a.workspace : nullptr, "workspace", need, 16, true)) != BSS_OK ||
+        (st = check_workspace(a.workspace, a.workspace_bytes, need)) != BSS_OK)
+        return st;
+    t[5].over = 4;
+    if ((st = check_outputs(t, 8)) != BSS_OK) return st;
+    Epilogue e = {};
+    e.bias = a.bias, e.gate = a.gate, e.residual = a.residual, e.out = a.out, e.pre = a.pre;
+    e.gate_stride = a.gate_stride, e.residual_stride = a.residual_stride;
+    e.out_stride = a.out_stride, e.pre_stride = a.pre_stride;
+    e.param_dtype = a.param_dtype, e.out_dtype = a.out_dtype, e.activation = a.activation;
+    e.residual_scale = a.residual_scale;
+    e.by_rows = FastDiv(static_cast<uint32_t>(a.rows_per_group));
+    return gemm<false, false>(a.x, a.x_stride, a.weight, a.weight_stride, a.rows, a.out_channels, a.in_channels, e, stream);
+}
+
+bss_status bss_linear_backward_workspace(const bss_linear_grads* args, int64_t* bytes) {
+    using namespace bss;
+    clear_error();
+    if (bytes == nullptr) return set_error(BSS_ERR_INVALID_ARG, "bytes is NULL");
+    *bytes = 0;
+    if (args == nullptr) return set_error(BSS_ERR_INVALID_ARG, "args is NULL");
+    bss_linear_grads a = *args;
+    const bss_status st = check_grads(a);
+    if (st != BSS_OK) return st;
+    *bytes = plan_of(a).bytes;
+    return BSS_OK;
+}
+
+bss_status bss_linear_backward(const bss_linear_grads* args, cudaStream_t stream) {
+    using namespace bss;
+    clear_error();
+    if (args == nullptr) return set_error(BSS_ERR_INVALID_ARG, "args is NULL");
+    bss_linear_grads a = *args;
+    bss_status st = check_grads(a);
+    if (st != BSS_OK) return st;
+    const GradPlan p = plan_of(a);
+    // what is not read is not looked at
+    if (a.dx == nullptr) a.weight = nullptr;
+    if (a.dweight == nullptr) a.x = nullptr;
+    if (a.activation == BSS_ACT_NONE && a.dgate == nullptr) a.pre = nullptr;
+    const int64_t n = a.out_channels, k = a.in_channels;
+    Operand t[10];
+    if ((st = check_matrix(&t[0], a.dout, "dout", a.rows, a.dout_stride, n, a.dout_dtype, false)) != BSS_OK ||
+        (st = check_matrix(&t[1], a.x, "x", a.rows, a.x_stride, k, BSS_DTYPE_BF16, false)) != BSS_OK ||
+        (st = check_matrix(&t[2], a.weight, "weight", n, a.weight_stride, k, BSS_DTYPE_BF16, false)) != BSS_OK ||
+        (st = check_matrix(&t[3], a.pre, "pre", a.rows, a.pre_stride, n, BSS_DTYPE_BF16, false)) != BSS_OK ||
+        (st = check_matrix(&t[4], a.gate, "gate", groups_of(a.rows, a.rows_per_group), a.gate_stride, n, a.param_dtype, false)) != BSS_OK ||
+        (st = check_matrix(&t[5], a.dx, "dx", a.rows, a.dx_stride, k, BSS_DTYPE_BF16, true)) != BSS_OK ||
+        (st = check_matrix(&t[6], a.dweight, "dweight", n, a.dweight_stride, k, a.dweight_dtype, true)) != BSS_OK ||
+        (st = check_run(&t[7], a.dbias, "dbias", 4 * n, 16, true)) != BSS_OK ||
+        (st = check_run(&t[8], a.dgate, "dgate", 4 * n * p.groups, 16, true)) != BSS_OK ||
+        (st = check_run(&t[9], p.bytes > 0 ? a.workspace : nullptr, "workspace", p.bytes, 16, true)) != BSS_OK ||
+        (st = check_workspace(a.workspace, a.workspace_bytes, p.bytes)) != BSS_OK ||
+        (st = check_outputs(t, 10)) != BSS_OK)
+        return st;
+    char* ws = static_cast<char*>(a.workspace);
+    const void* dz = a.dout;
+    int64_t dz_stride = a.dout_stride;
+    if (p.makes_dz || p.sums) {
+        DzArgs d = {};
+        d.dout = a.dout, d.gate = a.gate, d.pre = static_cast<const __nv_bfloat16*>(a.pre);
+        if (p.makes_dz) {
+            d.dz = reinterpret_cast<__nv_bfloat16*>(ws + p.dz_at);
+            dz = d.dz, dz_stride = n;
+        }
+        if (a.dbias != nullptr) d.dbias = reinterpret_cast<float*>(ws + p.dbias_at);
+        if (a.dgate != nullptr) d.dgate = p.chunks > 0 ? reinterpret_cast<float*>(ws + p.dgate_at) : a.dgate;
+        d.rows = a.rows, d.group_rows = a.gate != nullptr ? a.rows_per_group : a.rows;
+        d.dout_stride = a.dout_stride, d.pre_stride = a.pre_stride, d.gate_stride = a.gate_stride;
+        d.units = p.units, d.chunks = p.chunks;
+        d.n = a.out_channels, d.dout_dtype = a.dout_dtype, d.param_dtype = a.param_dtype;
+        switch (a.activation) {
+            case BSS_ACT_GELU_TANH: st = launch_dz<BSS_ACT_GELU_TANH>(d, p.blocks, stream); break;
+            case BSS_ACT_GELU: st = launch_dz<BSS_ACT_GELU>(d, p.blocks, stream); break;
+            case BSS_ACT_SILU: st = launch_dz<BSS_ACT_SILU>(d, p.blocks, stream); break;
+            default: st = launch_dz<BSS_ACT_NONE>(d, p.blocks, stream);
+        }
+        if (st != BSS_OK) return st;
+        const unsigned columns = static_cast<unsigned>((n + 31) / 32);
+        if (a.dbias != nullptr)
+            st = launch_behind(sum_parts_kernel, dim3(columns, 1), 256, stream, "bias gradient launch", d.dbias, a.dbias,
+                               p.blocks, a.out_channels);
+        if (st == BSS_OK && a.dgate != nullptr && p.chunks > 0)
+            st = launch_behind(sum_parts_kernel, dim3(columns, static_cast<unsigned>(p.groups)), 256, stream,
+                               "gate gradient launch", d.dgate, a.dgate, static_cast<int64_t>(p.chunks), a.out_channels);
+        if (st != BSS_OK) return st;
+    }
+    Epilogue e = {};
+    if (a.dx != nullptr) {
+        e.out = a.dx, e.out_stride = a.dx_stride, e.out_dtype = BSS_DTYPE_BF16;
+        st = gemm<false, true>(dz, dz_stride, a.weight, a.weight_stride, a.rows, k, n, e, stream);
+        if (st != BSS_OK) return st;
+    }
+    if (a.dweight != nullptr) {
+        e.out = a.dweight, e.out_stride = a.dweight_stride, e.out_dtype = a.dweight_dtype;
+        st = gemm<true, true>(dz, dz_stride, a.x, a.x_stride, n, k, a.rows, e, stream);
+    }
+    return st;
+}
+
+}  // extern "C"

@@ -296,6 +296,111 @@ bss_status bss_residual_norm_backward_workspace(const bss_residual_norm_grads* a
 /* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 bss_status bss_residual_norm_backward(const bss_residual_norm_grads* args, cudaStream_t stream);
 
+/* ------------------------------------------------------------ matrix products */
+
+enum {
+    BSS_ACT_NONE = 0,
+    BSS_ACT_GELU_TANH = 1, /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+    BSS_ACT_GELU = 2,      /* z / 2 (1 + erf(z / sqrt(2))) */
+    BSS_ACT_SILU = 3       /* z / (1 + exp(-z)) */
+};
+
+/* A linear layer with what follows it, for `rows` rows of in_channels channels:
+ *
+ *   z   = x weight^T + bias
+ *   out = residual_scale * residual + gate * activation(z)
+ *
+ * Products of bf16 values, sums and everything behind them in 32 bits, one
+ * rounding at the store.  (The tensor cores add 16 products at a time to a sum
+ * whose last bits are cut off, not rounded: about in_channels / 16 times 2^-24
+ * below its size at most, which shows in float outputs only.)
+ *   x           bf16 [rows][in_channels], rows x_stride elements apart.
+ *   weight      bf16 [out_channels][in_channels], rows weight_stride apart.
+ *   bias        param_dtype [out_channels], or NULL.
+ *   gate        param_dtype [groups][out_channels], groups gate_stride apart (not
+ *               used with one group), or NULL; row i belongs to group
+ *               i / rows_per_group, groups = ceil(rows / rows_per_group).
+ *   residual    out_dtype [rows][out_channels], or NULL (then residual_scale is 1).
+ *   out         out_dtype [rows][out_channels]; may equal residual (same stride).
+ *   pre         optional bf16 [rows][out_channels] output: z, which the backward
+ *               pass reads.  The activation takes the unrounded z.
+ *   workspace   device memory of at least the size that bss_linear_workspace gives,
+ *               16-byte aligned, used by this call only until its work is done;
+ *               NULL where that is 0.
+ * Outputs overlap no other tensor.  Tensors are 16-byte aligned, strides multiples
+ * of 8 elements of at most 2^28; in_channels and out_channels are multiples of 8,
+ * 8 .. 65536; rows < 2^31. */
+typedef struct {
+    int64_t rows;
+    int64_t rows_per_group;
+    int32_t in_channels, out_channels;
+    int32_t out_dtype, param_dtype;
+    int32_t activation;
+    float residual_scale;
+    const void* x;
+    const void* weight;
+    const void* bias;
+    const void* gate;
+    const void* residual;
+    void* out;
+    void* pre;
+    int64_t x_stride, weight_stride, gate_stride, residual_stride, out_stride, pre_stride;
+    void* workspace;
+    int64_t workspace_bytes;
+} bss_linear_args;
+
+/* Bytes of workspace that bss_linear needs for these arguments on the current
+ * device (its workspace fields are not looked at). */
+bss_status bss_linear_workspace(const bss_linear_args* args, int64_t* bytes);
+
+/* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+bss_status bss_linear(const bss_linear_args* args, cudaStream_t stream);
+
+/* Gradients of bss_linear, with dz = gate * dout * activation'(z):
+ *
+ *   dx = dz weight      dweight = dz^T x      dbias = sum over rows of dz
+ *   dgate = sum over a group's rows of dout * activation(z)
+ *
+ * (The residual's gradient is residual_scale * dout.)
+ *   dout        gradient of out, dout_dtype [rows][out_channels].
+ *   x, weight   the forward inputs; x is read for dweight, weight for dx.
+ *   pre         bf16, what the forward pass kept; read with an activation or for
+ *               dgate (else may be NULL).
+ *   gate        as in the forward pass.
+ *   dx          bf16 [rows][in_channels];
+ *   dweight     dweight_dtype [out_channels][in_channels], rows dweight_stride
+ *               apart;
+ *   dbias       float [out_channels]; dgate float [groups][out_channels], both
+ *               contiguous; all overwritten, each NULL when not wanted (one at
+ *               least is).  dgate needs gate.
+ * With an activation, a gate or a float dout, dz is rounded to bf16 before the two
+ * products (dbias and dgate are made from 32 bits).  Sums over rows are taken in a
+ * fixed order.  Alignment, strides and the workspace as for bss_linear. */
+typedef struct {
+    int64_t rows;
+    int64_t rows_per_group;
+    int32_t in_channels, out_channels;
+    int32_t dout_dtype, param_dtype, dweight_dtype;
+    int32_t activation;
+    const void* dout;
+    const void* x;
+    const void* weight;
+    const void* pre;
+    const void* gate;
+    void* dx;
+    void* dweight;
+    float* dbias;
+    float* dgate;
+    int64_t dout_stride, x_stride, weight_stride, pre_stride, gate_stride, dx_stride, dweight_stride;
+    void* workspace;
+    int64_t workspace_bytes;
+} bss_linear_grads;
+
+bss_status bss_linear_backward_workspace(const bss_linear_grads* args, int64_t* bytes);
+
+/* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+bss_status bss_linear_backward(const bss_linear_grads* args, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,89 @@
+"""Plain 64-bit references of the matrix products and the cross attention, with the
+magnitude of each result's terms, for ``_block_ref.check``.
+
+Roundings counted (in units of 2^-24 of the terms' magnitude):
+  a tensor core's sum of k products: every 16 of k the running sum is cut to 24
+  bits (one unit of its last place, 2 of 2^-24): 2 * k / 16, and 4 for the ends;
+  a tensor rounded to bf16 on the way (half a step, 2^-8): BF16 = 2^16;
+  an activation: exp of u (fast form: 2 + 1.2 |u| units in the last place, |u| its
+  own rounding) and a fast quotient: |u| < 90 where the value is not 0 to 1e-38,
+  so ACT = 512 covers value and slope."""
+import math
+
+import torch
+
+BF16 = 2 ** 16
+ACT = 512
+
+
+def chain(k):
+    return 2 * (k / 16 + 4)
+
+
+def act(z, kind):
+    """Value and slope of ACT_* in 64 bits (z float64)."""
+    if kind == 1:
+        # (1 + tanh u) / 2 = sigmoid(2 u): where the left side cancels (z < -6) it keeps
+        # no more than 1e-16 absolute in 64 bits, above a 32-bit rounding of values of 1e-10
+        c = 2 * math.sqrt(2 / math.pi)
+        s = torch.sigmoid(c * (z + 0.044715 * z ** 3))
+        return z * s, s + z * s * (1 - s) * c * (1 + 3 * 0.044715 * z * z)
+    if kind == 2:
+        half = 0.5 * torch.erfc(-z / math.sqrt(2))
+        return z * half, half + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    if kind == 3:
+        s = torch.sigmoid(z)
+        return z * s, s * (1 + z * (1 - s))
+    return z, torch.ones_like(z)
+
+
+def per_row(m, rows, group):
+    return m.double()[torch.arange(rows) // group]
+
+
+def linear(x, w, bias=None, kind=0, gate=None, residual=None, group=None, a=1.0):
+    """{name: (value, magnitude)} of out and pre; magnitudes hold CHAIN units of the product."""
+    x, w = x.double(), w.double()
+    rows = x.shape[0]
+    z, zm = x @ w.t(), x.abs() @ w.abs().t()
+    if bias is not None:
+        z, zm = z + bias.double(), zm + bias.double().abs()
+    v, _ = act(z, kind)
+    # slopes are at most 1.13
+    k = chain(x.shape[1]) + 4
+    vm = 1.13 * k * zm + (ACT if kind else 1) * v.abs()
+    if gate is not None:
+        g = per_row(gate, rows, group)
+        v, vm = v * g, (vm + v.abs()) * g.abs()
+    if residual is not None:
+        v, vm = v + a * residual.double(), vm + 4 * (v.abs() + abs(a) * residual.double().abs())
+    return {"out": (v, vm), "pre": (z, k * zm)}
+
+
+def group_sums(t, group):
+    rows = t.shape[0]
+    return torch.stack([t[i:i + group].sum(0) for i in range(0, rows, group)])
+
+
+def linear_grad(dout, x, w, pre=None, kind=0, gate=None, group=None):
+    """{name: (value, slack in units of 2^-24)}."""
+    d = dout.double()
+    rows = d.shape[0]
+    z = torch.zeros_like(d) if pre is None else pre.double()
+    v, s = act(z, kind)
+    out = {}
+    g = torch.ones_like(d)
+    if gate is not None:
+        g = per_row(gate, rows, group)
+        chain_g = ACT + 2 * group + 32
+        out["dgate"] = group_sums(d * v, group), chain_g * group_sums((d * v).abs(), group)
+    dz = d * g * s
+    # a slope is a difference of terms of at most 1.2
+    dzm = (d * g).abs() * (s.abs() if kind == 0 else torch.full_like(s, 1.2))
+    cut = 0 if kind == 0 and gate is None and dout.dtype == torch.bfloat16 else BF16
+    out["dbias"] = dz.sum(0), (ACT + rows + 32) * dzm.sum(0)
+    if w is not None:
+        out["dx"] = dz @ w.double(), (cut + ACT + chain(d.shape[1])) * (dzm @ w.double().abs())
+    if x is not None:
+        out["dweight"] = dz.t() @ x.double(), (cut + ACT + chain(rows)) * (dzm.t() @ x.double().abs())
+    return out
