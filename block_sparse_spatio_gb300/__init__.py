@@ -152,6 +152,18 @@ class _LinearGrads(ctypes.Structure):
                 + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)])
 
 
+class _StateTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("group_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _CrossArgs(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "rows_per_group")]
+                + [(n, ctypes.c_int32) for n in ("heads", "kv_heads", "head_dim", "keys")]
+                + [("softmax_scale", ctypes.c_float)] + [(n, _TokenTensor) for n in ("q", "O")]
+                + [(n, _StateTensor) for n in ("k", "v")] + [(n, ctypes.c_void_p) for n in ("lengths", "lse")])
+
+
 EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bss_tile_map_copy_csr",
             "bss_destroy_tile_map", "bss_permute", "bss_sparse_attention", "bss_dense_attention",
             "bss_get_device_status", "bss_status_string", "bss_last_error_message", "bss_version",
@@ -163,7 +175,7 @@ EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bs
             "bss_heads_from_tokens_backward_workspace", "bss_heads_from_tokens_backward",
             "bss_attention_step_tokens", "bss_residual_norm", "bss_residual_norm_backward_workspace",
             "bss_residual_norm_backward", "bss_linear_workspace", "bss_linear", "bss_linear_backward_workspace",
-            "bss_linear_backward")
+            "bss_linear_backward", "bss_cross_attention")
 
 
 def load(path: str | None = None):
@@ -245,6 +257,8 @@ def load(path: str | None = None):
     lib.bss_residual_norm_backward_workspace.restype = st
     lib.bss_residual_norm_backward.argtypes = [ctypes.POINTER(_ResidualNormGrads), p]
     lib.bss_residual_norm_backward.restype = st
+    lib.bss_cross_attention.argtypes = [ctypes.POINTER(_CrossArgs), p]
+    lib.bss_cross_attention.restype = st
     for name, args in (("linear", _LinearArgs), ("linear_backward", _LinearGrads)):
         getattr(lib, f"bss_{name}").argtypes = [ctypes.POINTER(args), p]
         getattr(lib, f"bss_{name}_workspace").argtypes = [ctypes.POINTER(args), i64p]
@@ -1132,3 +1146,68 @@ def linear_backward(dout, x=None, weight=None, dx=None, dweight=None, dbias=None
     lib = load()
     _with_workspace(a, lib.bss_linear_backward_workspace, lib.bss_linear_backward, workspace, stream, device)
     return dx, dweight
+
+
+# ---------------------------------------------------------------- cross attention
+
+def _rows_heads(t, name, shape, device):
+    """A [rows][heads][d] bf16 tensor's C form."""
+    import torch
+    if getattr(t, "dtype", None) != torch.bfloat16 or t.get_device() != device:
+        _on_device(t, name, device)
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be {tuple(shape)} (rows, heads, channels)")
+    rows, heads, channels = t.stride()
+    if channels != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    return _TokenTensor(t.data_ptr(), rows, heads)
+
+
+def _states(t, name, groups, d, device, like=None):
+    """(C form, keys, heads) of [groups][keys][heads][d] states ([keys][heads][d]: one group's)."""
+    import torch
+    if getattr(t, "dtype", None) != torch.bfloat16 or t.get_device() != device:
+        _on_device(t, name, device)
+        raise ValueError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() == 3:
+        t = t.unsqueeze(0)
+    if t.dim() != 4 or t.shape[0] != groups or t.shape[3] != d or (like is not None and t.shape[1:3] != like):
+        want = "keys, kv heads" if like is None else f"{like[0]}, {like[1]}"
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, must be ({groups}, {want}, {d}) (groups, states, heads, channels)")
+    group, token, head, channels = t.stride()
+    if channels != 1:
+        raise ValueError(f"{name}: the channels of a head must be contiguous")
+    return _StateTensor(t.data_ptr(), group, token, head), t.shape[1:3]
+
+
+def _rows_heads_shape(t, name):
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [rows][heads][channels]")
+    return t.shape
+
+
+def cross_attention(q, k, v, O, lengths=None, lse=None, rows_per_group: int | None = None,
+                    softmax_scale: float | None = None, stream=None):
+    """O <- attention of token-major q over an encoder's states (``bss_cross_attention``).
+
+    q, O: bf16 [rows][heads][d], d 64 or 128, rows and heads may be strided (O may
+    be q); k, v: bf16 [groups][states][kv_heads][d] (views of a packed projection
+    too; [states][kv_heads][d] with one group; a group stride of 0 shares one set
+    between the groups).  Row i attends to the states of group i // rows_per_group
+    (default: one group), head h to key head h // (heads // kv_heads).  lengths:
+    int32 [groups], the first so many states of a group are valid and the others
+    are not looked at (None: all); without any a row's O is 0 and its lse -inf.
+    lse: optional float32 [heads][rows] output for the backward pass.  Returns O."""
+    import torch
+    shape = rows, heads, d = _rows_heads_shape(q, "q")
+    device = _current_device()
+    group, (groups, _) = _groups(rows, rows_per_group, d)
+    k_t, like = _states(k, "k", groups, d, device)
+    a = _CrossArgs(rows, group, heads, like[1], d, like[0], 0.0 if softmax_scale is None else softmax_scale,
+                   _rows_heads(q, "q", shape, device), _rows_heads(O, "O", shape, device), k_t,
+                   _states(v, "v", groups, d, device, like)[0], _exact(lengths, "lengths", torch.int32, (groups,), device),
+                   _exact(lse, "lse", torch.float32, (heads, rows), device))
+    _check(load().bss_cross_attention(ctypes.byref(a), _stream_on(stream, device)))
+    return O

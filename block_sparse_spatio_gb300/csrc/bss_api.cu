@@ -144,6 +144,23 @@ bss_status encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, ui
     return BSS_OK;
 }
 
+bss_status encode_tmap_4d(CUtensorMap* map, const void* base, const uint64_t (&extent)[4],
+                          const uint64_t (&stride)[3], uint32_t box_inner, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    bss_status st = encode_fn(&enc);
+    if (st != BSS_OK) return st;
+    cuuint64_t dims[4], strides[3];
+    for (int i = 0; i < 4; ++i) dims[i] = extent[i];
+    for (int i = 0; i < 3; ++i) strides[i] = extent[i + 1] > 1 ? stride[i] : extent[0] * 2;
+    cuuint32_t box[4] = {box_inner, box_rows, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return set_error(BSS_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+    return BSS_OK;
+}
+
 bss_status check_mask_params(const bss_mask_params* p) { return validate_params(p); }
 
 }  // namespace bss

@@ -401,6 +401,53 @@ bss_status bss_linear_backward_workspace(const bss_linear_grads* args, int64_t* 
 /* Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 bss_status bss_linear_backward(const bss_linear_grads* args, cudaStream_t stream);
 
+/* ------------------------------------------------------------ cross attention */
+
+/* Keys or values of an encoder's states: element (group g, state t, head h,
+ * channel c) at data[g * group_stride + t * token_stride + h * head_stride + c]
+ * (strides in elements, multiples of 8; the stride of a dimension of size 1 is not
+ * used, the others are positive, a token's at most 2^28, the others at most 2^38).
+ * [groups][keys][kv_heads][d] tensors and views of a packed projection are of this
+ * form.  An input's group stride may be 0: one set of states for all groups. */
+typedef struct {
+    void* data; /* bf16, 16-byte aligned */
+    int64_t group_stride, token_stride, head_stride;
+} bss_state_tensor;
+
+/* Attention of `rows` tokens over an encoder's states of another length:
+ *
+ *   O[i][h] = sum over t of softmax_t(softmax_scale * q[i][h] . k[g][t][h']) v[g][t][h']
+ *
+ * with g = i / rows_per_group the row's group (a sample, or a piece of a clip with
+ * a prompt of its own; groups = ceil(rows / rows_per_group)), h' = h / (heads /
+ * kv_heads) the key head that h shares, and t over the group's valid states.
+ *   q, O        token-major [rows][heads][head_dim] (strides as bss_token_tensor,
+ *               positive where the dimension is larger than 1); O may be q (same
+ *               strides).
+ *   k, v        [groups][keys][kv_heads][head_dim].
+ *   lengths     device int32 [groups]: the first lengths[g] states of a group are
+ *               valid (taken as 0 below 0 and as keys above), the others are not
+ *               looked at, whatever they hold; NULL = all.  With none a row's O is
+ *               0 and its lse minus infinity.
+ *   lse         optional device float [heads][rows] output, 4-byte aligned: the
+ *               natural logarithm of the softmax's denominator, for the backward
+ *               pass.
+ *   softmax_scale  <= 0: 1 / sqrt(head_dim).
+ * head_dim 64 or 128; kv_heads divides heads, at most 65535; rows and keys < 2^31. */
+typedef struct {
+    int64_t rows;
+    int64_t rows_per_group;
+    int32_t heads, kv_heads, head_dim, keys;
+    float softmax_scale;
+    bss_token_tensor q, O;
+    bss_state_tensor k, v;
+    const int32_t* lengths;
+    float* lse;
+} bss_cross_args;
+
+/* One launch.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

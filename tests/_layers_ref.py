@@ -87,3 +87,37 @@ def linear_grad(dout, x, w, pre=None, kind=0, gate=None, group=None):
     if x is not None:
         out["dweight"] = dz.t() @ x.double(), (cut + ACT + chain(rows)) * (dzm.t() @ x.double().abs())
     return out
+
+
+# ---------------------------------------------------------------- cross attention
+
+def cross(q, k, v, lengths, group, scale=None):
+    """O and lse with their slacks, q [rows][H][d], k, v [groups][keys][Hk][d], in units of 2^-24.
+
+    A score is off by chain(d) units of its terms and 8 of itself (the scale, the
+    reference and the exponential's argument), its weight by as many relative ones, 4
+    of the exponential and a rounding to bf16 on the way to the product."""
+    q, k, v = q.double(), k.double(), v.double()
+    rows, H, d = q.shape
+    Hk = k.shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    O, Om = torch.zeros_like(q), torch.zeros_like(q)
+    lse = torch.full((H, rows), -math.inf, dtype=torch.float64)
+    lm = torch.zeros_like(lse)
+    for i, n in enumerate(lengths):
+        at = slice(i * group, min((i + 1) * group, rows))
+        n = min(max(n, 0), k.shape[1])
+        if n == 0:
+            continue
+        for h in range(H):
+            kk, vv = k[i, :n, h * Hk // H], v[i, :n, h * Hk // H]
+            s = q[at, h] @ kk.t() * scale
+            off = (chain(d) * (q[at, h].abs() @ kk.abs().t()) * scale + 8 * s.abs()).amax(1, keepdim=True)
+            top = s.amax(1, keepdim=True)
+            p = (s - top).exp()
+            l = p.sum(1, keepdim=True)
+            O[at, h] = p @ vv / l
+            Om[at, h] = (BF16 + 2 * off + 16 + chain(n) + n / 2) * (p @ vv.abs()) / l
+            lse[h, at] = (top + l.log())[:, 0]
+            lm[h, at] = (off + 8 * (top.abs() + l.log()) + 16 + n / 2)[:, 0]
+    return {"O": (O, Om), "lse": (lse, lm)}
