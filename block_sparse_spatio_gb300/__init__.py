@@ -164,6 +164,14 @@ class _CrossArgs(ctypes.Structure):
                 + [(n, _StateTensor) for n in ("k", "v")] + [(n, ctypes.c_void_p) for n in ("lengths", "lse")])
 
 
+class _CrossGrads(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("rows", "rows_per_group")]
+                + [(n, ctypes.c_int32) for n in ("heads", "kv_heads", "head_dim", "keys")]
+                + [("softmax_scale", ctypes.c_float)] + [(n, _TokenTensor) for n in ("dO", "q", "O", "dq")]
+                + [(n, _StateTensor) for n in ("k", "v", "dk", "dv")]
+                + [(n, ctypes.c_void_p) for n in ("lengths", "lse", "workspace")] + [("workspace_bytes", ctypes.c_int64)])
+
+
 EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bss_tile_map_copy_csr",
             "bss_destroy_tile_map", "bss_permute", "bss_sparse_attention", "bss_dense_attention",
             "bss_get_device_status", "bss_status_string", "bss_last_error_message", "bss_version",
@@ -175,7 +183,8 @@ EXPORTED = ("bss_build_tile_map", "bss_tile_map_stats", "bss_tile_map_dims", "bs
             "bss_heads_from_tokens_backward_workspace", "bss_heads_from_tokens_backward",
             "bss_attention_step_tokens", "bss_residual_norm", "bss_residual_norm_backward_workspace",
             "bss_residual_norm_backward", "bss_linear_workspace", "bss_linear", "bss_linear_backward_workspace",
-            "bss_linear_backward", "bss_cross_attention")
+            "bss_linear_backward", "bss_cross_attention",
+            "bss_cross_attention_backward_workspace", "bss_cross_attention_backward")
 
 
 def load(path: str | None = None):
@@ -259,7 +268,8 @@ def load(path: str | None = None):
     lib.bss_residual_norm_backward.restype = st
     lib.bss_cross_attention.argtypes = [ctypes.POINTER(_CrossArgs), p]
     lib.bss_cross_attention.restype = st
-    for name, args in (("linear", _LinearArgs), ("linear_backward", _LinearGrads)):
+    for name, args in (("linear", _LinearArgs), ("linear_backward", _LinearGrads),
+                       ("cross_attention_backward", _CrossGrads)):
         getattr(lib, f"bss_{name}").argtypes = [ctypes.POINTER(args), p]
         getattr(lib, f"bss_{name}_workspace").argtypes = [ctypes.POINTER(args), i64p]
         getattr(lib, f"bss_{name}").restype = getattr(lib, f"bss_{name}_workspace").restype = st
@@ -1211,3 +1221,30 @@ def cross_attention(q, k, v, O, lengths=None, lse=None, rows_per_group: int | No
                    _exact(lse, "lse", torch.float32, (heads, rows), device))
     _check(load().bss_cross_attention(ctypes.byref(a), _stream_on(stream, device)))
     return O
+
+
+def cross_attention_backward(dO, q, k, v, O, lse, dq, dk, dv, lengths=None, rows_per_group: int | None = None,
+                             softmax_scale: float | None = None, workspace=None, stream=None):
+    """Gradients of ``cross_attention`` (``bss_cross_attention_backward``).
+
+    dO: bf16 [rows][heads][d], the gradient of O; q, k, v, lengths: the forward
+    call's inputs, O and lse what it wrote; dq [rows][heads][d], dk and dv
+    [groups][states][kv_heads][d]: bf16 outputs, strided as the inputs may be
+    (views of one packed gradient, say), overwritten; states that are not valid
+    get zeros.  Sums over rows are taken in a fixed order.  workspace: taken from
+    torch's allocator when None.  Returns (dq, dk, dv)."""
+    import torch
+    shape = rows, heads, d = _rows_heads_shape(q, "q")
+    device = _current_device()
+    group, (groups, _) = _groups(rows, rows_per_group, d)
+    k_t, like = _states(k, "k", groups, d, device)
+    v_t, dk_t, dv_t = (_states(t, n, groups, d, device, like)[0] for t, n in ((v, "v"), (dk, "dk"), (dv, "dv")))
+    dO_t, q_t, O_t, dq_t = (_rows_heads(t, n, shape, device) for t, n in ((dO, "dO"), (q, "q"), (O, "O"), (dq, "dq")))
+    if lse is None:
+        raise ValueError("lse must be given")
+    a = _CrossGrads(rows, group, heads, like[1], d, like[0], 0.0 if softmax_scale is None else softmax_scale, dO_t, q_t,
+                    O_t, dq_t, k_t, v_t, dk_t, dv_t, _exact(lengths, "lengths", torch.int32, (groups,), device),
+                    _exact(lse, "lse", torch.float32, (heads, rows), device))
+    lib = load()
+    _with_workspace(a, lib.bss_cross_attention_backward_workspace, lib.bss_cross_attention_backward, workspace, stream, device)
+    return dq, dk, dv

@@ -448,6 +448,40 @@ typedef struct {
 /* One launch.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream);
 
+/* Gradients of bss_cross_attention, with P its softmax and D = sum of dO O a head:
+ *
+ *   dS = P (dO v - D)      dq = softmax_scale dS k      dv = P^T dO
+ *   dk = softmax_scale dS^T q       (dk, dv: summed over the heads that share a key head)
+ *
+ *   dO, q, k, v, O, lse, lengths   the gradient of O and the forward call's inputs and
+ *               outputs (here O is an input, and not q).  k and v have a group
+ *               stride of their own when there is more than one group.
+ *   dq          token-major [rows][heads][head_dim];
+ *   dk, dv      [groups][keys][kv_heads][head_dim], zero where a state is not
+ *               valid; at least two of groups, keys and kv_heads follow one another
+ *               without a gap, as in a view of a packed tensor.  All overwritten.
+ *   workspace   device memory of at least the size that
+ *               bss_cross_attention_backward_workspace gives, 16-byte aligned, used
+ *               by this call only until its work is done.
+ * Sums over rows are taken in a fixed order.  Outputs overlap no other tensor. */
+typedef struct {
+    int64_t rows;
+    int64_t rows_per_group;
+    int32_t heads, kv_heads, head_dim, keys;
+    float softmax_scale;
+    bss_token_tensor dO, q, O, dq;
+    bss_state_tensor k, v, dk, dv;
+    const int32_t* lengths;
+    const float* lse;
+    void* workspace;
+    int64_t workspace_bytes;
+} bss_cross_grads;
+
+bss_status bss_cross_attention_backward_workspace(const bss_cross_grads* args, int64_t* bytes);
+
+/* Three launches.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

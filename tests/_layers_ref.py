@@ -121,3 +121,40 @@ def cross(q, k, v, lengths, group, scale=None):
             lse[h, at] = (top + l.log())[:, 0]
             lm[h, at] = (off + 8 * (top.abs() + l.log()) + 16 + n / 2)[:, 0]
     return {"O": (O, Om), "lse": (lse, lm)}
+
+
+def cross_grad(do, q, k, v, O, lse, lengths, group, scale=None):
+    """{name: (value, slack in units of 2^-24)} of dq, dk, dv; O and lse as a forward pass kept them.
+
+    P is off as in ``cross``, with lse's own rounding; dS by P's, by its terms' chains
+    and by a rounding to bf16 on the way to the products."""
+    do, q, k, v, O, lse = (t.double() for t in (do, q, k, v, O, lse))
+    rows, H, d = q.shape
+    Hk = k.shape[2]
+    scale = d ** -0.5 if scale is None else scale
+    out = {n: (torch.zeros_like(t), torch.zeros_like(t)) for n, t in (("dq", q), ("dk", k), ("dv", v))}
+    for i, n in enumerate(lengths):
+        at = slice(i * group, min((i + 1) * group, rows))
+        m = at.stop - at.start
+        n = min(max(n, 0), k.shape[1])
+        if n == 0:
+            continue
+        for h in range(H):
+            j = h * Hk // H
+            qq, kk, vv, g = q[at, h], k[i, :n, j], v[i, :n, j], do[at, h]
+            s = qq @ kk.t() * scale
+            off = chain(d) * (qq.abs() @ kk.abs().t()) * scale + 8 * (s.abs() + lse[h, at, None].abs()) + 16
+            p = (s - lse[h, at, None]).exp()
+            D = (g * O[at, h]).sum(1, keepdim=True)
+            dp = g @ vv.t()
+            ds = p * (dp - D)
+            dse = p * ((BF16 + off) * (dp - D).abs() + chain(d) * (g.abs() @ vv.abs().t())
+                       + d * (g * O[at, h]).abs().sum(1, keepdim=True))
+            pe = p * (BF16 + off)
+            for name, to, value, slack in (
+                    ("dq", (at, h), scale * ds @ kk, scale * ((dse + chain(n) * ds.abs()) @ kk.abs())),
+                    ("dk", (i, slice(0, n), j), scale * ds.t() @ qq, scale * ((dse + (chain(m) + H) * ds.abs()).t() @ qq.abs())),
+                    ("dv", (i, slice(0, n), j), p.t() @ g, (pe + (chain(m) + H) * p).t() @ g.abs())):
+                out[name][0][to] += value
+                out[name][1][to] += slack
+    return out
