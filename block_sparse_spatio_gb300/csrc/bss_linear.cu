@@ -76,13 +76,16 @@ __device__ __forceinline__ void activate_both(float z, float& value, float& slop
 // ---------------------------------------------------------------- tile product
 // A tile of 128 CG rows and columns is made by CG CTAs (a pair's MMA takes half of
 // A and of B from each): warp 0 loads, warp 1 of the first CTA issues the MMAs,
-// warps 4 to 7 of each bring the accumulators of its 128 rows from TMEM to memory.
+// warps 4 to 11 of each bring the accumulators of its 128 rows from TMEM to memory,
+// a warp 32 rows of half of the columns, 128 bytes a row at a time through a piece of
+// shared memory of its own and a TMA store, which clips at the tensor's ends.
 // Two accumulators a CTA: the MMAs of the next tile run during this one's stores.
 constexpr int kTileK = 64;  // 128 bytes of bf16: one swizzle row
 constexpr int kOperand = 128 * kTileK * 2;
-constexpr int kStages = 6;
-constexpr int kThreads = 256;
-constexpr int kEpilogueWarp = 4;
+constexpr int kStages = 5;
+constexpr int kThreads = 384;
+constexpr int kEpilogueWarps = 8;
+constexpr int kPiece = 32 * 128;  // 32 rows of 128 bytes: a warp's two take turns
 
 struct Epilogue {
     const void* bias;
@@ -97,7 +100,7 @@ struct Epilogue {
 };
 
 struct GemmArgs {
-    CUtensorMap a, b;
+    CUtensorMap a, b, out, pre;
     int32_t m, n, kblocks;
     int32_t tiles_n, tiles;
     int* status;
@@ -105,7 +108,8 @@ struct GemmArgs {
 };
 
 struct GemmSmem {
-    static constexpr uint32_t kBars = kStages * 2 * kOperand;
+    static constexpr uint32_t kPieces = kStages * 2 * kOperand;
+    static constexpr uint32_t kBars = kPieces + kEpilogueWarps * 2 * kPiece;
     static constexpr uint32_t kBytes = kBars + (2 * kStages + 4) * 8 + 16;
     static constexpr uint32_t kAlloc = kBytes + 1024;  // the operands start on 1024 bytes
 };
@@ -140,15 +144,23 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int dtype, f
     }
 }
 
-template <int ACT>
-__device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t group, int col, float (&v)[8]) {
-    float w[8];
-    if (e.bias != nullptr) {
-        load_param8(e.bias, col, e.param_dtype, w);
+// 8 values of a row into a piece: its 16-byte units are swizzled like the TMA's.
+__device__ __forceinline__ void put8(uint8_t* row, int unit, const float (&v)[8]) {
+    *reinterpret_cast<uint4*>(row + ((unit ^ (threadIdx.x & 7)) << 4)) =
+        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+
+__device__ __forceinline__ void put8_float(uint8_t* row, int unit, const float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] += w[i];
-    }
-    if (e.pre != nullptr) store8(e.pre, row * e.pre_stride + col, BSS_DTYPE_BF16, v);
+    for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float4*>(row + (((unit + i) ^ (threadIdx.x & 7)) << 4)) =
+            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// z -> out, for 8 columns of a row; the residual's values are there already.
+template <int ACT>
+__device__ __forceinline__ void finish8(const Epilogue& e, int64_t group, int col, float (&v)[8], const float (&r)[8]) {
+    float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
     if (e.gate != nullptr) {
@@ -157,11 +169,9 @@ __device__ __forceinline__ void finish8(const Epilogue& e, int64_t row, int64_t 
         for (int i = 0; i < 8; ++i) v[i] *= w[i];
     }
     if (e.residual != nullptr) {
-        load8(e.residual, row * e.residual_stride + col, e.out_dtype, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(e.residual_scale, w[i], v[i]);
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(e.residual_scale, r[i], v[i]);
     }
-    store8(e.out, row * e.out_stride + col, e.out_dtype, v);
 }
 
 template <int CG, bool A_MN, bool B_MN, int ACT>
@@ -188,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + i, 1);
-            mbar_init(acc_empty + i, 4 * CG);
+            mbar_init(acc_empty + i, kEpilogueWarps * CG);
         }
         mbar_fence_init();
     }
@@ -285,35 +295,80 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 if (ok) commit(acc_full + buf);
             }
         }
-    } else if (warp >= kEpilogueWarp) {
-        const int quarter = warp & 3;
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, side = (warp - 4) >> 2;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-        uint32_t n_tile = 0;
+        uint8_t* pieces = smem + L::kPieces + (warp - 4) * 2 * kPiece;
+        const Epilogue& e = g.e;
+        const bool wide = e.out_dtype == BSS_DTYPE_F32;
+        uint32_t n_tile = 0, stores = 0;
+        // The piece to be written next.  With pre it has the first one and out the second,
+        // else out's take turns; the store that read it last must have done so.
+        auto piece = [&](int which) -> uint8_t* {
+            if (lane == 0) {
+                if (e.pre != nullptr) tma_store_wait_read<0>();
+                else tma_store_wait_read<1>();
+            }
+            __syncwarp();
+            return pieces + (e.pre != nullptr ? which : static_cast<int>(stores++ & 1)) * kPiece;
+        };
+        auto send = [&](const CUtensorMap* map, const uint8_t* from, int col, int row0) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tma_store_2d(map, from, col, row0);
+                tma_store_commit();
+            }
+        };
         for (int t = first; t < g.tiles; t += step, ++n_tile) {
             const int mt = t / g.tiles_n, nt = t - mt * g.tiles_n;
             const uint32_t buf = n_tile & 1;
+            const int row0 = mt * kTile + static_cast<int>(rank) * 128 + quarter * 32, row = row0 + lane;
+            const bool live = row < g.m;
+            const int64_t group = e.gate != nullptr && live ? e.by_rows.div(row) : 0;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + buf, (n_tile / 2) & 1, g.status))) break;
             tc_fence_after();
-            const int row = mt * kTile + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-            const int64_t group = g.e.gate != nullptr && row < g.m ? g.e.by_rows.div(row) : 0;
 #pragma unroll 1
-            for (int c = 0; c < static_cast<int>(kAccCols); c += 32) {
-                const int col = nt * kTile + c;
-                if (col >= g.n) break;
-                uint32_t r[32];
-                BSS_TMEM_LD32(tmem + lanes + buf * kAccCols + c, r);
-                tmem_wait_ld();
-                if (row < g.m) {
+            for (int c = side * (kTile / 2); c < (side + 1) * (kTile / 2); c += 64) {
+                const int col0 = nt * kTile + c;
+                if (col0 >= g.n || row0 >= g.m) break;
+                uint8_t *to_pre = nullptr, *to = nullptr;
+                if (e.pre != nullptr) to_pre = piece(0) + lane * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int col = col0 + 32 * h;
+                    if (h == 1 && col >= g.n) break;
+                    float r[4][8];
+                    if (e.residual != nullptr && live) {
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+                            if (col + 8 * u < g.n) load8(e.residual, row * e.residual_stride + col + 8 * u, e.out_dtype, r[u]);
+                    }
+                    uint32_t x[32];
+                    BSS_TMEM_LD32(tmem + lanes + buf * kAccCols + c + 32 * h, x);
+                    tmem_wait_ld();
+                    if (h == 0 || wide) to = piece(1) + lane * 128;
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        if (col + 8 * u < g.n) {
-                            float v[8];
+                        if (col + 8 * u >= g.n) break;
+                        float v[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[8 * u + i]);
-                            finish8<ACT>(g.e, row, group, col + 8 * u, v);
+                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[8 * u + i]);
+                        if (e.bias != nullptr) {
+                            float w[8];
+                            load_param8(e.bias, col + 8 * u, e.param_dtype, w);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) v[i] += w[i];
                         }
+                        if (e.pre != nullptr) put8(to_pre, 4 * h + u, v);
+                        finish8<ACT>(e, group, col + 8 * u, v, r[u]);
+                        if (wide) put8_float(to, 2 * u, v);
+                        else put8(to, 4 * h + u, v);
                     }
+                    if (wide) send(&g.out, to - lane * 128, col, row0);
                 }
+                if (!wide) send(&g.out, to - lane * 128, col0, row0);
+                if (e.pre != nullptr) send(&g.pre, to_pre - lane * 128, col0, row0);
             }
             tc_fence_before();
             __syncwarp();
@@ -322,6 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 else mbar_arrive(acc_empty + buf);
             }
         }
+        if (lane == 0) tma_store_wait_read_all();  // the pieces are read before the CTA ends
     }
 
     tc_fence_before();
@@ -478,6 +534,11 @@ bss_status launch_gemm(GemmArgs& g, cudaStream_t stream) {
     return cuda_check(cudaLaunchKernelEx(&config, kernel, g), "matrix product launch");
 }
 
+template <int ACT>
+bss_status launch_linear(GemmArgs& g, bool pair, cudaStream_t stream) {
+    return pair ? launch_gemm<2, false, false, ACT>(g, stream) : launch_gemm<1, false, false, ACT>(g, stream);
+}
+
 // D[m][n] = A B^T of k, then the epilogue.
 template <bool A_MN, bool B_MN>
 bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t m, int64_t n, int64_t k,
@@ -490,18 +551,22 @@ bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride
     if (st != BSS_OK) return st;
     st = B_MN ? operand_map(&g.b, b, k, b_stride, n, true) : operand_map(&g.b, b, n, b_stride, k, false);
     if (st != BSS_OK) return st;
+    if ((st = encode_tmap_rows(&g.out, e.out, e.out_dtype, n, m, e.out_stride * element_size(e.out_dtype), 32)) != BSS_OK) return st;
+    if (e.pre != nullptr && (st = encode_tmap_rows(&g.pre, e.pre, BSS_DTYPE_BF16, n, m, e.pre_stride * 2, 32)) != BSS_OK) return st;
     g.m = static_cast<int32_t>(m);
     g.n = static_cast<int32_t>(n);
     g.kblocks = static_cast<int32_t>((k + kTileK - 1) / kTileK);
     g.e = e;
+    const int64_t pairs = ((m + 255) / 256) * ((n + 255) / 256);
+    const bool pair = pairs >= num_sms() / 2;
     if constexpr (A_MN || B_MN) {
-        return launch_gemm<1, A_MN, B_MN, BSS_ACT_NONE>(g, stream);
+        return pair ? launch_gemm<2, A_MN, B_MN, BSS_ACT_NONE>(g, stream) : launch_gemm<1, A_MN, B_MN, BSS_ACT_NONE>(g, stream);
     } else {
         switch (e.activation) {
-            case BSS_ACT_GELU_TANH: return launch_gemm<1, false, false, BSS_ACT_GELU_TANH>(g, stream);
-            case BSS_ACT_GELU: return launch_gemm<1, false, false, BSS_ACT_GELU>(g, stream);
-            case BSS_ACT_SILU: return launch_gemm<1, false, false, BSS_ACT_SILU>(g, stream);
-            default: return launch_gemm<1, false, false, BSS_ACT_NONE>(g, stream);
+            case BSS_ACT_GELU_TANH: return launch_linear<BSS_ACT_GELU_TANH>(g, pair, stream);
+            case BSS_ACT_GELU: return launch_linear<BSS_ACT_GELU>(g, pair, stream);
+            case BSS_ACT_SILU: return launch_linear<BSS_ACT_SILU>(g, pair, stream);
+            default: return launch_linear<BSS_ACT_NONE>(g, pair, stream);
         }
     }
 }
