@@ -34,7 +34,8 @@ struct CrossArgs {
     CUtensorMap q, k, v;
     CrossShape s;
     int32_t tiles;  // of 256 rows in a group
-    int64_t items;
+    int32_t items;
+    FastDiv by_tiles;
     uint16_t* O;
     int64_t O_row, O_head;
     float* lse;
@@ -59,12 +60,12 @@ struct Item {
     bool two;                               // the second half has rows
 };
 
-__device__ __forceinline__ Item item_at(const CrossArgs& a, int64_t i) {
+__device__ __forceinline__ Item item_at(const CrossArgs& a, int i) {
     Item t;
-    const int64_t rest = i / a.s.heads;
-    t.head = static_cast<int>(i - rest * a.s.heads);
-    t.group = static_cast<int>(rest / a.tiles);
-    t.row0 = static_cast<int>(rest - static_cast<int64_t>(t.group) * a.tiles) * 256;
+    const int rest = a.s.by_heads.div(i);
+    t.head = i - rest * a.s.heads;
+    t.group = a.by_tiles.div(rest);
+    t.row0 = (rest - t.group * a.tiles) * 256;
     t.rows = a.s.rows_of(t.group) - t.row0;
     t.valid = t.rows > 0 ? a.s.valid(t.group) : 0;
     t.n = (t.valid + kKeyTile - 1) / kKeyTile;
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
             uint32_t fills = 0, q_fills[2] = {0, 0};
             uint32_t k_issued = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+            for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
                 const Item t = item_at(a, i);
                 if (t.n == 0) continue;
                 const int row = t.group * a.s.group_rows + t.row0;
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                                     t.head, q_full + h);
                     ++q_fills[h];
                 }
-                const int kv = t.head / a.s.share, g = a.s.shared_states ? 0 : t.group;
+                const int kv = a.s.by_share.div(t.head), g = a.s.shared_states ? 0 : t.group;
                 for (int j = 0; ok && j < t.n; ++j, ++fills) {
                     const uint32_t st = fills % kStages, parity = (fills / kStages - 1) & 1;
                     if (fills >= kStages) ok = mbar_wait(k_empty + st, parity, a.status);
@@ -201,9 +202,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
             };
             uint32_t fills = 0;                           // K and V tiles taken
             uint32_t q_taken[2] = {0, 0}, p_taken[2] = {0, 0};
-            int64_t i = blockIdx.x;
+            int i = blockIdx.x;
             Item t;
-            auto next_item = [&](int64_t from) {  // the first one with keys
+            auto next_item = [&](int from) {  // the first one with keys
                 for (i = from; i < a.items; i += gridDim.x) {
                     t = item_at(a, i);
                     if (t.n > 0) return true;
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
         const float c = a.s.scale_log2;
         uint32_t steps = 0;  // tiles of this half so far
         bool ok = true;
-        for (int64_t i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+        for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
             const Item t = item_at(a, i);
             if (t.rows <= h * kHalfRows) continue;
             const bool live = h * kHalfRows + r < t.rows;
@@ -430,7 +431,7 @@ bss_status launch_forward(CrossArgs& a, cudaStream_t stream) {
     int blocks;
     const bss_status st = resident_blocks(reinterpret_cast<const void*>(kernel), kThreads, CrossSmem<D>::kAlloc, &blocks);
     if (st != BSS_OK) return st;
-    const int64_t grid = a.items < num_sms() ? a.items : num_sms();
+    const int grid = a.items < num_sms() ? a.items : num_sms();
     kernel<<<static_cast<unsigned>(grid), kThreads, CrossSmem<D>::kAlloc, stream>>>(a);
     return cuda_check(cudaGetLastError(), "cross attention launch");
 }
@@ -516,6 +517,8 @@ CrossShape cross_shape(int64_t rows, int64_t rows_per_group, int32_t heads, int3
     s.keys = keys;
     s.shared_states = group_stride == 0 || s.groups == 1;
     s.lengths = lengths;
+    s.by_heads = FastDiv(static_cast<uint32_t>(heads));
+    s.by_share = FastDiv(static_cast<uint32_t>(s.share));
     s.scale_log2 = (softmax_scale > 0.0f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(head_dim))) * 1.4426950408889634f;
     return s;
 }
@@ -570,7 +573,10 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream) 
     a.s = cross_shape(p.rows, p.rows_per_group, p.heads, p.kv_heads, p.head_dim, p.keys, p.softmax_scale, p.lengths,
                       p.k.group_stride);
     a.tiles = static_cast<int32_t>((p.rows_per_group + 255) / 256);
-    a.items = groups * a.tiles * p.heads;
+    const int64_t items = groups * a.tiles * p.heads;
+    if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
+    a.items = static_cast<int32_t>(items);
+    a.by_tiles = FastDiv(static_cast<uint32_t>(a.tiles));
     a.O = static_cast<uint16_t*>(p.O.data);
     a.O_row = p.rows > 1 ? p.O.token_stride : 0;
     a.O_head = p.heads > 1 ? p.O.head_stride : 0;

@@ -21,6 +21,7 @@ struct CrossShape {
     int32_t shared_states;  // 1: one set of states for all groups
     const int32_t* lengths;
     float scale_log2;  // softmax_scale log2(e)
+    FastDiv by_heads, by_share;
 
     // valid keys of a group
     __device__ __forceinline__ int valid(int g) const {

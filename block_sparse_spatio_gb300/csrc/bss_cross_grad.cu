@@ -10,14 +10,16 @@
 // own.
 //
 // dq: a CTA takes items of (group, 128 rows, head); per key tile the products
-// S(t+1), dQ(t), dP(t+1) follow one another, so that P(t+1) is made beneath dQ(t) and
-// dP(t+1), dS(t) beneath S(t+1).  D is made here, once an item, and kept for the
-// second kernel.
+// S(t+1), dP(t+1), dQ(t) follow one another (two dP in TMEM), so that the P and dS of a
+// tile are made beneath the products of its neighbours.  D is made here, once an item,
+// and kept for the second kernel.
 //
-// dk, dv: the pairs of (key tile, row tile) of all heads lie in a line that is cut
-// into equal runs, one a CTA, whatever the lengths; a key tile's products are S(t+1),
-// dK(t), dP(t+1), dV(t+1) over its row tiles.  Where a run ends inside a key tile the
-// sums go to the workspace in 32 bits, and a third kernel adds them in their order.
+// dk, dv: the row tiles of all key heads lie in a line that is cut into equal runs, one
+// a team of CTAs; each CTA of a team has a key tile of its own, so that the team reads
+// a row tile about once from memory (single CTAs cutting the line of all pairs of
+// tiles read 1.58 GB for 75,600 x 10 x 128 over 512 states instead of 0.4).  A tile's
+// products are S(t+1), dK(t), dP(t+1), dV(t+1).  Where a run ends inside a head's rows
+// the sums go to the workspace in 32 bits, and a third kernel adds them in their order.
 #include "bss_cross.cuh"
 
 #include <cstring>
@@ -28,17 +30,19 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kElementwise = 256;  // threads 128 .. 383: a lane of TMEM and half of the columns
-constexpr uint32_t kRegsControl = 72, kRegsElementwise = 208;
+// Registers: 128 x 104 + 256 x 192 = 62,464 of the launch's 384 x 168 = 64,512.
+constexpr uint32_t kRegsControl = 104, kRegsElementwise = 192;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColS = 0, kColP = 128, kColA = 256, kColB = 384;  // S, dP, two accumulators
+constexpr uint32_t kColS = 0, kColP = 128, kColA = 256, kColB = 384;  // S, dP, two sums (or a second dP and one)
 
 struct GradArgs {
     CUtensorMap q, dO, k, v;
     CrossShape s;
     int32_t tiles;      // of 128 rows in a group
     int32_t key_tiles;  // of 128 keys in a group
-    int64_t items;      // of the first kernel
+    int32_t items;      // of the first kernel
     int32_t blocks;     // of the second
+    FastDiv by_tiles;
     const uint16_t* O;
     uint16_t *dq, *dk, *dv;
     int64_t O_row, O_head, dq_row, dq_head;
@@ -46,7 +50,7 @@ struct GradArgs {
     float scale;
     const float* lse;  // [heads][rows]
     float* delta;      // [heads][rows]
-    int64_t* starts;   // [groups + 1]: pairs of key and row tiles in front of a group
+    int64_t* starts;   // [groups + 1]: row tiles of all key heads in front of a group; [groups + 1]: most key tiles
     float* parts;      // [2 blocks][2][128][d]
     int* status;
 };
@@ -95,8 +99,8 @@ struct DqSmem {
     static constexpr uint32_t kQ = 0, kDO = kTile, kK = 2 * kTile, kV = kK + kKStages * kTile;
     static constexpr uint32_t kDelta = kV + kVStages * kTile;  // float [2][2][128]
     static constexpr uint32_t kBar = kDelta + 2048;
-    // q_full q_empty do_full do_empty k_full k_empty v_full v_empty s_full s_read dp_full ds_full dq_done[2] halves
-    static constexpr uint32_t kBars = 4 + 2 * kKStages + 2 * kVStages + 7;
+    // q_full q_empty do_full do_empty k_full k_empty v_full v_empty s_full s_read dp_full[2] ds_full[2] dq_done halves
+    static constexpr uint32_t kBars = 4 + 2 * kKStages + 2 * kVStages + 8;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 16;
 };
 
@@ -104,12 +108,12 @@ struct DqItem {
     int group, row0, rows, head, valid, n;
 };
 
-__device__ __forceinline__ DqItem dq_item(const GradArgs& a, int64_t i) {
+__device__ __forceinline__ DqItem dq_item(const GradArgs& a, int i) {
     DqItem t;
-    const int64_t rest = i / a.s.heads;
-    t.head = static_cast<int>(i - rest * a.s.heads);
-    t.group = static_cast<int>(rest / a.tiles);
-    t.row0 = static_cast<int>(rest - static_cast<int64_t>(t.group) * a.tiles) * 128;
+    const int rest = a.s.by_heads.div(i);
+    t.head = i - rest * a.s.heads;
+    t.group = a.by_tiles.div(rest);
+    t.row0 = (rest - t.group * a.tiles) * 128;
     t.rows = a.s.rows_of(t.group) - t.row0;
     t.valid = t.rows > 0 ? a.s.valid(t.group) : 0;
     t.n = (t.valid + kKeyTile - 1) / kKeyTile;
@@ -117,14 +121,18 @@ __device__ __forceinline__ DqItem dq_item(const GradArgs& a, int64_t i) {
 }
 
 // starts[], by one warp
-__device__ __forceinline__ void count_pairs(const GradArgs& a) {
+__device__ __forceinline__ void count_rows(const GradArgs& a) {
     const int lane = threadIdx.x & 31;
     int64_t before = 0;
+    int most = 0;
     for (int g0 = 0; g0 < a.s.groups; g0 += 32) {
         const int g = g0 + lane;
         int64_t n = 0;
-        if (g < a.s.groups)
-            n = static_cast<int64_t>((a.s.valid(g) + kKeyTile - 1) / kKeyTile) * ((a.s.rows_of(g) + 127) / 128) * a.s.heads;
+        if (g < a.s.groups) {
+            const int tiles = (a.s.valid(g) + kKeyTile - 1) / kKeyTile;
+            n = tiles > 0 ? static_cast<int64_t>((a.s.rows_of(g) + 127) / 128) * a.s.heads : 0;
+            most = tiles > most ? tiles : most;
+        }
         int64_t sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -134,7 +142,11 @@ __device__ __forceinline__ void count_pairs(const GradArgs& a) {
         if (g < a.s.groups) a.starts[g] = before + sum - n;
         before += __shfl_sync(0xFFFFFFFFu, sum, 31);
     }
-    if (lane == 0) a.starts[a.s.groups] = before;
+    most = __reduce_max_sync(0xFFFFFFFFu, most);
+    if (lane == 0) {
+        a.starts[a.s.groups] = before;
+        a.starts[a.s.groups + 1] = most;
+    }
 }
 
 template <int D>
@@ -153,9 +165,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     uint64_t* s_full = v_empty + kVStages;
     uint64_t* s_read = s_full + 1;
     uint64_t* dp_full = s_read + 1;
-    uint64_t* ds_full = dp_full + 1;
-    uint64_t* dq_done = ds_full + 1;
-    uint64_t* halves = dq_done + 2;  // both halves of a row's D are there
+    uint64_t* ds_full = dp_full + 2;
+    uint64_t* dq_done = ds_full + 2;
+    uint64_t* halves = dq_done + 1;  // both halves of a row's D are there
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(halves + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles could not be addressed
@@ -173,9 +185,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         mbar_init(s_full, 1);
         mbar_init(s_read, kElementwise);
         mbar_init(dp_full, 1);
+        mbar_init(dp_full + 1, 1);
         mbar_init(ds_full, kElementwise);
+        mbar_init(ds_full + 1, kElementwise);
         mbar_init(dq_done, 1);
-        mbar_init(dq_done + 1, 1);
         mbar_init(halves, kElementwise);
         mbar_fence_init();
     }
@@ -194,11 +207,11 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
             tma_prefetch_desc(&a.v);
             uint32_t items = 0, dos = 0, ks = 0, vs = 0;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+            for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
                 const DqItem t = dq_item(a, i);
                 if (t.n == 0) continue;
                 const int row = t.group * a.s.group_rows + t.row0;
-                const int kv = t.head / a.s.share, g = a.s.shared_states ? 0 : t.group;
+                const int kv = a.s.by_share.div(t.head), g = a.s.shared_states ? 0 : t.group;
                 if (items > 0) ok = mbar_wait(q_empty, (items - 1) & 1, a.status);
                 if (!ok) break;
                 mbar_arrive_expect_tx(q_full, L::kTile);
@@ -264,12 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                     }
                 }
             };
-            int64_t i = blockIdx.x;
-            DqItem t;
-            auto next_item = [&](int64_t from) {
-                for (i = from; i < a.items; i += gridDim.x) {
+            int i = blockIdx.x;
+            auto next_item = [&](DqItem& t) {  // the next one with keys, from i on
+                for (; i < a.items; i += gridDim.x) {
                     t = dq_item(a, i);
-                    if (t.n > 0) return true;
+                    if (t.n > 0) {
+                        i += gridDim.x;
+                        return true;
+                    }
                 }
                 return false;
             };
@@ -277,8 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                 const int left = it.valid - j * kKeyTile;
                 return left >= kKeyTile ? kKeyTile : (left + 15) & ~15;
             };
-            uint32_t step = 0, items = 0;  // of the products below: dQ's
-            // S of tile j of item `it`, which is step f
+            // S of tile j of an item, which is step f
             auto issue_s = [&](const DqItem& it, int j, uint32_t f, uint32_t item) {
                 const uint32_t st = f % kKStages;
                 if (j == 0 && !wait(q_full, item & 1)) return false;
@@ -292,49 +306,50 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                 if (j == it.n - 1) commit(q_empty);
                 return true;
             };
+            // dP into the buffer that dQ(f - 2), issued before, has read
             auto issue_dp = [&](const DqItem& it, int j, uint32_t f, uint32_t item) {
                 const uint32_t st = f % kVStages;
                 if (j == 0 && !wait(do_full, item & 1)) return false;
                 if (!wait(v_full + st, (f / kVStages) & 1)) return false;
                 tc_fence_after();
-                product(kColP, d_do, d_v + st * kTileStep, width(it, j));
-                commit(dp_full);
+                product(kColP + 128 * (f & 1), d_do, d_v + st * kTileStep, width(it, j));
+                commit(dp_full + (f & 1));
                 commit(v_empty + st);
                 if (j == it.n - 1) commit(do_empty);
                 return true;
             };
-            bool more = next_item(i);
-            bool ok = !more || (issue_s(t, 0, 0, 0) && issue_dp(t, 0, 0, 0));
+            DqItem cur, nxt;
+            uint32_t step = 0, item = 0;
+            bool more = next_item(cur);
+            bool ok = !more || (issue_s(cur, 0, 0, 0) && issue_dp(cur, 0, 0, 0));
             while (ok && more) {
-                const DqItem cur = t;
-                const uint32_t item = items;
+                more = next_item(nxt);
                 for (int j = 0; j < cur.n; ++j, ++step) {
-                    DqItem nxt = cur;
-                    int nj = j + 1;
-                    uint32_t n_item = item;
-                    bool has = true;
-                    if (nj == cur.n) {
-                        has = more = next_item(i + gridDim.x);
-                        nxt = t, nj = 0, n_item = item + 1;
+                    const bool last = j == cur.n - 1;
+                    if (!last) {
+                        if (!(ok = issue_s(cur, j + 1, step + 1, item) && issue_dp(cur, j + 1, step + 1, item))) break;
+                    } else if (more) {
+                        if (!(ok = issue_s(nxt, 0, step + 1, item + 1) && issue_dp(nxt, 0, step + 1, item + 1))) break;
                     }
-                    if (has && !(ok = issue_s(nxt, nj, step + 1, n_item))) break;
-                    if (!(ok = wait(ds_full, step & 1))) break;
+                    // of an item's first tile: only after the elementwise threads have read
+                    // the sums of the item before
+                    if (!(ok = wait(ds_full + (step & 1), (step >> 1) & 1))) break;
                     tc_fence_after();
                     const uint32_t st = step % kKStages;
                     if (leader) {
                         const int steps = width(cur, j) / 16;
                         for (int kk = 0; kk < steps; ++kk)
-                            umma_ts(tmem + kColA + 128 * (item & 1), tmem + kColP + packed_col(kk),
+                            umma_ts(tmem + kColB, tmem + kColP + 128 * (step & 1) + packed_col(kk),
                                     d_kt + st * kTileStep + static_cast<uint64_t>(kk * 128), idesc_dq, j > 0 || kk > 0);
                     }
                     commit(k_empty + st);
-                    if (j == cur.n - 1) commit(dq_done + (item & 1));
-                    if (has && !(ok = issue_dp(nxt, nj, step + 1, n_item))) break;
+                    if (last) commit(dq_done);
                 }
-                ++items;
+                cur = nxt;
+                ++item;
             }
         } else if (warp == 2 && blockIdx.x == 0) {
-            count_pairs(a);
+            count_rows(a);
         }
     } else {
         setmaxnreg_inc<kRegsElementwise>();
@@ -345,43 +360,59 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         float* exchange = reinterpret_cast<float*>(smem + L::kDelta);
         const float c = a.s.scale_log2;
         uint32_t step = 0, items = 0;
-        bool ok = true;
-        // the item whose dq is still to be stored
-        bool pending = false;
+        bool ok = true, pending = false;  // pending: the item before's dq is still to be stored
         uint16_t* out = nullptr;
         bool out_live = false;
         constexpr int kCols = D / 2;  // dq columns of a thread
         auto store_pending = [&]() {
-            const uint32_t item = items - 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(dq_done + (item & 1), (item >> 1) & 1, a.status))) return false;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(dq_done, (items - 1) & 1, a.status))) return false;
             tc_fence_after();
-            store_row<kCols / 32>(tmem + lanes + kColA + 128 * (item & 1) + half * kCols, out, a.scale, out_live);
+            store_row<kCols / 32>(tmem + lanes + kColB + half * kCols, out, a.scale, out_live);
+            tc_fence_before();
             pending = false;
             return true;
         };
-        for (int64_t i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
-            const DqItem t = dq_item(a, i);
-            if (t.rows <= 0) continue;
-            const bool live = r < t.rows;
-            const int64_t row = static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + r;
-            uint16_t* to = a.dq + row * a.dq_row + t.head * a.dq_head + half * kCols;
-            if (t.n == 0) {
-                if (live)
+        int i = blockIdx.x;
+        // the next item with keys; the rows of those without get zeros
+        auto next_item = [&](DqItem& t) {
+            for (; i < a.items; i += gridDim.x) {
+                t = dq_item(a, i);
+                if (t.n > 0) {
+                    i += gridDim.x;
+                    return true;
+                }
+                if (r < t.rows) {
+                    uint16_t* to = a.dq + (static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + r) * a.dq_row +
+                                   t.head * a.dq_head + half * kCols;
                     for (int u = 0; u < kCols / 8; ++u) reinterpret_cast<uint4*>(to)[u] = make_uint4(0, 0, 0, 0);
-                continue;
+                }
             }
-            // O of half of the channels, on its way while S and P are made
-            uint4 o[kCols / 8];
-            float lse2 = INFINITY;
-            if (live) {
-                const uint4* from = reinterpret_cast<const uint4*>(a.O + row * a.O_row + t.head * a.O_head + half * kCols);
+            return false;
+        };
+        auto row_of = [&](const DqItem& t) { return static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + r; };
+        // an item's O (half of the channels) and lse, fetched during the item before
+        uint4 o[kCols / 8];
+        float lse_next = 0.0f;
+        auto fetch = [&](const DqItem& t) {
+            if (r < t.rows) {
+                const uint4* from = reinterpret_cast<const uint4*>(a.O + row_of(t) * a.O_row + t.head * a.O_head + half * kCols);
 #pragma unroll
                 for (int u = 0; u < kCols / 8; ++u) o[u] = ld_row(from + u);
-                lse2 = a.lse[static_cast<int64_t>(t.head) * a.s.rows + row] * 1.4426950408889634f;
+                lse_next = a.lse[static_cast<int64_t>(t.head) * a.s.rows + row_of(t)];
             } else {
 #pragma unroll
                 for (int u = 0; u < kCols / 8; ++u) o[u] = make_uint4(0, 0, 0, 0);
+                lse_next = INFINITY;
             }
+        };
+        DqItem t, nxt;
+        bool more = next_item(t);
+        if (more) fetch(t);
+        while (ok && more) {
+            more = next_item(nxt);
+            const bool live = r < t.rows;
+            const int64_t row = row_of(t);
+            const float lse2 = lse_next * 1.4426950408889634f;
             float delta = 0.0f;
             for (int j = 0; j < t.n; ++j, ++step) {
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full, step & 1, a.status)))) break;
@@ -420,16 +451,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                     float* x = exchange + (items & 1) * 256;
                     x[half * 128 + r] = sum;
                     mbar_arrive(halves);
+                    if (pending && !(ok = store_pending())) break;
                     if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(halves, items & 1, a.status)))) break;
                     delta = x[r] + x[128 + r];
                     if (half == 0 && live) a.delta[static_cast<int64_t>(t.head) * a.s.rows + row] = delta;
                 }
-                if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(dp_full, step & 1, a.status)))) break;
+                if (j == t.n - 1 && more) fetch(nxt);
+                if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(dp_full + (step & 1), (step >> 1) & 1, a.status)))) break;
                 tc_fence_after();
                 {
+                    const uint32_t at = t_p + 128 * (step & 1);
                     uint32_t g[2][32];
-                    BSS_TMEM_LD32(t_p, g[0]);
-                    BSS_TMEM_LD32(t_p + 32, g[1]);
+                    BSS_TMEM_LD32(at, g[0]);
+                    BSS_TMEM_LD32(at + 32, g[1]);
                     tmem_wait_ld();
 #pragma unroll
                     for (int x = 0; x < 64; ++x) p[x] *= __uint_as_float(g[x >> 5][x & 31]) - delta;
@@ -438,18 +472,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                         for (int x = 0; x < 64; ++x)
                             if (x >= left) p[x] = 0.0f;
                     }
-                    store_packed(t_p, p);
+                    store_packed(at, p);
                 }
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(ds_full);
-                if (j == 0 && pending && !(ok = store_pending())) break;
+                // (two barriers: the next tile's dS may be there before this one's is taken)
+                mbar_arrive(ds_full + (step & 1));
             }
             if (!ok) break;
             ++items;
             pending = true;
-            out = to;
+            out = a.dq + row * a.dq_row + t.head * a.dq_head + half * kCols;
             out_live = live;
+            t = nxt;
         }
         if (ok && pending) store_pending();
     }
@@ -477,22 +512,48 @@ struct DkvSmem {
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 16;
 };
 
-// The run of a CTA, key tile by key tile.
+// A CTA's share: a run of the line of row tiles, for one key tile (or, with more of
+// them than CTAs, every so many).  Part: the run's piece of a key head's rows.
 struct Part {
-    int group, kv, tile, valid;  // the key tile
-    int per, row_tiles;          // its row tiles over all heads that share it, and those of one head
-    int first, last;             // of this run
-    int64_t end;                 // where the run goes on
+    int group, kv, tile, valid, rows;  // the key tile; rows of the group
+    int per;                           // row tiles of the head, over all heads that share it
+    int first, last;                   // of this piece
+    int64_t end;                       // where the run goes on
 };
 
-__device__ __forceinline__ int64_t run_begin(const GradArgs& a, int64_t total, int b) {
-    const int64_t each = total / a.blocks, rest = total - each * a.blocks;
-    return each * b + (b < rest ? b : rest);
+struct Share {
+    int64_t lo, hi, at;
+    int tile, step, tiles;  // this CTA's key tiles: tile, tile + step, ... below tiles
+};
+
+__device__ __forceinline__ int64_t run_begin(int64_t total, int teams, int team) {
+    const int64_t each = total / teams, rest = total - each * teams;
+    return each * team + (team < rest ? team : rest);
+}
+
+// Teams of CTAs: one a key tile each; at most as many as there are row tiles.
+__device__ __forceinline__ int teams_of(const GradArgs& a, int64_t total, int tiles) {
+    const int64_t teams = tiles > 0 && tiles <= a.blocks ? a.blocks / tiles : 1;
+    return static_cast<int>(teams < total ? teams : (total > 0 ? total : 1));
+}
+
+__device__ __forceinline__ Share share_of(const GradArgs& a, int block) {
+    const int64_t total = a.starts[a.s.groups];
+    Share s;
+    s.tiles = static_cast<int>(a.starts[a.s.groups + 1]);
+    const int teams = teams_of(a, total, s.tiles);
+    s.step = s.tiles <= a.blocks ? s.tiles : a.blocks;
+    const int team = s.step > 0 ? block / s.step : teams;
+    s.tile = team < teams ? block - team * s.step : s.tiles;
+    if (team < teams) s.lo = run_begin(total, teams, team), s.hi = run_begin(total, teams, team + 1);
+    else s.lo = s.hi = 0;
+    s.at = s.lo;
+    return s;
 }
 
 __device__ __forceinline__ Part part_at(const GradArgs& a, int64_t u, int64_t hi) {
     int lo_g = 0, hi_g = a.s.groups - 1;
-    while (lo_g < hi_g) {  // the last group that starts at or in front of u, among those with pairs
+    while (lo_g < hi_g) {  // the last group that starts at or in front of u: it has row tiles
         const int mid = (lo_g + hi_g + 1) >> 1;
         if (a.starts[mid] <= u) lo_g = mid;
         else hi_g = mid - 1;
@@ -500,18 +561,45 @@ __device__ __forceinline__ Part part_at(const GradArgs& a, int64_t u, int64_t hi
     Part p;
     p.group = lo_g;
     p.valid = a.s.valid(lo_g);
-    const int tiles = (p.valid + kKeyTile - 1) / kKeyTile;
-    p.row_tiles = (a.s.rows_of(lo_g) + 127) / 128;
-    p.per = p.row_tiles * a.s.share;
-    const int64_t local = u - a.starts[lo_g], seg = local / p.per;
-    p.first = static_cast<int>(local - seg * p.per);
-    p.kv = static_cast<int>(seg / tiles);
-    p.tile = static_cast<int>(seg - static_cast<int64_t>(p.kv) * tiles);
+    p.rows = a.s.rows_of(lo_g);
+    p.per = (p.rows + 127) / 128 * a.s.share;
+    const int64_t local = u - a.starts[lo_g];
+    p.kv = static_cast<int>(local / p.per);
+    p.first = static_cast<int>(local - static_cast<int64_t>(p.kv) * p.per);
     const int64_t seg_end = u - p.first + p.per;
     p.end = seg_end < hi ? seg_end : hi;
     p.last = p.first + static_cast<int>(p.end - u);
     return p;
 }
+
+// The share's next part with valid keys.
+__device__ __forceinline__ bool next_part(const GradArgs& a, Share& s, Part& p) {
+    while (s.tile < s.tiles) {
+        while (s.at < s.hi) {
+            p = part_at(a, s.at, s.hi);
+            s.at = p.end;
+            p.tile = s.tile;
+            if (s.tile * kKeyTile < p.valid) return true;
+        }
+        s.tile += s.step;
+        s.at = s.lo;
+    }
+    return false;
+}
+
+// A row tile: its head and first row in the group.
+struct RowTile {
+    int head, row0;
+    __device__ __forceinline__ void begin(const GradArgs& a, const Part& p) {
+        const int tiles = (p.rows + 127) / 128, h = p.first / tiles;
+        head = p.kv * a.s.share + h;
+        row0 = (p.first - h * tiles) * 128;
+    }
+    __device__ __forceinline__ void next(const Part& p) {
+        row0 += 128;
+        if (row0 >= p.rows) row0 = 0, ++head;
+    }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_constant__ GradArgs a) {
@@ -535,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     uint64_t* sums = ds_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t total = a.starts[a.s.groups];
-    const int64_t lo = run_begin(a, total, blockIdx.x), hi = run_begin(a, total, blockIdx.x + 1);
-    if (lo >= hi) return;
+    Share share = share_of(a, blockIdx.x);
+    Part p;
+    if (!next_part(a, share, p)) return;
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles could not be addressed
         record_status(a.status, BSS_ERR_CUDA);
         return;
@@ -564,10 +652,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // unit x of a part: its head and first row in the group
-    auto head_of = [&](const Part& p, int x) { return p.kv * a.s.share + x / p.row_tiles; };
-    auto row_of = [&](const Part& p, int x) { return (x % p.row_tiles) * 128; };
-
+    RowTile tile;
+    bool more = true;
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
         if (warp == 0 && lane == 0) {
@@ -577,8 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
             tma_prefetch_desc(&a.v);
             uint32_t parts = 0, vs = 0, qs = 0, dos = 0;
             bool ok = true;
-            for (int64_t u = lo; ok && u < hi;) {
-                const Part p = part_at(a, u, hi);
+            for (; ok && more; more = next_part(a, share, p)) {
                 const int g = a.s.shared_states ? 0 : p.group;
                 if (parts > 0) ok = mbar_wait(k_empty, (parts - 1) & 1, a.status);
                 if (!ok) break;
@@ -587,15 +672,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 for (int c = 0; c < kChunks; ++c)
                     tma_load_4d(smem + L::kK + c * kChunkBytesSw128, &a.k, c * 64, p.tile * kKeyTile, p.kv, g, k_full);
                 ++parts;
-                for (int x = p.first; x < p.last; ++x) {
+                tile.begin(a, p);
+                for (int x = p.first; x < p.last; ++x, tile.next(p)) {
                     const uint32_t sq = qs % kQStages, sd = dos % kDOStages;
-                    const int row = p.group * a.s.group_rows + row_of(p, x), head = head_of(p, x);
+                    const int row = p.group * a.s.group_rows + tile.row0;
                     if (qs >= kQStages) ok = mbar_wait(q_empty + sq, (qs / kQStages - 1) & 1, a.status);
                     if (!ok) break;
                     mbar_arrive_expect_tx(q_full + sq, L::kTile);
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c)
-                        tma_load_3d(smem + L::kQ + sq * L::kTile + c * kChunkBytesSw128, &a.q, c * 64, row, head, q_full + sq);
+                        tma_load_3d(smem + L::kQ + sq * L::kTile + c * kChunkBytesSw128, &a.q, c * 64, row, tile.head, q_full + sq);
                     ++qs;
                     if (x == p.first) {
                         if (parts > 1) ok = mbar_wait(v_empty, (parts - 2) & 1, a.status);
@@ -611,10 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                     mbar_arrive_expect_tx(do_full + sd, L::kTile);
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c)
-                        tma_load_3d(smem + L::kDO + sd * L::kTile + c * kChunkBytesSw128, &a.dO, c * 64, row, head, do_full + sd);
+                        tma_load_3d(smem + L::kDO + sd * L::kTile + c * kChunkBytesSw128, &a.dO, c * 64, row, tile.head, do_full + sd);
                     ++dos;
                 }
-                u = p.end;
             }
             // no copy may still be landing in shared memory at exit
             if (parts > 0) mbar_wait(k_full, (parts - 1) & 1, a.status);
@@ -637,10 +722,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
             auto commit = [&](uint64_t* bar) {
                 if (leader) tc_commit(bar);
             };
-            auto rows_in = [&](const Part& p, int x) {
-                const int left = a.s.rows_of(p.group) - row_of(p, x);
-                return left < 128 ? left : 128;
-            };
             auto product = [&](uint32_t col, uint64_t da, uint64_t db, int w) {
                 const uint32_t idesc = idesc_bf16_f32(128, 0, 0) | (static_cast<uint32_t>(w >> 3) << 17);
                 if (leader) {
@@ -656,16 +737,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                     for (int kk = 0; kk < w / 16; ++kk)
                         umma_ts(tmem + col, tmem + from + packed_col(kk), db + static_cast<uint64_t>(kk * 128), idesc_sum, add || kk > 0);
             };
-            // a cursor over the run's units
-            Part p = part_at(a, lo, hi);
-            int x = p.first;
+            // the row tile at the cursor, number f of the share
             uint32_t part = 0;
-            // S, dP and dV of unit f at the cursor
+            int x = p.first;
+            tile.begin(a, p);
+            auto rows_now = [&]() { return p.rows - tile.row0 < 128 ? p.rows - tile.row0 : 128; };
             auto issue_s = [&](uint32_t f) {
                 const uint32_t st = f % kQStages;
                 if (x == p.first && !wait(k_full, part & 1)) return false;
                 if (!wait(q_full + st, (f / kQStages) & 1)) return false;
-                const int n = rows_in(p, x);
+                const int n = rows_now();
                 if (n & 15) clear_rows<D>(smem + L::kQ + st * L::kTile, kChunkBytesSw128, n);
                 tc_fence_after();
                 product(kColS, d_k, d_q + st * kTileStep, (n + 15) & ~15);
@@ -677,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 const uint32_t st = f % kDOStages;
                 if (x == p.first && !wait(v_full, part & 1)) return false;
                 if (!wait(do_full + st, (f / kDOStages) & 1)) return false;
-                const int n = rows_in(p, x);
+                const int n = rows_now();
                 if (n & 15) clear_rows<D>(smem + L::kDO + st * L::kTile, kChunkBytesSw128, n);
                 tc_fence_after();
                 product(kColP, d_v, d_do + st * kTileStep, (n + 15) & ~15);
@@ -689,23 +770,24 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 const uint32_t st = f % kDOStages;
                 if (!wait(p_full, f & 1)) return false;
                 tc_fence_after();
-                sum_up(kColA, kColS, d_dot + st * kTileStep, (rows_in(p, x) + 15) & ~15, x > p.first);
+                sum_up(kColA, kColS, d_dot + st * kTileStep, (rows_now() + 15) & ~15, x > p.first);
                 commit(do_empty + st);
                 return true;
             };
             bool ok = issue_s(0) && issue_dp(0) && issue_dv(0);
-            const uint32_t units = static_cast<uint32_t>(hi - lo);
-            for (uint32_t f = 0; ok && f < units; ++f) {
-                const int w = (rows_in(p, x) + 15) & ~15;
-                const bool add = x > p.first, last = x == p.last - 1, more = f + 1 < units;
+            for (uint32_t f = 0; ok && more; ++f) {
+                const int w = (rows_now() + 15) & ~15;
+                const bool add = x > p.first, last = x == p.last - 1;
                 if (last) {
+                    more = next_part(a, share, p);
                     if (more) {
-                        p = part_at(a, p.end, hi);
                         x = p.first;
+                        tile.begin(a, p);
                         ++part;
                     }
                 } else {
                     ++x;
+                    tile.next(p);
                 }
                 if (more && !(ok = issue_s(f + 1))) break;
                 if (!(ok = wait(ds_full, f & 1))) break;
@@ -721,17 +803,16 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
             float* aux = reinterpret_cast<float*>(smem + L::kAux);
             uint32_t f = 0;
             bool ok = true;
-            for (int64_t u = lo; ok && u < hi;) {
-                const Part p = part_at(a, u, hi);
-                const int rows = a.s.rows_of(p.group);
-                for (int x = p.first; x < p.last; ++x, ++f) {
+            for (; ok && more; more = next_part(a, share, p)) {
+                tile.begin(a, p);
+                for (int x = p.first; x < p.last; ++x, ++f, tile.next(p)) {
                     const uint32_t st = f % kAuxStages;
-                    const int r = row_of(p, x) + i;
-                    const int64_t at = static_cast<int64_t>(head_of(p, x)) * a.s.rows + static_cast<int64_t>(p.group) * a.s.group_rows + r;
+                    const int r = tile.row0 + i;
+                    const int64_t at = static_cast<int64_t>(tile.head) * a.s.rows + static_cast<int64_t>(p.group) * a.s.group_rows + r;
                     float v[4];
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        const bool live = r + 64 * y < rows;
+                        const bool live = r + 64 * y < p.rows;
                         v[y] = live ? a.lse[at + 64 * y] * 1.4426950408889634f : INFINITY;
                         v[2 + y] = live ? a.delta[at + 64 * y] : 0.0f;
                     }
@@ -743,7 +824,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                     aux[st * 256 + 192 + i] = -v[3];
                     mbar_arrive(aux_full + st);
                 }
-                u = p.end;
             }
         }
     } else {
@@ -755,15 +835,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         const float* aux = reinterpret_cast<const float*>(smem + L::kAux) + half * 64;
         const float c = a.s.scale_log2;
         const uint64_t c2 = f2_pack(c, c);
+        Part& t = p;
         uint32_t f = 0, part = 0;
         bool ok = true;
-        for (int64_t u = lo; ok && u < hi; ++part) {
-            const Part t = part_at(a, u, hi);
+        for (; ok && more; more = next_part(a, share, t), ++part) {
             const int key = t.tile * kKeyTile + r;
             const bool live = key < t.valid;
             for (int x = t.first; x < t.last; ++x, ++f) {
                 const uint32_t st = f % kAuxStages;
-                float p[64];
+                float w[64];
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(aux_full + st, (f / kAuxStages) & 1, a.status)))) break;
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full, f & 1, a.status)))) break;
                 tc_fence_after();
@@ -780,14 +860,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                         float y0, y1, y2, y3;
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, l.x), y0, y1);
                         f2_unpack(f2_fma(f2_pack(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, l.y), y2, y3);
-                        p[4 * y] = ex2_approx(y0);
-                        p[4 * y + 1] = ex2_approx(y1);
-                        p[4 * y + 2] = ex2_approx(y2);
-                        p[4 * y + 3] = ex2_approx(y3);
+                        w[4 * y] = ex2_approx(y0);
+                        w[4 * y + 1] = ex2_approx(y1);
+                        w[4 * y + 2] = ex2_approx(y2);
+                        w[4 * y + 3] = ex2_approx(y3);
                     }
 #pragma unroll
-                    for (int y = 0; y < 64; ++y) p[y] = live ? p[y] : 0.0f;
-                    store_packed(t_s, p);
+                    for (int y = 0; y < 64; ++y) w[y] = live ? w[y] : 0.0f;
+                    store_packed(t_s, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -807,15 +887,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                         float y0, y1, y2, y3;
                         f2_unpack(f2_add(f2_pack(__uint_as_float(v[0]), __uint_as_float(v[1])), d.x), y0, y1);
                         f2_unpack(f2_add(f2_pack(__uint_as_float(v[2]), __uint_as_float(v[3])), d.y), y2, y3);
-                        p[4 * y] *= y0;
-                        p[4 * y + 1] *= y1;
-                        p[4 * y + 2] *= y2;
-                        p[4 * y + 3] *= y3;
+                        w[4 * y] *= y0;
+                        w[4 * y + 1] *= y1;
+                        w[4 * y + 2] *= y2;
+                        w[4 * y + 3] *= y3;
                     }
                     // a masked state's values may be anything
 #pragma unroll
-                    for (int y = 0; y < 64; ++y) p[y] = live ? p[y] : 0.0f;
-                    store_packed(t_p, p);
+                    for (int y = 0; y < 64; ++y) w[y] = live ? w[y] : 0.0f;
+                    store_packed(t_p, w);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -845,7 +925,6 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 }
             }
             tc_fence_before();
-            u = t.end;
         }
     }
 
@@ -859,20 +938,22 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- sums of parts, zeros
-// Block (b, y): the key tile in which run b ends, if it also begins there: the parts
-// of runs b, b + 1, ... in their order.  Key tiles without a valid state: zeros.
+// Block (b, y): the head's rows in which the run of CTA b ends, if they also begin
+// there: its part and those of the same key tile's CTAs in the teams behind, in their
+// order.  Key tiles without a valid state: zeros.
 template <int D>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ GradArgs a) {
     const int64_t total = a.starts[a.s.groups];
-    const int b = blockIdx.x;
-    const int64_t lo = run_begin(a, total, b), hi = run_begin(a, total, b + 1);
-    if (lo < hi) {
-        // the part that ends the run
-        Part p = part_at(a, hi - 1, hi);
-        const int64_t seg = hi - 1 - p.first;  // where its key tile begins
-        if (seg >= lo && seg + p.per > hi) {
-            int ends = b + 1;  // the run that holds the key tile's end
-            while (run_begin(a, total, ends + 1) < seg + p.per) ++ends;
+    const Share share = share_of(a, blockIdx.x);
+    const int teams = teams_of(a, total, share.tiles);
+    // (with more key tiles than CTAs there is one team, and no part of a head's rows)
+    if (share.tile < share.tiles && teams > 1 && share.lo < share.hi) {
+        const Part p = part_at(a, share.hi - 1, share.hi);
+        const int64_t begin = share.hi - 1 - p.first, end = begin + p.per;
+        if (begin >= share.lo && end > share.hi && share.tile * kKeyTile < p.valid) {
+            const int team = blockIdx.x / share.step;
+            int ends = team + 1;  // the team that has the head's last rows
+            while (run_begin(total, teams, ends + 1) < end) ++ends;
             constexpr int kVectors = 2 * 128 * D / 8;
             for (int i = blockIdx.y * 256 + threadIdx.x; i < kVectors; i += gridDim.y * 256) {
                 float v[8], w[8];
@@ -881,14 +962,14 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
                     const float4 x = from[0], y = from[1];
                     to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
                 };
-                fetch(2 * static_cast<int64_t>(b) + 1, v);
-                for (int run = b + 1; run <= ends; ++run) {
-                    fetch(2 * static_cast<int64_t>(run), w);
+                fetch(2 * static_cast<int64_t>(blockIdx.x) + 1, v);
+                for (int k = team + 1; k <= ends; ++k) {
+                    fetch(2 * (static_cast<int64_t>(k) * share.step + share.tile), w);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) v[x] += w[x];
                 }
                 const int which = i / (128 * D / 8), r = i / (D / 8) % 128, c = i % (D / 8) * 8;
-                const int key = p.tile * kKeyTile + r;
+                const int key = share.tile * kKeyTile + r;
                 if (key >= a.s.keys) continue;
                 uint16_t* to = which == 0 ? a.dv + p.group * a.dv_group + key * a.dv_token + p.kv * a.dv_head
                                           : a.dk + p.group * a.dk_group + key * a.dk_token + p.kv * a.dk_head;
@@ -923,7 +1004,7 @@ bss_status launch_backward(GradArgs& a, cudaStream_t stream) {
     bss_status st = resident_blocks(reinterpret_cast<const void*>(dq), kThreads, DqSmem<D>::kBytes, &blocks);
     if (st == BSS_OK) st = resident_blocks(reinterpret_cast<const void*>(dkv), kThreads, DkvSmem<D>::kBytes, &blocks);
     if (st != BSS_OK) return st;
-    const int64_t grid = a.items < num_sms() ? a.items : num_sms();
+    const int grid = a.items < num_sms() ? a.items : num_sms();
     dq<<<static_cast<unsigned>(grid), kThreads, DqSmem<D>::kBytes, stream>>>(a);
     if ((st = cuda_check(cudaGetLastError(), "query gradient launch")) != BSS_OK) return st;
     dkv<<<static_cast<unsigned>(a.blocks), kThreads, DkvSmem<D>::kBytes, stream>>>(a);
@@ -949,7 +1030,7 @@ Plan plan_of(const bss_cross_grads& a) {
     p.blocks = pairs < num_sms() ? static_cast<int32_t>(pairs) : num_sms();
     p.delta_at = 0;
     p.starts_at = aligned_up(a.rows * a.heads * 4);
-    p.parts_at = p.starts_at + aligned_up((groups + 1) * 8);
+    p.parts_at = p.starts_at + aligned_up((groups + 2) * 8);
     p.bytes = p.parts_at + 2ll * p.blocks * 2 * 128 * a.head_dim * 4;
     return p;
 }
@@ -1015,7 +1096,10 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
     a.s = cross_shape(p.rows, p.rows_per_group, p.heads, p.kv_heads, p.head_dim, p.keys, p.softmax_scale, p.lengths,
                       p.k.group_stride);
     a.tiles = plan.tiles, a.key_tiles = plan.key_tiles, a.blocks = plan.blocks;
-    a.items = groups * plan.tiles * p.heads;
+    const int64_t items = groups * plan.tiles * p.heads;
+    if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
+    a.items = static_cast<int32_t>(items);
+    a.by_tiles = FastDiv(static_cast<uint32_t>(plan.tiles));
     a.O = static_cast<const uint16_t*>(p.O.data);
     a.dq = static_cast<uint16_t*>(p.dq.data);
     a.dk = static_cast<uint16_t*>(p.dk.data);
