@@ -11,7 +11,7 @@
 //                 other half's two products to work in.  S_0 of the next item follows
 //                 the last S_0 of this one, so the tensor cores do not wait for the
 //                 end of an item.
-//   warps 4..11   softmax, one thread a row; O / l is written from registers.
+//   warps 4..11   softmax, one thread a row.
 // TMEM: S_h at 128 h (P_h as bf16 over its first 64 columns), O_h at 256 + 128 h.
 // A row's reference is the maximum of its first tile, moved only when the sum of a
 // later tile's P passes 2^16 (then O and l are rescaled).
@@ -49,8 +49,8 @@ struct CrossSmem {
     static constexpr uint32_t kK = 2 * kTile;
     static constexpr uint32_t kV = kK + kStages * kTile;
     static constexpr uint32_t kBar = kV + kStages * kTile;
-    // q_full[2] q_empty[2] k_full k_empty v_full v_empty [kStages] s_full[2] p_full[2] o_done[2]
-    static constexpr uint32_t kBars = 4 + 4 * kStages + 6;
+    // q_full[2] q_empty[2] k_full k_empty v_full v_empty [kStages] s_full[2] p_full[2] o_done[2] cleared
+    static constexpr uint32_t kBars = 4 + 4 * kStages + 7;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 16;
     static constexpr uint32_t kAlloc = kBytes + 1024;
 };
@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
     uint64_t* s_full = v_empty + kStages;
     uint64_t* p_full = s_full + 2;
     uint64_t* o_done = p_full + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(o_done + 2);
+    uint64_t* cleared = o_done + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
             mbar_init(p_full + i, 128);
             mbar_init(o_done + i, 1);
         }
+        mbar_init(cleared, 32);
         for (int i = 0; i < kStages; ++i) {
             mbar_init(k_full + i, 1);
             mbar_init(k_empty + i, 1);
@@ -173,9 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
             const uint64_t dv = desc_mnmajor_sw128(base + L::kV, 0);
             constexpr uint64_t kTileStep = L::kTile >> 4;
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, a.status));
-            };
+            // (no vote: only the leader's MMAs and commits count)
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.status); };
             auto commit = [&](uint64_t* bar) {
                 if (leader) tc_commit(bar);
             };
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                         umma_ts(tmem + kColO + 128 * h, tmem + kColS + 128 * h + kk * 8,
                                 dv + st * kTileStep + static_cast<uint64_t>(kk * 128), idesc_pv, add || kk > 0);
             };
-            uint32_t fills = 0;                           // K and V tiles taken
+            uint32_t fills = 0, clears = 0;               // K and V tiles taken
             uint32_t q_taken[2] = {0, 0}, p_taken[2] = {0, 0};
             int i = blockIdx.x;
             Item t;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                     commit(k_empty + st);  // both halves' S
                     if (!(ok = wait(v_full + st, parity))) break;
                     const int left = cur.valid - j * kKeyTile;
-                    if (left < w) clear_rows<D>(smem + L::kV + st * L::kTile, kChunkBytesSw128, left);
+                    if (left < w && !(ok = clear_rows<D>(smem + L::kV + st * L::kTile, left, cleared, clears, a.status))) break;
                     if (!(ok = wait(p_full + 0, p_taken[0]++ & 1))) break;
                     tc_fence_after();
                     issue_pv(0, st, w, j > 0);
@@ -387,27 +388,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_done + h, (steps - 1) & 1, a.status)))) break;
                 tc_fence_after();
             }
-            uint16_t* out = a.O + row * a.O_row + t.head * a.O_head;
-#pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t o[32];
-                if (t.n > 0) {
-                    BSS_TMEM_LD32(t_o + cc * 32, o);
-                    tmem_wait_ld();
-                } else {
+            const int row_w = t.row0 + h * kHalfRows + (warp & 3) * 32;  // the warp's first row in the group
+            uint16_t* out = a.O + (static_cast<int64_t>(t.group) * a.s.group_rows + row_w) * a.O_row + t.head * a.O_head;
+            if (t.n > 0) {
+                store_rows<D>(t_o, out, a.O_row, t.row0 + t.rows - row_w, inv);
+            } else if (live) {
+                uint4* to = reinterpret_cast<uint4*>(out + lane * a.O_row);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) o[x] = 0u;
-                }
-                if (live) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            w[x] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * x]) * inv, __uint_as_float(o[8 * u + 2 * x + 1]) * inv);
-                        reinterpret_cast<uint4*>(out + cc * 32)[u] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
+                for (int u = 0; u < D / 8; ++u) to[u] = make_uint4(0, 0, 0, 0);
             }
             if (a.lse != nullptr && live)
                 a.lse[static_cast<int64_t>(t.head) * a.s.rows + row] =
@@ -417,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
     }
 
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     if (warp == 1) {
         __syncwarp();

@@ -35,18 +35,76 @@ struct CrossShape {
     }
 };
 
-// Rows of a key tile that hold no valid state up to the next multiple of 16 (as far
-// as an MMA reads): zeroed, because a zero weight times what they hold may be NaN.
-// By one warp; ordered before the MMAs that it issues afterwards.
+// Rows of a tile that hold nothing valid, up to the next multiple of 16 (as far as an
+// MMA reads): zeroed, because a zero weight times what they hold may be NaN.  By one
+// warp, whose lanes meet at a barrier of their own (32 arrivals; a bounded wait, unlike
+// a warp's, in case one of them gave up elsewhere), before the MMAs it issues then.
 template <int D>
-__device__ __forceinline__ void clear_rows(uint8_t* tile, uint32_t chunk_bytes, int first) {
+__device__ __forceinline__ bool clear_rows(uint8_t* tile, int first, uint64_t* bar, uint32_t& uses, int* status) {
     const int lane = threadIdx.x & 31, end = (first + 15) & ~15;
     for (int i = lane; i < (end - first) * (D / 8); i += 32) {
         const int row = first + i / (D / 8), unit = i % (D / 8);
-        *reinterpret_cast<uint4*>(tile + (unit >> 3) * chunk_bytes + row * 128 + (unit & 7) * 16) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(tile + (unit >> 3) * kChunkBytesSw128 + row * 128 + (unit & 7) * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
-    __syncwarp();
+    mbar_arrive(bar);
+    return mbar_wait(bar, uses++ & 1, status);
+}
+
+// Groups of N lanes hold a row each, N 16-byte units of it a lane; afterwards lane i of
+// a group has unit i of its N rows.
+template <int N>
+__device__ __forceinline__ void transpose_units(uint4 (&u)[N]) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        const bool upper = (threadIdx.x & o) != 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (i & o) continue;
+            const uint4 send = upper ? u[i] : u[i | o];
+            uint4 got;
+            got.x = __shfl_xor_sync(0xFFFFFFFFu, send.x, o);
+            got.y = __shfl_xor_sync(0xFFFFFFFFu, send.y, o);
+            got.z = __shfl_xor_sync(0xFFFFFFFFu, send.z, o);
+            got.w = __shfl_xor_sync(0xFFFFFFFFu, send.w, o);
+            if (upper) u[i] = got;
+            else u[i | o] = got;
+        }
+    }
+}
+
+// COLS accumulator columns of the warp's 32 rows (a lane of TMEM each) times a factor
+// a row -> bf16 memory; `to`: the first row's first column, `rows` of them exist.  A
+// lane alone would write 16 bytes of 32 rows at a time (a cycle of the memory pipe
+// each); transposed, N lanes write N 16-byte units of one row together.
+template <int COLS>
+__device__ __forceinline__ void store_rows(uint32_t at, uint16_t* to, int64_t row_stride, int rows, float factor) {
+    constexpr int N = COLS < 64 ? COLS / 8 : 8;
+    const int lane = threadIdx.x & 31, unit = lane % N, first = lane - unit;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 8 * N) {
+        uint4 u[N];
+#pragma unroll
+        for (int b = 0; b < N / 4; ++b) {
+            uint32_t o[32];
+            BSS_TMEM_LD32(at + c + 32 * b, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    w[x] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * x]) * factor, __uint_as_float(o[8 * i + 2 * x + 1]) * factor);
+                u[4 * b + i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        transpose_units<N>(u);
+        uint16_t* p = to + c + unit * 8 + first * row_stride;
+#pragma unroll
+        for (int k = 0; k < N; ++k, p += row_stride)
+            if (first + k < rows) *reinterpret_cast<uint4*>(p) = u[k];
+        __syncwarp();
+    }
 }
 
 // ---------------------------------------------------------------- host side

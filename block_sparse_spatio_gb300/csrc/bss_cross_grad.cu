@@ -30,8 +30,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kElementwise = 256;  // threads 128 .. 383: a lane of TMEM and half of the columns
-// Registers: 128 x 104 + 256 x 192 = 62,464 of the launch's 384 x 168 = 64,512.
-constexpr uint32_t kRegsControl = 104, kRegsElementwise = 192;
+// Registers: 128 x 120 + 256 x 184 = 62,464 of the launch's 384 x 168 = 64,512.
+constexpr uint32_t kRegsControl = 120, kRegsElementwise = 184;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColA = 256, kColB = 384;  // S, dP, two sums (or a second dP and one)
 
@@ -43,9 +43,9 @@ struct GradArgs {
     int32_t items;      // of the first kernel
     int32_t blocks;     // of the second
     FastDiv by_tiles;
-    const uint16_t* O;
+    const uint16_t *O, *dO_rows;
     uint16_t *dq, *dk, *dv;
-    int64_t O_row, O_head, dq_row, dq_head;
+    int64_t O_row, O_head, dO_row, dO_head, dq_row, dq_head;
     int64_t dk_group, dk_token, dk_head, dv_group, dv_token, dv_head;
     float scale;
     const float* lse;  // [heads][rows]
@@ -69,27 +69,6 @@ __device__ __forceinline__ void store_packed(uint32_t at, const float (&v)[64]) 
     }
 }
 
-// A row's (or key's) accumulator columns [first, first + 32 NC) -> bf16 memory
-template <int NC>
-__device__ __forceinline__ void store_row(uint32_t at, uint16_t* to, float scale, bool live) {
-#pragma unroll
-    for (int cc = 0; cc < NC; ++cc) {
-        uint32_t o[32];
-        BSS_TMEM_LD32(at + cc * 32, o);
-        tmem_wait_ld();
-        if (live) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    w[x] = pack_bf16x2(__uint_as_float(o[8 * u + 2 * x]) * scale, __uint_as_float(o[8 * u + 2 * x + 1]) * scale);
-                reinterpret_cast<uint4*>(to + cc * 32)[u] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-    }
-}
-
 // ---------------------------------------------------------------- dq
 constexpr int kKStages = 3, kVStages = 2;
 
@@ -97,10 +76,11 @@ template <int D>
 struct DqSmem {
     static constexpr uint32_t kTile = 128 * D * 2;
     static constexpr uint32_t kQ = 0, kDO = kTile, kK = 2 * kTile, kV = kK + kKStages * kTile;
-    static constexpr uint32_t kDelta = kV + kVStages * kTile;  // float [2][2][128]
-    static constexpr uint32_t kBar = kDelta + 2048;
-    // q_full q_empty do_full do_empty k_full k_empty v_full v_empty s_full s_read dp_full[2] ds_full[2] dq_done halves
-    static constexpr uint32_t kBars = 4 + 2 * kKStages + 2 * kVStages + 8;
+    static constexpr uint32_t kAux = kV + kVStages * kTile;  // D, lse in base 2: float [item & 1][2][128]
+    static constexpr uint32_t kBar = kAux + 2048;
+    // q_full q_empty do_full do_empty k_full k_empty v_full v_empty s_full s_read dp_full[2] ds_full[2] dq_done
+    // aux_full[2] aux_empty[2] cleared
+    static constexpr uint32_t kBars = 4 + 2 * kKStages + 2 * kVStages + 12;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 16;
 };
 
@@ -167,8 +147,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     uint64_t* dp_full = s_read + 1;
     uint64_t* ds_full = dp_full + 2;
     uint64_t* dq_done = ds_full + 2;
-    uint64_t* halves = dq_done + 1;  // both halves of a row's D are there
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(halves + 1);
+    uint64_t* aux_full = dq_done + 1;
+    uint64_t* aux_empty = aux_full + 2;
+    uint64_t* cleared = aux_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (smem_u32(smem) & 1023u) {  // the swizzled tiles could not be addressed
         record_status(a.status, BSS_ERR_CUDA);
@@ -179,9 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(do_full, 1);
-        mbar_init(do_empty, 1 + kElementwise / 32);
+        mbar_init(do_empty, 1);
         for (int i = 0; i < kKStages; ++i) mbar_init(k_full + i, 1), mbar_init(k_empty + i, 1);
         for (int i = 0; i < kVStages; ++i) mbar_init(v_full + i, 1), mbar_init(v_empty + i, 1);
+        mbar_init(cleared, 32);
         mbar_init(s_full, 1);
         mbar_init(s_read, kElementwise);
         mbar_init(dp_full, 1);
@@ -189,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         mbar_init(ds_full, kElementwise);
         mbar_init(ds_full + 1, kElementwise);
         mbar_init(dq_done, 1);
-        mbar_init(halves, kElementwise);
+        for (int i = 0; i < 2; ++i) mbar_init(aux_full + i, 64), mbar_init(aux_empty + i, kElementwise);
         mbar_fence_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -261,9 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
             const uint64_t d_kt = desc_mnmajor_sw128(base + L::kK, 0);
             constexpr uint64_t kTileStep = L::kTile >> 4;
             constexpr uint32_t idesc_dq = idesc_bf16_f32(128, D, 1);
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, a.status));
-            };
+            // (no vote: only the leader's MMAs and commits count)
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.status); };
             auto commit = [&](uint64_t* bar) {
                 if (leader) tc_commit(bar);
             };
@@ -292,13 +274,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                 const int left = it.valid - j * kKeyTile;
                 return left >= kKeyTile ? kKeyTile : (left + 15) & ~15;
             };
+            uint32_t clears = 0;
             // S of tile j of an item, which is step f
             auto issue_s = [&](const DqItem& it, int j, uint32_t f, uint32_t item) {
                 const uint32_t st = f % kKStages;
                 if (j == 0 && !wait(q_full, item & 1)) return false;
                 if (!wait(k_full + st, (f / kKStages) & 1)) return false;
                 const int w = width(it, j), left = it.valid - j * kKeyTile;
-                if (left < w) clear_rows<D>(smem + L::kK + st * L::kTile, kChunkBytesSw128, left);
+                if (left < w && !clear_rows<D>(smem + L::kK + st * L::kTile, left, cleared, clears, a.status)) return false;
                 if (f > 0 && !wait(s_read, (f - 1) & 1)) return false;
                 tc_fence_after();
                 product(kColS, d_q, d_k + st * kTileStep, w);
@@ -348,8 +331,53 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                 cur = nxt;
                 ++item;
             }
-        } else if (warp == 2 && blockIdx.x == 0) {
-            count_rows(a);
+        } else if (warp >= 2) {
+            // D = sum dO O of an item's rows, and their lse, an item ahead: D / 8 lanes a row
+            if (warp == 2 && blockIdx.x == 0) count_rows(a);
+            constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
+            float* aux = reinterpret_cast<float*>(smem + L::kAux);
+            const int w = warp - 2, sub = lane / kLanes, unit = lane % kLanes;
+            uint32_t items = 0;
+            for (int i = blockIdx.x; i < a.items; i += gridDim.x) {
+                const DqItem t = dq_item(a, i);
+                if (t.n == 0) continue;
+                const uint32_t buf = items & 1;
+                if (items >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(aux_empty + buf, (items / 2 - 1) & 1, a.status))) break;
+                ++items;
+                float* x = aux + buf * 256;
+                const int64_t row0 = static_cast<int64_t>(t.group) * a.s.group_rows + t.row0;
+                const int64_t at = static_cast<int64_t>(t.head) * a.s.rows + row0;
+                const int mine = w * 64 + lane;  // and the row 32 behind it
+                const float l0 = mine < t.rows ? a.lse[at + mine] : INFINITY;
+                const float l1 = mine + 32 < t.rows ? a.lse[at + mine + 32] : INFINITY;
+                const uint16_t* g0 = a.dO_rows + row0 * a.dO_row + t.head * a.dO_head + unit * 8;
+                const uint16_t* o0 = a.O + row0 * a.O_row + t.head * a.O_head + unit * 8;
+#pragma unroll 1
+                for (int r0 = w * 64; r0 < w * 64 + 64; r0 += kBatch * kRows) {
+                    uint4 g[kBatch], o[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int r = r0 + k * kRows + sub;
+                        g[k] = o[k] = make_uint4(0, 0, 0, 0);
+                        if (r < t.rows) {
+                            g[k] = *reinterpret_cast<const uint4*>(g0 + r * a.dO_row);
+                            o[k] = ld_row(o0 + r * a.O_row);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        const int r = r0 + k * kRows + sub;
+                        const float sum = lane_sum<kLanes>(dot(unpack_bf16<false>(g[k]), unpack_bf16<false>(o[k])));
+                        if (unit == 0) {
+                            x[r] = sum;
+                            if (r < t.rows) a.delta[at + r] = sum;
+                        }
+                    }
+                }
+                x[128 + mine] = l0 * 1.4426950408889634f;
+                x[128 + mine + 32] = l1 * 1.4426950408889634f;
+                mbar_arrive(aux_full + buf);
+            }
         }
     } else {
         setmaxnreg_inc<kRegsElementwise>();
@@ -357,17 +385,18 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         const int r = threadIdx.x - 128 - half * 128;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + kColS + 64 * half, t_p = tmem + lanes + kColP + 64 * half;
-        float* exchange = reinterpret_cast<float*>(smem + L::kDelta);
+        const float* aux = reinterpret_cast<const float*>(smem + L::kAux);
         const float c = a.s.scale_log2;
         uint32_t step = 0, items = 0;
         bool ok = true, pending = false;  // pending: the item before's dq is still to be stored
         uint16_t* out = nullptr;
-        bool out_live = false;
+        int out_rows = 0;
         constexpr int kCols = D / 2;  // dq columns of a thread
+        const int row_w = (warp & 3) * 32;  // the warp's first row
         auto store_pending = [&]() {
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(dq_done, (items - 1) & 1, a.status))) return false;
             tc_fence_after();
-            store_row<kCols / 32>(tmem + lanes + kColB + half * kCols, out, a.scale, out_live);
+            store_rows<kCols>(tmem + lanes + kColB + half * kCols, out, a.dq_row, out_rows, a.scale);
             tc_fence_before();
             pending = false;
             return true;
@@ -389,31 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
             }
             return false;
         };
-        auto row_of = [&](const DqItem& t) { return static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + r; };
-        // an item's O (half of the channels) and lse, fetched during the item before
-        uint4 o[kCols / 8];
-        float lse_next = 0.0f;
-        auto fetch = [&](const DqItem& t) {
-            if (r < t.rows) {
-                const uint4* from = reinterpret_cast<const uint4*>(a.O + row_of(t) * a.O_row + t.head * a.O_head + half * kCols);
-#pragma unroll
-                for (int u = 0; u < kCols / 8; ++u) o[u] = ld_row(from + u);
-                lse_next = a.lse[static_cast<int64_t>(t.head) * a.s.rows + row_of(t)];
-            } else {
-#pragma unroll
-                for (int u = 0; u < kCols / 8; ++u) o[u] = make_uint4(0, 0, 0, 0);
-                lse_next = INFINITY;
-            }
-        };
         DqItem t, nxt;
         bool more = next_item(t);
-        if (more) fetch(t);
         while (ok && more) {
             more = next_item(nxt);
-            const bool live = r < t.rows;
-            const int64_t row = row_of(t);
-            const float lse2 = lse_next * 1.4426950408889634f;
-            float delta = 0.0f;
+            const float* x = aux + (items & 1) * 256 + r;
+            if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(aux_full + (items & 1), (items >> 1) & 1, a.status)))) break;
+            const float delta = x[0], lse2 = x[128];
+            mbar_arrive(aux_empty + (items & 1));
             for (int j = 0; j < t.n; ++j, ++step) {
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full, step & 1, a.status)))) break;
                 tc_fence_after();
@@ -435,28 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                         p[2 * x + 1] = ex2_approx(y1);
                     }
                 }
-                if (j == 0) {
-                    // D = sum dO O of the row: this half of the channels, then both
-                    if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(do_full, items & 1, a.status)))) break;
-                    float sum = 0.0f;
-                    const uint8_t* from = smem + L::kDO + (D == 128 ? half * kChunkBytesSw128 : 0) + r * 128;
-#pragma unroll
-                    for (int u = 0; u < kCols / 8; ++u) {
-                        const int unit = (D == 128 ? 0 : half * 4) + u;
-                        const uint4 g = *reinterpret_cast<const uint4*>(from + ((unit ^ (r & 7)) << 4));
-                        sum += dot(unpack_bf16<false>(g), unpack_bf16<false>(o[u]));
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(do_empty);
-                    float* x = exchange + (items & 1) * 256;
-                    x[half * 128 + r] = sum;
-                    mbar_arrive(halves);
-                    if (pending && !(ok = store_pending())) break;
-                    if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(halves, items & 1, a.status)))) break;
-                    delta = x[r] + x[128 + r];
-                    if (half == 0 && live) a.delta[static_cast<int64_t>(t.head) * a.s.rows + row] = delta;
-                }
-                if (j == t.n - 1 && more) fetch(nxt);
+                if (j == 0 && pending && !(ok = store_pending())) break;
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(dp_full + (step & 1), (step >> 1) & 1, a.status)))) break;
                 tc_fence_after();
                 {
@@ -482,14 +473,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
             if (!ok) break;
             ++items;
             pending = true;
-            out = a.dq + row * a.dq_row + t.head * a.dq_head + half * kCols;
-            out_live = live;
+            out = a.dq + (static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + row_w) * a.dq_row + t.head * a.dq_head + half * kCols;
+            out_rows = t.rows - row_w;
             t = nxt;
         }
         if (ok && pending) store_pending();
     }
 
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     if (warp == 1) {
         __syncwarp();
@@ -508,7 +500,8 @@ struct DkvSmem {
     static constexpr uint32_t kAux = kDO + kDOStages * kTile;  // lse in base 2, delta: float [stage][2][128]
     static constexpr uint32_t kBar = kAux + kAuxStages * 1024;
     // k_full k_empty v_full v_empty q_full q_empty do_full do_empty aux_full aux_empty s_full p_full dp_full ds_full sums
-    static constexpr uint32_t kBars = 4 + 2 * kQStages + 2 * kDOStages + 2 * kAuxStages + 5;
+    // cleared
+    static constexpr uint32_t kBars = 4 + 2 * kQStages + 2 * kDOStages + 2 * kAuxStages + 6;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 16;
 };
 
@@ -621,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     uint64_t* dp_full = p_full + 1;
     uint64_t* ds_full = dp_full + 1;
     uint64_t* sums = ds_full + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sums + 1);
+    uint64_t* cleared = sums + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     Share share = share_of(a, blockIdx.x);
     Part p;
@@ -644,6 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         mbar_init(dp_full, 1);
         mbar_init(ds_full, kElementwise);
         mbar_init(sums, 1);
+        mbar_init(cleared, 32);
         mbar_fence_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -711,34 +706,41 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
         } else if (warp == 1) {
             const bool leader = elect_one();
             const uint32_t base = smem_u32(smem);
-            const uint64_t d_k = desc_kmajor_sw128(base + L::kK, 0), d_v = desc_kmajor_sw128(base + L::kV, 0);
-            const uint64_t d_q = desc_kmajor_sw128(base + L::kQ, 0), d_do = desc_kmajor_sw128(base + L::kDO, 0);
-            const uint64_t d_qt = desc_mnmajor_sw128(base + L::kQ, 0), d_dot = desc_mnmajor_sw128(base + L::kDO, 0);
-            constexpr uint64_t kTileStep = L::kTile >> 4;
+            const uint32_t d_k = desc_lo_kmajor(base + L::kK), d_v = desc_lo_kmajor(base + L::kV);
+            const uint32_t d_q = desc_lo_kmajor(base + L::kQ), d_do = desc_lo_kmajor(base + L::kDO);
+            const uint32_t d_qt = desc_lo_mnmajor(base + L::kQ), d_dot = desc_lo_mnmajor(base + L::kDO);
+            constexpr uint32_t kTileStep = L::kTile >> 4;
             constexpr uint32_t idesc_sum = idesc_bf16_f32(128, D, 1);
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, a.status));
-            };
+            // (no vote: only the leader's MMAs and commits count)
+            auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.status); };
             auto commit = [&](uint64_t* bar) {
                 if (leader) tc_commit(bar);
             };
-            auto product = [&](uint32_t col, uint64_t da, uint64_t db, int w) {
+            // (a whole tile's products apart: nothing of theirs is computed at run time)
+            auto product = [&](uint32_t col, uint32_t da, uint32_t db, int w) {
                 const uint32_t idesc = idesc_bf16_f32(128, 0, 0) | (static_cast<uint32_t>(w >> 3) << 17);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t at = static_cast<uint64_t>((kk >> 2) * (kChunkBytesSw128 >> 4) + (kk & 3) * 2);
-                        umma_ss(tmem + col, da + at, db + at, idesc, kk > 0);
+                        const uint32_t at = (kk >> 2) * (kChunkBytesSw128 >> 4) + (kk & 3) * 2;
+                        umma_ss(tmem + col, desc_of(da + at), desc_of(db + at), idesc, kk > 0);
                     }
                 }
             };
-            auto sum_up = [&](uint32_t col, uint32_t from, uint64_t db, int w, bool add) {
-                if (leader)
+            auto sum_up = [&](uint32_t col, uint32_t from, uint32_t db, int w, bool add) {
+                if (w == 128) {
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_ts(tmem + col, tmem + from + packed_col(kk), desc_of(db + kk * 128), idesc_sum, add || kk > 0);
+                    }
+                } else if (leader) {
                     for (int kk = 0; kk < w / 16; ++kk)
-                        umma_ts(tmem + col, tmem + from + packed_col(kk), db + static_cast<uint64_t>(kk * 128), idesc_sum, add || kk > 0);
+                        umma_ts(tmem + col, tmem + from + packed_col(kk), desc_of(db + kk * 128), idesc_sum, add || kk > 0);
+                }
             };
             // the row tile at the cursor, number f of the share
-            uint32_t part = 0;
+            uint32_t part = 0, clears = 0;
             int x = p.first;
             tile.begin(a, p);
             auto rows_now = [&]() { return p.rows - tile.row0 < 128 ? p.rows - tile.row0 : 128; };
@@ -747,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 if (x == p.first && !wait(k_full, part & 1)) return false;
                 if (!wait(q_full + st, (f / kQStages) & 1)) return false;
                 const int n = rows_now();
-                if (n & 15) clear_rows<D>(smem + L::kQ + st * L::kTile, kChunkBytesSw128, n);
+                if ((n & 15) && !clear_rows<D>(smem + L::kQ + st * L::kTile, n, cleared, clears, a.status)) return false;
                 tc_fence_after();
                 product(kColS, d_k, d_q + st * kTileStep, (n + 15) & ~15);
                 commit(s_full);
@@ -759,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 if (x == p.first && !wait(v_full, part & 1)) return false;
                 if (!wait(do_full + st, (f / kDOStages) & 1)) return false;
                 const int n = rows_now();
-                if (n & 15) clear_rows<D>(smem + L::kDO + st * L::kTile, kChunkBytesSw128, n);
+                if ((n & 15) && !clear_rows<D>(smem + L::kDO + st * L::kTile, n, cleared, clears, a.status)) return false;
                 tc_fence_after();
                 product(kColP, d_v, d_do + st * kTileStep, (n + 15) & ~15);
                 commit(dp_full);
@@ -908,12 +910,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
             tc_fence_after();
             const uint32_t acc = tmem + lanes + (half == 0 ? kColA : kColB);
             if (t.first == 0 && t.last == t.per) {
-                uint16_t* to = half == 0 ? a.dv + t.group * a.dv_group + key * a.dv_token + t.kv * a.dv_head
-                                         : a.dk + t.group * a.dk_group + key * a.dk_token + t.kv * a.dk_head;
-                store_row<D / 32>(acc, to, half == 0 ? 1.0f : a.scale, key < a.s.keys);
+                const int key0 = t.tile * kKeyTile + (warp & 3) * 32;
+                uint16_t* to = half == 0 ? a.dv + t.group * a.dv_group + key0 * a.dv_token + t.kv * a.dv_head
+                                         : a.dk + t.group * a.dk_group + key0 * a.dk_token + t.kv * a.dk_head;
+                store_rows<D>(acc, to, half == 0 ? a.dv_token : a.dk_token, a.s.keys - key0, half == 0 ? 1.0f : a.scale);
             } else {
+                // [16 bytes of the channels][key]: the join reads them so
                 const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (t.first > 0 ? 0 : 1);
-                float* to = a.parts + ((slot * 2 + half) * 128 + r) * D;
+                uint4* to = reinterpret_cast<uint4*>(a.parts + (slot * 2 + half) * 128 * D) + r;
 #pragma unroll
                 for (int cc = 0; cc < D / 32; ++cc) {
                     uint32_t o[32];
@@ -921,7 +925,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                     tmem_wait_ld();
 #pragma unroll
                     for (int y = 0; y < 8; ++y)
-                        reinterpret_cast<uint4*>(to + cc * 32)[y] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                        to[(cc * 8 + y) * 128] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
                 }
             }
             tc_fence_before();
@@ -929,6 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     }
 
     tc_fence_before();
+    __syncwarp();
     __syncthreads();
     if (warp == 1) {
         __syncwarp();
@@ -954,12 +959,14 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
             const int team = blockIdx.x / share.step;
             int ends = team + 1;  // the team that has the head's last rows
             while (run_begin(total, teams, ends + 1) < end) ++ends;
+            // a thread sums 8 channels of a key: neighbours in a warp are neighbouring keys
             constexpr int kVectors = 2 * 128 * D / 8;
             for (int i = blockIdx.y * 256 + threadIdx.x; i < kVectors; i += gridDim.y * 256) {
+                const int which = i / (128 * D / 8), r = i % 128, c = i / 128 % (D / 8);
                 float v[8], w[8];
                 auto fetch = [&](int64_t slot, float (&to)[8]) {
-                    const float4* from = reinterpret_cast<const float4*>(a.parts + slot * 2 * 128 * D) + 2 * i;
-                    const float4 x = from[0], y = from[1];
+                    const float4* from = reinterpret_cast<const float4*>(a.parts + (slot * 2 + which) * 128 * D) + 2 * c * 128 + r;
+                    const float4 x = from[0], y = from[128];
                     to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
                 };
                 fetch(2 * static_cast<int64_t>(blockIdx.x) + 1, v);
@@ -968,14 +975,13 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 #pragma unroll
                     for (int x = 0; x < 8; ++x) v[x] += w[x];
                 }
-                const int which = i / (128 * D / 8), r = i / (D / 8) % 128, c = i % (D / 8) * 8;
                 const int key = share.tile * kKeyTile + r;
                 if (key >= a.s.keys) continue;
                 uint16_t* to = which == 0 ? a.dv + p.group * a.dv_group + key * a.dv_token + p.kv * a.dv_head
                                           : a.dk + p.group * a.dk_group + key * a.dk_token + p.kv * a.dk_head;
                 const float scale = which == 0 ? 1.0f : a.scale;
-                *reinterpret_cast<uint4*>(to + c) = make_uint4(pack2(v[0] * scale, v[1] * scale), pack2(v[2] * scale, v[3] * scale),
-                                                               pack2(v[4] * scale, v[5] * scale), pack2(v[6] * scale, v[7] * scale));
+                *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(pack2(v[0] * scale, v[1] * scale), pack2(v[2] * scale, v[3] * scale),
+                                                                   pack2(v[4] * scale, v[5] * scale), pack2(v[6] * scale, v[7] * scale));
             }
         }
     }
@@ -1101,11 +1107,13 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
     a.items = static_cast<int32_t>(items);
     a.by_tiles = FastDiv(static_cast<uint32_t>(plan.tiles));
     a.O = static_cast<const uint16_t*>(p.O.data);
+    a.dO_rows = static_cast<const uint16_t*>(p.dO.data);
     a.dq = static_cast<uint16_t*>(p.dq.data);
     a.dk = static_cast<uint16_t*>(p.dk.data);
     a.dv = static_cast<uint16_t*>(p.dv.data);
     auto stride = [](int64_t extent, int64_t s) { return extent > 1 ? s : 0; };
     a.O_row = stride(p.rows, p.O.token_stride), a.O_head = stride(p.heads, p.O.head_stride);
+    a.dO_row = stride(p.rows, p.dO.token_stride), a.dO_head = stride(p.heads, p.dO.head_stride);
     a.dq_row = stride(p.rows, p.dq.token_stride), a.dq_head = stride(p.heads, p.dq.head_stride);
     a.dk_group = stride(groups, p.dk.group_stride), a.dk_token = stride(p.keys, p.dk.token_stride);
     a.dk_head = stride(p.kv_heads, p.dk.head_stride);

@@ -357,6 +357,19 @@ __device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t tile_base, int k
     return smem_desc_sw128(tile_base + static_cast<uint32_t>(kk) * 2048u, chunk_bytes, 1024);
 }
 
+// The two descriptors above as 32-bit words: the upper one is the same for both, the
+// lower one takes the offsets of K steps and stages (in 16-byte units).
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo_kmajor(uint32_t tile_base) { return ((tile_base >> 4) & 0x3FFFu) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_lo_mnmajor(uint32_t tile_base, uint32_t chunk_bytes = kChunkBytesSw128) {
+    return ((tile_base >> 4) & 0x3FFFu) | ((chunk_bytes >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "n"(kDescHi));
+    return d;
+}
+
 // Instruction descriptor for kind::f16 with bf16 inputs and fp32 accumulate.
 //   bits 4-5 D format (1 = f32), 7-9 A format (1 = bf16), 10-12 B format
 //   (1 = bf16), bit 15 A major (0 = K-major), bit 16 B major (1 = MN-major),
