@@ -74,36 +74,54 @@ __device__ __forceinline__ void transpose_units(uint4 (&u)[N]) {
 }
 
 // COLS accumulator columns of the warp's 32 rows (a lane of TMEM each) times a factor
-// a row -> bf16 memory; `to`: the first row's first column, `rows` of them exist.  A
-// lane alone would write 16 bytes of 32 rows at a time (a cycle of the memory pipe
-// each); transposed, N lanes write N 16-byte units of one row together.
+// a row, as bf16: 16-byte units of a lane's own row.
 template <int COLS>
-__device__ __forceinline__ void store_rows(uint32_t at, uint16_t* to, int64_t row_stride, int rows, float factor) {
-    constexpr int N = COLS < 64 ? COLS / 8 : 8;
+__device__ __forceinline__ void read_rows(uint4 (&u)[COLS / 8], uint32_t at, float factor) {
+#pragma unroll
+    for (int c = 0; c < COLS / 32; ++c) {
+        uint32_t o[32];
+        BSS_TMEM_LD32(at + 32 * c, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                w[x] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * x]) * factor, __uint_as_float(o[8 * i + 2 * x + 1]) * factor);
+            u[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// They -> memory; `to`: the first row's first column, `rows` of the 32 exist.  A lane
+// alone would write 16 bytes of 32 rows at a time (a cycle of the memory pipe each);
+// transposed, 8 lanes write 128 bytes of one row together.
+template <int UNITS>
+__device__ __forceinline__ void write_rows(const uint4 (&v)[UNITS], uint16_t* to, int64_t row_stride, int rows) {
+    constexpr int N = UNITS < 8 ? UNITS : 8;
     const int lane = threadIdx.x & 31, unit = lane % N, first = lane - unit;
 #pragma unroll
-    for (int c = 0; c < COLS; c += 8 * N) {
+    for (int c = 0; c < UNITS; c += N) {
         uint4 u[N];
 #pragma unroll
-        for (int b = 0; b < N / 4; ++b) {
-            uint32_t o[32];
-            BSS_TMEM_LD32(at + c + 32 * b, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    w[x] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * x]) * factor, __uint_as_float(o[8 * i + 2 * x + 1]) * factor);
-                u[4 * b + i] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
+        for (int i = 0; i < N; ++i) u[i] = v[c + i];
         transpose_units<N>(u);
-        uint16_t* p = to + c + unit * 8 + first * row_stride;
+        uint16_t* p = to + (c + unit) * 8 + first * row_stride;
 #pragma unroll
         for (int k = 0; k < N; ++k, p += row_stride)
             if (first + k < rows) *reinterpret_cast<uint4*>(p) = u[k];
         __syncwarp();
+    }
+}
+
+template <int COLS>
+__device__ __forceinline__ void store_rows(uint32_t at, uint16_t* to, int64_t row_stride, int rows, float factor) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 64) {  // 128 bytes a row at a time
+        constexpr int kCols = COLS < 64 ? COLS : 64;
+        uint4 u[kCols / 8];
+        read_rows<kCols>(u, at + c, factor);
+        write_rows<kCols / 8>(u, to + c, row_stride, rows);
     }
 }
 

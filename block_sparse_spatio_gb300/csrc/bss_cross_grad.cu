@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kElementwise = 256;  // threads 128 .. 383: a lane of TMEM and half of the columns
-// Registers: 128 x 120 + 256 x 184 = 62,464 of the launch's 384 x 168 = 64,512.
+// Registers of the second kernel: 128 x 120 + 256 x 184 = 62,464 of the launch's 384 x 168 = 64,512.
 constexpr uint32_t kRegsControl = 120, kRegsElementwise = 184;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0, kColP = 128, kColA = 256, kColB = 384;  // S, dP, two sums (or a second dP and one)
@@ -43,9 +43,9 @@ struct GradArgs {
     int32_t items;      // of the first kernel
     int32_t blocks;     // of the second
     FastDiv by_tiles;
-    const uint16_t *O, *dO_rows;
+    const uint16_t* O;
     uint16_t *dq, *dk, *dv;
-    int64_t O_row, O_head, dO_row, dO_head, dq_row, dq_head;
+    int64_t O_row, O_head, dq_row, dq_head;
     int64_t dk_group, dk_token, dk_head, dv_group, dv_token, dv_head;
     float scale;
     const float* lse;  // [heads][rows]
@@ -59,6 +59,12 @@ struct GradArgs {
 // half of the columns keeps its bf16 values at the start of its own 64
 __device__ __forceinline__ uint32_t packed_col(int kk) { return static_cast<uint32_t>((kk >> 2) * 64 + (kk & 3) * 8); }
 
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ void store_packed(uint32_t at, const float (&v)[64]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -70,6 +76,19 @@ __device__ __forceinline__ void store_packed(uint32_t at, const float (&v)[64]) 
 }
 
 // ---------------------------------------------------------------- dq
+// d[g][n] += sum over 16 channels of a[g][c] b[n][c] for 8 rows each: lane 4 g + i gets
+// n = 2 i and 2 i + 1.
+__device__ __forceinline__ void add_rows_product(float (&d)[2], uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+    float unused0 = 0.0f, unused1 = 0.0f;
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%5}, {%7,%8}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(unused0), "+f"(unused1)
+                 : "r"(a0), "r"(0u), "r"(a1), "r"(b0), "r"(b1));
+}
+
+// Threads: 4 warps of control (loads, products), 4 that make D, 8 elementwise.
+// Registers: 128 x (88 + 152 + 2 x 136) = the launch's 512 x 128.
+constexpr int kDqThreads = 512, kAuxThreads = 128;
+constexpr uint32_t kDqRegsControl = 88, kDqRegsAux = 152, kDqRegsElementwise = 136;
 constexpr int kKStages = 3, kVStages = 2;
 
 template <int D>
@@ -79,8 +98,8 @@ struct DqSmem {
     static constexpr uint32_t kAux = kV + kVStages * kTile;  // D, lse in base 2: float [item & 1][2][128]
     static constexpr uint32_t kBar = kAux + 2048;
     // q_full q_empty do_full do_empty k_full k_empty v_full v_empty s_full s_read dp_full[2] ds_full[2] dq_done
-    // aux_full[2] aux_empty[2] cleared
-    static constexpr uint32_t kBars = 4 + 2 * kKStages + 2 * kVStages + 12;
+    // dq_read aux_full[2] aux_empty[2] cleared
+    static constexpr uint32_t kBars = 4 + 2 * kKStages + 2 * kVStages + 13;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 16;
 };
 
@@ -130,7 +149,7 @@ __device__ __forceinline__ void count_rows(const GradArgs& a) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(kDqThreads, 1) cross_dq_kernel(const __grid_constant__ GradArgs a) {
     using L = DqSmem<D>;
     constexpr int kChunks = D / 64;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -147,7 +166,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     uint64_t* dp_full = s_read + 1;
     uint64_t* ds_full = dp_full + 2;
     uint64_t* dq_done = ds_full + 2;
-    uint64_t* aux_full = dq_done + 1;
+    uint64_t* dq_read = dq_done + 1;
+    uint64_t* aux_full = dq_read + 1;
     uint64_t* aux_empty = aux_full + 2;
     uint64_t* cleared = aux_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + 1);
@@ -161,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         mbar_init(do_full, 1);
-        mbar_init(do_empty, 1);
+        mbar_init(do_empty, 1 + kAuxThreads / 32);
         for (int i = 0; i < kKStages; ++i) mbar_init(k_full + i, 1), mbar_init(k_empty + i, 1);
         for (int i = 0; i < kVStages; ++i) mbar_init(v_full + i, 1), mbar_init(v_empty + i, 1);
         mbar_init(cleared, 32);
@@ -172,7 +192,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         mbar_init(ds_full, kElementwise);
         mbar_init(ds_full + 1, kElementwise);
         mbar_init(dq_done, 1);
-        for (int i = 0; i < 2; ++i) mbar_init(aux_full + i, 64), mbar_init(aux_empty + i, kElementwise);
+        mbar_init(dq_read, kAuxThreads);
+        for (int i = 0; i < 2; ++i) mbar_init(aux_full + i, kAuxThreads), mbar_init(aux_empty + i, kElementwise);
         mbar_fence_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, kTmemCols);
@@ -182,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
     const uint32_t tmem = *tmem_slot;
 
     if (warp < 4) {
-        setmaxnreg_dec<kRegsControl>();
+        setmaxnreg_dec<kDqRegsControl>();
         if (warp == 0 && lane == 0) {
             tma_prefetch_desc(&a.q);
             tma_prefetch_desc(&a.dO);
@@ -239,23 +260,23 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
         } else if (warp == 1) {
             const bool leader = elect_one();
             const uint32_t base = smem_u32(smem);
-            const uint64_t d_q = desc_kmajor_sw128(base + L::kQ, 0), d_do = desc_kmajor_sw128(base + L::kDO, 0);
-            const uint64_t d_k = desc_kmajor_sw128(base + L::kK, 0), d_v = desc_kmajor_sw128(base + L::kV, 0);
-            const uint64_t d_kt = desc_mnmajor_sw128(base + L::kK, 0);
-            constexpr uint64_t kTileStep = L::kTile >> 4;
+            const uint32_t d_q = desc_lo_kmajor(base + L::kQ), d_do = desc_lo_kmajor(base + L::kDO);
+            const uint32_t d_k = desc_lo_kmajor(base + L::kK), d_v = desc_lo_kmajor(base + L::kV);
+            const uint32_t d_kt = desc_lo_mnmajor(base + L::kK);
+            constexpr uint32_t kTileStep = L::kTile >> 4;
             constexpr uint32_t idesc_dq = idesc_bf16_f32(128, D, 1);
             // (no vote: only the leader's MMAs and commits count)
             auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.status); };
             auto commit = [&](uint64_t* bar) {
                 if (leader) tc_commit(bar);
             };
-            auto product = [&](uint32_t col, uint64_t da, uint64_t db, int w) {  // 128 rows x w columns over d
+            auto product = [&](uint32_t col, uint32_t da, uint32_t db, int w) {  // 128 rows x w columns over d
                 const uint32_t idesc = idesc_bf16_f32(128, 0, 0) | (static_cast<uint32_t>(w >> 3) << 17);
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t at = static_cast<uint64_t>((kk >> 2) * (kChunkBytesSw128 >> 4) + (kk & 3) * 2);
-                        umma_ss(tmem + col, da + at, db + at, idesc, kk > 0);
+                        const uint32_t at = (kk >> 2) * (kChunkBytesSw128 >> 4) + (kk & 3) * 2;
+                        umma_ss(tmem + col, desc_of(da + at), desc_of(db + at), idesc, kk > 0);
                     }
                 }
             };
@@ -314,16 +335,21 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                     } else if (more) {
                         if (!(ok = issue_s(nxt, 0, step + 1, item + 1) && issue_dp(nxt, 0, step + 1, item + 1))) break;
                     }
-                    // of an item's first tile: only after the elementwise threads have read
-                    // the sums of the item before
                     if (!(ok = wait(ds_full + (step & 1), (step >> 1) & 1))) break;
+                    if (j == 0 && item > 0 && !(ok = wait(dq_read, (item - 1) & 1))) break;  // the sums of the item before
                     tc_fence_after();
                     const uint32_t st = step % kKStages;
-                    if (leader) {
-                        const int steps = width(cur, j) / 16;
-                        for (int kk = 0; kk < steps; ++kk)
-                            umma_ts(tmem + kColB, tmem + kColP + 128 * (step & 1) + packed_col(kk),
-                                    d_kt + st * kTileStep + static_cast<uint64_t>(kk * 128), idesc_dq, j > 0 || kk > 0);
+                    const int w = width(cur, j);
+                    const uint32_t from = tmem + kColP + 128 * (step & 1), db = d_kt + st * kTileStep;
+                    if (w == kKeyTile) {  // unrolled: 38 cycles a product of 16 keys instead of 110
+                        if (leader) {
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                umma_ts(tmem + kColB, from + packed_col(kk), desc_of(db + kk * 128), idesc_dq, j > 0 || kk > 0);
+                        }
+                    } else if (leader) {
+                        for (int kk = 0; kk < w / 16; ++kk)
+                            umma_ts(tmem + kColB, from + packed_col(kk), desc_of(db + kk * 128), idesc_dq, j > 0 || kk > 0);
                     }
                     commit(k_empty + st);
                     if (last) commit(dq_done);
@@ -331,100 +357,124 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                 cur = nxt;
                 ++item;
             }
-        } else if (warp >= 2) {
-            // D = sum dO O of an item's rows, and their lse, an item ahead: D / 8 lanes a row
-            if (warp == 2 && blockIdx.x == 0) count_rows(a);
-            constexpr int kLanes = D / 8, kRows = 32 / kLanes, kBatch = 8;
+        } else if (warp == 2 && blockIdx.x == 0) {
+            count_rows(a);
+        }
+    } else if (warp < 8) {
+        setmaxnreg_inc<kDqRegsAux>();
+        {
+            // D = sum dO O of an item's rows, and the sums of dq to memory.  dO is in shared
+            // memory; O and lse come from memory an item ahead, into registers.  (Both from
+            // memory: beside 224 KiB of shared memory the loads in flight have little room in
+            // L1, and 64 KiB an item took 7,500 cycles, more than a tile's products.)  8 rows'
+            // sums are the diagonal of a small matrix product: lane 4 g + c has 8 channels of
+            // every 32 of row g, the same ones for both operands.
+            constexpr int kParts = D / 32;  // 16-byte units of a lane and row
             float* aux = reinterpret_cast<float*>(smem + L::kAux);
-            const int w = warp - 2, sub = lane / kLanes, unit = lane % kLanes;
+            const int w = warp - 4, g = lane >> 2;  // 32 rows a warp
             uint32_t items = 0;
-            for (int i = blockIdx.x; i < a.items; i += gridDim.x) {
-                const DqItem t = dq_item(a, i);
-                if (t.n == 0) continue;
-                const uint32_t buf = items & 1;
-                if (items >= 2 && !__all_sync(0xFFFFFFFFu, mbar_wait(aux_empty + buf, (items / 2 - 1) & 1, a.status))) break;
-                ++items;
-                float* x = aux + buf * 256;
-                const int64_t row0 = static_cast<int64_t>(t.group) * a.s.group_rows + t.row0;
-                const int64_t at = static_cast<int64_t>(t.head) * a.s.rows + row0;
-                const int mine = w * 64 + lane;  // and the row 32 behind it
-                const float l0 = mine < t.rows ? a.lse[at + mine] : INFINITY;
-                const float l1 = mine + 32 < t.rows ? a.lse[at + mine + 32] : INFINITY;
-                const uint16_t* g0 = a.dO_rows + row0 * a.dO_row + t.head * a.dO_head + unit * 8;
-                const uint16_t* o0 = a.O + row0 * a.O_row + t.head * a.O_head + unit * 8;
-#pragma unroll 1
-                for (int r0 = w * 64; r0 < w * 64 + 64; r0 += kBatch * kRows) {
-                    uint4 g[kBatch], o[kBatch];
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int r = r0 + k * kRows + sub;
-                        g[k] = o[k] = make_uint4(0, 0, 0, 0);
-                        if (r < t.rows) {
-                            g[k] = *reinterpret_cast<const uint4*>(g0 + r * a.dO_row);
-                            o[k] = ld_row(o0 + r * a.O_row);
-                        }
+            bool ok = true;
+            auto first_row = [&](const DqItem& t) { return static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + w * 32; };
+            int i = blockIdx.x;
+            auto next_item = [&](DqItem& t) {  // the next one with keys; the rows of those without get zeros
+                for (; i < a.items; i += gridDim.x) {
+                    t = dq_item(a, i);
+                    if (t.n > 0) {
+                        i += gridDim.x;
+                        return true;
                     }
+                    uint16_t* to = a.dq + first_row(t) * a.dq_row + t.head * a.dq_head;
+                    for (int e = lane; e < 32 * (D / 8); e += 32)
+                        if (w * 32 + e / (D / 8) < t.rows)
+                            *reinterpret_cast<uint4*>(to + e / (D / 8) * a.dq_row + e % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+                }
+                return false;
+            };
+            uint4 o[4][kParts];
+            float lse = 0.0f;
+            auto fetch = [&](const DqItem& t) {
+                const int64_t row0 = first_row(t);
+                const int rows = t.rows - w * 32;  // of this warp's 32; rows that do not exist: another one in their place
+                const uint16_t* o0 = a.O + t.head * a.O_head + (lane & 3) * 8;
+                lse = lane < rows ? a.lse[static_cast<int64_t>(t.head) * a.s.rows + row0 + lane] : INFINITY;
 #pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        const int r = r0 + k * kRows + sub;
-                        const float sum = lane_sum<kLanes>(dot(unpack_bf16<false>(g[k]), unpack_bf16<false>(o[k])));
-                        if (unit == 0) {
-                            x[r] = sum;
-                            if (r < t.rows) a.delta[at + r] = sum;
-                        }
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t r = rows > 0 ? row0 + min(8 * k + g, rows - 1) : row0 - w * 32;
+#pragma unroll
+                    for (int c = 0; c < kParts; ++c) o[k][c] = ld_row(o0 + r * a.O_row + 32 * c);
+                }
+            };
+            auto store_last = [&](const DqItem& t) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait(dq_done, (items - 1) & 1, a.status))) return false;
+                tc_fence_after();
+                // out of TMEM at once: the next item's first sums wait for it
+                uint4 u[D / 8];
+                read_rows<D>(u, tmem + (static_cast<uint32_t>(w * 32) << 16) + kColB, a.scale);
+                tc_fence_before();
+                mbar_arrive(dq_read);
+                write_rows<D / 8>(u, a.dq + first_row(t) * a.dq_row + t.head * a.dq_head, a.dq_row, t.rows - w * 32);
+                return true;
+            };
+            DqItem t, nxt, last;
+            bool more = next_item(t);
+            if (more) fetch(t);
+            while (ok && more) {
+                const uint32_t buf = items & 1;
+                if (items >= 2 && !(ok = __all_sync(0xFFFFFFFFu, mbar_wait(aux_empty + buf, (items / 2 - 1) & 1, a.status)))) break;
+                if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(do_full, items & 1, a.status)))) break;
+                float* x = aux + buf * 256 + w * 32;
+                float* delta = a.delta + static_cast<int64_t>(t.head) * a.s.rows + first_row(t);
+                float d[4][2] = {};
+#pragma unroll
+                for (int c = 0; c < kParts; ++c) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 8 * k + g, unit = 4 * c + (lane & 3);
+                        const uint4 u = *reinterpret_cast<const uint4*>(smem + L::kDO + (unit >> 3) * kChunkBytesSw128 + (w * 32 + r) * 128 +
+                                                                        (((unit & 7) ^ (r & 7)) << 4));
+                        add_rows_product(d[k], u.x, u.y, o[k][c].x, o[k][c].y);
+                        add_rows_product(d[k], u.z, u.w, o[k][c].z, o[k][c].w);
                     }
                 }
-                x[128 + mine] = l0 * 1.4426950408889634f;
-                x[128 + mine + 32] = l1 * 1.4426950408889634f;
+                if ((lane & 3) == (g >> 1)) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int r = 8 * k + g;
+                        const float sum = g & 1 ? d[k][1] : d[k][0];
+                        x[r] = sum;
+                        if (w * 32 + r < t.rows) delta[r] = sum;
+                    }
+                }
+                x[128 + lane] = lse * 1.4426950408889634f;
                 mbar_arrive(aux_full + buf);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(do_empty);
+                if (items > 0 && !(ok = store_last(last))) break;
+                more = next_item(nxt);
+                if (more) fetch(nxt);
+                ++items;
+                last = t;
+                t = nxt;
             }
+            if (ok && items > 0) store_last(last);
         }
     } else {
-        setmaxnreg_inc<kRegsElementwise>();
-        const int half = (warp - 4) >> 2;
-        const int r = threadIdx.x - 128 - half * 128;
+        setmaxnreg_inc<kDqRegsElementwise>();
+        const int half = (warp - 8) >> 2;
+        const int r = threadIdx.x - 256 - half * 128;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + kColS + 64 * half, t_p = tmem + lanes + kColP + 64 * half;
         const float* aux = reinterpret_cast<const float*>(smem + L::kAux);
         const float c = a.s.scale_log2;
         uint32_t step = 0, items = 0;
-        bool ok = true, pending = false;  // pending: the item before's dq is still to be stored
-        uint16_t* out = nullptr;
-        int out_rows = 0;
-        constexpr int kCols = D / 2;  // dq columns of a thread
-        const int row_w = (warp & 3) * 32;  // the warp's first row
-        auto store_pending = [&]() {
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(dq_done, (items - 1) & 1, a.status))) return false;
-            tc_fence_after();
-            store_rows<kCols>(tmem + lanes + kColB + half * kCols, out, a.dq_row, out_rows, a.scale);
-            tc_fence_before();
-            pending = false;
-            return true;
-        };
-        int i = blockIdx.x;
-        // the next item with keys; the rows of those without get zeros
-        auto next_item = [&](DqItem& t) {
-            for (; i < a.items; i += gridDim.x) {
-                t = dq_item(a, i);
-                if (t.n > 0) {
-                    i += gridDim.x;
-                    return true;
-                }
-                if (r < t.rows) {
-                    uint16_t* to = a.dq + (static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + r) * a.dq_row +
-                                   t.head * a.dq_head + half * kCols;
-                    for (int u = 0; u < kCols / 8; ++u) reinterpret_cast<uint4*>(to)[u] = make_uint4(0, 0, 0, 0);
-                }
-            }
-            return false;
-        };
-        DqItem t, nxt;
-        bool more = next_item(t);
-        while (ok && more) {
-            more = next_item(nxt);
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+            const DqItem t = dq_item(a, i);
+            if (t.n == 0) continue;
             const float* x = aux + (items & 1) * 256 + r;
             if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(aux_full + (items & 1), (items >> 1) & 1, a.status)))) break;
-            const float delta = x[0], lse2 = x[128];
+            const float lse2 = x[128];
+            const uint64_t nd2 = f2_pack(-x[0], -x[0]);
             mbar_arrive(aux_empty + (items & 1));
             for (int j = 0; j < t.n; ++j, ++step) {
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full, step & 1, a.status)))) break;
@@ -447,37 +497,39 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dq_kernel(const __grid_cons
                         p[2 * x + 1] = ex2_approx(y1);
                     }
                 }
-                if (j == 0 && pending && !(ok = store_pending())) break;
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(dp_full + (step & 1), (step >> 1) & 1, a.status)))) break;
                 tc_fence_after();
                 {
                     const uint32_t at = t_p + 128 * (step & 1);
-                    uint32_t g[2][32];
-                    BSS_TMEM_LD32(at, g[0]);
-                    BSS_TMEM_LD32(at + 32, g[1]);
-                    tmem_wait_ld();
 #pragma unroll
-                    for (int x = 0; x < 64; ++x) p[x] *= __uint_as_float(g[x >> 5][x & 31]) - delta;
-                    if (left < 64) {
+                    for (int cc = 0; cc < 2; ++cc) {
+                        uint32_t g[32];
+                        BSS_TMEM_LD32(at + 32 * cc, g);
+                        tmem_wait_ld();
+                        float* v = p + 32 * cc;
 #pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            if (x >= left) p[x] = 0.0f;
+                        for (int x = 0; x < 16; ++x)
+                            f2_unpack(f2_mul(f2_pack(v[2 * x], v[2 * x + 1]),
+                                             f2_add(f2_pack(__uint_as_float(g[2 * x]), __uint_as_float(g[2 * x + 1])), nd2)),
+                                      v[2 * x], v[2 * x + 1]);
+                        if (left < 64) {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                if (32 * cc + x >= left) v[x] = 0.0f;
+                        }
+                        uint32_t w[16];
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) w[x] = pack_bf16x2(v[2 * x], v[2 * x + 1]);
+                        BSS_TMEM_ST16(at + 16 * cc, w);  // columns that are read already
                     }
-                    store_packed(at, p);
                 }
                 tmem_wait_st();
                 tc_fence_before();
                 // (two barriers: the next tile's dS may be there before this one's is taken)
                 mbar_arrive(ds_full + (step & 1));
             }
-            if (!ok) break;
             ++items;
-            pending = true;
-            out = a.dq + (static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + row_w) * a.dq_row + t.head * a.dq_head + half * kCols;
-            out_rows = t.rows - row_w;
-            t = nxt;
         }
-        if (ok && pending) store_pending();
     }
 
     tc_fence_before();
@@ -1007,11 +1059,11 @@ bss_status launch_backward(GradArgs& a, cudaStream_t stream) {
     auto dq = cross_dq_kernel<D>;
     auto dkv = cross_dkv_kernel<D>;
     int blocks;
-    bss_status st = resident_blocks(reinterpret_cast<const void*>(dq), kThreads, DqSmem<D>::kBytes, &blocks);
+    bss_status st = resident_blocks(reinterpret_cast<const void*>(dq), kDqThreads, DqSmem<D>::kBytes, &blocks);
     if (st == BSS_OK) st = resident_blocks(reinterpret_cast<const void*>(dkv), kThreads, DkvSmem<D>::kBytes, &blocks);
     if (st != BSS_OK) return st;
     const int grid = a.items < num_sms() ? a.items : num_sms();
-    dq<<<static_cast<unsigned>(grid), kThreads, DqSmem<D>::kBytes, stream>>>(a);
+    dq<<<static_cast<unsigned>(grid), kDqThreads, DqSmem<D>::kBytes, stream>>>(a);
     if ((st = cuda_check(cudaGetLastError(), "query gradient launch")) != BSS_OK) return st;
     dkv<<<static_cast<unsigned>(a.blocks), kThreads, DkvSmem<D>::kBytes, stream>>>(a);
     if ((st = cuda_check(cudaGetLastError(), "key gradient launch")) != BSS_OK) return st;
@@ -1107,13 +1159,11 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
     a.items = static_cast<int32_t>(items);
     a.by_tiles = FastDiv(static_cast<uint32_t>(plan.tiles));
     a.O = static_cast<const uint16_t*>(p.O.data);
-    a.dO_rows = static_cast<const uint16_t*>(p.dO.data);
     a.dq = static_cast<uint16_t*>(p.dq.data);
     a.dk = static_cast<uint16_t*>(p.dk.data);
     a.dv = static_cast<uint16_t*>(p.dv.data);
     auto stride = [](int64_t extent, int64_t s) { return extent > 1 ? s : 0; };
     a.O_row = stride(p.rows, p.O.token_stride), a.O_head = stride(p.heads, p.O.head_stride);
-    a.dO_row = stride(p.rows, p.dO.token_stride), a.dO_head = stride(p.heads, p.dO.head_stride);
     a.dq_row = stride(p.rows, p.dq.token_stride), a.dq_head = stride(p.heads, p.dq.head_stride);
     a.dk_group = stride(groups, p.dk.group_stride), a.dk_token = stride(p.keys, p.dk.token_stride);
     a.dk_head = stride(p.kv_heads, p.dk.head_stride);

@@ -100,7 +100,7 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
-// The 4-D form.
+// tma_load_3d with one dimension more.
 __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, int32_t c0, int32_t c1,
                                             int32_t c2, int32_t c3, uint64_t* bar) {
     asm volatile(
