@@ -145,16 +145,17 @@ bss_status encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, ui
 }
 
 bss_status encode_tmap_rows(CUtensorMap* map, const void* base, int dtype, uint64_t inner, uint64_t rows,
-                            uint64_t row_stride_bytes, uint32_t box_rows) {
+                            uint64_t row_stride_bytes, uint32_t box_rows, uint64_t planes, uint64_t plane_stride_bytes) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     bss_status st = encode_fn(&enc);
     if (st != BSS_OK) return st;
     const bool wide = dtype == BSS_DTYPE_F32;
-    cuuint64_t dims[2] = {inner, rows};
-    cuuint64_t strides[1] = {rows > 1 ? row_stride_bytes : 16 * ((inner * (wide ? 4 : 2) + 15) / 16)};
-    cuuint32_t box[2] = {wide ? 32u : 64u, box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+    const uint64_t row = rows > 1 ? row_stride_bytes : 16 * ((inner * (wide ? 4 : 2) + 15) / 16);
+    cuuint64_t dims[3] = {inner, rows, planes};
+    cuuint64_t strides[2] = {row, planes > 1 ? plane_stride_bytes : row};
+    cuuint32_t box[3] = {wide ? 32u : 64u, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
                      const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return set_error(BSS_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);

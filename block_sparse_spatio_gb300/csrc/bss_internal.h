@@ -124,9 +124,10 @@ int* device_status_ptr();  // per-device status word (device address)
 bss_status encode_tmap_3d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t heads,
                           uint64_t row_stride_bytes, uint64_t head_stride_bytes, uint32_t box_inner,
                           uint32_t box_rows);
-// A [rows][inner] matrix of bf16 or float (dtype BSS_DTYPE_*), tiles of 128 bytes x box_rows.
+// [planes][rows][inner] matrices of bf16 or float (dtype BSS_DTYPE_*), tiles of 128 bytes x box_rows.
 bss_status encode_tmap_rows(CUtensorMap* map, const void* base, int dtype, uint64_t inner, uint64_t rows,
-                            uint64_t row_stride_bytes, uint32_t box_rows);
+                            uint64_t row_stride_bytes, uint32_t box_rows, uint64_t planes = 1,
+                            uint64_t plane_stride_bytes = 16);
 // encode_tmap_3d with one dimension more; strides in bytes, extents of 1 take any stride.
 bss_status encode_tmap_4d(CUtensorMap* map, const void* base, const uint64_t (&extent)[4],
                           const uint64_t (&stride)[3], uint32_t box_inner, uint32_t box_rows);

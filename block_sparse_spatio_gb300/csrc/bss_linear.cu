@@ -16,6 +16,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "bss_args.h"
 #include "bss_rows.cuh"
@@ -50,26 +51,27 @@ __device__ __forceinline__ float activate(float z) {
     }
 }
 
-// Value and slope.  Beyond |z| = 20 (SiLU: 110) a slope is 0 or 1 to the last bit of
-// a float's range; held there, no product of an overflowed factor and a zero can
-// arise (NaN stays).
+// Value and slope.  Beyond |z| = 20 (SiLU: 110) the share of z that passes and the slope
+// are 0 or 1 to the last bit of a float's range; held there, no product of an overflowed
+// factor and a zero can arise (NaN stays).
 template <int ACT>
 __device__ __forceinline__ void activate_both(float z, float& value, float& slope) {
-    if constexpr (ACT == BSS_ACT_NONE) {
-        value = z, slope = 1.0f;
-        return;
-    }
-    value = activate<ACT>(z);
     constexpr float kEnd = ACT == BSS_ACT_SILU ? 110.0f : 20.0f;
     const float t = z > kEnd ? kEnd : (z < -kEnd ? -kEnd : z);
     if constexpr (ACT == BSS_ACT_GELU_TANH) {
         const float s = sigmoid(kTanhC * t * fmaf(kTanhD * t, t, 1.0f));
+        value = z * s;
         slope = fmaf(t * s * (1.0f - s), kTanhC * fmaf(3.0f * kTanhD * t, t, 1.0f), s);
     } else if constexpr (ACT == BSS_ACT_GELU) {
-        slope = fmaf(t, 0.39894228040143268f * __expf(-0.5f * t * t), 0.5f * erfcf(-0.70710678118654752f * t));
+        const float half = 0.5f * erfcf(-0.70710678118654752f * t);
+        value = z * half;
+        slope = fmaf(t, 0.39894228040143268f * __expf(-0.5f * t * t), half);
     } else if constexpr (ACT == BSS_ACT_SILU) {
         const float s = sigmoid(t);
+        value = z * s;
         slope = s * fmaf(t, 1.0f - s, 1.0f);
+    } else {
+        value = z, slope = 1.0f;
     }
 }
 
@@ -102,10 +104,15 @@ struct Epilogue {
 struct GemmArgs {
     CUtensorMap a, b, out, pre;
     int32_t m, n, kblocks;
-    int32_t tiles_n, tiles;
+    int32_t tiles_n, tiles, splits;  // of the contraction: split i takes the planes' sums i
     int* status;
     Epilogue e;
 };
+
+// The contraction's blocks of 64 that a split begins with.
+__device__ __forceinline__ int split_begin(const GemmArgs& g, int split) {
+    return static_cast<int>(static_cast<int64_t>(split) * g.kblocks / g.splits);
+}
 
 struct GemmSmem {
     static constexpr uint32_t kPieces = kStages * 2 * kOperand;
@@ -222,10 +229,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             };
             uint32_t fill = 0;
             bool ok = true;
-            for (int t = first; ok && t < g.tiles; t += step) {
+            for (int u = first; ok && u < g.tiles * g.splits; u += step) {
+                const int split = u / g.tiles, t = u - split * g.tiles;
                 const int mt = t / g.tiles_n, nt = t - mt * g.tiles_n;
+                const int end = split_begin(g, split + 1);
                 const int row_a = mt * kTile + static_cast<int>(rank) * 128, row_b = nt * kTile + static_cast<int>(rank) * 128;
-                for (int kb = 0; kb < g.kblocks; ++kb, ++fill) {
+                for (int kb = split_begin(g, split); kb < end; ++kb, ++fill) {
                     const uint32_t s = fill % kStages;
                     if (fill >= kStages) ok = mbar_wait(empty + s, (fill / kStages - 1) & 1, g.status);
                     if (!ok) break;
@@ -268,13 +277,14 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     else tc_commit(bar);
                 }
             };
-            for (int t = first; ok && t < g.tiles; t += step, ++n_tile) {
+            for (int u = first; ok && u < g.tiles * g.splits; u += step, ++n_tile) {
+                const int split = u / g.tiles, begin = split_begin(g, split), end = split_begin(g, split + 1);
                 const uint32_t buf = n_tile & 1;
                 if (n_tile >= 2)
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_empty + buf, (n_tile / 2 - 1) & 1, g.status));
                 if (!ok) break;
                 tc_fence_after();
-                for (int kb = 0; kb < g.kblocks; ++kb, ++fill) {
+                for (int kb = begin; kb < end; ++kb, ++fill) {
                     const uint32_t s = fill % kStages;
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(full + s, (fill / kStages) & 1, g.status));
                     if (!ok) break;
@@ -283,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         const uint64_t at = static_cast<uint64_t>(s) * (2 * kOperand >> 4);
 #pragma unroll
                         for (int kk = 0; kk < kTileK / 16; ++kk) {
-                            const uint32_t acc = kb > 0 || kk > 0 ? 1u : 0u;
+                            const uint32_t acc = kb > begin || kk > 0 ? 1u : 0u;
                             if constexpr (CG == 2)
                                 umma_ss_pair(tmem + buf * kAccCols, da0 + at + kk * kStepA, db0 + at + kk * kStepB, idesc, acc);
                             else
@@ -312,15 +322,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             __syncwarp();
             return pieces + (e.pre != nullptr ? which : static_cast<int>(stores++ & 1)) * kPiece;
         };
-        auto send = [&](const CUtensorMap* map, const uint8_t* from, int col, int row0) {
+        auto send = [&](const CUtensorMap* map, const uint8_t* from, int col, int row0, int plane) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
-                tma_store_2d(map, from, col, row0);
+                tma_store_3d(map, from, col, row0, plane);
                 tma_store_commit();
             }
         };
-        for (int t = first; t < g.tiles; t += step, ++n_tile) {
+        for (int u = first; u < g.tiles * g.splits; u += step, ++n_tile) {
+            const int split = u / g.tiles, t = u - split * g.tiles;
             const int mt = t / g.tiles_n, nt = t - mt * g.tiles_n;
             const uint32_t buf = n_tile & 1;
             const int row0 = mt * kTile + static_cast<int>(rank) * 128 + quarter * 32, row = row0 + lane;
@@ -365,10 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                         if (wide) put8_float(to, 2 * u, v);
                         else put8(to, 4 * h + u, v);
                     }
-                    if (wide) send(&g.out, to - lane * 128, col, row0);
+                    if (wide) send(&g.out, to - lane * 128, col, row0, split);
                 }
-                if (!wide) send(&g.out, to - lane * 128, col0, row0);
-                if (e.pre != nullptr) send(&g.pre, to_pre - lane * 128, col0, row0);
+                if (!wide) send(&g.out, to - lane * 128, col0, row0, split);
+                if (e.pre != nullptr) send(&g.pre, to_pre - lane * 128, col0, row0, 0);
             }
             tc_fence_before();
             __syncwarp();
@@ -392,6 +403,128 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     }
 }
 
+// Sums of the splits, then the epilogue: 8 columns a thread.
+struct FinishArgs {
+    const float* sums;  // [splits][m][n]
+    int32_t m, n, splits;
+    FastDiv by_vectors;
+    Epilogue e;
+};
+
+template <int ACT>
+__global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a) {
+    cudaGridDependencySynchronize();
+    const Epilogue& e = a.e;
+    const int64_t plane = static_cast<int64_t>(a.m) * a.n;
+    const uint32_t vectors = a.n / 8, all = a.m * vectors;  // below 2^31: the splits are of small results
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += gridDim.x * 256) {
+        const int row = a.by_vectors.div(i), col = static_cast<int>(i - row * vectors) * 8;
+        float v[8], w[8], r[8] = {};
+        load8(a.sums, row * static_cast<int64_t>(a.n) + col, BSS_DTYPE_F32, v);
+        for (int s = 1; s < a.splits; ++s) {
+            load8(a.sums, s * plane + row * static_cast<int64_t>(a.n) + col, BSS_DTYPE_F32, w);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] += w[x];
+        }
+        if (e.bias != nullptr) {
+            load_param8(e.bias, col, e.param_dtype, w);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) v[x] += w[x];
+        }
+        if (e.pre != nullptr) store8(e.pre, row * e.pre_stride + col, BSS_DTYPE_BF16, v);
+        if (e.residual != nullptr) load8(e.residual, row * e.residual_stride + col, e.out_dtype, r);
+        finish8<ACT>(e, e.gate != nullptr ? e.by_rows.div(row) : 0, col, v, r);
+        store8(e.out, row * e.out_stride + col, e.out_dtype, v);
+    }
+}
+
+// ---------------------------------------------------------------- few rows
+// The weights' bytes are the work: every warp streams its share of them straight into
+// the operand of a small matrix product (16 output channels a block; lane 4 g + c loads
+// 16 bytes of rows g and g + 8: channels that follow one another, the same ones of x's
+// rows), 8 warps share the contraction, and their sums meet in shared memory.
+constexpr int kFewRows = 16;
+constexpr int kFewWarps = 8;
+
+struct FewArgs {
+    const __nv_bfloat16 *x, *weight;
+    int64_t x_stride, weight_stride;
+    int32_t rows, inner, outer;
+    Epilogue e;
+};
+
+__device__ __forceinline__ void few_product(float (&d)[4], const uint4& w0, const uint4& w1, const uint4& x) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(w0.x), "r"(w1.x), "r"(w0.y), "r"(w1.y), "r"(x.x), "r"(x.y));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(w0.z), "r"(w1.z), "r"(w0.w), "r"(w1.w), "r"(x.z), "r"(x.w));
+}
+
+template <int NT, int ACT>  // NT: tiles of 8 rows
+__global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_constant__ FewArgs a) {
+    __shared__ float sums[kFewWarps][8 * NT][17];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = (lane & 3) * 8;
+    const int o0 = blockIdx.x * 16;
+    const uint4 none = make_uint4(0, 0, 0, 0);
+    // (output channels come in eights: the second eight may not exist)
+    const __nv_bfloat16* w0 = a.weight + (o0 + g) * a.weight_stride + c;
+    const __nv_bfloat16* w1 = w0 + 8 * a.weight_stride;
+    const bool both = o0 + 8 < a.outer;
+    float d[NT][4] = {};
+    constexpr int kBatch = NT == 1 ? 8 : 4;  // blocks of 32 channels in flight
+    const int blocks = (a.inner + 31) / 32, begin = blocks * warp / kFewWarps, end = blocks * (warp + 1) / kFewWarps;
+    for (int b = begin; b < end; b += kBatch) {
+        uint4 p[kBatch], q[kBatch], x[kBatch][NT];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int k = (b + i) * 32;
+            const bool live = b + i < end && k + c < a.inner;
+            p[i] = live ? ld_row(w0 + k) : none;
+            q[i] = live && both ? ld_row(w1 + k) : none;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                x[i][t] = live && 8 * t + g < a.rows
+                              ? __ldg(reinterpret_cast<const uint4*>(a.x + (8 * t + g) * a.x_stride + k + c)) : none;
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) few_product(d[t], p[i], q[i], x[i][t]);
+    }
+    // d: channels g and g + 8 of rows 2 (lane % 4) and the next
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int r = 8 * t + (lane & 3) * 2;
+        sums[warp][r][g] = d[t][0];
+        sums[warp][r + 1][g] = d[t][1];
+        sums[warp][r][g + 8] = d[t][2];
+        sums[warp][r + 1][g + 8] = d[t][3];
+    }
+    __syncthreads();
+    const Epilogue& e = a.e;
+    for (int i = threadIdx.x; i < 8 * NT * 16; i += 32 * kFewWarps) {
+        const int row = i >> 4, o = o0 + (i & 15);
+        if (row >= a.rows || o >= a.outer) continue;
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kFewWarps; ++w) z += sums[w][row][i & 15];
+        if (e.bias != nullptr) z += load_param(e.bias, o, e.param_dtype);
+        if (e.pre != nullptr) static_cast<__nv_bfloat16*>(e.pre)[row * e.pre_stride + o] = __float2bfloat16(z);
+        float v = activate<ACT>(z);
+        if (e.gate != nullptr) v *= load_param(e.gate, e.by_rows.div(row) * e.gate_stride + o, e.param_dtype);
+        if (e.out_dtype == BSS_DTYPE_F32) {
+            if (e.residual != nullptr) v = fmaf(e.residual_scale, static_cast<const float*>(e.residual)[row * e.residual_stride + o], v);
+            static_cast<float*>(e.out)[row * e.out_stride + o] = v;
+        } else {
+            if (e.residual != nullptr)
+                v = fmaf(e.residual_scale, __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[row * e.residual_stride + o]), v);
+            static_cast<__nv_bfloat16*>(e.out)[row * e.out_stride + o] = __float2bfloat16(v);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- dz and its sums over rows
 // A thread has 8 channels, a warp walks over rows; a block covers `unit` rows that
 // share a gate, or (small groups) whole groups, one a warp at a time.
@@ -409,7 +542,7 @@ struct DzArgs {
 
 constexpr int kDzWarps = 8;
 
-template <int ACT>
+template <int ACT, bool WIDE>  // WIDE: dout is float
 __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const __grid_constant__ DzArgs a) {
     __shared__ float sums[kDzWarps][2][32 * 9];  // a lane's 8 values 9 apart
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -440,18 +573,38 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < 8; ++i) gate[i] = 1.0f;
         if (a.gate != nullptr && live) load_param8(a.gate, group * a.gate_stride + c, a.param_dtype, gate);
-        for (int64_t row = begin + (small ? 0 : warp); live && row < end; row += small ? 1 : kDzWarps) {
-            float d[8], z[8] = {}, v, s;
-            load8(a.dout, row * a.dout_stride + c, a.dout_dtype, d);
-            if (a.pre != nullptr) load8(a.pre, row * a.pre_stride + c, BSS_DTYPE_BF16, z);
+        // several rows' loads at once: two of 16 bytes alone leave the memory idle
+        constexpr int kRows = WIDE ? 2 : 4;
+        const int64_t every = small ? 1 : kDzWarps;
+        for (int64_t row = begin + (small ? 0 : warp); live && row < end; row += kRows * every) {
+            float d[kRows][8], z[kRows][8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                activate_both<ACT>(z[i], v, s);
-                dg[i] = fmaf(d[i], v, dg[i]);
-                d[i] *= gate[i] * s;
-                db[i] += d[i];
+            for (int k = 0; k < kRows; ++k) {
+                const int64_t at = row + k * every < end ? row + k * every : row;
+                load8(a.dout, at * a.dout_stride + c, WIDE ? BSS_DTYPE_F32 : BSS_DTYPE_BF16, d[k]);
+                if (a.pre != nullptr) load8(a.pre, at * a.pre_stride + c, BSS_DTYPE_BF16, z[k]);
             }
-            if (a.dz != nullptr) store8(a.dz, row * a.n + c, BSS_DTYPE_BF16, d);
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                if (row + k * every >= end) break;
+                if (ACT != BSS_ACT_NONE || a.dgate != nullptr) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float v, s;
+                        activate_both<ACT>(z[k][i], v, s);
+                        dg[i] = fmaf(d[k][i], v, dg[i]);
+                        d[k][i] *= gate[i] * s;
+                        db[i] += d[k][i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        d[k][i] *= gate[i];
+                        db[i] += d[k][i];
+                    }
+                }
+                if (a.dz != nullptr) store8(a.dz, (row + k * every) * a.n + c, BSS_DTYPE_BF16, d[k]);
+            }
         }
         if (!small) break;
         if (a.dgate != nullptr && live) store8(a.dgate, group * a.n + c, BSS_DTYPE_F32, dg);
@@ -507,19 +660,49 @@ bss_status operand_map(CUtensorMap* map, const void* p, int64_t rows, int64_t st
     return encode_tmap_3d(map, p, width, rows, 1, bytes, bytes, 64, mn_major ? kTileK : 128);
 }
 
+// How a product is cut: by pairs of CTAs or single ones, and its contraction into splits,
+// whose sums a second kernel adds.  The least of a simple estimate in microseconds:
+// rounds of the tiles times a block of 64 of the contraction (pairs 0.38, single 0.25,
+// measured at 75,600 x 5,120 x 1,280), plus 4 for the second kernel and its bytes at
+// 5 TB/s.  (1,280 x 5,120 of 75,600: 752 us with one split, 100 tiles for 76 pairs.)
+struct Cut {
+    bool pair;
+    int splits;
+};
+
+Cut cut_of(int64_t m, int64_t n, int64_t k) {
+    const int64_t blocks = (k + kTileK - 1) / kTileK;
+    Cut best = {false, 1};
+    double least = 1e30;
+    for (int pair = 1; pair >= 0; --pair) {
+        const int64_t tile = pair ? 256 : 128, units = num_sms() / (pair ? 2 : 1);
+        const int64_t tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
+        for (int s = 1; s <= 16 && (s == 1 || s * 4 <= blocks); ++s) {
+            if (s > 1 && m * n > (int64_t(1) << 28)) break;
+            const double rounds = static_cast<double>((tiles * s + units - 1) / units);
+            double t = rounds * static_cast<double>((blocks + s - 1) / s) * (pair ? 0.38 : 0.25);
+            if (s > 1) t += 4.0 + 8.0 * s * m * n / 5e6;
+            if (t < least) least = t, best = {pair != 0, s};
+        }
+    }
+    return best;
+}
+
+int64_t cut_bytes(const Cut& c, int64_t m, int64_t n) { return c.splits > 1 ? 4 * c.splits * m * n : 0; }
+
 template <int CG, bool A_MN, bool B_MN, int ACT>
 bss_status launch_gemm(GemmArgs& g, cudaStream_t stream) {
     constexpr int kTile = 128 * CG;
     const int64_t tiles_m = (static_cast<int64_t>(g.m) + kTile - 1) / kTile;
     g.tiles_n = (g.n + kTile - 1) / kTile;
-    if (tiles_m * g.tiles_n > 0x7FFFFFFF) return set_error(BSS_ERR_UNSUPPORTED, "too many tiles");
+    if (tiles_m * g.tiles_n * g.splits > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many tiles");
     g.tiles = static_cast<int32_t>(tiles_m * g.tiles_n);
     auto kernel = gemm_kernel<CG, A_MN, B_MN, ACT>;
     int blocks;
     const bss_status st = resident_blocks(reinterpret_cast<const void*>(kernel), kThreads, GemmSmem::kAlloc, &blocks);
     if (st != BSS_OK) return st;
     int units = num_sms() / CG;
-    if (units > g.tiles) units = g.tiles;
+    if (units > g.tiles * g.splits) units = g.tiles * g.splits;
     cudaLaunchConfig_t config = {};
     config.gridDim = dim3(static_cast<unsigned>(units * CG));
     config.blockDim = dim3(kThreads);
@@ -539,10 +722,21 @@ bss_status launch_linear(GemmArgs& g, bool pair, cudaStream_t stream) {
     return pair ? launch_gemm<2, false, false, ACT>(g, stream) : launch_gemm<1, false, false, ACT>(g, stream);
 }
 
-// D[m][n] = A B^T of k, then the epilogue.
+// The kernel of an activation.
+template <typename F>
+bss_status by_activation(int activation, F&& f) {
+    switch (activation) {
+        case BSS_ACT_GELU_TANH: return f(std::integral_constant<int, BSS_ACT_GELU_TANH>());
+        case BSS_ACT_GELU: return f(std::integral_constant<int, BSS_ACT_GELU>());
+        case BSS_ACT_SILU: return f(std::integral_constant<int, BSS_ACT_SILU>());
+        default: return f(std::integral_constant<int, BSS_ACT_NONE>());
+    }
+}
+
+// D[m][n] = A B^T of k, then the epilogue; with splits through `sums`.
 template <bool A_MN, bool B_MN>
 bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride, int64_t m, int64_t n, int64_t k,
-                const Epilogue& e, cudaStream_t stream) {
+                const Cut& cut, float* sums, const Epilogue& e, cudaStream_t stream) {
     GemmArgs g;
     memset(&g, 0, sizeof(g));
     g.status = device_status_ptr();
@@ -551,24 +745,39 @@ bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride
     if (st != BSS_OK) return st;
     st = B_MN ? operand_map(&g.b, b, k, b_stride, n, true) : operand_map(&g.b, b, n, b_stride, k, false);
     if (st != BSS_OK) return st;
-    if ((st = encode_tmap_rows(&g.out, e.out, e.out_dtype, n, m, e.out_stride * element_size(e.out_dtype), 32)) != BSS_OK) return st;
-    if (e.pre != nullptr && (st = encode_tmap_rows(&g.pre, e.pre, BSS_DTYPE_BF16, n, m, e.pre_stride * 2, 32)) != BSS_OK) return st;
     g.m = static_cast<int32_t>(m);
     g.n = static_cast<int32_t>(n);
     g.kblocks = static_cast<int32_t>((k + kTileK - 1) / kTileK);
-    g.e = e;
-    const int64_t pairs = ((m + 255) / 256) * ((n + 255) / 256);
-    const bool pair = pairs >= num_sms() / 2;
-    if constexpr (A_MN || B_MN) {
-        return pair ? launch_gemm<2, A_MN, B_MN, BSS_ACT_NONE>(g, stream) : launch_gemm<1, A_MN, B_MN, BSS_ACT_NONE>(g, stream);
+    g.splits = cut.splits;
+    if (cut.splits > 1) {
+        g.e.out_dtype = BSS_DTYPE_F32;
+        st = encode_tmap_rows(&g.out, sums, BSS_DTYPE_F32, n, m, n * 4, 32, cut.splits, m * n * 4);
     } else {
-        switch (e.activation) {
-            case BSS_ACT_GELU_TANH: return launch_linear<BSS_ACT_GELU_TANH>(g, pair, stream);
-            case BSS_ACT_GELU: return launch_linear<BSS_ACT_GELU>(g, pair, stream);
-            case BSS_ACT_SILU: return launch_linear<BSS_ACT_SILU>(g, pair, stream);
-            default: return launch_linear<BSS_ACT_NONE>(g, pair, stream);
-        }
+        g.e = e;
+        st = encode_tmap_rows(&g.out, e.out, e.out_dtype, n, m, e.out_stride * element_size(e.out_dtype), 32);
+        if (st == BSS_OK && e.pre != nullptr) st = encode_tmap_rows(&g.pre, e.pre, BSS_DTYPE_BF16, n, m, e.pre_stride * 2, 32);
     }
+    if (st != BSS_OK) return st;
+    if constexpr (A_MN || B_MN)
+        st = cut.pair ? launch_gemm<2, A_MN, B_MN, BSS_ACT_NONE>(g, stream) : launch_gemm<1, A_MN, B_MN, BSS_ACT_NONE>(g, stream);
+    else
+        st = by_activation(g.e.activation, [&](auto act) { return launch_linear<decltype(act)::value>(g, cut.pair, stream); });
+    if (st != BSS_OK || cut.splits == 1) return st;
+    FinishArgs f;
+    f.sums = sums, f.m = g.m, f.n = g.n, f.splits = cut.splits, f.by_vectors = FastDiv(static_cast<uint32_t>(n / 8)), f.e = e;
+    int64_t blocks = (m * (n / 8) + 255) / 256;
+    if (blocks > 8ll * num_sms()) blocks = 8ll * num_sms();
+    return by_activation(e.activation, [&](auto act) {
+        return launch_behind(finish_kernel<decltype(act)::value>, dim3(static_cast<unsigned>(blocks)), 256, stream, "split sums launch", f);
+    });
+}
+
+template <int ACT>
+bss_status launch_few(const FewArgs& f, cudaStream_t stream) {
+    const unsigned blocks = static_cast<unsigned>((f.outer + 15) / 16);
+    if (f.rows <= 8) few_rows_kernel<1, ACT><<<blocks, 32 * kFewWarps, 0, stream>>>(f);
+    else few_rows_kernel<2, ACT><<<blocks, 32 * kFewWarps, 0, stream>>>(f);
+    return cuda_check(cudaGetLastError(), "few rows launch");
 }
 
 bss_status check_sizes(int64_t rows, int64_t* rows_per_group, int32_t in, int32_t out, int32_t activation) {
@@ -593,7 +802,11 @@ bss_status check_linear(bss_linear_args& a) {
     return BSS_OK;
 }
 
-int64_t linear_need(const bss_linear_args&) { return 0; }
+bool takes_few(const bss_linear_args& a) { return a.rows <= kFewRows; }
+
+int64_t linear_need(const bss_linear_args& a) {
+    return takes_few(a) ? 0 : cut_bytes(cut_of(a.rows, a.out_channels, a.in_channels), a.rows, a.out_channels);
+}
 
 int64_t groups_of(int64_t rows, int64_t per) { return (rows + per - 1) / per; }
 
@@ -602,7 +815,8 @@ struct GradPlan {
     bool makes_dz, sums;
     int64_t groups, units, blocks, parts;  // parts: partial sums a group (of dgate), of dbias: blocks
     int32_t chunks;
-    int64_t dz_at, dbias_at, dgate_at, bytes;
+    int64_t dz_at, dbias_at, dgate_at, sums_at, bytes;
+    Cut dx, dweight;  // both products' split sums take turns in one place
 };
 
 int64_t aligned_up(int64_t v) { return (v + 255) / 256 * 256; }
@@ -646,6 +860,18 @@ GradPlan plan_of(const bss_linear_grads& a) {
         p.dgate_at = p.bytes;
         p.bytes += aligned_up(p.blocks * n * 4);
     }
+    int64_t sums = 0;
+    if (a.dx != nullptr) {
+        p.dx = cut_of(a.rows, a.in_channels, n);
+        sums = cut_bytes(p.dx, a.rows, a.in_channels);
+    }
+    if (a.dweight != nullptr) {
+        p.dweight = cut_of(n, a.in_channels, a.rows);
+        const int64_t b = cut_bytes(p.dweight, n, a.in_channels);
+        if (b > sums) sums = b;
+    }
+    p.sums_at = p.bytes;
+    p.bytes += sums;
     return p;
 }
 
@@ -668,7 +894,9 @@ bss_status check_grads(bss_linear_grads& a) {
 template <int ACT>
 bss_status launch_dz(const DzArgs& d, int64_t blocks, cudaStream_t stream) {
     const unsigned columns = static_cast<unsigned>((d.n + 255) / 256);
-    dz_kernel<ACT><<<dim3(columns, static_cast<unsigned>(blocks)), 32 * kDzWarps, 0, stream>>>(d);
+    const dim3 grid(columns, static_cast<unsigned>(blocks));
+    if (d.dout_dtype == BSS_DTYPE_F32) dz_kernel<ACT, true><<<grid, 32 * kDzWarps, 0, stream>>>(d);
+    else dz_kernel<ACT, false><<<grid, 32 * kDzWarps, 0, stream>>>(d);
     return cuda_check(cudaGetLastError(), "dz launch");
 }
 
@@ -718,7 +946,15 @@ bss_status bss_linear(const bss_linear_args* args, cudaStream_t stream) {
     e.param_dtype = a.param_dtype, e.out_dtype = a.out_dtype, e.activation = a.activation;
     e.residual_scale = a.residual_scale;
     e.by_rows = FastDiv(static_cast<uint32_t>(a.rows_per_group));
-    return gemm<false, false>(a.x, a.x_stride, a.weight, a.weight_stride, a.rows, a.out_channels, a.in_channels, e, stream);
+    if (takes_few(a)) {
+        FewArgs f;
+        f.x = static_cast<const __nv_bfloat16*>(a.x), f.weight = static_cast<const __nv_bfloat16*>(a.weight);
+        f.x_stride = a.x_stride, f.weight_stride = a.weight_stride;
+        f.rows = static_cast<int32_t>(a.rows), f.inner = a.in_channels, f.outer = a.out_channels, f.e = e;
+        return by_activation(a.activation, [&](auto act) { return launch_few<decltype(act)::value>(f, stream); });
+    }
+    return gemm<false, false>(a.x, a.x_stride, a.weight, a.weight_stride, a.rows, a.out_channels, a.in_channels,
+                              cut_of(a.rows, a.out_channels, a.in_channels), static_cast<float*>(a.workspace), e, stream);
 }
 
 bss_status bss_linear_backward_workspace(const bss_linear_grads* args, int64_t* bytes) {
@@ -762,6 +998,7 @@ bss_status bss_linear_backward(const bss_linear_grads* args, cudaStream_t stream
         (st = check_outputs(t, 10)) != BSS_OK)
         return st;
     char* ws = static_cast<char*>(a.workspace);
+    float* sums = reinterpret_cast<float*>(ws + p.sums_at);
     const void* dz = a.dout;
     int64_t dz_stride = a.dout_stride;
     if (p.makes_dz || p.sums) {
@@ -777,12 +1014,7 @@ bss_status bss_linear_backward(const bss_linear_grads* args, cudaStream_t stream
         d.dout_stride = a.dout_stride, d.pre_stride = a.pre_stride, d.gate_stride = a.gate_stride;
         d.units = p.units, d.chunks = p.chunks;
         d.n = a.out_channels, d.dout_dtype = a.dout_dtype, d.param_dtype = a.param_dtype;
-        switch (a.activation) {
-            case BSS_ACT_GELU_TANH: st = launch_dz<BSS_ACT_GELU_TANH>(d, p.blocks, stream); break;
-            case BSS_ACT_GELU: st = launch_dz<BSS_ACT_GELU>(d, p.blocks, stream); break;
-            case BSS_ACT_SILU: st = launch_dz<BSS_ACT_SILU>(d, p.blocks, stream); break;
-            default: st = launch_dz<BSS_ACT_NONE>(d, p.blocks, stream);
-        }
+        st = by_activation(a.activation, [&](auto act) { return launch_dz<decltype(act)::value>(d, p.blocks, stream); });
         if (st != BSS_OK) return st;
         const unsigned columns = static_cast<unsigned>((n + 31) / 32);
         if (a.dbias != nullptr)
@@ -796,12 +1028,12 @@ bss_status bss_linear_backward(const bss_linear_grads* args, cudaStream_t stream
     Epilogue e = {};
     if (a.dx != nullptr) {
         e.out = a.dx, e.out_stride = a.dx_stride, e.out_dtype = BSS_DTYPE_BF16;
-        st = gemm<false, true>(dz, dz_stride, a.weight, a.weight_stride, a.rows, k, n, e, stream);
+        st = gemm<false, true>(dz, dz_stride, a.weight, a.weight_stride, a.rows, k, n, p.dx, sums, e, stream);
         if (st != BSS_OK) return st;
     }
     if (a.dweight != nullptr) {
         e.out = a.dweight, e.out_stride = a.dweight_stride, e.out_dtype = a.dweight_dtype;
-        st = gemm<true, true>(dz, dz_stride, a.x, a.x_stride, n, k, a.rows, e, stream);
+        st = gemm<true, true>(dz, dz_stride, a.x, a.x_stride, n, k, a.rows, p.dweight, sums, e, stream);
     }
     return st;
 }

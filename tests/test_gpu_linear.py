@@ -178,3 +178,21 @@ def test_same_bits_again(bss):
         b = backward(bss, rows, inner, outer, kind=1, gate=True, group=rows // 3)
         for k in a:
             assert torch.equal(a[k].view(torch.int16), b[k].view(torch.int16)), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [0, 1])
+def test_pairs_of_ctas(bss, kind):
+    """Results of many 256 x 256 tiles, ragged at every end."""
+    forward(bss, 20003, 72, 264, kind=kind, pre=True, gate=True, residual=True, group=777, pad=8)
+    backward(bss, 20003, 264, 72, kind=kind)
+    backward(bss, 70, 2056, 2568, kind=kind, dw=F32 if kind else BF, pad=8)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,inner,outer", [(20, 4096, 136), (130, 3000, 264), (512, 4096, 640)])
+@pytest.mark.parametrize("out", [BF, F32])
+def test_split_contraction(bss, rows, inner, outer, out):
+    forward(bss, rows, inner, outer, kind=1, out=out, pre=True, gate=True, residual=True, a=0.5, group=max(1, rows // 3), pad=8)
+    forward(bss, rows, inner, outer, out=out, bias=False, residual=True, inplace=True)
+    backward(bss, inner, rows // 4 * 8, outer, dw=out)
