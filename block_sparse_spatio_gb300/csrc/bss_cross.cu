@@ -170,10 +170,9 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
         } else if (warp == 1) {
             const bool leader = elect_one();
             const uint32_t base = smem_u32(smem);
-            const uint64_t dq = desc_kmajor_sw128(base + L::kQ, 0);
-            const uint64_t dk = desc_kmajor_sw128(base + L::kK, 0);
-            const uint64_t dv = desc_mnmajor_sw128(base + L::kV, 0);
-            constexpr uint64_t kTileStep = L::kTile >> 4;
+            const uint32_t dq = desc_lo_kmajor(base + L::kQ), dk = desc_lo_kmajor(base + L::kK);
+            const uint32_t dv = desc_lo_mnmajor(base + L::kV);
+            constexpr uint32_t kTileStep = L::kTile >> 4;
             constexpr uint32_t idesc_pv = idesc_bf16_f32(128, D, 1);
             // (no vote: only the leader's MMAs and commits count)
             auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, a.status); };
@@ -190,16 +189,21 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                 if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t at = static_cast<uint64_t>((kk >> 2) * (kChunkBytesSw128 >> 4) + (kk & 3) * 2);
-                        umma_ss(tmem + kColS + 128 * h, dq + h * kTileStep + at, dk + st * kTileStep + at, idesc, kk > 0);
+                        const uint32_t at = (kk >> 2) * (kChunkBytesSw128 >> 4) + (kk & 3) * 2;
+                        umma_ss(tmem + kColS + 128 * h, desc_of(dq + h * kTileStep + at), desc_of(dk + st * kTileStep + at), idesc, kk > 0);
                     }
                 }
             };
             auto issue_pv = [&](int h, uint32_t st, int w, bool add) {
-                if (leader)
-                    for (int kk = 0; kk < w / 16; ++kk)
-                        umma_ts(tmem + kColO + 128 * h, tmem + kColS + 128 * h + kk * 8,
-                                dv + st * kTileStep + static_cast<uint64_t>(kk * 128), idesc_pv, add || kk > 0);
+                const uint32_t o = tmem + kColO + 128 * h, p = tmem + kColS + 128 * h, b = dv + st * kTileStep;
+                if (w == kKeyTile) {  // unrolled: a loop takes 110 cycles a product of 16 keys, which lasts 64
+                    if (leader) {
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk) umma_ts(o, p + kk * 8, desc_of(b + kk * 128), idesc_pv, add || kk > 0);
+                    }
+                } else if (leader) {
+                    for (int kk = 0; kk < w / 16; ++kk) umma_ts(o, p + kk * 8, desc_of(b + kk * 128), idesc_pv, add || kk > 0);
+                }
             };
             uint32_t fills = 0, clears = 0;               // K and V tiles taken
             uint32_t q_taken[2] = {0, 0}, p_taken[2] = {0, 0};

@@ -27,51 +27,76 @@ namespace {
 constexpr int kMaxWidth = 65536;
 
 // ---------------------------------------------------------------- activations
-// sigmoid(x) = 1 / (1 + exp(-x)); exp past the float range gives 0 or infinity and
-// the quotient its limit.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+__device__ __forceinline__ float rcp_approx(float x) {  // 1 / infinity = 0
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// tanh form: (1 + tanh u) / 2 = sigmoid(2 u), which keeps the small values of
+// 1 / (1 + 2^a); 2^a past the float range gives 0 or infinity and the quotient its limit.
+__device__ __forceinline__ float2 share_of(float2 a) {
+    const float2 e = __fadd2_rn(make_float2(ex2_approx(a.x), ex2_approx(a.y)), f2(1.0f));
+    return make_float2(rcp_approx(e.x), rcp_approx(e.y));
+}
+
+// tanh form: (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)), which keeps the small values of
 // negative z exact to a few roundings (1 + tanh u does not).
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanhC = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhD = 0.044715f;
 
+// The share of z that passes, of SiLU and the tanh form: w = z^2.
 template <int ACT>
-__device__ __forceinline__ float activate(float z) {
-    if constexpr (ACT == BSS_ACT_GELU_TANH) {
-        // z sigmoid(u), not z / (1 + exp(-u)): with exp at infinity the quotient would
-        // still be right, a fast division's would not
-        return z * sigmoid(kTanhC * z * fmaf(kTanhD * z, z, 1.0f));
-    } else if constexpr (ACT == BSS_ACT_GELU) {
-        return 0.5f * z * erfcf(-0.70710678118654752f * z);
-    } else if constexpr (ACT == BSS_ACT_SILU) {
-        return z * sigmoid(z);
-    } else {
-        return z;
+__device__ __forceinline__ float2 smooth_share(float2 z, float2 w) {
+    if constexpr (ACT == BSS_ACT_GELU_TANH)
+        return share_of(__fmul2_rn(z, __ffma2_rn(w, f2(-kTanhC * kTanhD * kLog2e), f2(-kTanhC * kLog2e))));
+    else
+        return share_of(__fmul2_rn(z, f2(-kLog2e)));
+}
+
+__device__ __forceinline__ float erf_share(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
+
+// (z times the share, not a quotient: with an infinite exponential the share is 0)
+template <int ACT>
+__device__ __forceinline__ float2 activate(float2 z) {
+    if constexpr (ACT == BSS_ACT_GELU) return __fmul2_rn(z, make_float2(erf_share(z.x), erf_share(z.y)));
+    else if constexpr (ACT != BSS_ACT_NONE) return __fmul2_rn(z, smooth_share<ACT>(z, __fmul2_rn(z, z)));
+    else return z;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z) { return activate<ACT>(make_float2(z, 0.0f)).x; }
+
+template <int ACT>
+__device__ __forceinline__ void activate8(float (&v)[8]) {
+    if constexpr (ACT != BSS_ACT_NONE) {
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+            const float2 y = activate<ACT>(make_float2(v[i], v[i + 1]));
+            v[i] = y.x, v[i + 1] = y.y;
+        }
     }
 }
 
-// Value and slope.  Beyond |z| = 20 (SiLU: 110) the share of z that passes and the slope
-// are 0 or 1 to the last bit of a float's range; held there, no product of an overflowed
-// factor and a zero can arise (NaN stays).
+// Share and slope.  Beyond |z| = 20 (SiLU: 110) both are 0 or 1 to the last bit of a
+// float's range; with z held there (t), no product of an overflowed factor and a zero can
+// arise.  A NaN is not held: it stays in the share, and by it in the slope.
 template <int ACT>
-__device__ __forceinline__ void activate_both(float z, float& value, float& slope) {
+__device__ __forceinline__ void share_and_slope(float2 z, float2& share, float2& slope) {
     constexpr float kEnd = ACT == BSS_ACT_SILU ? 110.0f : 20.0f;
-    const float t = z > kEnd ? kEnd : (z < -kEnd ? -kEnd : z);
-    if constexpr (ACT == BSS_ACT_GELU_TANH) {
-        const float s = sigmoid(kTanhC * t * fmaf(kTanhD * t, t, 1.0f));
-        value = z * s;
-        slope = fmaf(t * s * (1.0f - s), kTanhC * fmaf(3.0f * kTanhD * t, t, 1.0f), s);
-    } else if constexpr (ACT == BSS_ACT_GELU) {
-        const float half = 0.5f * erfcf(-0.70710678118654752f * t);
-        value = z * half;
-        slope = fmaf(t, 0.39894228040143268f * __expf(-0.5f * t * t), half);
-    } else if constexpr (ACT == BSS_ACT_SILU) {
-        const float s = sigmoid(t);
-        value = z * s;
-        slope = s * fmaf(t, 1.0f - s, 1.0f);
+    const float2 t = make_float2(fminf(fmaxf(z.x, -kEnd), kEnd), fminf(fmaxf(z.y, -kEnd), kEnd));
+    if constexpr (ACT == BSS_ACT_GELU) {
+        share = make_float2(erf_share(z.x), erf_share(z.y));
+        slope = make_float2(fmaf(t.x, 0.39894228040143268f * __expf(-0.5f * t.x * t.x), share.x),
+                            fmaf(t.y, 0.39894228040143268f * __expf(-0.5f * t.y * t.y), share.y));
     } else {
-        value = z, slope = 1.0f;
+        // share (1 + (1 - share) u') with u' z times the derivative of the exponent
+        const float2 w = __fmul2_rn(t, t);
+        share = smooth_share<ACT>(z, w);
+        float2 q = t;
+        if constexpr (ACT == BSS_ACT_GELU_TANH) q = __fmul2_rn(t, __ffma2_rn(w, f2(3.0f * kTanhC * kTanhD), f2(kTanhC)));
+        const float2 rest = __ffma2_rn(share, f2(-1.0f), f2(1.0f));
+        slope = __fmul2_rn(share, __ffma2_rn(q, rest, f2(1.0f)));
     }
 }
 
@@ -168,8 +193,7 @@ __device__ __forceinline__ void put8_float(uint8_t* row, int unit, const float (
 template <int ACT>
 __device__ __forceinline__ void finish8(const Epilogue& e, int64_t group, int col, float (&v)[8], const float (&r)[8]) {
     float w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(v[i]);
+    activate8<ACT>(v);
     if (e.gate != nullptr) {
         load_param8(e.gate, group * e.gate_stride + col, e.param_dtype, w);
 #pragma unroll
@@ -542,7 +566,7 @@ struct DzArgs {
 
 constexpr int kDzWarps = 8;
 
-template <int ACT, bool WIDE>  // WIDE: dout is float
+template <int ACT, bool WIDE, bool GATED>  // WIDE: dout is float
 __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const __grid_constant__ DzArgs a) {
     __shared__ float sums[kDzWarps][2][32 * 9];  // a lane's 8 values 9 apart
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -583,25 +607,25 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const __grid_constant
                 const int64_t at = row + k * every < end ? row + k * every : row;
                 load8(a.dout, at * a.dout_stride + c, WIDE ? BSS_DTYPE_F32 : BSS_DTYPE_BF16, d[k]);
                 if (a.pre != nullptr) load8(a.pre, at * a.pre_stride + c, BSS_DTYPE_BF16, z[k]);
+                else z[k][0] = z[k][1] = z[k][2] = z[k][3] = z[k][4] = z[k][5] = z[k][6] = z[k][7] = 0.0f;
             }
 #pragma unroll
             for (int k = 0; k < kRows; ++k) {
                 if (row + k * every >= end) break;
-                if (ACT != BSS_ACT_NONE || a.dgate != nullptr) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float v, s;
-                        activate_both<ACT>(z[k][i], v, s);
-                        dg[i] = fmaf(d[k][i], v, dg[i]);
-                        d[k][i] *= gate[i] * s;
-                        db[i] += d[k][i];
+                for (int i = 0; i < 8; i += 2) {
+                    float2 x = make_float2(d[k][i], d[k][i + 1]), share = f2(1.0f), slope = f2(1.0f);
+                    const float2 at = make_float2(z[k][i], z[k][i + 1]);
+                    if constexpr (ACT != BSS_ACT_NONE) share_and_slope<ACT>(at, share, slope);
+                    if constexpr (GATED) {
+                        const float2 v = __fmul2_rn(at, share);
+                        const float2 s = __ffma2_rn(x, v, make_float2(dg[i], dg[i + 1]));
+                        dg[i] = s.x, dg[i + 1] = s.y;
+                        x = __fmul2_rn(x, make_float2(gate[i], gate[i + 1]));
                     }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        d[k][i] *= gate[i];
-                        db[i] += d[k][i];
-                    }
+                    if constexpr (ACT != BSS_ACT_NONE) x = __fmul2_rn(x, slope);
+                    db[i] += x.x, db[i + 1] += x.y;
+                    d[k][i] = x.x, d[k][i + 1] = x.y;
                 }
                 if (a.dz != nullptr) store8(a.dz, (row + k * every) * a.n + c, BSS_DTYPE_BF16, d[k]);
             }
@@ -895,8 +919,10 @@ template <int ACT>
 bss_status launch_dz(const DzArgs& d, int64_t blocks, cudaStream_t stream) {
     const unsigned columns = static_cast<unsigned>((d.n + 255) / 256);
     const dim3 grid(columns, static_cast<unsigned>(blocks));
-    if (d.dout_dtype == BSS_DTYPE_F32) dz_kernel<ACT, true><<<grid, 32 * kDzWarps, 0, stream>>>(d);
-    else dz_kernel<ACT, false><<<grid, 32 * kDzWarps, 0, stream>>>(d);
+    const bool wide = d.dout_dtype == BSS_DTYPE_F32;
+    auto kernel = d.gate != nullptr ? (wide ? dz_kernel<ACT, true, true> : dz_kernel<ACT, false, true>)
+                                    : (wide ? dz_kernel<ACT, true, false> : dz_kernel<ACT, false, false>);
+    kernel<<<grid, 32 * kDzWarps, 0, stream>>>(d);
     return cuda_check(cudaGetLastError(), "dz launch");
 }
 
