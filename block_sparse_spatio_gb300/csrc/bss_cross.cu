@@ -11,7 +11,10 @@
 //                 other half's two products to work in.  S_0 of the next item follows
 //                 the last S_0 of this one, so the tensor cores do not wait for the
 //                 end of an item.
-//   warps 4..11   softmax, one thread a row.
+//   warps 4..7    bring O / l and lse of a finished half to memory, while
+//   warps 8..15   go on with the softmax of the next item, one thread a row (when they
+//                 stored O themselves an item of 4 key tiles took 16,000 cycles, a third
+//                 of them stores and waits for the last product).
 // TMEM: S_h at 128 h (P_h as bf16 over its first 64 columns), O_h at 256 + 128 h.
 // A row's reference is the maximum of its first tile, moved only when the sum of a
 // later tile's P passes 2^16 (then O and l are rescaled).
@@ -23,15 +26,15 @@
 namespace bss {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kStages = 2;
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kSumLimit = 65536.0f;
-// Registers: 128 x 72 + 256 x 208 = 62,464 of the launch's 384 x 168 = 64,512.
-constexpr uint32_t kRegsControl = 72, kRegsSoftmax = 208;
+// Registers: 128 x (72 + 104 + 2 x 168) = the launch's 512 x 128.
+constexpr uint32_t kRegsControl = 72, kRegsStore = 104, kRegsSoftmax = 168;
 
 struct CrossArgs {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;
     CrossShape s;
     int32_t tiles;  // of 256 rows in a group
     int32_t items;
@@ -48,11 +51,13 @@ struct CrossSmem {
     static constexpr uint32_t kQ = 0;
     static constexpr uint32_t kK = 2 * kTile;
     static constexpr uint32_t kV = kK + kStages * kTile;
-    static constexpr uint32_t kBar = kV + kStages * kTile;
-    // q_full[2] q_empty[2] k_full k_empty v_full v_empty [kStages] s_full[2] p_full[2] o_done[2] cleared
-    static constexpr uint32_t kBars = 4 + 4 * kStages + 7;
+    static constexpr uint32_t kO = kV + kStages * kTile;  // 32 rows of each of the storing warps
+    static constexpr uint32_t kSums = kO + kTile;         // l: float [half][item & 1][128]
+    static constexpr uint32_t kBar = kSums + 2048;
+    // q_full[2] q_empty[2] k_full k_empty v_full v_empty [kStages] s_full[2] p_full[2] o_done[2] o_final[2] o_read[2]
+    // l_full[2][2] cleared
+    static constexpr uint32_t kBars = 4 + 4 * kStages + 15;
     static constexpr uint32_t kBytes = kBar + kBars * 8 + 16;
-    static constexpr uint32_t kAlloc = kBytes + 1024;
 };
 
 struct Item {
@@ -77,8 +82,11 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid_constant__ CrossArgs a) {
     using L = CrossSmem<D>;
     constexpr int kChunks = D / 64;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {  // the swizzled tiles could not be addressed
+        record_status(a.status, BSS_ERR_CUDA);
+        return;
+    }
     uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + L::kBar);
     uint64_t* q_empty = q_full + 2;
     uint64_t* k_full = q_empty + 2;
@@ -88,7 +96,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
     uint64_t* s_full = v_empty + kStages;
     uint64_t* p_full = s_full + 2;
     uint64_t* o_done = p_full + 2;
-    uint64_t* cleared = o_done + 2;
+    uint64_t* o_final = o_done + 2;
+    uint64_t* o_read = o_final + 2;
+    uint64_t* l_full = o_read + 2;
+    uint64_t* cleared = l_full + 4;  // (l_full: by half and item & 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -99,6 +110,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
             mbar_init(s_full + i, 1);
             mbar_init(p_full + i, 128);
             mbar_init(o_done + i, 1);
+            mbar_init(o_final + i, 1);
+            mbar_init(o_read + i, 128);
+            mbar_init(l_full + i, 128);
+            mbar_init(l_full + 2 + i, 128);
         }
         mbar_init(cleared, 32);
         for (int i = 0; i < kStages; ++i) {
@@ -206,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                 }
             };
             uint32_t fills = 0, clears = 0;               // K and V tiles taken
-            uint32_t q_taken[2] = {0, 0}, p_taken[2] = {0, 0};
+            uint32_t q_taken[2] = {0, 0}, p_taken[2] = {0, 0}, items[2] = {0, 0};
             int i = blockIdx.x;
             Item t;
             auto next_item = [&](int from) {  // the first one with keys
@@ -245,9 +260,12 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                     const int left = cur.valid - j * kKeyTile;
                     if (left < w && !(ok = clear_rows<D>(smem + L::kV + st * L::kTile, left, cleared, clears, a.status))) break;
                     if (!(ok = wait(p_full + 0, p_taken[0]++ & 1))) break;
+                    // an item's first product: the O before has been read
+                    if (j == 0 && items[0]++ > 0 && !(ok = wait(o_read + 0, items[0] & 1))) break;
                     tc_fence_after();
                     issue_pv(0, st, w, j > 0);
                     commit(o_done + 0);
+                    if (j == cur.n - 1) commit(o_final + 0);
                     if (j + 1 < cur.n) {
                         const uint32_t f = fills + 1;
                         if (!(ok = wait(k_full + f % kStages, (f / kStages) & 1))) break;
@@ -261,28 +279,93 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                     }
                     if (cur.two) {
                         if (!(ok = wait(p_full + 1, p_taken[1]++ & 1))) break;
+                        if (j == 0 && items[1]++ > 0 && !(ok = wait(o_read + 1, items[1] & 1))) break;
                         tc_fence_after();
                         issue_pv(1, st, w, j > 0);
                         commit(o_done + 1);
+                        if (j == cur.n - 1) commit(o_final + 1);
                     }
                     commit(v_empty + st);
                 }
             }
         }
+    } else if (warp < 8) {
+        setmaxnreg_dec<kRegsStore>();
+        const int w = warp - 4, r = threadIdx.x - 128;
+        const uint32_t lanes = static_cast<uint32_t>(w * 32) << 16;
+        const float* sums = reinterpret_cast<const float*>(smem + L::kSums) + r;
+        uint8_t* mine = smem + L::kO + w * (32 * D * 2);  // 64 columns of 32 rows, 128 bytes a row, twice over for 128
+        uint32_t items[2] = {0, 0};
+        bool ok = true;
+        for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
+            const Item t = item_at(a, i);
+            if (t.rows <= 0) continue;
+#pragma unroll 1
+            for (int h = 0; h < (t.two ? 2 : 1); ++h) {
+                const int row0 = t.row0 + h * kHalfRows + w * 32, rows = t.row0 + t.rows - row0;  // the warp's, in the group
+                const int64_t first = static_cast<int64_t>(t.group) * a.s.group_rows + row0;
+                uint16_t* out = a.O + first * a.O_row + t.head * a.O_head;
+                if (t.n == 0) {  // no states
+                    for (int e = lane; e < 32 * (D / 8); e += 32)
+                        if (e / (D / 8) < rows) *reinterpret_cast<uint4*>(out + e / (D / 8) * a.O_row + e % (D / 8) * 8) = make_uint4(0, 0, 0, 0);
+                    if (a.lse != nullptr && lane < rows) a.lse[static_cast<int64_t>(t.head) * a.s.rows + first + lane] = -INFINITY;
+                    continue;
+                }
+                const uint32_t n = h == 0 ? items[0]++ : items[1]++;
+                if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(l_full + 2 * h + (n & 1), (n >> 1) & 1, a.status)))) break;
+                const float l = sums[(h * 2 + (n & 1)) * 128];
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if (lane == 0) tma_store_wait_read_all();  // the store before has read its rows
+                if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_final + h, n & 1, a.status)))) break;
+                tc_fence_after();
+                const uint32_t t_o = tmem + lanes + kColO + 128 * h;
+#pragma unroll
+                for (int c = 0; c < D; c += 64) {
+                    uint4 u[8];
+                    read_rows<64>(u, t_o + c, inv);
+                    if (c + 64 == D) {
+                        tc_fence_before();
+                        mbar_arrive(o_read + h);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(mine + c * 64 + lane * 128 + ((k ^ (lane & 7)) << 4)) = u[k];
+                }
+                if (rows >= 32) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int c = 0; c < D; c += 64) tma_store_3d(&a.o, mine + c * 64, c, static_cast<int>(first), t.head);
+                        tma_store_commit();
+                    }
+                } else {  // what lies behind the group's last row is another's
+                    __syncwarp();
+                    for (int e = lane; e < 32 * (D / 8); e += 32) {
+                        const int row = e / (D / 8), unit = e % (D / 8);
+                        if (row < rows)
+                            *reinterpret_cast<uint4*>(out + row * a.O_row + unit * 8) =
+                                *reinterpret_cast<const uint4*>(mine + (unit >> 3) * 4096 + row * 128 + (((unit & 7) ^ (row & 7)) << 4));
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) tma_store_wait_read_all();
     } else {
         setmaxnreg_inc<kRegsSoftmax>();
-        const int h = (warp - 4) >> 2;
-        const int r = threadIdx.x - 128 - h * 128;
+        const int h = (warp - 8) >> 2;
+        const int r = threadIdx.x - 256 - h * 128;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t t_s = tmem + lanes + kColS + 128 * h, t_o = tmem + lanes + kColO + 128 * h;
+        float* sums = reinterpret_cast<float*>(smem + L::kSums) + h * 256 + r;
+        uint32_t items = 0;
         const float c = a.s.scale_log2;
         uint32_t steps = 0;  // tiles of this half so far
         bool ok = true;
         for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
             const Item t = item_at(a, i);
-            if (t.rows <= h * kHalfRows) continue;
-            const bool live = h * kHalfRows + r < t.rows;
-            const int64_t row = static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + h * kHalfRows + r;
+            if (t.rows <= h * kHalfRows || t.n == 0) continue;
             float m = 0.0f, l = 0.0f;
             for (int j = 0; j < t.n; ++j, ++steps) {
                 if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(s_full + h, steps & 1, a.status)))) break;
@@ -290,24 +373,31 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                 const int left = t.valid - j * kKeyTile;
                 auto pass = [&](auto masked_tag) -> bool {
                     constexpr bool MASKED = decltype(masked_tag)::value;
-                    uint32_t s[4][32], pk[64];
+                    // 64 columns at a time, twice over for the first tile's maximum
+                    uint32_t pk[64];
+                    auto load = [&](uint32_t (&s)[2][32], int hf) {
+                        BSS_TMEM_LD32(t_s + 64 * hf, s[0]);
+                        BSS_TMEM_LD32(t_s + 64 * hf + 32, s[1]);
+                        tmem_wait_ld();
+                        if constexpr (MASKED) {
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc) BSS_TMEM_LD32(t_s + 32 * cc, s[cc]);
-                    tmem_wait_ld();
-                    if constexpr (MASKED) {
-#pragma unroll
-                        for (int cc = 0; cc < 4; ++cc)
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                if (cc * 32 + x >= left) s[cc][x] = 0xFF800000u;  // minus infinity
-                    }
+                            for (int x = 0; x < 64; ++x)
+                                if (64 * hf + x >= left) s[x >> 5][x & 31] = 0xFF800000u;  // minus infinity
+                        }
+                    };
                     if (j == 0) {
                         float mx[4];
 #pragma unroll
-                        for (int cc = 0; cc < 4; ++cc) {
-                            mx[cc] = __uint_as_float(s[cc][0]);
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t s[2][32];
+                            load(s, hf);
 #pragma unroll
-                            for (int x = 1; x < 32; ++x) mx[cc] = fmaxf(mx[cc], __uint_as_float(s[cc][x]));
+                            for (int q = 0; q < 2; ++q) {
+                                float& top = mx[2 * hf + q];
+                                top = __uint_as_float(s[q][0]);
+#pragma unroll
+                                for (int x = 1; x < 32; ++x) top = fmaxf(top, __uint_as_float(s[q][x]));
+                            }
                         }
                         m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
                     }
@@ -315,16 +405,19 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                     const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-ref, -ref);
                     uint64_t sum_a = 0ull, sum_b = 0ull;
 #pragma unroll
-                    for (int cc = 0; cc < 4; ++cc)
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t s[2][32];
+                        load(s, hf);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
+                        for (int x = 0; x < 32; ++x) {
                             float y0, y1;
-                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[cc][2 * x]), __uint_as_float(s[cc][2 * x + 1])), c2, nm2), y0, y1);
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(s[x >> 4][2 * (x & 15)]), __uint_as_float(s[x >> 4][2 * (x & 15) + 1])), c2, nm2), y0, y1);
                             const float p0 = ex2_approx(y0), p1 = ex2_approx(y1);
                             if (x & 1) sum_b = f2_add(sum_b, f2_pack(p0, p1));
                             else sum_a = f2_add(sum_a, f2_pack(p0, p1));
-                            pk[16 * cc + x] = pack_bf16x2(p0, p1);
+                            pk[32 * hf + x] = pack_bf16x2(p0, p1);
                         }
+                    }
                     float a0, a1, b0, b1;
                     f2_unpack(sum_a, a0, a1);
                     f2_unpack(sum_b, b0, b1);
@@ -387,24 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                 mbar_arrive(p_full + h);
             }
             if (!ok) break;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (t.n > 0) {
-                if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(o_done + h, (steps - 1) & 1, a.status)))) break;
-                tc_fence_after();
-            }
-            const int row_w = t.row0 + h * kHalfRows + (warp & 3) * 32;  // the warp's first row in the group
-            uint16_t* out = a.O + (static_cast<int64_t>(t.group) * a.s.group_rows + row_w) * a.O_row + t.head * a.O_head;
-            if (t.n > 0) {
-                store_rows<D>(t_o, out, a.O_row, t.row0 + t.rows - row_w, inv);
-            } else if (live) {
-                uint4* to = reinterpret_cast<uint4*>(out + lane * a.O_row);
-#pragma unroll
-                for (int u = 0; u < D / 8; ++u) to[u] = make_uint4(0, 0, 0, 0);
-            }
-            if (a.lse != nullptr && live)
-                a.lse[static_cast<int64_t>(t.head) * a.s.rows + row] =
+            // (the buffer before last: its O was read before this item's products began)
+            sums[(items & 1) * 128] = l;
+            mbar_arrive(l_full + 2 * h + (items & 1));
+            ++items;
+            if (a.lse != nullptr && h * kHalfRows + r < t.rows)
+                a.lse[static_cast<int64_t>(t.head) * a.s.rows + static_cast<int64_t>(t.group) * a.s.group_rows + t.row0 + h * kHalfRows + r] =
                     l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-            tc_fence_before();
         }
     }
 
@@ -422,10 +504,10 @@ template <int D>
 bss_status launch_forward(CrossArgs& a, cudaStream_t stream) {
     auto kernel = cross_forward_kernel<D>;
     int blocks;
-    const bss_status st = resident_blocks(reinterpret_cast<const void*>(kernel), kThreads, CrossSmem<D>::kAlloc, &blocks);
+    const bss_status st = resident_blocks(reinterpret_cast<const void*>(kernel), kThreads, CrossSmem<D>::kBytes, &blocks);
     if (st != BSS_OK) return st;
     const int grid = a.items < num_sms() ? a.items : num_sms();
-    kernel<<<static_cast<unsigned>(grid), kThreads, CrossSmem<D>::kAlloc, stream>>>(a);
+    kernel<<<static_cast<unsigned>(grid), kThreads, CrossSmem<D>::kBytes, stream>>>(a);
     return cuda_check(cudaGetLastError(), "cross attention launch");
 }
 
@@ -560,6 +642,7 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream) 
     CrossArgs a;
     memset(&a, 0, sizeof(a));
     if ((st = row_heads_map(&a.q, p.q, p.rows, p.heads, p.head_dim, kHalfRows)) != BSS_OK ||
+        (st = row_heads_map(&a.o, p.O, p.rows, p.heads, p.head_dim, 32)) != BSS_OK ||
         (st = states_map(&a.k, p.k, groups, p.keys, p.kv_heads, p.head_dim, kKeyTile)) != BSS_OK ||
         (st = states_map(&a.v, p.v, groups, p.keys, p.kv_heads, p.head_dim, kKeyTile)) != BSS_OK)
         return st;

@@ -86,8 +86,10 @@ __device__ __forceinline__ void read_rows(uint4 (&u)[COLS / 8], uint32_t at, flo
         for (int i = 0; i < 4; ++i) {
             uint32_t w[4];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                w[x] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * x]) * factor, __uint_as_float(o[8 * i + 2 * x + 1]) * factor);
+            for (int x = 0; x < 4; ++x) {
+                const float2 y = __fmul2_rn(make_float2(__uint_as_float(o[8 * i + 2 * x]), __uint_as_float(o[8 * i + 2 * x + 1])), f2(factor));
+                w[x] = pack_bf16x2(y.x, y.y);
+            }
             u[4 * c + i] = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
