@@ -30,8 +30,8 @@ constexpr int kThreads = 512;
 constexpr int kStages = 2;
 constexpr uint32_t kColS = 0, kColO = 256, kTmemCols = 512;
 constexpr float kSumLimit = 65536.0f;
-// Registers: 128 x (72 + 104 + 2 x 168) = the launch's 512 x 128.
-constexpr uint32_t kRegsControl = 72, kRegsStore = 104, kRegsSoftmax = 168;
+// Registers: 128 x (64 + 96 + 2 x 176) = the launch's 512 x 128.
+constexpr uint32_t kRegsControl = 64, kRegsStore = 96, kRegsSoftmax = 176;
 
 struct CrossArgs {
     CUtensorMap q, k, v, o;
@@ -211,13 +211,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
             };
             auto issue_pv = [&](int h, uint32_t st, int w, bool add) {
                 const uint32_t o = tmem + kColO + 128 * h, p = tmem + kColS + 128 * h, b = dv + st * kTileStep;
-                if (w == kKeyTile) {  // unrolled: a loop takes 110 cycles a product of 16 keys, which lasts 64
-                    if (leader) {
+                if (leader) {  // unrolled: a loop takes 110 cycles a product of 16 keys, which lasts 64
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk) umma_ts(o, p + kk * 8, desc_of(b + kk * 128), idesc_pv, add || kk > 0);
-                    }
-                } else if (leader) {
-                    for (int kk = 0; kk < w / 16; ++kk) umma_ts(o, p + kk * 8, desc_of(b + kk * 128), idesc_pv, add || kk > 0);
+                    for (int kk = 0; kk < 8; ++kk)
+                        if (kk * 16 < w) umma_ts(o, p + kk * 8, desc_of(b + kk * 128), idesc_pv, add || kk > 0);
                 }
             };
             uint32_t fills = 0, clears = 0;               // K and V tiles taken
@@ -258,7 +255,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                     commit(k_empty + st);  // both halves' S
                     if (!(ok = wait(v_full + st, parity))) break;
                     const int left = cur.valid - j * kKeyTile;
-                    if (left < w && !(ok = clear_rows<D>(smem + L::kV + st * L::kTile, left, cleared, clears, a.status))) break;
+                    // (behind the last state of all a load gives zeros)
+                    if (left < w && cur.valid < a.s.keys && !(ok = clear_rows<D>(smem + L::kV + st * L::kTile, left, cleared, clears, a.status))) break;
                     if (!(ok = wait(p_full + 0, p_taken[0]++ & 1))) break;
                     // an item's first product: the O before has been read
                     if (j == 0 && items[0]++ > 0 && !(ok = wait(o_read + 0, items[0] & 1))) break;
@@ -381,8 +379,14 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                         tmem_wait_ld();
                         if constexpr (MASKED) {
 #pragma unroll
-                            for (int x = 0; x < 64; ++x)
-                                if (64 * hf + x >= left) s[x >> 5][x & 31] = 0xFF800000u;  // minus infinity
+                            for (int q = 0; q < 2; ++q) {
+                                const int valid = left - 64 * hf - 32 * q;
+                                if (valid < 32) {
+#pragma unroll
+                                    for (int x = 0; x < 32; ++x)
+                                        if (x >= valid) s[q][x] = 0xFF800000u;  // minus infinity
+                                }
+                            }
                         }
                     };
                     if (j == 0) {

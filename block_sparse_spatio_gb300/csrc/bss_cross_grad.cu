@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_kernel(const __grid_co
                 if (j == 0 && !wait(q_full, item & 1)) return false;
                 if (!wait(k_full + st, (f / kKStages) & 1)) return false;
                 const int w = width(it, j), left = it.valid - j * kKeyTile;
-                if (left < w && !clear_rows<D>(smem + L::kK + st * L::kTile, left, cleared, clears, a.status)) return false;
+                if (left < w && it.valid < a.s.keys && !clear_rows<D>(smem + L::kK + st * L::kTile, left, cleared, clears, a.status)) return false;
                 if (f > 0 && !wait(s_read, (f - 1) & 1)) return false;
                 tc_fence_after();
                 product(kColS, d_q, d_k + st * kTileStep, w);
@@ -795,13 +795,15 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
             uint32_t part = 0, clears = 0;
             int x = p.first;
             tile.begin(a, p);
+            // behind the last row of all a load gives zeros; behind another group's there are rows
+            auto last_rows = [&]() { return p.group == a.s.groups - 1; };
             auto rows_now = [&]() { return p.rows - tile.row0 < 128 ? p.rows - tile.row0 : 128; };
             auto issue_s = [&](uint32_t f) {
                 const uint32_t st = f % kQStages;
                 if (x == p.first && !wait(k_full, part & 1)) return false;
                 if (!wait(q_full + st, (f / kQStages) & 1)) return false;
                 const int n = rows_now();
-                if ((n & 15) && !clear_rows<D>(smem + L::kQ + st * L::kTile, n, cleared, clears, a.status)) return false;
+                if ((n & 15) && !last_rows() && !clear_rows<D>(smem + L::kQ + st * L::kTile, n, cleared, clears, a.status)) return false;
                 tc_fence_after();
                 product(kColS, d_k, d_q + st * kTileStep, (n + 15) & ~15);
                 commit(s_full);
@@ -813,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 if (x == p.first && !wait(v_full, part & 1)) return false;
                 if (!wait(do_full + st, (f / kDOStages) & 1)) return false;
                 const int n = rows_now();
-                if ((n & 15) && !clear_rows<D>(smem + L::kDO + st * L::kTile, n, cleared, clears, a.status)) return false;
+                if ((n & 15) && !last_rows() && !clear_rows<D>(smem + L::kDO + st * L::kTile, n, cleared, clears, a.status)) return false;
                 tc_fence_after();
                 product(kColP, d_v, d_do + st * kTileStep, (n + 15) & ~15);
                 commit(dp_full);
