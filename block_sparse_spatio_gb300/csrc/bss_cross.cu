@@ -643,6 +643,8 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream) 
     if ((st = check_outputs(t, 6)) != BSS_OK) return st;
     if ((p.k.group_stride == 0) != (p.v.group_stride == 0) && groups > 1)
         return set_error(BSS_ERR_UNSUPPORTED, "k and v must both be shared by the groups, or neither");
+    const int64_t tiles = (p.rows_per_group + 255) / 256, items = groups * tiles * p.heads;
+    if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
     CrossArgs a;
     memset(&a, 0, sizeof(a));
     if ((st = row_heads_map(&a.q, p.q, p.rows, p.heads, p.head_dim, kHalfRows)) != BSS_OK ||
@@ -652,9 +654,7 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream) 
         return st;
     a.s = cross_shape(p.rows, p.rows_per_group, p.heads, p.kv_heads, p.head_dim, p.keys, p.softmax_scale, p.lengths,
                       p.k.group_stride);
-    a.tiles = static_cast<int32_t>((p.rows_per_group + 255) / 256);
-    const int64_t items = groups * a.tiles * p.heads;
-    if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
+    a.tiles = static_cast<int32_t>(tiles);
     a.items = static_cast<int32_t>(items);
     a.by_tiles = FastDiv(static_cast<uint32_t>(a.tiles));
     a.O = static_cast<uint16_t*>(p.O.data);

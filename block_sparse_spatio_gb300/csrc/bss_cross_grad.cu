@@ -1146,6 +1146,8 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
         return st;
     if (groups > 1 && (p.k.group_stride == 0 || p.v.group_stride == 0))
         return set_error(BSS_ERR_UNSUPPORTED, "gradients of states shared by several groups: give one group");
+    const int64_t items = groups * plan.tiles * p.heads;
+    if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
     GradArgs a;
     memset(&a, 0, sizeof(a));
     if ((st = row_heads_map(&a.q, p.q, p.rows, p.heads, p.head_dim, kHalfRows)) != BSS_OK ||
@@ -1156,8 +1158,6 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
     a.s = cross_shape(p.rows, p.rows_per_group, p.heads, p.kv_heads, p.head_dim, p.keys, p.softmax_scale, p.lengths,
                       p.k.group_stride);
     a.tiles = plan.tiles, a.key_tiles = plan.key_tiles, a.blocks = plan.blocks;
-    const int64_t items = groups * plan.tiles * p.heads;
-    if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
     a.items = static_cast<int32_t>(items);
     a.by_tiles = FastDiv(static_cast<uint32_t>(plan.tiles));
     a.O = static_cast<const uint16_t*>(p.O.data);
