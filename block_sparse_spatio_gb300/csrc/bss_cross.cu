@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    cudaGridDependencySynchronize();
 
     if (warp < 4) {
         setmaxnreg_dec<kRegsControl>();
@@ -511,8 +512,8 @@ bss_status launch_forward(CrossArgs& a, cudaStream_t stream) {
     const bss_status st = resident_blocks(reinterpret_cast<const void*>(kernel), kThreads, CrossSmem<D>::kBytes, &blocks);
     if (st != BSS_OK) return st;
     const int grid = a.items < num_sms() ? a.items : num_sms();
-    kernel<<<static_cast<unsigned>(grid), kThreads, CrossSmem<D>::kBytes, stream>>>(a);
-    return cuda_check(cudaGetLastError(), "cross attention launch");
+    return launch_behind_with(kernel, dim3(static_cast<unsigned>(grid)), kThreads, CrossSmem<D>::kBytes, 1, stream,
+                              "cross attention launch", a);
 }
 
 }  // namespace

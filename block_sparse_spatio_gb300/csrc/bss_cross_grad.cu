@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_kernel(const __grid_co
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    cudaGridDependencySynchronize();
 
     if (warp < 4) {
         setmaxnreg_dec<kDqRegsControl>();
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     uint64_t* cleared = sums + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cleared + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    cudaGridDependencySynchronize();
     Share share = share_of(a, blockIdx.x);
     Part p;
     if (!next_part(a, share, p)) return;
@@ -1002,6 +1004,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
 // order.  Key tiles without a valid state: zeros.
 template <int D>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ GradArgs a) {
+    cudaGridDependencySynchronize();
     const int64_t total = a.starts[a.s.groups];
     const Share share = share_of(a, blockIdx.x);
     const int teams = teams_of(a, total, share.tiles);
@@ -1065,12 +1068,13 @@ bss_status launch_backward(GradArgs& a, cudaStream_t stream) {
     if (st == BSS_OK) st = resident_blocks(reinterpret_cast<const void*>(dkv), kThreads, DkvSmem<D>::kBytes, &blocks);
     if (st != BSS_OK) return st;
     const int grid = a.items < num_sms() ? a.items : num_sms();
-    dq<<<static_cast<unsigned>(grid), kDqThreads, DqSmem<D>::kBytes, stream>>>(a);
-    if ((st = cuda_check(cudaGetLastError(), "query gradient launch")) != BSS_OK) return st;
-    dkv<<<static_cast<unsigned>(a.blocks), kThreads, DkvSmem<D>::kBytes, stream>>>(a);
-    if ((st = cuda_check(cudaGetLastError(), "key gradient launch")) != BSS_OK) return st;
-    cross_join_kernel<D><<<dim3(static_cast<unsigned>(a.blocks), 8), 256, 0, stream>>>(a);
-    return cuda_check(cudaGetLastError(), "key gradient sums launch");
+    st = launch_behind_with(dq, dim3(static_cast<unsigned>(grid)), kDqThreads, DqSmem<D>::kBytes, 1, stream, "query gradient launch", a);
+    if (st == BSS_OK)
+        st = launch_behind_with(dkv, dim3(static_cast<unsigned>(a.blocks)), kThreads, DkvSmem<D>::kBytes, 1, stream, "key gradient launch", a);
+    if (st == BSS_OK)
+        st = launch_behind_with(cross_join_kernel<D>, dim3(static_cast<unsigned>(a.blocks), 8), 256, 0, 1, stream,
+                                "key gradient sums launch", a);
+    return st;
 }
 
 int64_t aligned_up(int64_t v) { return (v + 255) / 256 * 256; }

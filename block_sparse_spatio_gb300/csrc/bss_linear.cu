@@ -127,7 +127,7 @@ struct Epilogue {
 };
 
 struct GemmArgs {
-    CUtensorMap a, b, out, pre;
+    CUtensorMap a, b, out, pre, residual;
     int32_t m, n, kblocks;
     int32_t tiles_n, tiles, splits;  // of the contraction: split i takes the planes' sums i
     int* status;
@@ -142,7 +142,8 @@ __device__ __forceinline__ int split_begin(const GemmArgs& g, int split) {
 struct GemmSmem {
     static constexpr uint32_t kPieces = kStages * 2 * kOperand;
     static constexpr uint32_t kBars = kPieces + kEpilogueWarps * 2 * kPiece;
-    static constexpr uint32_t kBytes = kBars + (2 * kStages + 4) * 8 + 16;
+    // full, empty [kStages], accumulators full, empty [2], residual [kEpilogueWarps][2]
+    static constexpr uint32_t kBytes = kBars + (2 * kStages + 4 + 2 * kEpilogueWarps) * 8 + 16;
     static constexpr uint32_t kAlloc = kBytes + 1024;  // the operands start on 1024 bytes
 };
 
@@ -189,6 +190,24 @@ __device__ __forceinline__ void put8_float(uint8_t* row, int unit, const float (
             make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
 }
 
+__device__ __forceinline__ void get8(const uint8_t* row, int unit, float (&v)[8]) {
+    const uint4 q = *reinterpret_cast<const uint4*>(row + ((unit ^ (threadIdx.x & 7)) << 4));
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ void get8_float(const uint8_t* row, int unit, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 q = *reinterpret_cast<const float4*>(row + (((unit + i) ^ (threadIdx.x & 7)) << 4));
+        v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+    }
+}
+
 // z -> out, for 8 columns of a row; the residual's values are there already.
 template <int ACT>
 __device__ __forceinline__ void finish8(const Epilogue& e, int64_t group, int col, float (&v)[8], const float (&r)[8]) {
@@ -214,7 +233,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     uint64_t* empty = full + kStages;
     uint64_t* acc_full = empty + kStages;
     uint64_t* acc_empty = acc_full + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    uint64_t* arrived = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(arrived + 2 * kEpilogueWarps);
     constexpr int kTile = 128 * CG;
     constexpr uint32_t kAccCols = 128 * CG;  // a CTA's accumulator: its 128 rows, the tile's columns
 
@@ -231,6 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             mbar_init(acc_full + i, 1);
             mbar_init(acc_empty + i, kEpilogueWarps * CG);
         }
+        for (int i = 0; i < 2 * kEpilogueWarps; ++i) mbar_init(arrived + i, 1);
         mbar_fence_init();
     }
     if (warp == 1) {
@@ -242,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    cudaGridDependencySynchronize();
 
     if (warp == 0) {
         if (lane == 0) {
@@ -334,17 +356,26 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         uint8_t* pieces = smem + L::kPieces + (warp - 4) * 2 * kPiece;
         const Epilogue& e = g.e;
-        const bool wide = e.out_dtype == BSS_DTYPE_F32;
-        uint32_t n_tile = 0, stores = 0;
-        // The piece to be written next.  With pre it has the first one and out the second,
-        // else out's take turns; the store that read it last must have done so.
-        auto piece = [&](int which) -> uint8_t* {
+        const bool wide = e.out_dtype == BSS_DTYPE_F32, staged_pre = e.pre != nullptr && !wide, adds = e.residual != nullptr;
+        const int width = wide ? 32 : 64, begin_c = side * (kTile / 2), end_c = begin_c + kTile / 2;
+        const int units = g.tiles * g.splits;
+        // Where a piece's columns lie; false past the tensor's ends.
+        auto place = [&](int u, int c, int& col, int& row0) {
+            const int t = u % g.tiles, mt = t / g.tiles_n;
+            col = (t - mt * g.tiles_n) * kTile + c;
+            row0 = mt * kTile + static_cast<int>(rank) * 128 + quarter * 32;
+            return col < g.n && row0 < g.m;
+        };
+        uint32_t n_tile = 0, chunk = 0, taken[2] = {0, 0}, asked[2] = {0, 0};
+        // out's pieces take turns; with pre it has the first one and out the second.  The
+        // store that read a piece last must have done so before it is written again.
+        auto piece_of = [&](uint32_t i) { return staged_pre ? 1u : i & 1; };
+        auto free_piece = [&]() {
             if (lane == 0) {
-                if (e.pre != nullptr) tma_store_wait_read<0>();
+                if (staged_pre) tma_store_wait_read<0>();
                 else tma_store_wait_read<1>();
             }
             __syncwarp();
-            return pieces + (e.pre != nullptr ? which : static_cast<int>(stores++ & 1)) * kPiece;
         };
         auto send = [&](const CUtensorMap* map, const uint8_t* from, int col, int row0, int plane) {
             fence_proxy_async_smem();
@@ -354,56 +385,79 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 tma_store_commit();
             }
         };
-        for (int u = first; u < g.tiles * g.splits; u += step, ++n_tile) {
-            const int split = u / g.tiles, t = u - split * g.tiles;
-            const int mt = t / g.tiles_n, nt = t - mt * g.tiles_n;
+        // The residual comes into the piece that its sum leaves from, a piece ahead.
+        auto ask = [&](int u, int c) {
+            int col, row0;
+            while (u < units && (c >= end_c || !place(u, c, col, row0))) u += step, c = begin_c;
+            if (u >= units) return;
+            const uint32_t p = piece_of(chunk);
+            if (lane == 0) {
+                mbar_arrive_expect_tx(arrived + (warp - 4) * 2 + p, kPiece);
+                tma_load_3d(pieces + p * kPiece, &g.residual, col, row0, 0, arrived + (warp - 4) * 2 + p);
+            }
+            if (p == 0) ++asked[0];
+            else ++asked[1];
+        };
+        if (adds) ask(first, begin_c);
+        bool ok = true;
+        for (int u = first; ok && u < units; u += step, ++n_tile) {
             const uint32_t buf = n_tile & 1;
-            const int row0 = mt * kTile + static_cast<int>(rank) * 128 + quarter * 32, row = row0 + lane;
-            const bool live = row < g.m;
-            const int64_t group = e.gate != nullptr && live ? e.by_rows.div(row) : 0;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait(acc_full + buf, (n_tile / 2) & 1, g.status))) break;
+            int col0, row0;
+            place(u, begin_c, col0, row0);
+            const int split = u / g.tiles, row = row0 + lane;
+            const int64_t group = e.gate != nullptr && row < g.m ? e.by_rows.div(row) : 0;
+            if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_full + buf, (n_tile / 2) & 1, g.status)))) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = side * (kTile / 2); c < (side + 1) * (kTile / 2); c += 64) {
-                const int col0 = nt * kTile + c;
-                if (col0 >= g.n || row0 >= g.m) break;
-                uint8_t *to_pre = nullptr, *to = nullptr;
-                if (e.pre != nullptr) to_pre = piece(0) + lane * 128;
+            for (int c = begin_c; c < end_c; c += width) {
+                if (!place(u, c, col0, row0)) break;
+                const uint32_t p = piece_of(chunk);
+                uint8_t* to = pieces + p * kPiece + lane * 128;
+                if (adds) {
+                    const uint32_t n = p == 0 ? taken[0]++ : taken[1]++;
+                    if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(arrived + (warp - 4) * 2 + p, n & 1, g.status)))) break;
+                } else {
+                    free_piece();
+                }
+                ++chunk;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int col = col0 + 32 * h;
-                    if (h == 1 && col >= g.n) break;
-                    float r[4][8];
-                    if (e.residual != nullptr && live) {
-#pragma unroll
-                        for (int u = 0; u < 4; ++u)
-                            if (col + 8 * u < g.n) load8(e.residual, row * e.residual_stride + col + 8 * u, e.out_dtype, r[u]);
-                    }
+                    if (h == 1 && (wide || col >= g.n)) break;
                     uint32_t x[32];
                     BSS_TMEM_LD32(tmem + lanes + buf * kAccCols + c + 32 * h, x);
                     tmem_wait_ld();
-                    if (h == 0 || wide) to = piece(1) + lane * 128;
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        if (col + 8 * u >= g.n) break;
-                        float v[8];
+                    for (int k = 0; k < 4; ++k) {
+                        if (col + 8 * k >= g.n) break;
+                        float v[8], r[8] = {};
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[8 * u + i]);
+                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[8 * k + i]);
                         if (e.bias != nullptr) {
                             float w[8];
-                            load_param8(e.bias, col + 8 * u, e.param_dtype, w);
+                            load_param8(e.bias, col + 8 * k, e.param_dtype, w);
 #pragma unroll
                             for (int i = 0; i < 8; ++i) v[i] += w[i];
                         }
-                        if (e.pre != nullptr) put8(to_pre, 4 * h + u, v);
-                        finish8<ACT>(e, group, col + 8 * u, v, r[u]);
-                        if (wide) put8_float(to, 2 * u, v);
-                        else put8(to, 4 * h + u, v);
+                        if (e.pre != nullptr) {
+                            if (staged_pre) put8(pieces + lane * 128, 4 * h + k, v);
+                            else if (row < g.m) store8(e.pre, row * e.pre_stride + col + 8 * k, BSS_DTYPE_BF16, v);
+                        }
+                        if (adds) {
+                            if (wide) get8_float(to, 2 * k, r);
+                            else get8(to, 4 * h + k, r);
+                        }
+                        finish8<ACT>(e, group, col + 8 * k, v, r);
+                        if (wide) put8_float(to, 2 * k, v);
+                        else put8(to, 4 * h + k, v);
                     }
-                    if (wide) send(&g.out, to - lane * 128, col, row0, split);
                 }
-                if (!wide) send(&g.out, to - lane * 128, col0, row0, split);
-                if (e.pre != nullptr) send(&g.pre, to_pre - lane * 128, col0, row0, 0);
+                send(&g.out, to - lane * 128, col0, row0, split);
+                if (staged_pre) send(&g.pre, pieces, col0, row0, 0);
+                if (adds) {
+                    free_piece();
+                    ask(u, c + width);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -412,7 +466,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 else mbar_arrive(acc_empty + buf);
             }
         }
-        if (lane == 0) tma_store_wait_read_all();  // the pieces are read before the CTA ends
+        if (lane == 0) {
+            // no copy may still be landing, the pieces are read before the CTA ends
+            for (int p = 0; p < 2; ++p)
+                if (asked[p] > taken[p]) mbar_wait(arrived + (warp - 4) * 2 + p, (asked[p] - 1) & 1, g.status);
+            tma_store_wait_read_all();
+        }
     }
 
     tc_fence_before();
@@ -496,6 +555,7 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
     const __nv_bfloat16* w0 = a.weight + (o0 + g) * a.weight_stride + c;
     const __nv_bfloat16* w1 = w0 + 8 * a.weight_stride;
     const bool both = o0 + 8 < a.outer;
+    cudaGridDependencySynchronize();
     float d[NT][4] = {};
     constexpr int kBatch = NT == 1 ? 8 : 4;  // blocks of 32 channels in flight
     const int blocks = (a.inner + 31) / 32, begin = blocks * warp / kFewWarps, end = blocks * (warp + 1) / kFewWarps;
@@ -586,6 +646,7 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const __grid_constant
         if (end > a.rows) end = a.rows;
     }
     const int64_t last_group = (blockIdx.y + 1) * a.units;  // small groups
+    cudaGridDependencySynchronize();
     float db[8] = {}, dg[8] = {}, gate[8];
     while (true) {
         if (small) {
@@ -727,18 +788,8 @@ bss_status launch_gemm(GemmArgs& g, cudaStream_t stream) {
     if (st != BSS_OK) return st;
     int units = num_sms() / CG;
     if (units > g.tiles * g.splits) units = g.tiles * g.splits;
-    cudaLaunchConfig_t config = {};
-    config.gridDim = dim3(static_cast<unsigned>(units * CG));
-    config.blockDim = dim3(kThreads);
-    config.dynamicSmemBytes = GemmSmem::kAlloc;
-    config.stream = stream;
-    cudaLaunchAttribute attribute = {};
-    attribute.id = cudaLaunchAttributeClusterDimension;
-    attribute.val.clusterDim.x = CG;
-    attribute.val.clusterDim.y = attribute.val.clusterDim.z = 1;
-    config.attrs = &attribute;
-    config.numAttrs = CG == 2 ? 1 : 0;
-    return cuda_check(cudaLaunchKernelEx(&config, kernel, g), "matrix product launch");
+    return launch_behind_with(kernel, dim3(static_cast<unsigned>(units * CG)), kThreads, GemmSmem::kAlloc, CG, stream,
+                              "matrix product launch", g);
 }
 
 template <int ACT>
@@ -779,7 +830,9 @@ bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride
     } else {
         g.e = e;
         st = encode_tmap_rows(&g.out, e.out, e.out_dtype, n, m, e.out_stride * element_size(e.out_dtype), 32);
-        if (st == BSS_OK && e.pre != nullptr) st = encode_tmap_rows(&g.pre, e.pre, BSS_DTYPE_BF16, n, m, e.pre_stride * 2, 32);
+        if (st == BSS_OK && e.residual != nullptr)
+            st = encode_tmap_rows(&g.residual, e.residual, e.out_dtype, n, m, e.residual_stride * element_size(e.out_dtype), 32);
+        if (st == BSS_OK && e.pre != nullptr && e.out_dtype == BSS_DTYPE_BF16) st = encode_tmap_rows(&g.pre, e.pre, BSS_DTYPE_BF16, n, m, e.pre_stride * 2, 32);
     }
     if (st != BSS_OK) return st;
     if constexpr (A_MN || B_MN)
@@ -799,9 +852,8 @@ bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride
 template <int ACT>
 bss_status launch_few(const FewArgs& f, cudaStream_t stream) {
     const unsigned blocks = static_cast<unsigned>((f.outer + 15) / 16);
-    if (f.rows <= 8) few_rows_kernel<1, ACT><<<blocks, 32 * kFewWarps, 0, stream>>>(f);
-    else few_rows_kernel<2, ACT><<<blocks, 32 * kFewWarps, 0, stream>>>(f);
-    return cuda_check(cudaGetLastError(), "few rows launch");
+    return launch_behind(f.rows <= 8 ? few_rows_kernel<1, ACT> : few_rows_kernel<2, ACT>, dim3(blocks), 32 * kFewWarps, stream,
+                         "few rows launch", f);
 }
 
 bss_status check_sizes(int64_t rows, int64_t* rows_per_group, int32_t in, int32_t out, int32_t activation) {
@@ -922,8 +974,7 @@ bss_status launch_dz(const DzArgs& d, int64_t blocks, cudaStream_t stream) {
     const bool wide = d.dout_dtype == BSS_DTYPE_F32;
     auto kernel = d.gate != nullptr ? (wide ? dz_kernel<ACT, true, true> : dz_kernel<ACT, false, true>)
                                     : (wide ? dz_kernel<ACT, true, false> : dz_kernel<ACT, false, false>);
-    kernel<<<grid, 32 * kDzWarps, 0, stream>>>(d);
-    return cuda_check(cudaGetLastError(), "dz launch");
+    return launch_behind(kernel, grid, 32 * kDzWarps, stream, "dz launch", d);
 }
 
 }  // namespace

@@ -203,20 +203,31 @@ struct FastDiv {
 // ---------------------------------------------------------------- host side
 // A kernel launched behind another one of the same stream, its launch overlapping
 // that one's end: it calls cudaGridDependencySynchronize() before it reads what
-// the other wrote.
+// the other wrote, or writes anything.  With this much dynamic shared memory, in
+// clusters of so many blocks.
 template <typename... Params, typename... Args>
-bss_status launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, const char* what,
-                         Args... args) {
+bss_status launch_behind_with(void (*kernel)(Params...), dim3 grid, int threads, int smem, int cluster, cudaStream_t stream,
+                              const char* what, const Args&... args) {
     cudaLaunchConfig_t config = {};
     config.gridDim = grid;
     config.blockDim = dim3(static_cast<unsigned>(threads));
+    config.dynamicSmemBytes = static_cast<size_t>(smem);
     config.stream = stream;
-    cudaLaunchAttribute attribute = {};
-    attribute.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attribute.val.programmaticStreamSerializationAllowed = 1;
-    config.attrs = &attribute;
-    config.numAttrs = 1;
+    cudaLaunchAttribute attributes[2] = {};
+    attributes[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attributes[0].val.programmaticStreamSerializationAllowed = 1;
+    attributes[1].id = cudaLaunchAttributeClusterDimension;
+    attributes[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attributes[1].val.clusterDim.y = attributes[1].val.clusterDim.z = 1;
+    config.attrs = attributes;
+    config.numAttrs = cluster > 1 ? 2 : 1;
     return cuda_check(cudaLaunchKernelEx(&config, kernel, static_cast<Params>(args)...), what);
+}
+
+template <typename... Params, typename... Args>
+bss_status launch_behind(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, const char* what,
+                         Args... args) {
+    return launch_behind_with(kernel, grid, threads, 0, 1, stream, what, args...);
 }
 
 }  // namespace bss
