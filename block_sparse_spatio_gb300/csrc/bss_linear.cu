@@ -177,34 +177,62 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int dtype, f
     }
 }
 
-// 8 values of a row into a piece: its 16-byte units are swizzled like the TMA's.
-__device__ __forceinline__ void put8(uint8_t* row, int unit, const float (&v)[8]) {
-    *reinterpret_cast<uint4*>(row + ((unit ^ (threadIdx.x & 7)) << 4)) =
-        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+// 32 values of a lane's row in a piece: its 16-byte units are swizzled like the TMA's.
+__device__ __forceinline__ uint8_t* unit_at(uint8_t* row, int unit) { return row + ((unit ^ (threadIdx.x & 7)) << 4); }
+
+__device__ __forceinline__ void put32(uint8_t* row, int unit, const float2 (&v)[16]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4*>(unit_at(row, unit + k)) =
+            make_uint4(pack2(v[4 * k].x, v[4 * k].y), pack2(v[4 * k + 1].x, v[4 * k + 1].y), pack2(v[4 * k + 2].x, v[4 * k + 2].y),
+                       pack2(v[4 * k + 3].x, v[4 * k + 3].y));
 }
 
-__device__ __forceinline__ void put8_float(uint8_t* row, int unit, const float (&v)[8]) {
+__device__ __forceinline__ void put32_float(uint8_t* row, const float2 (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<float4*>(row + (((unit + i) ^ (threadIdx.x & 7)) << 4)) =
-            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<float4*>(unit_at(row, k)) = make_float4(v[2 * k].x, v[2 * k].y, v[2 * k + 1].x, v[2 * k + 1].y);
 }
 
-__device__ __forceinline__ void get8(const uint8_t* row, int unit, float (&v)[8]) {
-    const uint4 q = *reinterpret_cast<const uint4*>(row + ((unit ^ (threadIdx.x & 7)) << 4));
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void get32(uint8_t* row, int unit, float2 (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    for (int k = 0; k < 4; ++k) {
+        const uint4 q = *reinterpret_cast<const uint4*>(unit_at(row, unit + k));
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * k + i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
     }
 }
 
-__device__ __forceinline__ void get8_float(const uint8_t* row, int unit, float (&v)[8]) {
+__device__ __forceinline__ void get32_float(uint8_t* row, float2 (&v)[16]) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const float4 q = *reinterpret_cast<const float4*>(row + (((unit + i) ^ (threadIdx.x & 7)) << 4));
-        v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+    for (int k = 0; k < 8; ++k) {
+        const float4 q = *reinterpret_cast<const float4*>(unit_at(row, k));
+        v[2 * k] = make_float2(q.x, q.y), v[2 * k + 1] = make_float2(q.z, q.w);
+    }
+}
+
+// A row's 32 parameters from a column on (NULL: all the same value).
+__device__ __forceinline__ void load_params32(const void* base, int64_t at, int col, int n, int dtype, float none, float2 (&v)[16]) {
+    if (base == nullptr) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = f2(none);
+    } else if (dtype == BSS_DTYPE_F32) {
+        const float* p = static_cast<const float*>(base) + at;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float4 q = __ldg(reinterpret_cast<const float4*>(p + min(col + 4 * k, n - 4)));
+            v[2 * k] = make_float2(q.x, q.y), v[2 * k + 1] = make_float2(q.z, q.w);
+        }
+    } else {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(base) + at;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint4 q = __ldg(reinterpret_cast<const uint4*>(p + min(col + 8 * k, n - 8)));
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[4 * k + i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+        }
     }
 }
 
@@ -236,6 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     uint64_t* arrived = acc_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(arrived + 2 * kEpilogueWarps);
     constexpr int kTile = 128 * CG;
+    constexpr bool kPlain = A_MN || B_MN;    // a gradient: nothing behind the product
     constexpr uint32_t kAccCols = 128 * CG;  // a CTA's accumulator: its 128 rows, the tile's columns
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -422,35 +451,51 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 ++chunk;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && wide) break;
                     const int col = col0 + 32 * h;
-                    if (h == 1 && (wide || col >= g.n)) break;
+                    // Everything is loaded before anything is computed, without a branch in
+                    // between (with one for every 8 columns a tile's epilogue took 20,000
+                    // cycles).  Columns past the end take the last ones' parameters; the
+                    // stores clip them.
+                    float2 bias[16], gate[16];
+                    if constexpr (!kPlain) {
+                        load_params32(e.bias, 0, col, g.n, e.param_dtype, 0.0f, bias);
+                        load_params32(e.gate, group * e.gate_stride, col, g.n, e.param_dtype, 1.0f, gate);
+                    }
                     uint32_t x[32];
                     BSS_TMEM_LD32(tmem + lanes + buf * kAccCols + c + 32 * h, x);
                     tmem_wait_ld();
+                    float2 v[16];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (col + 8 * k >= g.n) break;
-                        float v[8], r[8] = {};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(x[8 * k + i]);
-                        if (e.bias != nullptr) {
-                            float w[8];
-                            load_param8(e.bias, col + 8 * k, e.param_dtype, w);
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) v[i] += w[i];
-                        }
-                        if (e.pre != nullptr) {
-                            if (staged_pre) put8(pieces + lane * 128, 4 * h + k, v);
-                            else if (row < g.m) store8(e.pre, row * e.pre_stride + col + 8 * k, BSS_DTYPE_BF16, v);
-                        }
-                        if (adds) {
-                            if (wide) get8_float(to, 2 * k, r);
-                            else get8(to, 4 * h + k, r);
-                        }
-                        finish8<ACT>(e, group, col + 8 * k, v, r);
-                        if (wide) put8_float(to, 2 * k, v);
-                        else put8(to, 4 * h + k, v);
+                    for (int i = 0; i < 16; ++i) {
+                        v[i] = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+                        if constexpr (!kPlain) v[i] = __fadd2_rn(v[i], bias[i]);
                     }
+                    if constexpr (!kPlain) {
+                        if (e.pre != nullptr) {
+                            if (staged_pre) {
+                                put32(pieces + lane * 128, 4 * h, v);
+                            } else if (row < g.m) {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (col + 8 * k < g.n)
+                                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(e.pre) + row * e.pre_stride + col + 8 * k) =
+                                            make_uint4(pack2(v[4 * k].x, v[4 * k].y), pack2(v[4 * k + 1].x, v[4 * k + 1].y),
+                                                       pack2(v[4 * k + 2].x, v[4 * k + 2].y), pack2(v[4 * k + 3].x, v[4 * k + 3].y));
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) v[i] = __fmul2_rn(activate<ACT>(v[i]), gate[i]);
+                        if (adds) {
+                            float2 r[16];
+                            if (wide) get32_float(to, r);
+                            else get32(to, 4 * h, r);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) v[i] = __ffma2_rn(r[i], f2(e.residual_scale), v[i]);
+                        }
+                    }
+                    if (wide) put32_float(to, v);
+                    else put32(to, 4 * h, v);
                 }
                 send(&g.out, to - lane * 128, col0, row0, split);
                 if (staged_pre) send(&g.pre, pieces, col0, row0, 0);
