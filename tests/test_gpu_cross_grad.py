@@ -86,6 +86,12 @@ def test_long(bss, d):
     run(bss, q, k, v, group, [260, 129, 30])
 
 
+def test_more_key_tiles_than_ctas(bss):
+    run(bss, *case(130, 1, 64, 20000)[:4])
+    q, k, v, group, _ = case(40, 2, 64, 20100, group=20, Hk=1)
+    run(bss, q, k, v, group, [20100, 300])
+
+
 def test_same_bits_again(bss):
     a = case(5000, 2, 128, 200)[:4]
     for x, y in zip(run(bss, *a), run(bss, *a)):
