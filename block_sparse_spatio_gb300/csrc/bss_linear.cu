@@ -112,6 +112,9 @@ constexpr int kOperand = 128 * kTileK * 2;
 constexpr int kStages = 5;
 constexpr int kThreads = 384;
 constexpr int kEpilogueWarps = 8;
+// CTAs of a cluster that share a tile: with 8 not all clusters find room at once (256 x
+// 1,280 -> 1,280: 18 us instead of 8).
+constexpr int kMostJoined = 4;
 constexpr int kPiece = 32 * 128;  // 32 rows of 128 bytes: a warp's two take turns
 
 struct Epilogue {
@@ -236,23 +239,32 @@ __device__ __forceinline__ void load_params32(const void* base, int64_t at, int 
     }
 }
 
-// z -> out, for 8 columns of a row; the residual's values are there already.
+// From the product of 8 columns of a row to memory.
 template <int ACT>
-__device__ __forceinline__ void finish8(const Epilogue& e, int64_t group, int col, float (&v)[8], const float (&r)[8]) {
-    float w[8];
+__device__ __forceinline__ void end_row8(const Epilogue& e, int row, int col, float (&v)[8], float (&w)[8]) {
+    if (e.bias != nullptr) {
+        load_param8(e.bias, col, e.param_dtype, w);
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] += w[x];
+    }
+    if (e.pre != nullptr) store8(e.pre, row * e.pre_stride + col, BSS_DTYPE_BF16, v);
     activate8<ACT>(v);
     if (e.gate != nullptr) {
-        load_param8(e.gate, group * e.gate_stride + col, e.param_dtype, w);
+        load_param8(e.gate, e.by_rows.div(row) * e.gate_stride + col, e.param_dtype, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= w[i];
     }
     if (e.residual != nullptr) {
+        load8(e.residual, row * e.residual_stride + col, e.out_dtype, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(e.residual_scale, r[i], v[i]);
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(e.residual_scale, w[i], v[i]);
     }
+    store8(e.out, row * e.out_stride + col, e.out_dtype, v);
 }
 
-template <int CG, bool A_MN, bool B_MN, int ACT>
+// JOIN: a cluster of `splits` CTAs makes one tile, each a share of the contraction; their
+// sums meet through shared memory, each CTA taking as many of the rows to the end.
+template <int CG, bool A_MN, bool B_MN, int ACT, bool JOIN>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmArgs g) {
     using L = GemmSmem;
     extern __shared__ uint8_t smem_raw[];
@@ -269,7 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = CG == 2 ? cluster_rank() : 0;
-    const int first = blockIdx.x / CG, step = gridDim.x / CG;
+    const int share = JOIN ? static_cast<int>(cluster_rank()) : 0;
+    const int units = JOIN ? g.tiles : g.tiles * g.splits;
+    const int first = JOIN ? blockIdx.x / g.splits : blockIdx.x / CG, step = JOIN ? g.tiles : gridDim.x / CG;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -304,8 +318,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             };
             uint32_t fill = 0;
             bool ok = true;
-            for (int u = first; ok && u < g.tiles * g.splits; u += step) {
-                const int split = u / g.tiles, t = u - split * g.tiles;
+            for (int u = first; ok && u < units; u += step) {
+                const int split = JOIN ? share : u / g.tiles, t = JOIN ? u : u - split * g.tiles;
                 const int mt = t / g.tiles_n, nt = t - mt * g.tiles_n;
                 const int end = split_begin(g, split + 1);
                 const int row_a = mt * kTile + static_cast<int>(rank) * 128, row_b = nt * kTile + static_cast<int>(rank) * 128;
@@ -352,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                     else tc_commit(bar);
                 }
             };
-            for (int u = first; ok && u < g.tiles * g.splits; u += step, ++n_tile) {
-                const int split = u / g.tiles, begin = split_begin(g, split), end = split_begin(g, split + 1);
+            for (int u = first; ok && u < units; u += step, ++n_tile) {
+                const int split = JOIN ? share : u / g.tiles, begin = split_begin(g, split), end = split_begin(g, split + 1);
                 const uint32_t buf = n_tile & 1;
                 if (n_tile >= 2)
                     ok = __all_sync(0xFFFFFFFFu, mbar_wait(acc_empty + buf, (n_tile / 2 - 1) & 1, g.status));
@@ -387,7 +401,24 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
         const Epilogue& e = g.e;
         const bool wide = e.out_dtype == BSS_DTYPE_F32, staged_pre = e.pre != nullptr && !wide, adds = e.residual != nullptr;
         const int width = wide ? 32 : 64, begin_c = side * (kTile / 2), end_c = begin_c + kTile / 2;
-        const int units = g.tiles * g.splits;
+        if constexpr (JOIN) {
+            // the sums of 32 rows and half of the columns, where the operands were: a row of
+            // 512 bytes, its 16-byte units swizzled by the row
+            if (__all_sync(0xFFFFFFFFu, mbar_wait(acc_full, 0, g.status))) {
+                tc_fence_after();
+                uint8_t* to = smem + (quarter * 32 + lane) * 512;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t x[32];
+                    BSS_TMEM_LD32(tmem + lanes + side * 64 + 32 * c, x);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(to + ((side * 16 + c * 8 + (k ^ (lane & 7))) << 4)) =
+                            make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                }
+            }
+        } else {
         // Where a piece's columns lie; false past the tensor's ends.
         auto place = [&](int u, int c, int& col, int& row0) {
             const int t = u % g.tiles, mt = t / g.tiles_n;
@@ -517,12 +548,49 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
                 if (asked[p] > taken[p]) mbar_wait(arrived + (warp - 4) * 2 + p, (asked[p] - 1) & 1, g.status);
             tma_store_wait_read_all();
         }
+        }
     }
 
     tc_fence_before();
     __syncwarp();
-    if constexpr (CG == 2) cluster_sync();
-    else __syncthreads();
+    if constexpr (JOIN) {
+        cluster_sync();
+        if (warp >= 4) {
+            // 16 threads a row, 8 columns each; all shares' loads at once, added in their order
+            const int t = first, mt = t / g.tiles_n, end = 128 * (share + 1) / g.splits;
+            const int unit = (threadIdx.x & 15) * 2, col = (t - mt * g.tiles_n) * kTile + unit * 4;
+            for (int r = 128 * share / g.splits + (static_cast<int>(threadIdx.x) - 128) / 16; r < end; r += 16) {
+                const int row = mt * kTile + r;
+                if (row >= g.m || col >= g.n) continue;
+                const uint32_t at = static_cast<uint32_t>(r) * 512 + ((unit & ~7) << 4);
+                const uint32_t first_unit = at + (((unit & 7) ^ (r & 7)) << 4), second_unit = at + ((((unit & 7) + 1) ^ (r & 7)) << 4);
+                float4 x[kMostJoined], y[kMostJoined];
+#pragma unroll
+                for (int s = 0; s < kMostJoined; ++s) {
+                    if (s < g.splits) {
+                        const uint32_t from = map_to_rank(smem, s);
+                        x[s] = lds_cluster(from + first_unit);
+                        y[s] = lds_cluster(from + second_unit);
+                    }
+                }
+                float v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, y[0].x, y[0].y, y[0].z, y[0].w}, w[8];
+#pragma unroll
+                for (int s = 1; s < kMostJoined; ++s) {
+                    if (s < g.splits) {
+                        v[0] += x[s].x, v[1] += x[s].y, v[2] += x[s].z, v[3] += x[s].w;
+                        v[4] += y[s].x, v[5] += y[s].y, v[6] += y[s].z, v[7] += y[s].w;
+                    }
+                }
+                end_row8<ACT>(g.e, row, col, v, w);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // the others have read
+    } else if constexpr (CG == 2) {
+        cluster_sync();
+    } else {
+        __syncthreads();
+    }
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
@@ -542,27 +610,18 @@ struct FinishArgs {
 template <int ACT>
 __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ FinishArgs a) {
     cudaGridDependencySynchronize();
-    const Epilogue& e = a.e;
     const int64_t plane = static_cast<int64_t>(a.m) * a.n;
     const uint32_t vectors = a.n / 8, all = a.m * vectors;  // below 2^31: the splits are of small results
     for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < all; i += gridDim.x * 256) {
         const int row = a.by_vectors.div(i), col = static_cast<int>(i - row * vectors) * 8;
-        float v[8], w[8], r[8] = {};
+        float v[8], w[8];
         load8(a.sums, row * static_cast<int64_t>(a.n) + col, BSS_DTYPE_F32, v);
         for (int s = 1; s < a.splits; ++s) {
             load8(a.sums, s * plane + row * static_cast<int64_t>(a.n) + col, BSS_DTYPE_F32, w);
 #pragma unroll
             for (int x = 0; x < 8; ++x) v[x] += w[x];
         }
-        if (e.bias != nullptr) {
-            load_param8(e.bias, col, e.param_dtype, w);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] += w[x];
-        }
-        if (e.pre != nullptr) store8(e.pre, row * e.pre_stride + col, BSS_DTYPE_BF16, v);
-        if (e.residual != nullptr) load8(e.residual, row * e.residual_stride + col, e.out_dtype, r);
-        finish8<ACT>(e, e.gate != nullptr ? e.by_rows.div(row) : 0, col, v, r);
-        store8(e.out, row * e.out_stride + col, e.out_dtype, v);
+        end_row8<ACT>(a.e, row, col, v, w);
     }
 }
 
@@ -570,7 +629,8 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
 // The weights' bytes are the work: every warp streams its share of them straight into
 // the operand of a small matrix product (16 output channels a block; lane 4 g + c loads
 // 16 bytes of rows g and g + 8: channels that follow one another, the same ones of x's
-// rows), 8 warps share the contraction, and their sums meet in shared memory.
+// rows), 8 warps share the contraction, and their sums meet in shared memory.  1,280 ->
+// 7,680: one row 4.2 us (19.7 MB of weights), 16 rows 6.0; by tiles 17 rows 8.4.
 constexpr int kFewRows = 16;
 constexpr int kFewWarps = 8;
 
@@ -795,14 +855,18 @@ bss_status operand_map(CUtensorMap* map, const void* p, int64_t rows, int64_t st
 // rounds of the tiles times a block of 64 of the contraction (pairs 0.38, single 0.25,
 // measured at 75,600 x 5,120 x 1,280), plus 4 for the second kernel and its bytes at
 // 5 TB/s.  (1,280 x 5,120 of 75,600: 752 us with one split, 100 tiles for 76 pairs.)
+// Where the tiles leave CTAs over, a cluster of them shares a tile and nothing goes
+// through memory (512 x 4,096 -> 1,280: 11.7 us, with a second kernel 11.2, but calls
+// one after another 12.8 instead of 20.4: no workspace, one launch).
 struct Cut {
     bool pair;
     int splits;
+    bool join;  // the splits are a cluster's
 };
 
 Cut cut_of(int64_t m, int64_t n, int64_t k) {
     const int64_t blocks = (k + kTileK - 1) / kTileK;
-    Cut best = {false, 1};
+    Cut best = {false, 1, false};
     double least = 1e30;
     for (int pair = 1; pair >= 0; --pair) {
         const int64_t tile = pair ? 256 : 128, units = num_sms() / (pair ? 2 : 1);
@@ -812,34 +876,39 @@ Cut cut_of(int64_t m, int64_t n, int64_t k) {
             const double rounds = static_cast<double>((tiles * s + units - 1) / units);
             double t = rounds * static_cast<double>((blocks + s - 1) / s) * (pair ? 0.38 : 0.25);
             if (s > 1) t += 4.0 + 8.0 * s * m * n / 5e6;
-            if (t < least) least = t, best = {pair != 0, s};
+            if (t < least) least = t, best = {pair != 0, s, false};
+        }
+        for (int s = 2; !pair && s <= kMostJoined && tiles * s <= units && s * 2 <= blocks; ++s) {
+            const double t = static_cast<double>((blocks + s - 1) / s) * 0.25 + 1.5;
+            if (t < least) least = t, best = {false, s, true};
         }
     }
     return best;
 }
 
-int64_t cut_bytes(const Cut& c, int64_t m, int64_t n) { return c.splits > 1 ? 4 * c.splits * m * n : 0; }
+int64_t cut_bytes(const Cut& c, int64_t m, int64_t n) { return c.splits > 1 && !c.join ? 4 * c.splits * m * n : 0; }
 
-template <int CG, bool A_MN, bool B_MN, int ACT>
+template <int CG, bool A_MN, bool B_MN, int ACT, bool JOIN = false>
 bss_status launch_gemm(GemmArgs& g, cudaStream_t stream) {
     constexpr int kTile = 128 * CG;
     const int64_t tiles_m = (static_cast<int64_t>(g.m) + kTile - 1) / kTile;
     g.tiles_n = (g.n + kTile - 1) / kTile;
     if (tiles_m * g.tiles_n * g.splits > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many tiles");
     g.tiles = static_cast<int32_t>(tiles_m * g.tiles_n);
-    auto kernel = gemm_kernel<CG, A_MN, B_MN, ACT>;
+    auto kernel = gemm_kernel<CG, A_MN, B_MN, ACT, JOIN>;
     int blocks;
     const bss_status st = resident_blocks(reinterpret_cast<const void*>(kernel), kThreads, GemmSmem::kAlloc, &blocks);
     if (st != BSS_OK) return st;
     int units = num_sms() / CG;
-    if (units > g.tiles * g.splits) units = g.tiles * g.splits;
-    return launch_behind_with(kernel, dim3(static_cast<unsigned>(units * CG)), kThreads, GemmSmem::kAlloc, CG, stream,
-                              "matrix product launch", g);
+    if (JOIN || units > g.tiles * g.splits) units = g.tiles * g.splits;
+    return launch_behind_with(kernel, dim3(static_cast<unsigned>(units * CG)), kThreads, GemmSmem::kAlloc, JOIN ? g.splits : CG,
+                              stream, "matrix product launch", g);
 }
 
-template <int ACT>
-bss_status launch_linear(GemmArgs& g, bool pair, cudaStream_t stream) {
-    return pair ? launch_gemm<2, false, false, ACT>(g, stream) : launch_gemm<1, false, false, ACT>(g, stream);
+template <bool A_MN, bool B_MN, int ACT>
+bss_status launch_cut(GemmArgs& g, const Cut& cut, cudaStream_t stream) {
+    if (cut.join) return launch_gemm<1, A_MN, B_MN, ACT, true>(g, stream);
+    return cut.pair ? launch_gemm<2, A_MN, B_MN, ACT>(g, stream) : launch_gemm<1, A_MN, B_MN, ACT>(g, stream);
 }
 
 // The kernel of an activation.
@@ -869,7 +938,10 @@ bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride
     g.n = static_cast<int32_t>(n);
     g.kblocks = static_cast<int32_t>((k + kTileK - 1) / kTileK);
     g.splits = cut.splits;
-    if (cut.splits > 1) {
+    const bool through_memory = cut.splits > 1 && !cut.join;
+    if (cut.join) {
+        g.e = e;
+    } else if (through_memory) {
         g.e.out_dtype = BSS_DTYPE_F32;
         st = encode_tmap_rows(&g.out, sums, BSS_DTYPE_F32, n, m, n * 4, 32, cut.splits, m * n * 4);
     } else {
@@ -881,10 +953,10 @@ bss_status gemm(const void* a, int64_t a_stride, const void* b, int64_t b_stride
     }
     if (st != BSS_OK) return st;
     if constexpr (A_MN || B_MN)
-        st = cut.pair ? launch_gemm<2, A_MN, B_MN, BSS_ACT_NONE>(g, stream) : launch_gemm<1, A_MN, B_MN, BSS_ACT_NONE>(g, stream);
+        st = launch_cut<A_MN, B_MN, BSS_ACT_NONE>(g, cut, stream);
     else
-        st = by_activation(g.e.activation, [&](auto act) { return launch_linear<decltype(act)::value>(g, cut.pair, stream); });
-    if (st != BSS_OK || cut.splits == 1) return st;
+        st = by_activation(g.e.activation, [&](auto act) { return launch_cut<false, false, decltype(act)::value>(g, cut, stream); });
+    if (st != BSS_OK || !through_memory) return st;
     FinishArgs f;
     f.sums = sums, f.m = g.m, f.n = g.n, f.splits = cut.splits, f.by_vectors = FastDiv(static_cast<uint32_t>(n / 8)), f.e = e;
     int64_t blocks = (m * (n / 8) + 255) / 256;

@@ -269,6 +269,13 @@ __device__ __forceinline__ uint32_t map_to_rank(const void* p, uint32_t rank) {
     return a;
 }
 
+// 16 bytes of another CTA's shared memory.
+__device__ __forceinline__ float4 lds_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
