@@ -1,22 +1,28 @@
 /*
- * bss_block.h -- C ABI of the operators on either side of the attention step in
- * a video transformer's block (implemented by the same library as bss.h).
+ * bss_block.h -- C ABI of the operators around the attention step in a video
+ * transformer's block (implemented by the same library as bss.h).
  *
  * A block turns its token stream x into the next one around an attention call:
  *
  *   h = modulated norm of x             bss_residual_norm (x only)
- *   q, k, v = projections of h          the caller's matrix products
+ *   q, k, v = projections of h          bss_linear
  *   Qh, Kh, Vh = heads of q, k, v       bss_heads_from_tokens: Q/K norm, rotary
  *                                       positions of the (time, height, width)
  *                                       axes, head-major layout with temporal
  *                                       heads in (H,W,F) order
  *   O = block-sparse attention          bss_sparse_attention_split, or both in
  *                                       one call: bss_attention_step_tokens
- *   y = projection of O                 the caller's matrix product
+ *   y = projection of O                 bss_linear
  *   r = a x + gate * y                  bss_residual_norm, which also writes the
- *   h = modulated norm of r             next block's input in the same pass
+ *   h = modulated norm of r             next layer's input in the same pass (or
+ *                                       bss_linear, in the product's epilogue)
+ *   c = attention over an encoder's     bss_cross_attention, between two
+ *       states (a prompt)               bss_linear
+ *   feed-forward layer                  bss_linear with an activation, then with
+ *                                       a gate and the residual
  *
- * Each operator has its backward pass.  The blog has no counterpart to these
+ * Each of these operators has its backward pass (the block-sparse attention has
+ * none).  The blog has no counterpart to these
  * calls: it treats Q, K, V as given; its section "Arrange tokens for efficient
  * temporal access" fixes the layout that bss_heads_from_tokens writes.
  *
