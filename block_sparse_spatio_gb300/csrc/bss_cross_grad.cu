@@ -52,6 +52,7 @@ struct GradArgs {
     float* delta;      // [heads][rows]
     int64_t* starts;   // [groups + 1]: row tiles of all key heads in front of a group; [groups + 1]: most key tiles
     float* parts;      // [2 blocks][2][128][d]
+    int4* joins;       // [blocks]: group (or -1), key head, key tile and further parts of what a CTA leaves to be joined
     int* status;
 };
 
@@ -633,6 +634,25 @@ __device__ __forceinline__ bool next_part(const GradArgs& a, Share& s, Part& p) 
     return false;
 }
 
+// The head's rows in which a CTA's run ends, if they also begin there: its own part is
+// the first, the same key tile's CTAs in the teams behind have the others.  (With more
+// key tiles than CTAs there is one team, and no part of a head's rows.)
+__device__ __forceinline__ int4 to_join(const GradArgs& a, const Share& s) {
+    const int64_t total = a.starts[a.s.groups];
+    const int teams = teams_of(a, total, s.tiles);
+    if (teams > 1 && s.lo < s.hi) {
+        const Part p = part_at(a, s.hi - 1, s.hi);
+        const int64_t begin = s.hi - 1 - p.first, end = begin + p.per;
+        if (begin >= s.lo && end > s.hi && s.tile * kKeyTile < p.valid) {
+            const int team = blockIdx.x / s.step;
+            int last = team + 1;  // the team that has the head's last rows
+            while (run_begin(total, teams, last + 1) < end) ++last;
+            return make_int4(p.group, p.kv, s.tile, last - team);
+        }
+    }
+    return make_int4(-1, 0, 0, 0);
+}
+
 // A row tile: its head and first row in the group.
 struct RowTile {
     int head, row0;
@@ -673,9 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
     cudaGridDependencySynchronize();
     Share share = share_of(a, blockIdx.x);
     Part p;
-    if (!next_part(a, share, p)) return;
-    if (smem_u32(smem) & 1023u) {  // the swizzled tiles could not be addressed
-        record_status(a.status, BSS_ERR_CUDA);
+    const bool works = next_part(a, share, p), placed = (smem_u32(smem) & 1023u) == 0;
+    if (!works || !placed) {
+        if (!placed) record_status(a.status, BSS_ERR_CUDA);  // the swizzled tiles could not be addressed
+        if (threadIdx.x == 0) a.joins[blockIdx.x] = make_int4(-1, 0, 0, 0);
         return;
     }
 
@@ -757,6 +778,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 mbar_wait(q_full + f % kQStages, (f / kQStages) & 1, a.status);
             for (uint32_t f = dos > kDOStages ? dos - kDOStages : 0; f < dos; ++f)
                 mbar_wait(do_full + f % kDOStages, (f / kDOStages) & 1, a.status);
+        } else if (warp == 0 && lane == 1) {
+            a.joins[blockIdx.x] = to_join(a, share);
         } else if (warp == 1) {
             const bool leader = elect_one();
             const uint32_t base = smem_u32(smem);
@@ -999,47 +1022,38 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
 }
 
 // ---------------------------------------------------------------- sums of parts, zeros
-// Block (b, y): the head's rows in which the run of CTA b ends, if they also begin
-// there: its part and those of the same key tile's CTAs in the teams behind, in their
-// order.  Key tiles without a valid state: zeros.
+// Block (b, y): the parts that begin with CTA b's, in their order.  Key tiles without a
+// valid state: zeros.
 template <int D>
 __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__ GradArgs a) {
     cudaGridDependencySynchronize();
-    const int64_t total = a.starts[a.s.groups];
-    const Share share = share_of(a, blockIdx.x);
-    const int teams = teams_of(a, total, share.tiles);
-    // (with more key tiles than CTAs there is one team, and no part of a head's rows)
-    if (share.tile < share.tiles && teams > 1 && share.lo < share.hi) {
-        const Part p = part_at(a, share.hi - 1, share.hi);
-        const int64_t begin = share.hi - 1 - p.first, end = begin + p.per;
-        if (begin >= share.lo && end > share.hi && share.tile * kKeyTile < p.valid) {
-            const int team = blockIdx.x / share.step;
-            int ends = team + 1;  // the team that has the head's last rows
-            while (run_begin(total, teams, ends + 1) < end) ++ends;
-            // a thread sums 8 channels of a key: neighbours in a warp are neighbouring keys
-            constexpr int kVectors = 2 * 128 * D / 8;
-            for (int i = blockIdx.y * 256 + threadIdx.x; i < kVectors; i += gridDim.y * 256) {
-                const int which = i / (128 * D / 8), r = i % 128, c = i / 128 % (D / 8);
-                float v[8], w[8];
-                auto fetch = [&](int64_t slot, float (&to)[8]) {
-                    const float4* from = reinterpret_cast<const float4*>(a.parts + (slot * 2 + which) * 128 * D) + 2 * c * 128 + r;
-                    const float4 x = from[0], y = from[128];
-                    to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
-                };
-                fetch(2 * static_cast<int64_t>(blockIdx.x) + 1, v);
-                for (int k = team + 1; k <= ends; ++k) {
-                    fetch(2 * (static_cast<int64_t>(k) * share.step + share.tile), w);
+    const int4 join = a.joins[blockIdx.x];
+    if (join.x >= 0) {
+        const int tiles = static_cast<int>(a.starts[a.s.groups + 1]), step = tiles <= a.blocks ? tiles : a.blocks;
+        // a thread sums 8 channels of a key: neighbours in a warp are neighbouring keys
+        constexpr int kVectors = 2 * 128 * D / 8;
+        for (int i = blockIdx.y * 256 + threadIdx.x; i < kVectors; i += gridDim.y * 256) {
+            const int which = i / (128 * D / 8), r = i % 128, c = i / 128 % (D / 8);
+            float v[8], w[8];
+            auto fetch = [&](int64_t slot, float (&to)[8]) {
+                const float4* from = reinterpret_cast<const float4*>(a.parts + (slot * 2 + which) * 128 * D) + 2 * c * 128 + r;
+                const float4 x = from[0], y = from[128];
+                to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
+            };
+            fetch(2 * static_cast<int64_t>(blockIdx.x) + 1, v);
+#pragma unroll 4
+            for (int k = 1; k <= join.w; ++k) {
+                fetch(2 * (static_cast<int64_t>(blockIdx.x) + static_cast<int64_t>(k) * step), w);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x) v[x] += w[x];
-                }
-                const int key = share.tile * kKeyTile + r;
-                if (key >= a.s.keys) continue;
-                uint16_t* to = which == 0 ? a.dv + p.group * a.dv_group + key * a.dv_token + p.kv * a.dv_head
-                                          : a.dk + p.group * a.dk_group + key * a.dk_token + p.kv * a.dk_head;
-                const float scale = which == 0 ? 1.0f : a.scale;
-                *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(pack2(v[0] * scale, v[1] * scale), pack2(v[2] * scale, v[3] * scale),
-                                                                   pack2(v[4] * scale, v[5] * scale), pack2(v[6] * scale, v[7] * scale));
+                for (int x = 0; x < 8; ++x) v[x] += w[x];
             }
+            const int key = join.z * kKeyTile + r;
+            if (key >= a.s.keys) continue;
+            uint16_t* to = which == 0 ? a.dv + join.x * a.dv_group + key * a.dv_token + join.y * a.dv_head
+                                      : a.dk + join.x * a.dk_group + key * a.dk_token + join.y * a.dk_head;
+            const float scale = which == 0 ? 1.0f : a.scale;
+            *reinterpret_cast<uint4*>(to + 8 * c) = make_uint4(pack2(v[0] * scale, v[1] * scale), pack2(v[2] * scale, v[3] * scale),
+                                                               pack2(v[4] * scale, v[5] * scale), pack2(v[6] * scale, v[7] * scale));
         }
     }
     if (a.s.lengths == nullptr) return;
@@ -1080,7 +1094,7 @@ bss_status launch_backward(GradArgs& a, cudaStream_t stream) {
 int64_t aligned_up(int64_t v) { return (v + 255) / 256 * 256; }
 
 struct Plan {
-    int64_t delta_at, starts_at, parts_at, bytes;
+    int64_t delta_at, starts_at, joins_at, parts_at, bytes;
     int32_t tiles, key_tiles, blocks;
 };
 
@@ -1094,7 +1108,8 @@ Plan plan_of(const bss_cross_grads& a) {
     p.blocks = pairs < num_sms() ? static_cast<int32_t>(pairs) : num_sms();
     p.delta_at = 0;
     p.starts_at = aligned_up(a.rows * a.heads * 4);
-    p.parts_at = p.starts_at + aligned_up((groups + 2) * 8);
+    p.joins_at = p.starts_at + aligned_up((groups + 2) * 8);
+    p.parts_at = p.joins_at + aligned_up(p.blocks * 16ll);
     p.bytes = p.parts_at + 2ll * p.blocks * 2 * 128 * a.head_dim * 4;
     return p;
 }
@@ -1180,6 +1195,7 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
     char* ws = static_cast<char*>(p.workspace);
     a.delta = reinterpret_cast<float*>(ws + plan.delta_at);
     a.starts = reinterpret_cast<int64_t*>(ws + plan.starts_at);
+    a.joins = reinterpret_cast<int4*>(ws + plan.joins_at);
     a.parts = reinterpret_cast<float*>(ws + plan.parts_at);
     a.status = device_status_ptr();
     if (a.status == nullptr) return set_error(BSS_ERR_CUDA, "cannot resolve the device status word");

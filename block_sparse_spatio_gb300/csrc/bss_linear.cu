@@ -824,22 +824,33 @@ __global__ void __launch_bounds__(32 * kDzWarps) dz_kernel(const __grid_constant
     }
 }
 
-// out[j][c] = sum over i of partial[j * parts + i][c], in a fixed order: a block's
-// eight warps take every eighth part each.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* partial, float* out, int64_t parts, int32_t n) {
+// Sums of parts in a fixed order, a block's eight warps taking every eighth part each:
+// row 0 of the grid has dbias, of all blocks' parts, the others a group's dgate each.
+struct SumArgs {
+    const float *bias_parts, *gate_parts;  // NULL: not wanted
+    float *dbias, *dgate;
+    int64_t blocks;
+    int32_t chunks, n;
+};
+
+__global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ SumArgs a) {
     __shared__ float sums[8][32];
     cudaGridDependencySynchronize();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x * 32 + lane;
+    const bool bias = blockIdx.y == 0 && a.bias_parts != nullptr;
+    const int64_t group = a.bias_parts != nullptr ? blockIdx.y - 1ll : blockIdx.y, parts = bias ? a.blocks : a.chunks;
+    const float* from = bias ? a.bias_parts : a.gate_parts + group * a.chunks * a.n;
     float s = 0.0f;
-    if (c < n)
-        for (int64_t i = warp; i < parts; i += 8) s += partial[(blockIdx.y * parts + i) * n + c];
+    if (c < a.n)
+#pragma unroll 4
+        for (int64_t i = warp; i < parts; i += 8) s += from[i * a.n + c];
     sums[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < n) {
+    if (warp == 0 && c < a.n) {
 #pragma unroll
         for (int w = 1; w < 8; ++w) s += sums[w][lane];
-        out[static_cast<int64_t>(blockIdx.y) * n + c] = s;
+        (bias ? a.dbias : a.dgate + group * a.n)[c] = s;
     }
 }
 
@@ -1211,12 +1222,11 @@ bss_status bss_linear_backward(const bss_linear_grads* args, cudaStream_t stream
         st = by_activation(a.activation, [&](auto act) { return launch_dz<decltype(act)::value>(d, p.blocks, stream); });
         if (st != BSS_OK) return st;
         const unsigned columns = static_cast<unsigned>((n + 31) / 32);
-        if (a.dbias != nullptr)
-            st = launch_behind(sum_parts_kernel, dim3(columns, 1), 256, stream, "bias gradient launch", d.dbias, a.dbias,
-                               p.blocks, a.out_channels);
-        if (st == BSS_OK && a.dgate != nullptr && p.chunks > 0)
-            st = launch_behind(sum_parts_kernel, dim3(columns, static_cast<unsigned>(p.groups)), 256, stream,
-                               "gate gradient launch", d.dgate, a.dgate, static_cast<int64_t>(p.chunks), a.out_channels);
+        SumArgs sum = {d.dbias, p.chunks > 0 ? d.dgate : nullptr, a.dbias, a.dgate, p.blocks, p.chunks, a.out_channels};
+        const int64_t sum_rows = (sum.bias_parts != nullptr) + (sum.gate_parts != nullptr ? p.groups : 0);
+        if (sum_rows > 0)
+            st = launch_behind(sum_parts_kernel, dim3(columns, static_cast<unsigned>(sum_rows)), 256, stream,
+                               "bias and gate gradient launch", sum);
         if (st != BSS_OK) return st;
     }
     Epilogue e = {};
