@@ -11,6 +11,10 @@
 //   z   A = x [rows][in]     K-major   B = W [out][in]  K-major
 //   dx  A = dz [rows][out]   K-major   B = W [out][in]  MN-major
 //   dW  A = dz [rows][out]   MN-major  B = x [rows][in] MN-major
+//
+// 75,600 x 1,280 -> 5,120 with GELU 625 us, 75,600 x 5,120 -> 1,280 with gate and residual
+// 620 (1,585 and 1,600 TFLOP/s, 91 and 92% of what cuBLAS sustains under the power limit,
+// which bounds both); the gradients of the former 1,503: dz 300, dx 607, dW 614.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -107,6 +111,9 @@ __device__ __forceinline__ void share_and_slope(float2 z, float2& share, float2&
 // a warp 32 rows of half of the columns, 128 bytes a row at a time through a piece of
 // shared memory of its own and a TMA store, which clips at the tensor's ends.
 // Two accumulators a CTA: the MMAs of the next tile run during this one's stores.
+// Bound by the tensor cores: one launch alone (37,800 x 5,120 -> 1,280) 1,857 TFLOP/s with the
+// tensor pipe 92% active; pairs of CTAs because each then reads half of B from shared
+// memory (a pair's block of 64 takes 0.38 us for four times the work of a single's 0.25).
 constexpr int kTileK = 64;  // 128 bytes of bf16: one swizzle row
 constexpr int kOperand = 128 * kTileK * 2;
 constexpr int kStages = 5;
@@ -715,8 +722,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
 }
 
 // ---------------------------------------------------------------- dz and its sums over rows
-// A thread has 8 channels, a warp walks over rows; a block covers `unit` rows that
-// share a gate, or (small groups) whole groups, one a warp at a time.
+// A thread has 8 channels, a warp walks over rows; a block covers `units` rows that
+// share a gate, or (small groups) whole groups, one a warp at a time.  Bound by DRAM:
+// 37,800 x 5,120 with GELU's slope and the bias sums 184 us, 6,310 GB/s (95% of a copy).
 struct DzArgs {
     const void* dout;
     const __nv_bfloat16* pre;
