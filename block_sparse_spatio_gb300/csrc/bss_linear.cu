@@ -58,13 +58,33 @@ __device__ __forceinline__ float2 smooth_share(float2 z, float2 w) {
         return share_of(__fmul2_rn(z, f2(-kLog2e)));
 }
 
-__device__ __forceinline__ float erf_share(float z) { return 0.5f * erfcf(-0.70710678118654752f * z); }
+// The error function's form: the share of -|z| is e(z) g(|z|) with e = exp(-z^2 / 2) and g =
+// erfc(|z| / sqrt(2)) / (2 e), smooth and like 1 / |z| far out: t times a polynomial of
+// degree 8 in t = 1 / (1 + 0.34 |z|), fitted for the least relative error over 0..14.5 (3.4e-8,
+// 3e-7 with its roundings; e is 0 behind).  75,600 x 1,280 -> 5,120 with a bias: 690 us, with
+// erfcf in its place 1,175 (the tanh form 604, no activation 605).
+constexpr float kErfSlope = 0.34f;
+
+__device__ __forceinline__ float2 erf_share(float2 z, float2& e) {
+    constexpr float kErfFit[9] = {0.1356215775f, 0.1360922903f, 0.1153511703f, 0.1147158891f, -0.0431121476f,
+                                  0.1997268051f, -0.2708797455f, 0.1383616030f, -0.0258774385f};
+    const float2 w = __fmul2_rn(z, z), by = __ffma2_rn(make_float2(fabsf(z.x), fabsf(z.y)), f2(kErfSlope), f2(1.0f));
+    const float2 t = make_float2(rcp_approx(by.x), rcp_approx(by.y)), u = __fmul2_rn(w, f2(-0.5f * kLog2e));
+    e = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+    float2 g = f2(kErfFit[8]);
+#pragma unroll
+    for (int i = 7; i >= 0; --i) g = __ffma2_rn(g, t, f2(kErfFit[i]));
+    const float2 low = __fmul2_rn(__fmul2_rn(e, t), g), high = __ffma2_rn(low, f2(-1.0f), f2(1.0f));
+    return make_float2(z.x < 0.0f ? low.x : high.x, z.y < 0.0f ? low.y : high.y);
+}
 
 // (z times the share, not a quotient: with an infinite exponential the share is 0)
 template <int ACT>
 __device__ __forceinline__ float2 activate(float2 z) {
-    if constexpr (ACT == BSS_ACT_GELU) return __fmul2_rn(z, make_float2(erf_share(z.x), erf_share(z.y)));
-    else if constexpr (ACT != BSS_ACT_NONE) return __fmul2_rn(z, smooth_share<ACT>(z, __fmul2_rn(z, z)));
+    if constexpr (ACT == BSS_ACT_GELU) {
+        float2 e;
+        return __fmul2_rn(z, erf_share(z, e));
+    } else if constexpr (ACT != BSS_ACT_NONE) return __fmul2_rn(z, smooth_share<ACT>(z, __fmul2_rn(z, z)));
     else return z;
 }
 
@@ -90,9 +110,9 @@ __device__ __forceinline__ void share_and_slope(float2 z, float2& share, float2&
     constexpr float kEnd = ACT == BSS_ACT_SILU ? 110.0f : 20.0f;
     const float2 t = make_float2(fminf(fmaxf(z.x, -kEnd), kEnd), fminf(fmaxf(z.y, -kEnd), kEnd));
     if constexpr (ACT == BSS_ACT_GELU) {
-        share = make_float2(erf_share(z.x), erf_share(z.y));
-        slope = make_float2(fmaf(t.x, 0.39894228040143268f * __expf(-0.5f * t.x * t.x), share.x),
-                            fmaf(t.y, 0.39894228040143268f * __expf(-0.5f * t.y * t.y), share.y));
+        float2 e;
+        share = erf_share(z, e);
+        slope = __ffma2_rn(__fmul2_rn(t, f2(0.39894228040143268f)), e, share);
     } else {
         // share (1 + (1 - share) u') with u' z times the derivative of the exponent
         const float2 w = __fmul2_rn(t, t);

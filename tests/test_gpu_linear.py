@@ -196,3 +196,26 @@ def test_split_contraction(bss, rows, inner, outer, out):
     forward(bss, rows, inner, outer, kind=1, out=out, pre=True, gate=True, residual=True, a=0.5, group=max(1, rows // 3), pad=8)
     forward(bss, rows, inner, outer, out=out, bias=False, residual=True, inplace=True)
     backward(bss, inner, rows // 4 * 8, outer, dw=out)
+
+
+@pytest.mark.gpu
+def test_error_function(bss):
+    """GELU by the error function in 32 bits over its whole range.  In units of 2^-24 of the
+    share: its fit and the polynomial's roundings 5, the quotient 3, two products 2, the
+    exponential 4 and three roundings of its argument z^2 / 2, the last steps 2."""
+    n = 4096
+    z = torch.linspace(-12.5, 12.5, n).to(BF)
+    w = torch.zeros(n, 8, dtype=BF)
+    w[:, 0] = z
+    x = torch.zeros(1, 8, dtype=BF)
+    x[0, 0] = 1
+    o, slope = torch.empty(1, n, dtype=F32, device=DEV), torch.empty(n, dtype=F32, device=DEV)
+    bss.linear(x.to(DEV), w.to(DEV), o, activation=2)
+    bss.linear_backward(torch.ones(1, n, dtype=BF, device=DEV), pre=z[None].to(DEV), dbias=slope, activation=2)
+    z = z.double()
+    value, want = L.act(z, 2)
+    units = 16 + 1.5 * z * z
+    share = 0.5 * torch.erfc(-z / 2 ** 0.5)
+    assert ((o[0].double().cpu() - value).abs() <= units * 2.0 ** -24 * value.abs()).all()
+    phi = (want - share).abs()
+    assert ((slope.double().cpu() - want).abs() <= units * 2.0 ** -24 * (share + phi) + 2.0 ** -24 * want.abs()).all()
