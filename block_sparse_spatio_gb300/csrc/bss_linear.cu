@@ -643,6 +643,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
         const int row = a.by_vectors.div(i), col = static_cast<int>(i - row * vectors) * 8;
         float v[8], w[8];
         load8(a.sums, row * static_cast<int64_t>(a.n) + col, BSS_DTYPE_F32, v);
+#pragma unroll 8
         for (int s = 1; s < a.splits; ++s) {
             load8(a.sums, s * plane + row * static_cast<int64_t>(a.n) + col, BSS_DTYPE_F32, w);
 #pragma unroll
@@ -871,7 +872,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const __grid_constant__ 
     const float* from = bias ? a.bias_parts : a.gate_parts + group * a.chunks * a.n;
     float s = 0.0f;
     if (c < a.n)
-#pragma unroll 4
+#pragma unroll 8
         for (int64_t i = warp; i < parts; i += 8) s += from[i * a.n + c];
     sums[warp][lane] = s;
     __syncthreads();
@@ -893,7 +894,8 @@ bss_status operand_map(CUtensorMap* map, const void* p, int64_t rows, int64_t st
 // whose sums a second kernel adds.  The least of a simple estimate in microseconds:
 // rounds of the tiles times a block of 64 of the contraction (pairs 0.38, single 0.25,
 // measured at 75,600 x 5,120 x 1,280), plus 4 for the second kernel and its bytes at
-// 5 TB/s.  (1,280 x 5,120 of 75,600: 752 us with one split, 100 tiles for 76 pairs.)
+// 5 TB/s.  (1,280 x 5,120 of 75,600: 752 us with one split, 100 tiles for 76 pairs.)  Up to 64
+// splits: the gradients of 75,600 x 64 -> 64 without a bias 38 -> 29 us against at most 16.
 // Where the tiles leave CTAs over, a cluster of them shares a tile and nothing goes
 // through memory (512 x 4,096 -> 1,280: 11.7 us, with a second kernel 11.2, but calls
 // one after another 12.8 instead of 20.4: no workspace, one launch).
@@ -910,7 +912,7 @@ Cut cut_of(int64_t m, int64_t n, int64_t k) {
     for (int pair = 1; pair >= 0; --pair) {
         const int64_t tile = pair ? 256 : 128, units = num_sms() / (pair ? 2 : 1);
         const int64_t tiles = ((m + tile - 1) / tile) * ((n + tile - 1) / tile);
-        for (int s = 1; s <= 16 && (s == 1 || s * 4 <= blocks); ++s) {
+        for (int s = 1; s <= 64 && (s == 1 || s * 4 <= blocks); ++s) {
             if (s > 1 && m * n > (int64_t(1) << 28)) break;
             const double rounds = static_cast<double>((tiles * s + units - 1) / units);
             double t = rounds * static_cast<double>((blocks + s - 1) / s) * (pair ? 0.38 : 0.25);
@@ -1062,9 +1064,11 @@ GradPlan plan_of(const bss_linear_grads& a) {
     // without a gate all rows are one group here
     const int64_t per = a.gate != nullptr ? a.rows_per_group : a.rows;
     p.groups = groups_of(a.rows, per);
-    // about 16 blocks an SM over all columns, of 32 rows at least
+    // about 16 blocks an SM over all columns, 4 of a column (every one leaves a row of sums
+    // to be added: with 16 of a column dbias of 75,600 x 64 took 28 us instead of 8), of 32
+    // rows at least
     const int64_t columns = (n + 255) / 256;
-    int64_t want = 16ll * num_sms() / columns;
+    int64_t want = (columns > 4 ? 16ll : 4 * columns) * num_sms() / columns;
     if (want < 1) want = 1;
     int64_t rows = (a.rows + want - 1) / want;
     if (rows < 32) rows = 32;

@@ -219,3 +219,10 @@ def test_error_function(bss):
     assert ((o[0].double().cpu() - value).abs() <= units * 2.0 ** -24 * value.abs()).all()
     phi = (want - share).abs()
     assert ((slope.double().cpu() - want).abs() <= units * 2.0 ** -24 * (share + phi) + 2.0 ** -24 * want.abs()).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", [0, 2])
+def test_many_splits(bss, kind):
+    """A long contraction of few results: more splits than a cluster's or a pair's."""
+    backward(bss, 20011, 64, 72, kind=kind)
