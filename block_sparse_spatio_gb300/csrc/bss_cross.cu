@@ -18,10 +18,13 @@
 // TMEM: S_h at 128 h (P_h as bf16 over its first 64 columns), O_h at 256 + 128 h.
 // A row's reference is the maximum of its first tile, moved only when the sum of a
 // later tile's P passes 2^16 (then O and l are rescaled).
+// P is rounded to bf16 on the way to its product, because the tensor cores take both
+// operands in one type and 32-bit ones at an eighth of the rate; l sums the unrounded P.
 //
-// 75,600 x 10 x 128 over 512 states, lse kept: 153 us (1,290 TFLOP/s).  Bound by shared
-// memory: a step of both halves moves 272 KB (2,125 cycles at 128 bytes) beneath 2,048
-// cycles of products.  Over 128 states 69 us, of which Q and O alone are 59 at a copy's rate.
+// 75,600 x 10 x 128 over 512 states, lse kept: 153 us (1,290 TFLOP/s).  A further key tile
+// costs 31.9 us (1,554 TFLOP/s, 90% of what cuBLAS sustains under the power limit; a step of both
+// halves moves 272 KB of shared memory, 2,125 cycles at 128 bytes, beneath 2,048 cycles
+// of products), the ends of the items 18 us.  Over 128 states 69 us, of which Q and O alone are 59 at a copy's rate.
 #include "bss_cross.cuh"
 
 #include <cstring>

@@ -20,6 +20,9 @@
 // tiles read 1.58 GB for 75,600 x 10 x 128 over 512 states instead of 0.4).  A tile's
 // products are S(t+1), dK(t), dP(t+1), dV(t+1).  Where a run ends inside a head's rows
 // the sums go to the workspace in 32 bits, and a third kernel adds them in their order.
+// P and dS are rounded to bf16 on the way to their products (the tensor cores take both
+// operands in one type), dS once more beside the result's own rounding: errors are 1.4
+// times those of a gradient in 32 bits that is rounded at its store.
 //
 // 75,600 x 10 x 128 over 512 states: 532 us (930 TFLOP/s of five products, 1,300 of the seven
 // made): dq 251, dk and dv 257, their sums 14.  Both are bound by shared memory: dq moves
