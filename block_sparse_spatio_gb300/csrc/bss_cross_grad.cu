@@ -20,6 +20,8 @@
 // tiles read 1.58 GB for 75,600 x 10 x 128 over 512 states instead of 0.4).  A tile's
 // products are S(t+1), dK(t), dP(t+1), dV(t+1).  Where a run ends inside a head's rows
 // the sums go to the workspace in 32 bits, and a third kernel adds them in their order.
+// With a few rows neither: one kernel without tiles, in 32 bits.
+//
 // P and dS are rounded to bf16 on the way to their products (the tensor cores take both
 // operands in one type), dS once more beside the result's own rounding: errors are 1.4
 // times those of a gradient in 32 bits that is rounded at its store.
@@ -1081,6 +1083,143 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
     }
 }
 
+// ---------------------------------------------------------------- few rows
+// A few rows a group (a token, a handful of queries) fill no tile: everything in 32 bits,
+// eight lanes a key with d / 8 channels each, four keys a warp at once.  The first blocks
+// have dq, one a row and head, and go over all its keys; the others have dk and dv of 32
+// keys each and go over the rows of all heads that share them.  No sums between blocks, no
+// workspace.  Bound by a key's chain of load, two sums of eight lanes and an exponential.
+struct FewGradArgs {
+    CrossShape s;
+    const uint16_t *q, *dO, *O, *k, *v;
+    uint16_t *dq, *dk, *dv;
+    int64_t q_row, q_head, dO_row, dO_head, O_row, O_head, dq_row, dq_head;
+    int64_t k_group, k_token, k_head, v_group, v_token, v_head;
+    int64_t dk_group, dk_token, dk_head, dv_group, dv_token, dv_head;
+    float scale;
+    const float* lse;  // [heads][rows]
+    int32_t dq_blocks, key_blocks;
+};
+
+constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
+
+// A lane's channels of a row: 16-byte units 8 apart.
+template <int N>
+__device__ __forceinline__ void load_part(const uint16_t* row, int unit, float (&x)[8 * N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4*>(row + 8 * (unit + 8 * i));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+        }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_part(uint16_t* row, int unit, const float (&x)[8 * N], float scale) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        *reinterpret_cast<uint4*>(row + 8 * (unit + 8 * i)) =
+            make_uint4(pack2(x[8 * i] * scale, x[8 * i + 1] * scale), pack2(x[8 * i + 2] * scale, x[8 * i + 3] * scale),
+                       pack2(x[8 * i + 4] * scale, x[8 * i + 5] * scale), pack2(x[8 * i + 6] * scale, x[8 * i + 7] * scale));
+}
+
+// The eight lanes' sum of products.
+template <int N>
+__device__ __forceinline__ float dot_part(const float (&x)[8 * N], const float (&y)[8 * N]) {
+    float a = 0.0f, b = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8 * N; i += 2) a = fmaf(x[i], y[i], a), b = fmaf(x[i + 1], y[i + 1], b);
+    a += b;
+#pragma unroll
+    for (int m = 1; m < 8; m *= 2) a += __shfl_xor_sync(0xFFFFFFFFu, a, m);
+    return a;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kFewThreads) cross_few_kernel(const __grid_constant__ FewGradArgs a) {
+    constexpr int N = D / 64;
+    constexpr float kLog2e = 1.4426950408889634f;
+    __shared__ float sums[kFewWarps][D];
+    const int warp = threadIdx.x >> 5, unit = threadIdx.x & 7, slot = (threadIdx.x >> 3) & 3;
+    cudaGridDependencySynchronize();
+    if (static_cast<int>(blockIdx.x) < a.dq_blocks) {
+        const int row = blockIdx.x / a.s.heads, h = blockIdx.x - row * a.s.heads, kv = h / a.s.share;
+        const int group = row / a.s.group_rows, n = a.s.valid(group);
+        float q[8 * N], g[8 * N], x[8 * N], sum[8 * N] = {};
+        load_part<N>(a.O + row * a.O_row + h * a.O_head, unit, x);
+        load_part<N>(a.dO + row * a.dO_row + h * a.dO_head, unit, g);
+        load_part<N>(a.q + row * a.q_row + h * a.q_head, unit, q);
+        const float delta = dot_part<N>(g, x), lse = a.lse[static_cast<int64_t>(h) * a.s.rows + row] * kLog2e;
+        const uint16_t* k = a.k + group * a.k_group + kv * a.k_head;
+        const uint16_t* v = a.v + group * a.v_group + kv * a.v_head;
+#pragma unroll 2
+        for (int first = warp * 4; first < n; first += kFewWarps * 4) {
+            const int64_t key = min(first + slot, n - 1);
+            float y[8 * N];
+            load_part<N>(k + key * a.k_token, unit, x);
+            load_part<N>(v + key * a.v_token, unit, y);
+            const float s = dot_part<N>(q, x), dp = dot_part<N>(g, y);
+            const float p = ex2_approx(fmaf(s, a.s.scale_log2, -lse)), ds = p * (dp - delta);
+            if (first + slot < n)
+#pragma unroll
+                for (int i = 0; i < 8 * N; ++i) sum[i] = fmaf(ds, x[i], sum[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8 * N; ++i) {
+            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 8);
+            sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 16);
+            if (slot == 0) sums[warp][8 * (unit + 8 * (i / 8)) + i % 8] = sum[i];
+        }
+        __syncthreads();
+        if (threadIdx.x < 8) {
+#pragma unroll
+            for (int i = 0; i < 8 * N; ++i) {
+                sum[i] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kFewWarps; ++w) sum[i] += sums[w][8 * (unit + 8 * (i / 8)) + i % 8];
+            }
+            store_part<N>(a.dq + row * a.dq_row + h * a.dq_head, unit, sum, a.scale);
+        }
+        return;
+    }
+    const int block = blockIdx.x - a.dq_blocks, rest = block / a.key_blocks;
+    const int group = rest / a.s.kv_heads, kv = rest - group * a.s.kv_heads, n = a.s.valid(group);
+    const int64_t key = (block - rest * a.key_blocks) * (kFewWarps * 4) + warp * 4 + slot;
+    const bool live = key < n;
+    float k[8 * N] = {}, v[8 * N] = {}, dk[8 * N] = {}, dv[8 * N] = {};
+    if (live) {
+        load_part<N>(a.k + group * a.k_group + key * a.k_token + kv * a.k_head, unit, k);
+        load_part<N>(a.v + group * a.v_group + key * a.v_token + kv * a.v_head, unit, v);
+    }
+    const int row0 = group * a.s.group_rows, rows = a.s.rows_of(group), pairs = n > 0 ? rows * a.s.share : 0;
+#pragma unroll 2
+    for (int i = 0; i < pairs; ++i) {
+        const int h = kv * a.s.share + i / rows, row = row0 + i % rows;
+        float q[8 * N], g[8 * N], o[8 * N];
+        load_part<N>(a.q + row * a.q_row + h * a.q_head, unit, q);
+        load_part<N>(a.dO + row * a.dO_row + h * a.dO_head, unit, g);
+        load_part<N>(a.O + row * a.O_row + h * a.O_head, unit, o);
+        const float lse = a.lse[static_cast<int64_t>(h) * a.s.rows + row] * kLog2e;
+        const float s = dot_part<N>(q, k), dp = dot_part<N>(g, v), delta = dot_part<N>(g, o);
+        const float p = ex2_approx(fmaf(s, a.s.scale_log2, -lse)), ds = p * (dp - delta);
+#pragma unroll
+        for (int c = 0; c < 8 * N; ++c) {
+            dk[c] = fmaf(ds, q[c], dk[c]);
+            dv[c] = fmaf(p, g[c], dv[c]);
+        }
+    }
+    if (key >= a.s.keys) return;
+    if (!live)
+#pragma unroll
+        for (int c = 0; c < 8 * N; ++c) dk[c] = dv[c] = 0.0f;
+    store_part<N>(a.dk + group * a.dk_group + key * a.dk_token + kv * a.dk_head, unit, dk, a.scale);
+    store_part<N>(a.dv + group * a.dv_group + key * a.dv_token + kv * a.dv_head, unit, dv, 1.0f);
+}
+
 template <int D>
 bss_status launch_backward(GradArgs& a, cudaStream_t stream) {
     auto dq = cross_dq_kernel<D>;
@@ -1104,12 +1243,22 @@ int64_t aligned_up(int64_t v) { return (v + 255) / 256 * 256; }
 struct Plan {
     int64_t delta_at, starts_at, joins_at, parts_at, bytes;
     int32_t tiles, key_tiles, blocks;
+    bool few;
 };
+
+// Groups of a few rows, and few pairs of rows and keys in all, go without tiles (us on the
+// device, without and with them): 10 heads x 128, 1 row over 512 states 7.8 and 18.9, 8 over
+// 2,048 (2^17.3 pairs) 26.5 and 37.0, 16 (2^18.3) 45 and 37; one row over 8,192 140 and 112; 40
+// heads, 16 rows over 512 (2^18.3) 48 and 23.  A call by itself takes 19 us instead of 34: one launch
+// instead of three, and no workspace.
+constexpr int kFewRows = 16, kFewKeys = 4096;
+constexpr int64_t kFewPairs = 1 << 18;
 
 // rows_per_group at most rows
 Plan plan_of(const bss_cross_grads& a) {
     Plan p;
     const int64_t groups = (a.rows + a.rows_per_group - 1) / a.rows_per_group;
+    p.few = a.rows_per_group <= kFewRows && a.keys <= kFewKeys && a.rows * a.heads <= kFewPairs / a.keys;
     p.tiles = static_cast<int32_t>((a.rows_per_group + 127) / 128);
     p.key_tiles = static_cast<int32_t>((static_cast<int64_t>(a.keys) + kKeyTile - 1) / kKeyTile);
     const double pairs = static_cast<double>(groups) * p.tiles * p.key_tiles * a.heads;
@@ -1118,7 +1267,7 @@ Plan plan_of(const bss_cross_grads& a) {
     p.starts_at = aligned_up(a.rows * a.heads * 4);
     p.joins_at = p.starts_at + aligned_up((groups + 2) * 8);
     p.parts_at = p.joins_at + aligned_up(p.blocks * 16ll);
-    p.bytes = p.parts_at + 2ll * p.blocks * 2 * 128 * a.head_dim * 4;
+    p.bytes = p.few ? 0 : p.parts_at + 2ll * p.blocks * 2 * 128 * a.head_dim * 4;
     return p;
 }
 
@@ -1173,6 +1322,35 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
         return st;
     if (groups > 1 && (p.k.group_stride == 0 || p.v.group_stride == 0))
         return set_error(BSS_ERR_UNSUPPORTED, "gradients of states shared by several groups: give one group");
+    auto stride = [](int64_t extent, int64_t s) { return extent > 1 ? s : 0; };
+    const CrossShape shape = cross_shape(p.rows, p.rows_per_group, p.heads, p.kv_heads, p.head_dim, p.keys, p.softmax_scale,
+                                         p.lengths, p.k.group_stride);
+    const float scale = p.softmax_scale > 0.0f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.head_dim));
+    if (plan.few) {
+        FewGradArgs f;
+        memset(&f, 0, sizeof(f));
+        f.s = shape, f.scale = scale, f.lse = p.lse;
+        auto rows_of = [&](const bss_token_tensor& t, auto*& to, int64_t& row, int64_t& head) {
+            to = static_cast<uint16_t*>(t.data), row = stride(p.rows, t.token_stride), head = stride(p.heads, t.head_stride);
+        };
+        auto states_of = [&](const bss_state_tensor& t, auto*& to, int64_t& group, int64_t& token, int64_t& head) {
+            to = static_cast<uint16_t*>(t.data), group = stride(groups, t.group_stride);
+            token = stride(p.keys, t.token_stride), head = stride(p.kv_heads, t.head_stride);
+        };
+        rows_of(p.q, f.q, f.q_row, f.q_head);
+        rows_of(p.dO, f.dO, f.dO_row, f.dO_head);
+        rows_of(p.O, f.O, f.O_row, f.O_head);
+        rows_of(p.dq, f.dq, f.dq_row, f.dq_head);
+        states_of(p.k, f.k, f.k_group, f.k_token, f.k_head);
+        states_of(p.v, f.v, f.v_group, f.v_token, f.v_head);
+        states_of(p.dk, f.dk, f.dk_group, f.dk_token, f.dk_head);
+        states_of(p.dv, f.dv, f.dv_group, f.dv_token, f.dv_head);
+        f.dq_blocks = static_cast<int32_t>(p.rows * p.heads);
+        f.key_blocks = static_cast<int32_t>((p.keys + kFewWarps * 4ll - 1) / (kFewWarps * 4));
+        const unsigned blocks = static_cast<unsigned>(f.dq_blocks + groups * p.kv_heads * f.key_blocks);
+        return launch_behind(p.head_dim == 128 ? cross_few_kernel<128> : cross_few_kernel<64>, dim3(blocks), kFewThreads, stream,
+                             "few rows' gradient launch", f);
+    }
     const int64_t items = groups * plan.tiles * p.heads;
     if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
     GradArgs a;
@@ -1182,8 +1360,7 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
         (st = states_map(&a.k, p.k, groups, p.keys, p.kv_heads, p.head_dim, kKeyTile)) != BSS_OK ||
         (st = states_map(&a.v, p.v, groups, p.keys, p.kv_heads, p.head_dim, kKeyTile)) != BSS_OK)
         return st;
-    a.s = cross_shape(p.rows, p.rows_per_group, p.heads, p.kv_heads, p.head_dim, p.keys, p.softmax_scale, p.lengths,
-                      p.k.group_stride);
+    a.s = shape;
     a.tiles = plan.tiles, a.key_tiles = plan.key_tiles, a.blocks = plan.blocks;
     a.items = static_cast<int32_t>(items);
     a.by_tiles = FastDiv(static_cast<uint32_t>(plan.tiles));
@@ -1191,14 +1368,13 @@ bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_
     a.dq = static_cast<uint16_t*>(p.dq.data);
     a.dk = static_cast<uint16_t*>(p.dk.data);
     a.dv = static_cast<uint16_t*>(p.dv.data);
-    auto stride = [](int64_t extent, int64_t s) { return extent > 1 ? s : 0; };
     a.O_row = stride(p.rows, p.O.token_stride), a.O_head = stride(p.heads, p.O.head_stride);
     a.dq_row = stride(p.rows, p.dq.token_stride), a.dq_head = stride(p.heads, p.dq.head_stride);
     a.dk_group = stride(groups, p.dk.group_stride), a.dk_token = stride(p.keys, p.dk.token_stride);
     a.dk_head = stride(p.kv_heads, p.dk.head_stride);
     a.dv_group = stride(groups, p.dv.group_stride), a.dv_token = stride(p.keys, p.dv.token_stride);
     a.dv_head = stride(p.kv_heads, p.dv.head_stride);
-    a.scale = p.softmax_scale > 0.0f ? p.softmax_scale : 1.0f / sqrtf(static_cast<float>(p.head_dim));
+    a.scale = scale;
     a.lse = p.lse;
     char* ws = static_cast<char*>(p.workspace);
     a.delta = reinterpret_cast<float*>(ws + plan.delta_at);

@@ -468,7 +468,7 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream);
  *               without a gap, as in a view of a packed tensor.  All overwritten.
  *   workspace   device memory of at least the size that
  *               bss_cross_attention_backward_workspace gives, 16-byte aligned, used
- *               by this call only until its work is done.
+ *               by this call only until its work is done; NULL where that is 0.
  * Sums over rows are taken in a fixed order.  Outputs overlap no other tensor. */
 typedef struct {
     int64_t rows;
@@ -485,7 +485,8 @@ typedef struct {
 
 bss_status bss_cross_attention_backward_workspace(const bss_cross_grads* args, int64_t* bytes);
 
-/* Three launches.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+/* Three launches; one, without a workspace, where groups have few rows (16 at most) and the
+ * call few pairs of rows and keys.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_t stream);
 
 #ifdef __cplusplus

@@ -117,3 +117,28 @@ def test_rows_stay_apart(bss):
         check(dq[rows], *ref["dq"], 1, "dq")
         check(dk[g:g + 1], *ref["dk"], 1, "dk")
         check(dv[g:g + 1], *ref["dv"], 1, "dv")
+
+
+@pytest.mark.parametrize("rows,group,H,Hk,d,keys", [
+    (1, 1, 1, 1, 64, 1), (1, 1, 10, 10, 128, 512), (1, 1, 6, 3, 128, 20), (5, 5, 4, 1, 64, 333), (8, 8, 2, 2, 128, 2048),
+    (7, 2, 6, 2, 64, 33), (23, 8, 8, 1, 128, 31), (64, 1, 2, 2, 64, 129), (8, 8, 8, 8, 64, 4096), (16, 16, 2, 1, 64, 40)])
+@pytest.mark.parametrize("layout", ["plain", "packed", "heads", "by_head"])
+def test_few_rows(bss, rows, group, H, Hk, d, keys, layout):
+    q, k, v, group, G = case(rows, H, d, keys, group=group, Hk=Hk)
+    run(bss, q, k, v, group, layout=layout)
+    run(bss, q, k, v, group, [(keys, 0, (keys + 1) // 2, 1, max(keys - 3, 0))[(i + 2) % 5] for i in range(G)], layout=layout)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_in_32_bits(bss, d, monkeypatch):
+    """A few rows' P and dS are not rounded on the way: nothing but the results' own rounding."""
+    monkeypatch.setattr(L, "BF16", 0)
+    q, k, v, group, _ = case(6, 6, d, 75, group=2, Hk=3)
+    run(bss, q, k, v, group, [75, 10, 1])
+
+
+def test_few_rows_beside_tiles(bss):
+    """The largest calls without tiles and the smallest with them."""
+    for rows, keys in ((8, 4096), (8, 4097), (16, 64), (17, 64), (1, 5000)):
+        q, k, v, group, _ = case(rows, 8, 64, keys, Hk=4)
+        run(bss, q, k, v, group)
