@@ -1089,6 +1089,14 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 // have dq, one a row and head, and go over all its keys; the others have dk and dv of 32
 // keys each and go over the rows of all heads that share them.  No sums between blocks, no
 // workspace.  Bound by a key's chain of load, two sums of eight lanes and an exponential.
+// Taken for a few rows of a key head and few pairs of rows and keys (us on the device, without
+// and with tiles): 10 heads x 128, one row over 512 / 2,048 states 6.2 / 16.3 and 18.9 / 37.1, 8
+// rows 12.5 / 26.7 and 18.9 / 37.0, 16 rows 17.8 / 50.5 and 19.0 / 36.9; 40 heads, 8 rows over 512
+// (2^17.3 pairs) 30.7 and 23.1.  A call by itself takes 19 us instead of 34: one launch instead
+// of three, and no workspace.
+constexpr int kFewRows = 16;
+constexpr int64_t kFewPairs = 1 << 17;
+
 struct FewGradArgs {
     CrossShape s;
     const uint16_t *q, *dO, *O, *k, *v;
@@ -1100,44 +1108,6 @@ struct FewGradArgs {
     const float* lse;  // [heads][rows]
     int32_t dq_blocks, key_blocks;
 };
-
-constexpr int kFewThreads = 256, kFewWarps = kFewThreads / 32;
-
-// A lane's channels of a row: 16-byte units 8 apart.
-template <int N>
-__device__ __forceinline__ void load_part(const uint16_t* row, int unit, float (&x)[8 * N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const uint4 u = *reinterpret_cast<const uint4*>(row + 8 * (unit + 8 * i));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-    }
-}
-
-template <int N>
-__device__ __forceinline__ void store_part(uint16_t* row, int unit, const float (&x)[8 * N], float scale) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        *reinterpret_cast<uint4*>(row + 8 * (unit + 8 * i)) =
-            make_uint4(pack2(x[8 * i] * scale, x[8 * i + 1] * scale), pack2(x[8 * i + 2] * scale, x[8 * i + 3] * scale),
-                       pack2(x[8 * i + 4] * scale, x[8 * i + 5] * scale), pack2(x[8 * i + 6] * scale, x[8 * i + 7] * scale));
-}
-
-// The eight lanes' sum of products.
-template <int N>
-__device__ __forceinline__ float dot_part(const float (&x)[8 * N], const float (&y)[8 * N]) {
-    float a = 0.0f, b = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8 * N; i += 2) a = fmaf(x[i], y[i], a), b = fmaf(x[i + 1], y[i + 1], b);
-    a += b;
-#pragma unroll
-    for (int m = 1; m < 8; m *= 2) a += __shfl_xor_sync(0xFFFFFFFFu, a, m);
-    return a;
-}
 
 template <int D>
 __global__ void __launch_bounds__(kFewThreads) cross_few_kernel(const __grid_constant__ FewGradArgs a) {
@@ -1246,19 +1216,12 @@ struct Plan {
     bool few;
 };
 
-// Groups of a few rows, and few pairs of rows and keys in all, go without tiles (us on the
-// device, without and with them): 10 heads x 128, 1 row over 512 states 7.8 and 18.9, 8 over
-// 2,048 (2^17.3 pairs) 26.5 and 37.0, 16 (2^18.3) 45 and 37; one row over 8,192 140 and 112; 40
-// heads, 16 rows over 512 (2^18.3) 48 and 23.  A call by itself takes 19 us instead of 34: one launch
-// instead of three, and no workspace.
-constexpr int kFewRows = 16, kFewKeys = 4096;
-constexpr int64_t kFewPairs = 1 << 18;
 
 // rows_per_group at most rows
 Plan plan_of(const bss_cross_grads& a) {
     Plan p;
     const int64_t groups = (a.rows + a.rows_per_group - 1) / a.rows_per_group;
-    p.few = a.rows_per_group <= kFewRows && a.keys <= kFewKeys && a.rows * a.heads <= kFewPairs / a.keys;
+    p.few = a.rows_per_group * (a.heads / a.kv_heads) <= kFewRows && a.rows * a.heads <= kFewPairs / a.keys;
     p.tiles = static_cast<int32_t>((a.rows_per_group + 127) / 128);
     p.key_tiles = static_cast<int32_t>((static_cast<int64_t>(a.keys) + kKeyTile - 1) / kKeyTile);
     const double pairs = static_cast<double>(groups) * p.tiles * p.key_tiles * a.heads;

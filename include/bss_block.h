@@ -485,8 +485,8 @@ typedef struct {
 
 bss_status bss_cross_attention_backward_workspace(const bss_cross_grads* args, int64_t* bytes);
 
-/* Three launches; one, without a workspace, where groups have few rows (16 at most) and the
- * call few pairs of rows and keys.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+/* Three launches; one, without a workspace, where at most 16 rows and heads share a
+ * group's key head and the call has few pairs of rows and keys.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 bss_status bss_cross_attention_backward(const bss_cross_grads* args, cudaStream_t stream);
 
 #ifdef __cplusplus

@@ -155,3 +155,43 @@ def test_rows_stay_apart(bss):
     good[3, 0] = good[250, 1] = False
     check(O[:400].cpu()[good], ref[good], slack[good], 1, "O")
     assert torch.isnan(O[3, 0]).all() and torch.isnan(O[400:]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,group,H,Hk,d,keys", [
+    (1, 1, 1, 1, 64, 1), (1, 1, 10, 10, 128, 512), (1, 1, 6, 3, 128, 20), (5, 5, 4, 1, 64, 333), (8, 8, 2, 2, 128, 2048),
+    (7, 2, 6, 2, 64, 33), (23, 8, 8, 1, 128, 63), (64, 1, 2, 2, 64, 129), (8, 8, 8, 8, 64, 4096), (16, 16, 2, 1, 64, 65)])
+@pytest.mark.parametrize("layout", ["plain", "packed", "heads", "by_head"])
+def test_few_rows(bss, rows, group, H, Hk, d, keys, layout):
+    q, k, v, group, G = case(rows, H, d, keys, group=group, Hk=Hk)
+    run(bss, q, k, v, group, layout=layout)
+    run(bss, q, k, v, group, [(keys, 0, (keys + 1) // 2, 1, max(keys - 3, 0))[(i + 2) % 5] for i in range(G)], layout=layout,
+        in_place=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_few_rows_in_32_bits(bss, d, monkeypatch):
+    """A few rows' P is not rounded on the way: nothing but the result's own rounding."""
+    monkeypatch.setattr(L, "BF16", 0)
+    q, k, v, group, _ = case(6, 6, d, 75, group=2, Hk=3)
+    run(bss, q, k, v, group, [75, 10, 1])
+    run(bss, 8 * q, k, v, group, [75, 10, 1])
+
+
+@pytest.mark.gpu
+def test_few_rows_beside_tiles(bss):
+    """The largest calls without tiles and the smallest with them."""
+    for rows, keys in ((19, 64), (20, 64), (19, 300), (1, 5000)):
+        q, k, v, group, _ = case(rows, 8, 64, keys, Hk=4)
+        run(bss, q, k, v, group)
+
+
+@pytest.mark.gpu
+def test_few_rows_share_states(bss):
+    """One set of states for all groups, by a group stride of 0."""
+    q, k, v, _, _ = case(6, 2, 64, 70)
+    O = torch.empty_like(q).to(DEV)
+    kd, vd = (t.to(DEV).expand(3, -1, -1, -1) for t in (k, v))
+    bss.cross_attention(q.to(DEV), kd, vd, O, rows_per_group=2)
+    check(O, *L.cross(q, k, v, [70], 6)["O"], 1, "O")

@@ -139,6 +139,6 @@ def test_few_rows_in_32_bits(bss, d, monkeypatch):
 
 def test_few_rows_beside_tiles(bss):
     """The largest calls without tiles and the smallest with them."""
-    for rows, keys in ((8, 4096), (8, 4097), (16, 64), (17, 64), (1, 5000)):
+    for rows, keys in ((8, 2048), (8, 2049), (9, 64), (1, 5000)):
         q, k, v, group, _ = case(rows, 8, 64, keys, Hk=4)
         run(bss, q, k, v, group)
