@@ -738,7 +738,8 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream) 
         (st = check_row_heads(&t[4], p.O, "O", p.rows, p.heads, p.head_dim, true)) != BSS_OK ||
         (st = check_run(&t[5], p.lse, "lse", 4 * p.rows * p.heads, 4, true)) != BSS_OK)
         return st;
-    t[4].over = 0;
+    // over q only element by element (with as many rows as heads a transposed view has the same bytes)
+    if ((p.rows <= 1 || p.O.token_stride == p.q.token_stride) && (p.heads <= 1 || p.O.head_stride == p.q.head_stride)) t[4].over = 0;
     if ((st = check_outputs(t, 6)) != BSS_OK) return st;
     if ((p.k.group_stride == 0) != (p.v.group_stride == 0) && groups > 1)
         return set_error(BSS_ERR_UNSUPPORTED, "k and v must both be shared by the groups, or neither");
