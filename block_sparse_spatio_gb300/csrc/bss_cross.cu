@@ -40,9 +40,14 @@ constexpr float kSumLimit = 65536.0f;
 // Registers: 128 x (64 + 96 + 2 x 176) = the launch's 512 x 128.
 constexpr uint32_t kRegsControl = 64, kRegsStore = 96, kRegsSoftmax = 176;
 
+// A tile of queries holds rows of its group alone, zeros behind them: the next group's may
+// be written over by another CTA at that moment (O over q), and a row's large scores move
+// the references of its whole warp.  Hence a dimension of groups in the map of those that
+// have all of group_rows rows, and a map of its own for a shorter last one.
 struct CrossArgs {
-    CUtensorMap q, k, v, o;
+    CUtensorMap q, q_rest, k, v, o;
     CrossShape s;
+    int32_t whole;  // groups of group_rows rows
     int32_t tiles;  // of 256 rows in a group
     int32_t items;
     FastDiv by_tiles;
@@ -150,7 +155,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
             for (int i = blockIdx.x; ok && i < a.items; i += gridDim.x) {
                 const Item t = item_at(a, i);
                 if (t.n == 0) continue;
-                const int row = t.group * a.s.group_rows + t.row0;
+                const bool rest = t.group >= a.whole;
+                const CUtensorMap* q = rest ? &a.q_rest : &a.q;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (h == 1 && !t.two) break;
@@ -159,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                     mbar_arrive_expect_tx(q_full + h, L::kTile);
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c)
-                        tma_load_3d(smem + L::kQ + h * L::kTile + c * kChunkBytesSw128, &a.q, c * 64, row + h * kHalfRows,
-                                    t.head, q_full + h);
+                        tma_load_4d(smem + L::kQ + h * L::kTile + c * kChunkBytesSw128, q, c * 64, t.row0 + h * kHalfRows, t.head,
+                                    rest ? 0 : t.group, q_full + h);
                     ++q_fills[h];
                 }
                 const int kv = a.s.by_share.div(t.head), g = a.s.shared_states ? 0 : t.group;
@@ -764,12 +770,23 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream) 
     if (items > 0x7FFFFFFF - 4096) return set_error(BSS_ERR_UNSUPPORTED, "too many rows and heads");
     CrossArgs a;
     memset(&a, 0, sizeof(a));
-    if ((st = row_heads_map(&a.q, p.q, p.rows, p.heads, p.head_dim, kHalfRows)) != BSS_OK ||
+    const int64_t whole = p.rows / p.rows_per_group, rest = p.rows - whole * p.rows_per_group;
+    auto queries_map = [&](CUtensorMap* map, int64_t group, int64_t rows, int64_t groups) {
+        const uint64_t row = static_cast<uint64_t>(stride(p.rows, p.q.token_stride)) * 2;
+        return encode_tmap_4d(map, static_cast<const char*>(p.q.data) + group * p.rows_per_group * row,
+                              {static_cast<uint64_t>(p.head_dim), static_cast<uint64_t>(rows), static_cast<uint64_t>(p.heads),
+                               static_cast<uint64_t>(groups)},
+                              {row, static_cast<uint64_t>(p.q.head_stride) * 2, static_cast<uint64_t>(p.rows_per_group) * row}, 64,
+                              kHalfRows);
+    };
+    if ((st = queries_map(&a.q, 0, p.rows_per_group, whole)) != BSS_OK ||
+        (rest > 0 && (st = queries_map(&a.q_rest, whole, rest, 1)) != BSS_OK) ||
         (st = row_heads_map(&a.o, p.O, p.rows, p.heads, p.head_dim, 32)) != BSS_OK ||
         (st = states_map(&a.k, p.k, groups, p.keys, p.kv_heads, p.head_dim, kKeyTile)) != BSS_OK ||
         (st = states_map(&a.v, p.v, groups, p.keys, p.kv_heads, p.head_dim, kKeyTile)) != BSS_OK)
         return st;
     a.s = shape;
+    a.whole = static_cast<int32_t>(whole);
     a.tiles = static_cast<int32_t>(tiles);
     a.items = static_cast<int32_t>(items);
     a.by_tiles = FastDiv(static_cast<uint32_t>(a.tiles));
