@@ -17,7 +17,8 @@
 //                 of them stores and waits for the last product).
 // TMEM: S_h at 128 h (P_h as bf16 over its first 64 columns), O_h at 256 + 128 h.
 // A row's reference is the maximum of its first tile, moved only when the sum of a
-// later tile's P passes 2^16 (then O and l are rescaled).
+// later tile's P passes 2^16 (then O and l are rescaled), or when no score so far was
+// above minus infinity.
 // P is rounded to bf16 on the way to its product, because the tensor cores take both
 // operands in one type and 32-bit ones at an eighth of the rate; l sums the unrounded P.
 //
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
                     f2_unpack(sum_a, a0, a1);
                     f2_unpack(sum_b, b0, b1);
                     const float sum = (a0 + a1) + (b0 + b1);
-                    if (j > 0 && __any_sync(0xFFFFFFFFu, sum > kSumLimit)) return false;
+                    if (j > 0 && __any_sync(0xFFFFFFFFu, sum > kSumLimit || m == -INFINITY)) return false;
                     l += sum;
 #pragma unroll
                     for (int q4 = 0; q4 < 4; ++q4) BSS_TMEM_ST16(t_s + 16 * q4, (pk + 16 * q4));
