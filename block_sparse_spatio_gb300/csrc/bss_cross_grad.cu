@@ -76,6 +76,10 @@ __device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
     return d;
 }
 
+// A row's lse in base 2.  Without a score above minus infinity its P is 0: an lse of plus
+// infinity makes it so.
+__device__ __forceinline__ float lse_base2(float lse) { return lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f; }
+
 __device__ __forceinline__ void store_packed(uint32_t at, const float (&v)[64]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -408,7 +412,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_kernel(const __grid_co
                 const int64_t row0 = first_row(t);
                 const int rows = t.rows - w * 32;  // of this warp's 32; rows that do not exist: another one in their place
                 const uint16_t* o0 = a.O + t.head * a.O_head + (lane & 3) * 8;
-                lse = lane < rows ? a.lse[static_cast<int64_t>(t.head) * a.s.rows + row0 + lane] : INFINITY;
+                lse = lane < rows ? lse_base2(a.lse[static_cast<int64_t>(t.head) * a.s.rows + row0 + lane]) : INFINITY;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int64_t r = rows > 0 ? row0 + min(8 * k + g, rows - 1) : row0 - w * 32;
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kDqThreads, 1) cross_dq_kernel(const __grid_co
                         if (w * 32 + r < t.rows) delta[r] = sum;
                     }
                 }
-                x[128 + lane] = lse * 1.4426950408889634f;
+                x[128 + lane] = lse;
                 mbar_arrive(aux_full + buf);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(do_empty);
@@ -904,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const bool live = r + 64 * y < p.rows;
-                        v[y] = live ? a.lse[at + 64 * y] * 1.4426950408889634f : INFINITY;
+                        v[y] = live ? lse_base2(a.lse[at + 64 * y]) : INFINITY;
                         v[2 + y] = live ? a.delta[at + 64 * y] : 0.0f;
                     }
                     if (f >= kAuxStages) ok = mbar_wait(aux_empty + st, (f / kAuxStages - 1) & 1, a.status);
@@ -1112,7 +1116,6 @@ struct FewGradArgs {
 template <int D>
 __global__ void __launch_bounds__(kFewThreads) cross_few_kernel(const __grid_constant__ FewGradArgs a) {
     constexpr int N = D / 64;
-    constexpr float kLog2e = 1.4426950408889634f;
     __shared__ float sums[kFewWarps][D];
     const int warp = threadIdx.x >> 5, unit = threadIdx.x & 7, slot = (threadIdx.x >> 3) & 3;
     cudaGridDependencySynchronize();
@@ -1123,7 +1126,7 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_kernel(const __grid_con
         load_part<N>(a.O + row * a.O_row + h * a.O_head, unit, x);
         load_part<N>(a.dO + row * a.dO_row + h * a.dO_head, unit, g);
         load_part<N>(a.q + row * a.q_row + h * a.q_head, unit, q);
-        const float delta = dot_part<N>(g, x), lse = a.lse[static_cast<int64_t>(h) * a.s.rows + row] * kLog2e;
+        const float delta = dot_part<N>(g, x), lse = lse_base2(a.lse[static_cast<int64_t>(h) * a.s.rows + row]);
         const uint16_t* k = a.k + group * a.k_group + kv * a.k_head;
         const uint16_t* v = a.v + group * a.v_group + kv * a.v_head;
 #pragma unroll 2
@@ -1173,7 +1176,7 @@ __global__ void __launch_bounds__(kFewThreads) cross_few_kernel(const __grid_con
         load_part<N>(a.q + row * a.q_row + h * a.q_head, unit, q);
         load_part<N>(a.dO + row * a.dO_row + h * a.dO_head, unit, g);
         load_part<N>(a.O + row * a.O_row + h * a.O_head, unit, o);
-        const float lse = a.lse[static_cast<int64_t>(h) * a.s.rows + row] * kLog2e;
+        const float lse = lse_base2(a.lse[static_cast<int64_t>(h) * a.s.rows + row]);
         const float s = dot_part<N>(q, k), dp = dot_part<N>(g, v), delta = dot_part<N>(g, o);
         const float p = ex2_approx(fmaf(s, a.s.scale_log2, -lse)), ds = p * (dp - delta);
 #pragma unroll

@@ -434,7 +434,8 @@ typedef struct {
  *   lengths     device int32 [groups]: the first lengths[g] states of a group are
  *               valid (taken as 0 below 0 and as keys above), the others are not
  *               looked at, whatever they hold; NULL = all.  With none a row's O is
- *               0 and its lse minus infinity.
+ *               0 and its lse minus infinity; so they are where all its scores are
+ *               minus infinity.
  *   lse         optional device float [heads][rows] output, 4-byte aligned: the
  *               natural logarithm of the softmax's denominator, for the backward
  *               pass.
