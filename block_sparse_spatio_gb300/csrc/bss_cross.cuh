@@ -116,13 +116,17 @@ __device__ __forceinline__ void write_rows(const uint4 (&v)[UNITS], uint16_t* to
     }
 }
 
+// Both; a lane whose row is not live writes zeros.
 template <int COLS>
-__device__ __forceinline__ void store_rows(uint32_t at, uint16_t* to, int64_t row_stride, int rows, float factor) {
+__device__ __forceinline__ void store_rows(uint32_t at, uint16_t* to, int64_t row_stride, int rows, float factor, bool live) {
 #pragma unroll
     for (int c = 0; c < COLS; c += 64) {  // 128 bytes a row at a time
         constexpr int kCols = COLS < 64 ? COLS : 64;
         uint4 u[kCols / 8];
         read_rows<kCols>(u, at + c, factor);
+#pragma unroll
+        for (int i = 0; i < kCols / 8; ++i)
+            if (!live) u[i] = make_uint4(0, 0, 0, 0);
         write_rows<kCols / 8>(u, to + c, row_stride, rows);
     }
 }

@@ -998,7 +998,8 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 mbar_arrive(aux_empty + st);
             }
             if (!ok) break;
-            // the key tile's sums: half 0 has dv, half 1 dk
+            // the key tile's sums: half 0 has dv, half 1 dk.  A masked state's are zeros, also
+            // where a row's dO or q is no number: 0 times it would not be.
             if (!(ok = __all_sync(0xFFFFFFFFu, mbar_wait(sums, part & 1, a.status)))) break;
             tc_fence_after();
             const uint32_t acc = tmem + lanes + (half == 0 ? kColA : kColB);
@@ -1006,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                 const int key0 = t.tile * kKeyTile + (warp & 3) * 32;
                 uint16_t* to = half == 0 ? a.dv + t.group * a.dv_group + key0 * a.dv_token + t.kv * a.dv_head
                                          : a.dk + t.group * a.dk_group + key0 * a.dk_token + t.kv * a.dk_head;
-                store_rows<D>(acc, to, half == 0 ? a.dv_token : a.dk_token, a.s.keys - key0, half == 0 ? 1.0f : a.scale);
+                store_rows<D>(acc, to, half == 0 ? a.dv_token : a.dk_token, a.s.keys - key0, half == 0 ? 1.0f : a.scale, live);
             } else {
                 // [16 bytes of the channels][key]: the join reads them so
                 const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (t.first > 0 ? 0 : 1);
@@ -1018,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads, 1) cross_dkv_kernel(const __grid_con
                     tmem_wait_ld();
 #pragma unroll
                     for (int y = 0; y < 8; ++y)
-                        to[(cc * 8 + y) * 128] = make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]);
+                        to[(cc * 8 + y) * 128] = live ? make_uint4(o[4 * y], o[4 * y + 1], o[4 * y + 2], o[4 * y + 3]) : make_uint4(0, 0, 0, 0);
                 }
             }
             tc_fence_before();
