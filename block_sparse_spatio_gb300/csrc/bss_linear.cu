@@ -1047,7 +1047,7 @@ int64_t groups_of(int64_t rows, int64_t per) { return (rows + per - 1) / per; }
 // How the rows are dealt to blocks for dz and its sums, and the workspace.
 struct GradPlan {
     bool makes_dz, sums;
-    int64_t groups, units, blocks, parts;  // parts: partial sums a group (of dgate), of dbias: blocks
+    int64_t groups, units, blocks;
     int32_t chunks;
     int64_t dz_at, dbias_at, dgate_at, sums_at, bytes;
     Cut dx, dweight;  // both products' split sums take turns in one place
