@@ -1209,7 +1209,7 @@ def cross_attention(q, k, v, O, lengths=None, lse=None, rows_per_group: int | No
     (default: one group), head h to key head h // (heads // kv_heads).  lengths:
     int32 [groups], the first so many states of a group are valid and the others
     are not looked at (None: all); without any a row's O is 0 and its lse -inf.
-    lse: optional float32 [heads][rows] output for the backward pass.  Returns O."""
+    softmax_scale: None or not positive: 1 / sqrt(d).  lse: optional float32 [heads][rows] output for the backward pass.  Returns O."""
     import torch
     shape = rows, heads, d = _rows_heads_shape(q, "q")
     device = _current_device()
@@ -1231,7 +1231,7 @@ def cross_attention_backward(dO, q, k, v, O, lse, dq, dk, dv, lengths=None, rows
     call's inputs, O and lse what it wrote; dq [rows][heads][d], dk and dv
     [groups][states][kv_heads][d]: bf16 outputs, strided as the inputs may be
     (views of one packed gradient, say), overwritten; states that are not valid
-    get zeros.  Sums over rows are taken in a fixed order.  workspace: taken from
+    get zeros.  States shared by several groups (a group stride of 0) are refused.  Sums over rows are taken in a fixed order.  workspace: taken from
     torch's allocator when None.  Returns (dq, dk, dv)."""
     import torch
     shape = rows, heads, d = _rows_heads_shape(q, "q")

@@ -22,7 +22,7 @@
 // P is rounded to bf16 on the way to its product, because the tensor cores take both
 // operands in one type and 32-bit ones at an eighth of the rate; l sums the unrounded P.
 //
-// 75,600 x 10 x 128 over 512 states, lse kept: 153 us (1,290 TFLOP/s).  A further key tile
+// 75,600 x 10 x 128 over 512 states, lse kept: 156 us (1,270 TFLOP/s).  A further key tile
 // costs 31.9 us (1,554 TFLOP/s, 90% of what cuBLAS sustains under the power limit; a step of both
 // halves moves 272 KB of shared memory, 2,125 cycles at 128 bytes, beneath 2,048 cycles
 // of products), the ends of the items 18 us.  Over 128 states 69 us, of which Q and O alone are 59 at a copy's rate.
@@ -523,10 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1) cross_forward_kernel(const __grid
 // A few rows a group fill no tile: a block takes a row and head, in 32 bits, eight lanes a
 // key, eight keys a warp at once; every eight lanes keep their own maximum and sums, which
 // are brought to one maximum at the end, in a fixed order.  Taken while every row and head
-// has an SM (us on the device, without and with tiles): 10 heads x 128, one row over 32 / 512 /
-// 2,048 states 2.7 / 5.5 / 14.8 and 4.9 / 8.2 / 22.7; 160 rows and heads 4.5 / 10.2 / 28.1 and
-// 5.1 / 8.4 / 22.8.  Bound by a round's chain of load, sum of eight lanes and exponentials
-// (0.4 us for 128 keys).
+// has an SM.  Heads of 128 over 64 / 512 / 2,048 / 8,192 states, us on the device, without
+// tiles and with: 10 rows and heads 2.7 / 5.3 / 14.6 / 51 and 4.8 / 8.1 / 22.5 / 80, 80 of
+// them 2.8 / 5.5 / 14.9 / 52 and 4.9 / 8.2 / 22.5 / 80, 150 of them 2.8 / 5.6 / 15.2 / 52 and
+// 5.0 / 8.3 / 22.7 / 80; 160 of them, a second round of blocks, 10.2 over 512 and 8.4.  Tiles
+// would be faster only where each row has states of its own that leave L2 together (150 rows and
+// heads, 2,048 states each, 157 MB: 30.1 and 27.5); 32 bits are kept there.  Bound by a round's
+// chain of load, sum of eight lanes and exponentials (0.4 us for 128 keys).
 struct FewArgs {
     CrossShape s;
     const uint16_t *q, *k, *v;

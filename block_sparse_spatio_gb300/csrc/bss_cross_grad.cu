@@ -5,9 +5,10 @@
 //
 // Two kernels, each with its own P and dS (7 products of rows x keys x d where 5
 // would do): one has the rows in TMEM's lanes and sums dq over the keys, the other
-// the keys and sums dk and dv over the rows.  One kernel would need dq's sums over
-// the key tiles in memory: atomics, whose order changes results, or a pass of their
-// own.
+// the keys and sums dk and dv over the rows.  One kernel would have to bring dq's sums
+// over the key tiles together: in memory by atomics, whose order changes results, or by a
+// pass of their own; or, for a few key tiles, in the shared memory of a cluster that holds
+// one a CTA, in a fixed order, which has not been built.
 //
 // dq: a CTA takes items of (group, 128 rows, head); per key tile the products
 // S(t+1), dP(t+1), dQ(t) follow one another (two dP in TMEM), so that the P and dS of a
@@ -26,8 +27,8 @@
 // operands in one type), dS once more beside the result's own rounding: errors are 1.4
 // times those of a gradient in 32 bits that is rounded at its store.
 //
-// 75,600 x 10 x 128 over 512 states: 532 us (930 TFLOP/s of five products, 1,300 of the seven
-// made): dq 251, dk and dv 257, their sums 14.  Both are bound by shared memory: dq moves
+// 75,600 x 10 x 128 over 512 states: 538 us (920 TFLOP/s of five products, 1,290 of the seven
+// made): dq 251, dk and dv 257, their sums 14 (one by one).  Both are bound by shared memory: dq moves
 // 240 KB a step (1,920 cycles at 128 bytes) beneath 1,536 cycles of products, dk and dv 256
 // KB and the rows' statistics (over 2,048 cycles) beneath 2,048.
 #include "bss_cross.cuh"
@@ -1091,7 +1092,7 @@ __global__ void __launch_bounds__(256) cross_join_kernel(const __grid_constant__
 // ---------------------------------------------------------------- few rows
 // A few rows a group (a token, a handful of queries) fill no tile: everything in 32 bits,
 // eight lanes a key with d / 8 channels each, four keys a warp at once.  The first blocks
-// have dq, one a row and head, and go over all its keys; the others have dk and dv of 32
+// have dq, one a row and head, and go over all its keys; the others have dk and dv of 64
 // keys each and go over the rows of all heads that share them.  No sums between blocks, no
 // workspace.  Bound by a key's chain of load, two sums of eight lanes and an exponential.
 // Taken for a few rows of a key head and few pairs of rows and keys (us on the device, without

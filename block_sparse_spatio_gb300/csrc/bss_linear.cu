@@ -12,9 +12,9 @@
 //   dx  A = dz [rows][out]   K-major   B = W [out][in]  MN-major
 //   dW  A = dz [rows][out]   MN-major  B = x [rows][in] MN-major
 //
-// 75,600 x 1,280 -> 5,120 with GELU 625 us, 75,600 x 5,120 -> 1,280 with gate and residual
-// 620 (1,585 and 1,600 TFLOP/s, 91 and 92% of what cuBLAS sustains under the power limit,
-// which bounds both); the gradients of the former 1,503: dz 300, dx 607, dW 614.
+// 75,600 x 1,280 -> 5,120 with GELU 636 us, 75,600 x 5,120 -> 1,280 with gate and residual
+// 630 (1,558 and 1,574 TFLOP/s, 90 and 91% of what cuBLAS sustains under the power limit,
+// which bounds both); the gradients of the former 1,539 (dz 300, dx and dW about 610 each).
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -60,9 +60,9 @@ __device__ __forceinline__ float2 smooth_share(float2 z, float2 w) {
 
 // The error function's form: the share of -|z| is e(z) g(|z|) with e = exp(-z^2 / 2) and g =
 // erfc(|z| / sqrt(2)) / (2 e), smooth and like 1 / |z| far out: t times a polynomial of
-// degree 8 in t = 1 / (1 + 0.34 |z|), fitted for the least relative error over 0..14.5 (3.4e-8,
-// 3e-7 with its roundings; e is 0 behind).  75,600 x 1,280 -> 5,120 with a bias: 690 us, with
-// erfcf in its place 1,175 (the tanh form 604, no activation 605).
+// degree 8 in t = 1 / (1 + 0.34 |z|), fitted for the least relative error over 0..14.5 (5.7e-8
+// with the coefficients as floats, 3e-7 with its roundings; e is 0 behind).  75,600 x 1,280 ->
+// 5,120 with a bias: 682 us (the tanh form 627, no activation 549), with erfcf in its place 1,175.
 constexpr float kErfSlope = 0.34f;
 
 __device__ __forceinline__ float2 erf_share(float2 z, float2& e) {
@@ -658,7 +658,8 @@ __global__ void __launch_bounds__(256) finish_kernel(const __grid_constant__ Fin
 // the operand of a small matrix product (16 output channels a block; lane 4 g + c loads
 // 16 bytes of rows g and g + 8: channels that follow one another, the same ones of x's
 // rows), 8 warps share the contraction, and their sums meet in shared memory.  1,280 ->
-// 7,680: one row 4.2 us (19.7 MB of weights), 16 rows 6.0; by tiles 17 rows 8.4.
+// 7,680: one row 4.7 us with the 19.7 MB of weights in L2 (9.0 from memory), 16 rows 6.8; by
+// tiles 17 rows 9.5.
 constexpr int kFewRows = 16;
 constexpr int kFewWarps = 8;
 
@@ -744,7 +745,9 @@ __global__ void __launch_bounds__(32 * kFewWarps) few_rows_kernel(const __grid_c
 
 // ---------------------------------------------------------------- dz and its sums over rows
 // A thread has 8 channels, a warp walks over rows; a block covers `units` rows that
-// share a gate, or (small groups) whole groups, one a warp at a time.  Bound by DRAM:
+// share a gate, or (small groups) whole groups, one a warp at a time.  dz is rounded to
+// bf16, the type of the other operand of both products that read it (the tensor cores take
+// both in one); dbias and dgate are summed from the 32-bit values.  Bound by DRAM:
 // 37,800 x 5,120 with GELU's slope and the bias sums 184 us, 6,310 GB/s (95% of a copy).
 struct DzArgs {
     const void* dout;

@@ -440,6 +440,8 @@ typedef struct {
  *               natural logarithm of the softmax's denominator, for the backward
  *               pass.
  *   softmax_scale  <= 0: 1 / sqrt(head_dim).
+ * Sums in 32 bits; the softmax's weights are rounded to bf16 on the way to their
+ * product with v, their sum is not (with rows * heads up to the number of SMs neither).
  * head_dim 64 or 128; kv_heads divides heads, at most 65535; rows and keys < 2^31. */
 typedef struct {
     int64_t rows;
@@ -462,7 +464,9 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream);
  *
  *   dO, q, k, v, O, lse, lengths   the gradient of O and the forward call's inputs and
  *               outputs (here O is an input, and not q).  k and v have a group
- *               stride of their own when there is more than one group.
+ *               stride of their own when there is more than one group: states that
+ *               several groups share are refused (with equal lengths the groups are
+ *               one; else give each its copy and add the copies' gradients).
  *   dq          token-major [rows][heads][head_dim];
  *   dk, dv      [groups][keys][kv_heads][head_dim], zero where a state is not
  *               valid; at least two of groups, keys and kv_heads follow one another
@@ -470,7 +474,9 @@ bss_status bss_cross_attention(const bss_cross_args* args, cudaStream_t stream);
  *   workspace   device memory of at least the size that
  *               bss_cross_attention_backward_workspace gives, 16-byte aligned, used
  *               by this call only until its work is done; NULL where that is 0.
- * Sums over rows are taken in a fixed order.  Outputs overlap no other tensor. */
+ * P and dS are rounded to bf16 on the way to their products (in the call of one
+ * launch they are not).  Sums over rows are taken in a fixed order.  Outputs overlap
+ * no other tensor. */
 typedef struct {
     int64_t rows;
     int64_t rows_per_group;
